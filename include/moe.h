@@ -438,6 +438,179 @@ MOE_API int moe_graphs_run(moe_graphs *graphs, int T, const void *x, void *out, 
 /* Frees the graph executables and the handle (not the arena). */
 MOE_API int moe_graphs_destroy(moe_graphs *graphs);
 
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder layer, for callers that run a whole layer
+ * around the MoE block: projections with 4-bit weights, rotary positions with
+ * the write into a paged key/value cache, and attention of the new tokens over
+ * that cache.  The conventions at the top of this file hold for these calls
+ * too (device pointers, 16-byte alignment, host-side validation before any
+ * launch, no allocation or synchronisation, graph capturable).
+ *
+ * A batch is n_seqs sequences.  Sequence b brings a chunk of new tokens, rows
+ * [cu_q[b], cu_q[b+1]) of q, k, v and out, and holds kv_len[b] keys, its new
+ * tokens' own among them (they are its last ones): new token j of a chunk of n
+ * has the place kv_len[b] - n + j in its sequence.  Place p is slot p mod
+ * page_size of page block_table[b][p / page_size].  Rows from cu_q[n_seqs] on
+ * (padding of a graph's batch) are neither read nor written.
+ *
+ * Sizes: 0 <= n_tokens <= 2^20, 0 <= n_seqs <= 2^16, n_kv_heads divides
+ * n_heads <= 1024, head_dim a multiple of 8 up to 256, max_pages * page_size
+ * and n_pages below 2^31.  max_q bounds the longest chunk (0 <= max_q <=
+ * n_tokens): the host knows it, and the kernel that suits it is chosen from it.
+ * dtype: MOE_DT_F32 or MOE_DT_BF16, for q, k, v, out and the cache.
+ *
+ * Device data is checked on the device: a page number outside [0, n_pages)
+ * among those a sequence uses, a chunk longer than max_q, a kv_len outside
+ * [0, max_pages * page_size] or a cu_q that falls or leaves [0, n_tokens]
+ * records MOE_ERR_DEVICE in the workspace's error word (moe_read_device_error).
+ * Nothing outside the arrays is touched then; that sequence's results are
+ * unspecified.
+ */
+typedef struct {
+    int32_t n_tokens, n_seqs;
+    int32_t n_heads, n_kv_heads, head_dim;
+    int32_t page_size, n_pages, max_pages;
+    int32_t max_q;
+    int32_t dtype;
+} moe_attn_shape;
+
+/* The sequences of a batch (device arrays): cu_q [n_seqs + 1], kv_len [n_seqs],
+ * block_table [n_seqs][max_pages] (entries past a sequence's last page are not
+ * read).  These need only their natural 4-byte alignment. */
+typedef struct {
+    const int32_t *cu_q;
+    const int32_t *kv_len;
+    const int32_t *block_table;
+} moe_attn_batch;
+
+/* The paged cache: slot s of head h of page p starts at element
+ * p * page_stride + h * head_stride + s * token_stride of k and of v, head_dim
+ * consecutive elements.  Strides are in elements, each a multiple of 16 bytes,
+ * so [pages][heads][slots][dim] and [pages][slots][heads][dim] both fit. */
+typedef struct {
+    void *k, *v;
+    int64_t page_stride, head_stride, token_stride;
+} moe_kv_cache;
+
+/*
+ * Workspace bytes of moe_rope_append and moe_paged_attention for this shape
+ * (host only, no CUDA call): 256-byte aligned, its first 2048 bytes (error word
+ * and counters) zeroed once before first use.  moe_rope_append needs those 2048
+ * bytes only.
+ */
+MOE_API int moe_attn_workspace_size(const moe_attn_shape *shape, size_t *bytes);
+
+/* Scaling of the rotation rates f_i = base^(-2i / rot_dim) for contexts longer
+ * than the trained ones, by `factor`:
+ *   LINEAR  f_i / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in the place of base
+ *   YARN    pairs that turn more than 32 times within trained_len positions keep
+ *           f_i, pairs that turn less than once take f_i / factor, the others a
+ *           linear ramp over i between; the rotated part is multiplied by
+ *           1 + 0.1 ln(factor) */
+enum moe_rope_scaling { MOE_ROPE_NONE = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3 };
+
+/*
+ * The rotation table (host only, no CUDA call): turns[i], i < rot_dim / 2, is
+ * the part of a full turn that pair i advances by each position, in units of
+ * 2^-64 turn, and *mscale the factor on the rotated part.  The kernel multiplies
+ * turns[i] by the position modulo 2^64, so that the angle's fraction of a turn
+ * is as exact at position 10^6 as at 1.  Copy turns to the device once.
+ * rot_dim: a multiple of 16 up to 256.  base > 1, factor >= 1 and, for YARN,
+ * trained_len > 0, else MOE_ERR_SHAPE.
+ */
+MOE_API int moe_rope_turns(int32_t rot_dim, int32_t scaling, double base, double factor, int32_t trained_len,
+                           uint64_t *turns, float *mscale);
+
+/*
+ * Rotary positions: the first rot_dim elements of a head (a multiple of 16, at
+ * most head_dim) are rotated in pairs, the others pass through.  Pair i is
+ * elements (2i, 2i+1) when interleaved, else (i, i + rot_dim/2):
+ *   (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t), t = position * f_i
+ * turns: DEVICE copy of moe_rope_turns' table.  q_gamma / k_gamma: NULL, or the
+ * weights [head_dim] (dtype of the shape) of an RMS norm of each q / k head
+ * before the rotation: x / sqrt(mean x^2 + eps) * gamma.
+ */
+typedef struct {
+    int32_t rot_dim;
+    int32_t interleaved;
+    float mscale;
+    float eps;
+    const uint64_t *turns;
+    const void *q_gamma, *k_gamma;
+} moe_rope;
+
+/*
+ * Normalises (if asked), rotates and stores the new tokens: q_out = rotated q,
+ * the rotated k and the plain v go to the cache slots of the tokens' places.
+ * Computed in fp32, rounded once.
+ *   q [n_tokens][n_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim]:
+ *     token rows q_stride / k_stride / v_stride elements apart (multiples of 16
+ *     bytes: slices of one projection's output), heads contiguous in a row
+ *   positions [n_tokens] int32 or NULL: the position of each token's rotation
+ *     (NULL: its place in the sequence)
+ *   q_out [n_tokens][n_heads][head_dim], rows q_out_stride apart; may be q itself
+ * A token whose place is negative (kv_len shorter than the chunk) is rotated but
+ * not stored.
+ */
+MOE_API int moe_rope_append(const moe_attn_shape *shape, const moe_rope *rope, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const moe_kv_cache *cache, const moe_attn_batch *batch, const int32_t *positions,
+                            void *q_out, int64_t q_out_stride, void *workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
+
+/*
+ * Attention of the new tokens over the cache, causal, with grouped heads (query
+ * head i reads key head i / (n_heads / n_kv_heads)): new token j of a chunk of n
+ * sees the keys at places 0 .. kv_len - n + j,
+ *   out = sum_p softmax_p(scale * q . k_p) v_p.
+ * A token that sees no key gets out = 0 and lse = -inf.  Slots at or past kv_len
+ * may hold anything (NaN included).  Scores, the softmax's maximum and sum and
+ * the output accumulate in fp32; with bf16 the probabilities are rounded to bf16
+ * for the product with v.  Results do not depend on timing (bitwise
+ * deterministic).
+ *   q, out [n_tokens][n_heads][head_dim], token rows q_stride / out_stride
+ *     elements apart (multiples of 16 bytes)
+ *   lse [n_tokens][n_heads] fp32 or NULL: natural log of the sum of
+ *     exp(scale * q . k_p)
+ *   scale: finite, else MOE_ERR_SHAPE
+ */
+MOE_API int moe_paged_attention(const moe_attn_shape *shape, const void *q, int64_t q_stride,
+                                const moe_kv_cache *cache, const moe_attn_batch *batch, float scale, void *out,
+                                int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
+
+/* Sizes of moe_q4_linear: T rows of x, K inputs, N outputs; 0 <= T <= 2^18,
+ * K a multiple of 8, N >= 1, K and N at most 2^22, q_block even and dividing K.
+ * x and the residual are bf16; out_dtype MOE_DT_BF16 or MOE_DT_F32. */
+typedef struct {
+    int32_t T, K, N;
+    int32_t out_dtype;
+    int32_t q_block;
+} moe_q4_linear_shape;
+
+/* One weight matrix [N][K] in the 4-bit format of moe_q4: codes [N][K/2] bytes,
+ * scales [N][K/q_block] bf16 (device), the codebook by value. */
+typedef struct {
+    const void *codes;
+    const void *scales;
+    float codebook[16];
+} moe_q4_weight;
+
+/*
+ * out = x . W^T (+ residual) with a 4-bit W, for decode batches (one pass over
+ * the weights for up to 64 rows; more rows repeat it):
+ *   out[t][n] = sum_k codebook[code[n][k]] * scale[n][k / q_block] * x[t][k]
+ *               (+ residual[t][n]),
+ * accumulated in fp32, rounded once.
+ *   x [T][K] bf16, rows x_stride elements apart (a multiple of 8)
+ *   residual [T][N] bf16, rows residual_stride apart, or NULL; out [T][N], rows
+ *     out_stride apart (any stride >= N); residual may be out itself
+ */
+MOE_API int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64_t x_stride,
+                          const moe_q4_weight *weight, const void *residual, int64_t residual_stride, void *out,
+                          int64_t out_stride, moe_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 MOE_API const char *moe_status_string(int status);
 

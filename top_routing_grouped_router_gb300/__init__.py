@@ -20,7 +20,9 @@ __all__ = [
     "moe_forward", "moe_forward_launches", "moe_read_device_error", "moe_status_string", "EXPORTED_SYMBOLS",
     "moe_forward_static_scratch", "moe_forward_rmsnorm", "moe_forward_lora", "moe_graph_buckets", "moe_graphs_arena_size",
     "DecodeGraphs", "moe_lora_pack_size", "moe_lora_pack", "pack_lora", "moe_static_scratch_read_error",
-    "moe_debug_set_waits",
+    "moe_debug_set_waits", "MoEAttnShape", "MoEAttnBatch", "MoEKVCache", "MoERope", "MoEQ4LinearShape", "MoEQ4Weight",
+    "make_attn_shape", "make_attn_batch", "make_kv_cache", "make_rope", "make_q4_linear_shape", "make_q4_weight",
+    "moe_attn_workspace_size", "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear",
 ]
 
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_Q4 = 0, 1, 2
@@ -33,7 +35,8 @@ EXPORTED_SYMBOLS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_group
                     "moe_forward", "moe_forward_launches", "moe_read_device_error", "moe_status_string",
                     "moe_forward_static_scratch", "moe_forward_rmsnorm", "moe_forward_lora", "moe_graph_buckets", "moe_graphs_arena_size", "moe_graphs_create",
                     "moe_graphs_bucket", "moe_graphs_run", "moe_graphs_destroy", "moe_lora_pack_size", "moe_lora_pack",
-                    "moe_static_scratch_read_error", "moe_debug_set_waits")
+                    "moe_static_scratch_read_error", "moe_debug_set_waits", "moe_attn_workspace_size",
+                    "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear")
 
 
 class MoEError(RuntimeError):
@@ -59,6 +62,34 @@ class MoEQ4(ctypes.Structure):
                 ("down_scales", ctypes.c_void_p), ("codebook", ctypes.c_float * 16)]
 
 
+class MoEAttnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_seqs", "n_heads", "n_kv_heads", "head_dim", "page_size",
+                                              "n_pages", "max_pages", "max_q", "dtype")]
+
+
+class MoEAttnBatch(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
+class MoEKVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class MoERope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_gamma", ctypes.c_void_p),
+                ("k_gamma", ctypes.c_void_p)]
+
+
+class MoEQ4LinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "out_dtype", "q_block")]
+
+
+class MoEQ4Weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("codebook", ctypes.c_float * 16)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -70,7 +101,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"CUDA library {library_path} is missing: build it with "
                                f"`python -m top_routing_grouped_router_gb300.build`")
         L = ctypes.CDLL(library_path)
-        vp, sz, i32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p
+        vp, sz, i32p, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
         sp = ctypes.POINTER(MoEShape)
         q4p = ctypes.POINTER(MoEQ4)
         sig = {
@@ -96,6 +127,12 @@ def lib() -> ctypes.CDLL:
             "moe_graphs_destroy": [vp],
             "moe_lora_pack_size": [sp, ctypes.POINTER(ctypes.c_size_t)],
             "moe_lora_pack": [sp, ctypes.POINTER(MoELora), vp, sz, vp],
+            "moe_attn_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t)],
+            "moe_rope_turns": [ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_double, ctypes.c_int32, vp,
+                               ctypes.POINTER(ctypes.c_float)],
+            "moe_rope_append": [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp],
+            "moe_paged_attention": [vp, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
+            "moe_q4_linear": [vp, vp, i64, vp, vp, i64, vp, i64, vp],
         }
         for name, argtypes in sig.items():
             f = getattr(L, name)
@@ -329,3 +366,114 @@ class DecodeGraphs:
             self.close()
         except Exception:
             pass
+
+
+# ---- the attention half of a decoder layer ----------------------------------------------
+
+_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def make_attn_shape(n_tokens, n_seqs, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, max_q,
+                    act="bf16") -> MoEAttnShape:
+    return MoEAttnShape(int(n_tokens), int(n_seqs), int(n_heads), int(n_kv_heads), int(head_dim), int(page_size),
+                        int(n_pages), int(max_pages), int(max_q), _DT[act] if isinstance(act, str) else int(act))
+
+
+def make_attn_batch(cu_q, kv_len, block_table) -> MoEAttnBatch:
+    """The sequences of a batch: int32 device tensors cu_q [B + 1], kv_len [B], block_table [B][max_pages]."""
+    for t in (cu_q, kv_len, block_table):
+        if not isinstance(t, int) and not (t.is_contiguous() and t.element_size() == 4):
+            raise ValueError("cu_q, kv_len and block_table are contiguous int32 tensors")
+    out = MoEAttnBatch(_ptr(cu_q), _ptr(kv_len), _ptr(block_table))
+    out.tensors = (cu_q, kv_len, block_table)
+    return out
+
+
+def make_kv_cache(k, v) -> MoEKVCache:
+    """A paged cache over device tensors k, v of logical shape [pages][kv heads][slots][head dim]: any strides (the
+    same for both) whose last is 1, so a [pages][slots][heads][dim] cache is passed as its transpose(1, 2)."""
+    if k.stride() != v.stride() or k.shape != v.shape or k.stride(3) != 1:
+        raise ValueError("k and v need equal shapes and strides, and contiguous head elements")
+    out = MoEKVCache(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2))
+    out.tensors = (k, v)
+    return out
+
+
+def moe_rope_turns(rot_dim, scaling="none", base=10000.0, factor=1.0, trained_len=0):
+    """(turns, mscale): the rotation table as a list of rot_dim / 2 integers in units of 2^-64 turn (host only)."""
+    turns = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
+    mscale = ctypes.c_float(0)
+    _check(lib().moe_rope_turns(int(rot_dim), _SCALING[scaling] if isinstance(scaling, str) else int(scaling),
+                                float(base), float(factor), int(trained_len), turns, ctypes.byref(mscale)),
+           "moe_rope_turns")
+    return list(turns), mscale.value
+
+
+def make_rope(rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, trained_len=0, q_gamma=None,
+              k_gamma=None, eps=1e-6, device=None) -> MoERope:
+    """The moe_rope struct with its table on `device`; q_gamma / k_gamma are the optional head norms' weights.  The
+    struct keeps the table and the weights alive."""
+    import torch
+    turns, mscale = moe_rope_turns(rot_dim, scaling, base, factor, trained_len)
+    table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device or "cuda")
+    out = MoERope(int(rot_dim), int(bool(interleaved)), mscale, float(eps), _ptr(table), _ptr(q_gamma),
+                  _ptr(k_gamma))
+    out.tensors = (table, q_gamma, k_gamma)
+    return out
+
+
+def make_q4_linear_shape(T, K, N, out="bf16", q_block=64) -> MoEQ4LinearShape:
+    return MoEQ4LinearShape(int(T), int(K), int(N), _DT[out] if isinstance(out, str) else int(out), int(q_block))
+
+
+def make_q4_weight(codes, scales, codebook) -> MoEQ4Weight:
+    """One 4-bit weight matrix: codes [N][K/2] uint8, scales [N][K/q_block] bf16, 16 codebook values (host)."""
+    out = MoEQ4Weight(_ptr(codes), _ptr(scales), (ctypes.c_float * 16)(*[float(c) for c in codebook]))
+    out.tensors = (codes, scales)
+    return out
+
+
+def _row_stride(t, what):
+    """Elements between the rows of a [rows][heads][dim] or [rows][cols] tensor whose rows are contiguous."""
+    st = t.stride()
+    if st[-1] != 1 or (len(st) == 3 and st[1] != t.shape[2] and t.shape[1] != 1):
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return st[0]
+
+
+def moe_attn_workspace_size(shape: MoEAttnShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_attn_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_attn_workspace_size")
+    return n.value
+
+
+def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, workspace=None, stream=None):
+    """q_out = rotated q; rotated k and v into their cache slots.  q, q_out [N][heads][dim], k, v [N][kv heads][dim]
+    (rows may be slices of a wider tensor)."""
+    rc = lib().moe_rope_append(ctypes.byref(shape), ctypes.byref(rope), q.data_ptr(), _row_stride(q, "q"),
+                               k.data_ptr(), _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"),
+                               ctypes.byref(cache), ctypes.byref(batch), _ptr(positions), q_out.data_ptr(),
+                               _row_stride(q_out, "q_out"), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if rc:
+        _check(rc, "moe_rope_append")
+
+
+def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, workspace=None, stream=None):
+    """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5."""
+    if lse is not None and not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    rc = lib().moe_paged_attention(ctypes.byref(shape), q.data_ptr(), _row_stride(q, "q"), ctypes.byref(cache),
+                                   ctypes.byref(batch), shape.head_dim ** -0.5 if scale is None else scale,
+                                   out.data_ptr(), _row_stride(out, "out"), _ptr(lse), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream))
+    if rc:
+        _check(rc, "moe_paged_attention")
+
+
+def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
+    """out = x . W^T (+ residual) with a 4-bit weight (make_q4_weight)."""
+    rc = lib().moe_q4_linear(ctypes.byref(shape), x.data_ptr(), _row_stride(x, "x"), ctypes.byref(weight),
+                             _ptr(residual), 0 if residual is None else _row_stride(residual, "residual"),
+                             out.data_ptr(), _row_stride(out, "out"), _stream(stream))
+    if rc:
+        _check(rc, "moe_q4_linear")

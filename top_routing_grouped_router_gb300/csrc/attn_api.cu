@@ -1,6 +1,7 @@
 // attn_api.cu -- the extern "C" entry points of the attention half of a decoder layer:
 // host-side validation, workspace sizes and the choice of kernel.
 #include "attn.cuh"
+#include "tc_common.cuh"
 
 #include <cmath>
 
@@ -98,7 +99,7 @@ extern "C" {
 int moe_attn_workspace_size(const moe_attn_shape *shape, size_t *bytes) {
     if (!bytes) return MOE_ERR_NULLPTR;
     MOE_TRY(validate(shape));
-    *bytes = kHdrBytes + attn::generic_ws_bytes(*shape);
+    *bytes = kHdrBytes + (attn::decode_supported(*shape) ? attn::decode_ws_bytes(*shape) : attn::generic_ws_bytes(*shape));
     return MOE_OK;
 }
 
@@ -180,8 +181,10 @@ int moe_paged_attention(const moe_attn_shape *shape, const void *q, int64_t q_st
     attn::Args a = make_args(s, *cache, *batch, q, q_stride, out, out_stride, workspace);
     a.lse = lse;
     a.scale = scale;
-    return launch_rc(attn::launch_generic(a, s.dtype, s, static_cast<char *>(workspace) + kHdrBytes,
-                                          reinterpret_cast<cudaStream_t>(stream)));
+    char *hdr = static_cast<char *>(workspace), *ws = hdr + kHdrBytes;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (attn::decode_supported(s)) return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), st));
+    return launch_rc(attn::launch_generic(a, s.dtype, s, ws, st));
 }
 
 int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64_t x_stride, const moe_q4_weight *weight,

@@ -10,8 +10,8 @@
 //
 // All (sequence, key head) pairs are laid end to end as steps of 16 keys, and every CTA takes
 // an equal share of that line, whatever the lengths.  A pair that a CTA holds whole is written
-// out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTA that
-// arrives last joins them in order, so the bits do not depend on timing.
+// out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
+// arrive last join them in the order of the keys, so the bits do not depend on timing.
 #include "attn.cuh"
 
 namespace moe {
@@ -33,7 +33,6 @@ struct Cfg {
     static constexpr int kRing = kStages * kStageBytes;
     static constexpr int kSmem = kWarps * kRing;  // also the join's buffers
     static_assert(kWarps * kRows * (D + 2) * 4 <= kSmem, "");
-    static_assert(kMaxGrid * kRows * 4 <= kSmem, "");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -67,19 +66,19 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ int steps_of(const Seq &s) { return s.q_len ? max(1, (s.kv_len + kStep - 1) / kStep) : 0; }
 
-// Sums (and with `mine` prefix-sums) one value a thread over the block.
-__device__ __forceinline__ int64_t block_scan(int64_t n, int64_t *total, int64_t *scratch) {
+// Exclusive prefix of one value a thread over the block, and the sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t n, uint32_t *total, uint32_t *scratch) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t incl = n;
+    uint32_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
     }
     __syncthreads();
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int64_t before = 0, sum = 0;
+    uint32_t before = 0, sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         before += w < warp ? scratch[w] : 0;
@@ -89,69 +88,199 @@ __device__ __forceinline__ int64_t block_scan(int64_t n, int64_t *total, int64_t
     return before + incl - n;
 }
 
+// The line of all steps cut into `ctas` shares that differ by at most one step: the first
+// `more` shares hold each + 1.
+struct Shares {
+    uint32_t each, more;
+    __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ uint32_t owner(uint32_t step) const {
+        const uint32_t edge = more * (each + 1);
+        return step < edge ? step / (each + 1) : more + (step - edge) / each;
+    }
+};
+
+// Partial results in the workspace.  A CTA leaves at most two: of the pair that its share
+// begins inside (slot 2 cta) and of the pair that begins in its share and goes on (slot
+// 2 cta + 1).  The CTAs of a pair are joined in groups of kGroup in the order of their keys,
+// then the groups, so that no CTA reads hundreds of partial results alone.  Each arrival is a
+// field of one word per CTA, the CTA that the pair or group starts in: bits 0-9 count the
+// groups of the pair that starts there, 10-19 the members of that pair's first group, 20-29
+// those of a later group that starts there.
+constexpr uint32_t kGroup = 16;
+constexpr int kJoinBatch = 8;  // parts whose outputs are requested together
+
+struct Parts {
+    uint32_t *words;
+    float *o;     // [slot][row][D]
+    float2 *ml;   // [slot][row]
+};
+
+// Adds one arrival; true for the last of n, which also puts the field back to 0.
+__device__ __forceinline__ bool arrive_last(uint32_t *word, int shift, uint32_t n, int *flag) {
+    __syncthreads();  // the block's partial results are written
+    if (threadIdx.x == 0) {
+        uint32_t old;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(1u << shift) : "memory");
+        const bool last = ((old >> shift) & 1023u) == n - 1;
+        if (last) atomicSub(word, n << shift);
+        *flag = last;
+    }
+    __syncthreads();
+    return *flag != 0;
+}
+
+// Joins parts [0, n) (their slots from slot_of) of `rows` rows; emit(row, d, float4, m, l).
+// sm: float2 [kJoinBatch][kRows] per batch of parts, then per-row results.
+template <int D, typename SlotOf, typename Emit>
+__device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows, float *sm, SlotOf slot_of, Emit emit) {
+    constexpr int PER = kRows * D / 4 / kThreads;  // float4 positions of a thread
+    const int tid = threadIdx.x;
+    const int mr = tid & (kRows - 1), mi = tid / kRows;  // (row, part) whose (max, sum) the thread reads
+    float4 acc[PER];
+    float m[PER], l[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        m[e] = kNegInf;
+        l[e] = 0.f;
+    }
+    float2 *sml = reinterpret_cast<float2 *>(sm);
+    for (uint32_t k0 = 0; k0 < n; k0 += kJoinBatch) {
+        float2 ml = make_float2(kNegInf, 0.f);
+        if (k0 + mi < n && mr < rows) {
+            const float *q = &p.ml[slot_of(k0 + mi) * kRows + mr].x;
+            asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "l"(q));
+        }
+        float4 v[PER][kJoinBatch];
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+            const uint32_t kk = min(k0 + k, n - 1);  // past the last: read again, with factor 0
+            const float *src = p.o + slot_of(kk) * kRows * D;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = e * kThreads + tid;
+                v[e][k] = i < rows * (D / 4) ? ldp16f(src + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        __syncthreads();
+        sml[mi * kRows + mr] = ml;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int r = (e * kThreads + tid) / (D / 4);
+            float mn = m[e];
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) mn = fmaxf(mn, sml[k * kRows + r].x);
+            const float f0 = m[e] == kNegInf ? 0.f : ex2(m[e] - mn);
+            acc[e].x *= f0;
+            acc[e].y *= f0;
+            acc[e].z *= f0;
+            acc[e].w *= f0;
+            l[e] *= f0;
+            m[e] = mn;
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                const float2 x = sml[k * kRows + r];
+                const float f = x.x == kNegInf ? 0.f : ex2(x.x - mn);
+                l[e] = fmaf(f, x.y, l[e]);
+                acc[e].x = fmaf(f, v[e][k].x, acc[e].x);
+                acc[e].y = fmaf(f, v[e][k].y, acc[e].y);
+                acc[e].z = fmaf(f, v[e][k].z, acc[e].z);
+                acc[e].w = fmaf(f, v[e][k].w, acc[e].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const int i = e * kThreads + tid;
+        if (i < rows * (D / 4)) emit(i / (D / 4), i % (D / 4) * 4, acc[e], m[e], l[e]);
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, int *counters, float *part_o, float2 *part_ml) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Parts parts) {
     using C = Cfg<D>;
     constexpr int NT = D / 8;        // 8-column tiles of O
     constexpr int KS = D / 16;       // 16-element steps of the head dimension
     constexpr int CH = D / 8;        // 16-byte pieces of a row
     constexpr int RPI = 32 / CH;     // rows a warp copies per instruction
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t scratch[kWarps + 2];
+    __shared__ uint32_t scratch[kWarps];
+    __shared__ uint32_t first[2];  // this CTA's first sequence and that sequence's first step
+    __shared__ Seq first_seq;
     __shared__ int last_flag;
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    const int G = a.group, Hkv = a.n_kv_heads;
+    const uint32_t G = a.group, Hkv = a.n_kv_heads;
 
     // this CTA's share of all steps
-    int64_t n0 = 0, total = 0;
+    uint32_t n0 = 0, before0 = 0, total = 0;
+    Seq s{};
     for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-        int64_t n = 0, sum;
-        if (b0 + tid < a.n_seqs) n = (int64_t)steps_of(load_seq(a, b0 + tid)) * Hkv;
-        if (b0 == 0) n0 = n;
-        block_scan(n, &sum, scratch);
+        uint32_t n = 0, sum;
+        if (b0 + tid < a.n_seqs) {
+            const Seq x = load_seq(a, b0 + tid);
+            n = steps_of(x) * Hkv;
+            if (b0 == 0) s = x;
+        }
+        const uint32_t before = block_scan(n, &sum, scratch);
+        if (b0 == 0) {
+            n0 = n;
+            before0 = before;
+        }
         total += sum;
     }
-    // no more CTAs than leave every warp a step
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kWarps));
-    const int64_t cta = blockIdx.x;
-    if (cta >= ctas || total == 0) return;
-    const int64_t u_end = (cta + 1) * total / ctas;
-    int64_t u = cta * total / ctas;
+    // no more CTAs than leave every warp two steps: fewer parts to join
+    const uint32_t ctas = max(1u, min(gridDim.x, total / (2 * kWarps))), cta = blockIdx.x;
+    const Shares sh{total / ctas, total % ctas};
+    if (cta >= ctas) return;
+    uint32_t u = sh.begin(cta);
+    const uint32_t u_end = sh.begin(cta + 1);
     if (u >= u_end) return;
-    int b = 0;
-    int64_t base = 0;  // first step of sequence b
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-        int64_t n = n0, sum;
-        if (b0 > 0) n = b0 + tid < a.n_seqs ? (int64_t)steps_of(load_seq(a, b0 + tid)) * Hkv : 0;
-        const int64_t before = base + block_scan(n, &sum, scratch);
-        if (u >= before && u < before + n) {
-            scratch[kWarps] = b0 + tid;
-            scratch[kWarps + 1] = before;
+    if (u >= before0 && u - before0 < n0) {
+        first[0] = tid;
+        first[1] = before0;
+        first_seq = s;
+    }
+    if (a.n_seqs > kThreads) {
+        uint32_t base = 0;
+        for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+            uint32_t n = 0, sum;
+            Seq x{};
+            if (b0 + tid < a.n_seqs) {
+                x = load_seq(a, b0 + tid);
+                n = steps_of(x) * Hkv;
+            }
+            const uint32_t before = base + block_scan(n, &sum, scratch);
+            if (u >= before && u - before < n) {
+                first[0] = b0 + tid;
+                first[1] = before;
+                first_seq = x;
+            }
+            base += sum;
+            if (u < base) break;
         }
-        if (u < base + sum) break;
-        base += sum;
     }
     __syncthreads();
-    b = int(scratch[kWarps]);
-    base = scratch[kWarps + 1];
+    int b = int(first[0]);
+    uint32_t base = first[1];
+    s = first_seq;
+    uint32_t steps = steps_of(s);
 
     const uint32_t ring = smem_addr(smem) + warp * C::kRing;
     const float sl2 = a.scale * kLog2e;
-    Seq s = load_seq(a, b);
-    int steps = steps_of(s);
 
     while (u < u_end) {
-        while (u >= base + (int64_t)steps * Hkv) {  // the next sequence with a chunk
-            base += (int64_t)steps * Hkv;
+        while (u - base >= steps * Hkv) {  // the next sequence with a chunk
+            base += steps * Hkv;
             s = load_seq(a, ++b);
             steps = steps_of(s);
         }
-        const int h = int((u - base) / steps);
-        const int64_t item = base + (int64_t)h * steps;  // its first step
-        const int step0 = int(u - item), step1 = int(min((int64_t)steps, u_end - item));
-        const int rows = min(s.q_len * G, kRows), past = s.kv_len - s.q_len;
+        const uint32_t h = (u - base) / steps;
+        const uint32_t item = base + h * steps;  // its first step
+        const int step0 = int(u - item), step1 = int(min(steps, u_end - item));
+        const int rows = min(s.q_len * int(G), kRows), past = s.kv_len - s.q_len;
 
         // the warp's keys: steps step0 + warp, + kWarps, ...  Lane r < 16 finds the cache offset of
         // key row r, one step before it is copied.
@@ -180,24 +309,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, in
             cp_commit();
         };
         int64_t next = find_row(0);
+
+        // Q as A fragments: rows g and g + 8, columns 16 ks + 2 t4 (+1) and + 8; a row past the
+        // last reads the first one's and is zeroed, so that all loads go out together
+        uint32_t q[KS][4];
+        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (int64_t)s.q0 * a.q_stride + (int64_t)h * G * D + t4 * 2;
+        const bool on0 = g < rows, on1 = g + 8 < rows;
+        const uint32_t r0 = on0 ? g : 0, r1 = on1 ? g + 8 : 0, j0 = r0 / G, j1 = r1 / G;
+        const uint16_t *q0 = qp + j0 * a.q_stride + (r0 - j0 * G) * D, *q1 = qp + j1 * a.q_stride + (r1 - j1 * G) * D;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[ks][e] = ldp(reinterpret_cast<const uint32_t *>(((e & 1) ? q1 : q0) + ks * 16 + (e >> 1) * 8));
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) {
             const int64_t cur = next;
             next = find_row(i + 1);
             copy(i, cur);
         }
-
-        // Q as A fragments: rows g and g + 8, columns 16 ks + 2 t4 (+1) and + 8
-        uint32_t q[KS][4];
-        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (int64_t)s.q0 * a.q_stride + (int64_t)h * G * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = g + (e & 1) * 8, c = ks * 16 + t4 * 2 + (e >> 1) * 8;
-                q[ks][e] = r < rows ? ldp(reinterpret_cast<const uint32_t *>(qp + (r / G) * a.q_stride + (r % G) * D + c)) : 0u;
-            }
-        const int seen0 = g < rows ? past + g / G + 1 : 0, seen1 = g + 8 < rows ? past + (g + 8) / G + 1 : 0;
+            for (int e = 0; e < 4; ++e) q[ks][e] = ((e & 1) ? on1 : on0) ? q[ks][e] : 0u;
+        const int seen0 = on0 ? past + int(j0) + 1 : 0, seen1 = on1 ? past + int(j1) + 1 : 0;
         const int seen_all = past + 1;  // keys that every row sees
         float o[NT][4];
 #pragma unroll
@@ -299,15 +434,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, in
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             *reinterpret_cast<float2 *>(jo + (warp * kRows + g) * D + j * 8 + t4 * 2) = make_float2(o[j][0], o[j][1]);
-            *reinterpret_cast<float2 *>(jo + (warp * kRows + g + 8) * D + j * 8 + t4 * 2) = make_float2(o[j][2], o[j][3]);
+            if (rows > 8)
+                *reinterpret_cast<float2 *>(jo + (warp * kRows + g + 8) * D + j * 8 + t4 * 2) = make_float2(o[j][2], o[j][3]);
         }
         if (t4 == 0) {
             jm[warp * kRows + g] = make_float2(m0, l0);
             jm[warp * kRows + g + 8] = make_float2(m1, l1);
         }
         __syncthreads();
-        const int64_t c0 = ((item + 1) * ctas - 1) / total, c1 = ((item + steps) * ctas - 1) / total;
-        const bool whole = c0 == c1;
+        auto write_out = [&](int r, int d, float4 v, float m, float l) {
+            const uint32_t j = uint32_t(r) / G, head = h * G + (r - j * G);
+            const int64_t tok = s.q0 + j;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D + d) =
+                make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            if (a.lse && d == 0) a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+        };
+        auto write_part = [&](size_t slot, int r, int d, float4 v, float m, float l) {
+            *reinterpret_cast<float4 *>(parts.o + (slot * kRows + r) * D + d) = v;
+            if (d == 0) parts.ml[slot * kRows + r] = make_float2(m, l);
+        };
+        const bool whole = step0 == 0 && step1 == int(steps);
+        const uint32_t c0 = step0 == 0 ? cta : sh.owner(item);
         const size_t slot = (size_t)cta * 2 + (cta == c0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -326,61 +474,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, in
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            const int tok = s.q0 + r / G, head = h * G + r % G;
-            if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D + d) =
-                    make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                if (a.lse && d == 0)
-                    a.lse[(size_t)tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-            } else {
-                *reinterpret_cast<float4 *>(part_o + (slot * kRows + r) * D + d) = acc;
-                if (d == 0) part_ml[slot * kRows + r] = make_float2(m, l);
-            }
+            if (whole)
+                write_out(r, d, acc, m, l);
+            else
+                write_part(slot, r, d, acc, m, l);
         }
         if (!whole) {
-            __syncthreads();
-            if (tid == 0) last_flag = arrive_acq_rel(counters + c0) == int(c1 - c0);
-            __syncthreads();
-            if (last_flag) {
-                const int n = int(c1 - c0) + 1;
-                if (tid == 0) counters[c0] = 0;  // as the next call expects it
-                float *fac = reinterpret_cast<float *>(smem);  // [part][row]
-                auto slot_of = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
-                for (int r = warp; r < rows; r += kWarps) {
-                    float m = kNegInf, l = 0.f;
-                    for (int i = lane; i < n; i += 32) m = fmaxf(m, ldp(&part_ml[slot_of(i) * kRows + r].x));
-#pragma unroll
-                    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-                    for (int i = lane; i < n; i += 32) {
-                        const float *p = &part_ml[slot_of(i) * kRows + r].x;
-                        const float f = ldp(p) == kNegInf ? 0.f : ex2(ldp(p) - m);
-                        fac[i * kRows + r] = f;
-                        l = fmaf(f, ldp(p + 1), l);
-                    }
-                    l = warp_sum(l);
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    for (int i = lane; i < n; i += 32) fac[i * kRows + r] *= inv;
-                    if (a.lse && lane == 0)
-                        a.lse[(size_t)(s.q0 + r / G) * a.n_heads + h * G + r % G] =
-                            l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-                }
-                __syncthreads();
-                for (int i = tid; i < rows * (D / 4); i += kThreads) {
-                    const int r = i / (D / 4), d = i % (D / 4) * 4;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = 0; k < n; ++k) {
-                        const float4 v = ldp16f(part_o + (slot_of(k) * kRows + r) * D + d);
-                        const float f = fac[k * kRows + r];
-                        acc.x = fmaf(f, v.x, acc.x);
-                        acc.y = fmaf(f, v.y, acc.y);
-                        acc.z = fmaf(f, v.z, acc.z);
-                        acc.w = fmaf(f, v.w, acc.w);
-                    }
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + (s.q0 + r / G) * a.out_stride +
-                                               (int64_t)(h * G + r % G) * D + d) =
-                        make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+            const uint32_t c1 = step1 == int(steps) ? cta : sh.owner(item + steps - 1);
+            const uint32_t n = c1 - c0 + 1, groups = (n + kGroup - 1) / kGroup, k = (cta - c0) / kGroup;
+            const uint32_t first_cta = c0 + k * kGroup, members = min(kGroup, n - k * kGroup);
+            auto slot_of = [&](uint32_t i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };  // i-th CTA of the pair
+            float *sm = reinterpret_cast<float *>(smem);
+            if (arrive_last(parts.words + first_cta, k == 0 ? 10 : 20, members, &last_flag)) {
+                auto member = [&](uint32_t i) { return slot_of(k * kGroup + i); };
+                if (groups == 1) {
+                    join_parts<D>(parts, members, rows, sm, member, write_out);
+                } else {
+                    const size_t to = slot_of(k * kGroup);  // in the place of the group's first
+                    join_parts<D>(parts, members, rows, sm, member,
+                                  [&](int r, int d, float4 v, float m, float l) { write_part(to, r, d, v, m, l); });
+                    if (arrive_last(parts.words + c0, 0, groups, &last_flag))
+                        join_parts<D>(parts, groups, rows, sm, [&](uint32_t i) { return slot_of(i * kGroup); }, write_out);
                 }
             }
         }
@@ -395,16 +509,18 @@ cudaError_t launch_typed(const Args &a, char *hdr, char *ws, int grid, cudaStrea
     if (e != cudaSuccess) return e;
     float *o = reinterpret_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(o + (size_t)kMaxGrid * 2 * kRows * D);
-    return launch_pdl(decode_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, a,
-                      reinterpret_cast<int *>(hdr + kCounters), o, ml);
+    const Parts p{reinterpret_cast<uint32_t *>(hdr + kCounters), o, ml};
+    return launch_pdl(decode_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, a, p);
 }
 
 }  // namespace
 
-// bf16, head sizes 64 and 128, and at most 16 query rows a key head.
+// bf16, head sizes 64 and 128, at most 16 query rows a key head, and a line of steps that
+// 32 bits count even if every sequence fills its row of the block table.
 bool decode_supported(const moe_attn_shape &s) {
+    const double steps = double(s.n_seqs) * s.n_kv_heads * ((double)s.max_pages * s.page_size / kStep + 1);
     return s.dtype == MOE_DT_BF16 && (s.head_dim == 64 || s.head_dim == 128) &&
-           (int64_t)s.max_q * (s.n_heads / s.n_kv_heads) <= kRows;
+           (int64_t)s.max_q * (s.n_heads / s.n_kv_heads) <= kRows && steps < 2147483648.0;
 }
 size_t decode_ws_bytes(const moe_attn_shape &s) { return (size_t)kMaxGrid * 2 * kRows * (s.head_dim + 2) * 4; }
 

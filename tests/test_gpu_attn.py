@@ -212,6 +212,21 @@ def test_attention_graph_and_streams():
         assert ((x.out.cpu().double() - out).abs() <= tol).all()
 
 
+def test_attention_wait_that_runs_out():
+    # the softmax arrivals of the chunk kernel can never be enough: the wait ends after its limit
+    # with an error recorded, and the next ordinary call is right
+    bt = make_batch(*ATTN["chunk over cache"], seed=7)
+    d = Dev(bt)
+    moe.moe_debug_set_waits(1_000_000, 1)
+    try:
+        assert d.attend(0.1) == -7
+    finally:
+        moe.moe_debug_set_waits()
+    assert d.attend(0.1) == 0
+    out, _, tol, _ = attention(bt, 0.1)
+    assert ((d.out.cpu().double() - out).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_attention_far_pages(q_len):
     # element offsets past 2^32 in the cache: the pages of a small batch lie at its far end

@@ -146,6 +146,9 @@ cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, ch
 bool decode_supported(const moe_attn_shape &s);
 size_t decode_ws_bytes(const moe_attn_shape &s);
 cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
+bool chunk_supported(const moe_attn_shape &s);
+size_t chunk_ws_bytes(const moe_attn_shape &s);
+cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int dtype, const Partials &p, cudaStream_t st);
 
 }  // namespace attn

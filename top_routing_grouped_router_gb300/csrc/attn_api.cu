@@ -99,7 +99,9 @@ extern "C" {
 int moe_attn_workspace_size(const moe_attn_shape *shape, size_t *bytes) {
     if (!bytes) return MOE_ERR_NULLPTR;
     MOE_TRY(validate(shape));
-    *bytes = kHdrBytes + (attn::decode_supported(*shape) ? attn::decode_ws_bytes(*shape) : attn::generic_ws_bytes(*shape));
+    *bytes = kHdrBytes + (attn::decode_supported(*shape)  ? attn::decode_ws_bytes(*shape)
+                          : attn::chunk_supported(*shape) ? attn::chunk_ws_bytes(*shape)
+                                                          : attn::generic_ws_bytes(*shape));
     return MOE_OK;
 }
 
@@ -184,6 +186,7 @@ int moe_paged_attention(const moe_attn_shape *shape, const void *q, int64_t q_st
     char *hdr = static_cast<char *>(workspace), *ws = hdr + kHdrBytes;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (attn::decode_supported(s)) return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), st));
+    if (attn::chunk_supported(s)) return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), st));
     return launch_rc(attn::launch_generic(a, s.dtype, s, ws, st));
 }
 

@@ -1,0 +1,761 @@
+// attn_chunk.cu -- attention of chunks of new tokens over the paged cache on the 5th-generation
+// tensor cores (bf16, head sizes 64 and 128).
+//
+// The query rows that share a key head (tokens x heads of the group) form tiles of up to 128
+// rows.  A CTA works on two tiles at a time ("item": a sequence, a key head, 2 x 128 rows) and
+// goes over the keys in steps of 128:
+//   S_t = Q_t K^T      M = 128, N = 128, into TMEM
+//   P_t = 2^(S_t - m)  by four warps per tile, one row a thread, written over S_t as bf16
+//   O_t += P_t V       A = P_t from TMEM, V as it lies in the cache (keys x head: N-major)
+// The MMA warp issues P0 V, S0', P1 V, S1': while one tile's softmax runs, the tensor cores work
+// on the other's products.  The running maximum m may lag behind: only when a row's maximum
+// grows by more than 2^8 is O rescaled (by the softmax warps, in TMEM); until then the larger
+// probabilities are exact in bf16 terms all the same, since the scale of a row cancels.
+//
+// K and V tiles come by TMA through the block table, one box a page.  All items are laid end
+// to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
+// share's end leave fp32 partial results that a second kernel joins.
+#include "attn.cuh"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 320;   // warps 0-3, 4-7: softmax of tile 0, 1; warp 8: MMA; warp 9: loads
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kM = 128, kKeys = 128;
+constexpr int kMaxCtas = 160;   // one per SM (152)
+constexpr int kMaxSegs = 16;    // segments prepared at a time
+constexpr float kLag = 8.f;     // log2 of the growth of a row's maximum that O tolerates
+constexpr int kJoinRows = 16;   // rows of a block of the join kernel
+
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kM * D * 2;                  // one Q tile, one K or V stage
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 2048;
+    static_assert(kSmem <= 232448, "");
+};
+
+// One item, or the part of it in this CTA's share.
+struct Seg {
+    int b, h, tok0, q0, q_len, kv_len;  // tok0: first token of the chunk in the item
+    int step0, step1;                   // key steps of this share
+    int slot;                           // -1: whole item; else the slot of the partial results
+    int tiles;                          // 1 or 2
+};
+// What the join kernel needs of an item that starts in a CTA's share and goes on past it.
+struct Rec {
+    int n, h, tok0, q0, q_len, last;  // n: parts (0: none); last: the last CTA
+};
+
+// sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0, by the Euclid-like recursion.
+__device__ __forceinline__ uint64_t floor_sum(uint64_t n, uint32_t m, uint32_t a, uint64_t b) {
+    uint64_t sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const uint64_t y = (uint64_t)a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const uint32_t t = a;
+        a = m;
+        m = t;
+    }
+    return sum;
+}
+
+// Steps of item i of a chunk: the keys that its last token sees, at least one step.
+__device__ __forceinline__ uint32_t item_steps(const Seq &s, uint32_t i, uint32_t tt2) {
+    const int64_t keys = min((int64_t)s.kv_len - s.q_len + (int64_t)(i + 1) * tt2, (int64_t)s.kv_len);
+    return keys <= kKeys ? 1u : uint32_t((keys + kKeys - 1) / kKeys);
+}
+__device__ __forceinline__ uint32_t items_of(const Seq &s, uint32_t tt2) { return (s.q_len + tt2 - 1) / tt2; }
+
+// Steps of items [0, i) of a chunk.
+__device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, uint32_t tt2) {
+    if (i == 0) return 0;
+    const uint32_t n = items_of(s, tt2);
+    const uint32_t last = i == n ? item_steps(s, n - 1, tt2) : 0;
+    const uint32_t full = i == n ? n - 1 : i;  // items that hold tt2 tokens
+    const int64_t past = (int64_t)s.kv_len - s.q_len;
+    // items that see no key have one step each
+    uint32_t none = 0;
+    if (past < 0) none = min((uint64_t)full, (uint64_t)(-past) / tt2);
+    const uint64_t b = uint64_t(past + (int64_t)(none + 1) * tt2 + kKeys - 1);  // > kKeys - 1
+    return none + uint32_t(floor_sum(full - none, kKeys, tt2, b)) + last;
+}
+
+struct Shares {
+    uint32_t each, more;
+    __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ uint32_t owner(uint32_t step) const {
+        const uint32_t edge = more * (each + 1);
+        return step < edge ? step / (each + 1) : more + (step - edge) / each;
+    }
+};
+
+// TMEM columns.
+constexpr uint32_t kColS = 0, kColO = 256;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 32 columns of this thread's TMEM lane, no wait; the wait is tmem_ld_done.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t ta, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(ta)
+        : "memory");
+}
+// Waits for every load of the thread; r passes through so that no use moves above the wait.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[128]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Matrix descriptor of a V tile as the B operand of P V: keys x 64-element slabs of the head,
+// 128-byte rows (one key's 64 elements), 128-byte swizzle, N-major: 8-key groups 1024 B apart
+// (stride offset), slabs kKeys * 128 B apart (leading offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t((kKeys * 128) >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+struct Ctx {
+    Args a;
+    uint32_t tt;        // tokens of a tile
+    float *part_o;      // [slot][2 * kM][D]
+    float2 *part_ml;    // [slot][2 * kM]
+    Rec *rec;           // [kMaxCtas]
+    unsigned long long wait_ns;
+    int extra_need;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ CUtensorMap map_q,
+                                                            const __grid_constant__ CUtensorMap map_k,
+                                                            const __grid_constant__ CUtensorMap map_v,
+                                                            const __grid_constant__ Ctx c) {
+    using C = Cfg<D>;
+    constexpr int kSlabs = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *ctrl = smem + (2 + C::kStages) * C::kTile;
+    uint64_t *kv_full = reinterpret_cast<uint64_t *>(ctrl);  // [kStages]
+    uint64_t *kv_empty = kv_full + C::kStages;               // [kStages]
+    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
+    uint64_t *drain = o_empty + 2;
+    Seg *segs = reinterpret_cast<Seg *>(drain + 1);  // [kMaxSegs]
+    uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
+    int *nseg = reinterpret_cast<int *>(scan + 16);
+    volatile int *abort = nseg + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(nseg + 2);
+    uint32_t *cursor = tmem_slot + 1;  // [4]: sequence, its first step, its steps per head, step within the line
+    Seq *cur_seq = reinterpret_cast<Seq *>(cursor + 4);
+
+    const Args &a = c.a;
+    const Waits wt{a.err, abort, c.wait_ns, smem_u32(const_cast<int *>(abort))};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t tt = c.tt, tt2 = 2 * tt, G = a.group, Hkv = a.n_kv_heads;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&kv_full[i]), 1);
+            mbar_init(smem_u32(&kv_empty[i]), 1);
+        }
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_empty), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&s_full[t]), 1);
+            mbar_init(smem_u32(&p_full[t]), kM + c.extra_need);
+            mbar_init(smem_u32(&o_full[t]), 1);
+            mbar_init(smem_u32(&o_empty[t]), kM);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // ---------------------------------------------------------------- the CTA's share
+    // Steps of all heads of the sequences, scanned over the block in chunks of kThreads.
+    auto scan_block = [&](uint32_t n, uint32_t *sum) {
+        uint32_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        uint32_t before = 0, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            before += w < warp ? scan[w] : 0;
+            total += scan[w];
+        }
+        *sum = total;
+        return before + incl - n;
+    };
+    auto seq_steps = [&](const Seq &s) { return steps_before(s, items_of(s, tt2), tt2); };
+    uint32_t total = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+        uint32_t n = 0, sum;
+        if (b0 + tid < a.n_seqs) n = seq_steps(load_seq(a, b0 + tid)) * Hkv;
+        scan_block(n, &sum);
+        total += sum;
+    }
+    const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, total / 2));
+    const Shares sh{total / ctas, total % ctas};
+    const uint32_t u_begin = cta < ctas ? sh.begin(cta) : 0, u_end = cta < ctas ? sh.begin(cta + 1) : 0;
+    if (tid == 0) c.rec[cta].n = 0;
+    if (u_begin < u_end) {
+        uint32_t base = 0;
+        for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+            uint32_t n = 0, sum;
+            Seq s{};
+            if (b0 + tid < a.n_seqs) {
+                s = load_seq(a, b0 + tid);
+                n = seq_steps(s) * Hkv;
+            }
+            const uint32_t before = base + scan_block(n, &sum);
+            if (u_begin >= before && u_begin - before < n) {
+                cursor[0] = b0 + tid;
+                cursor[1] = before;
+                cursor[2] = n / Hkv;
+                *cur_seq = s;
+            }
+            base += sum;
+            if (u_begin < base) break;
+        }
+        if (tid == 0) cursor[3] = u_begin;
+    }
+    __syncthreads();
+
+    // ---------------------------------------------------------------- roles
+    int stage = 0;                      // ring position: load and MMA warps
+    uint32_t phase = 0;
+    uint32_t q_phase = 0, s_phase = 0, o_phase = 0;
+    uint32_t p_phase = 0, oe_phase = 3;  // bit t: tile t
+    uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
+    bool ok = true;
+
+    for (uint32_t u = u_begin; u < u_end && ok;) {
+        // up to kMaxSegs segments, found by warp 0
+        if (warp == 0) {
+            int b = int(cursor[0]);
+            uint32_t first = cursor[1], per_head = cursor[2], w = cursor[3];
+            Seq s = *cur_seq;
+            int k = 0;
+            uint32_t h = 0, i = 0, item0 = 0;
+            bool located = false;
+            while (w < u_end && k < kMaxSegs) {
+                if (!located) {
+                    while (w - first >= per_head * Hkv) {  // the next sequence with a chunk
+                        first += per_head * Hkv;
+                        s = load_seq(a, ++b);
+                        per_head = seq_steps(s);
+                    }
+                    h = (w - first) / per_head;
+                    const uint32_t rem = w - first - h * per_head;
+                    // the last item that begins at or before rem: 32 candidates a round
+                    uint32_t lo = 0, n = items_of(s, tt2);
+                    while (n > 1) {
+                        const uint32_t each = (n + 31) / 32;
+                        const uint32_t cand = lo + lane * each;
+                        const bool at = lane * each < n && steps_before(s, cand, tt2) <= rem;
+                        const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, at));
+                        lo += last * each;
+                        n = min(each, n - last * each);
+                    }
+                    i = lo;
+                    item0 = first + h * per_head + steps_before(s, i, tt2);
+                    located = true;
+                }
+                const uint32_t steps = item_steps(s, i, tt2);
+                const uint32_t end = min(item0 + steps, u_end);
+                const bool whole = w == item0 && end == item0 + steps;
+                if (lane == 0) {
+                    Seg g;
+                    g.b = b;
+                    g.h = int(h);
+                    g.tok0 = int(i * tt2);
+                    g.q0 = s.q0;
+                    g.q_len = s.q_len;
+                    g.kv_len = s.kv_len;
+                    g.step0 = int(w - item0);
+                    g.step1 = int(end - item0);
+                    g.slot = whole ? -1 : int(cta * 2 + (w == item0 ? 1 : 0));
+                    g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
+                    segs[k] = g;
+                    if (!whole && w == item0) {
+                        const int last = int(sh.owner(item0 + steps - 1));
+                        c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len, last};
+                    }
+                }
+                ++k;
+                w = end;
+                if (end == item0 + steps) {
+                    item0 += steps;
+                    if (++i == items_of(s, tt2)) {
+                        i = 0;
+                        ++h;
+                        if (h == Hkv) located = false;  // the next sequence
+                    }
+                }
+            }
+            if (lane == 0) {
+                *nseg = k;
+                cursor[0] = b;
+                cursor[1] = first;
+                cursor[2] = per_head;
+                cursor[3] = w;
+                *cur_seq = s;
+            }
+        }
+        __syncthreads();
+        const int ns = *nseg;
+        u = cursor[3];
+
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------ loads
+            const int ps = a.page_size, box = min(ps, kKeys);
+            for (int k = 0; k < ns && ok; ++k) {
+                const Seg g = segs[k];
+                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                const int boxes_max = kKeys / box;
+                auto page_of = [&](int step) {  // lane i: the page of box i of the step
+                    const int p = step * kKeys + lane * box;
+                    return lane < boxes_max && p < keys ? load_page(a, g.b, p / ps) : -1;
+                };
+                int page = page_of(g.step0);
+                ok = mbar_wait(smem_u32(q_empty), q_phase ^ 1, wt);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const int rows = int(G * tt);
+                    mbar_arrive_expect_tx(smem_u32(q_full), uint32_t(g.tiles * rows * D * 2));
+                    for (int t = 0; t < g.tiles; ++t)
+                        for (int d = 0; d < kSlabs; ++d)
+                            tma_load_3d(smem_u32(smem + t * C::kTile + d * kM * 128), &map_q, d * 64, int(g.h * G),
+                                        g.q0 + g.tok0 + t * int(tt), smem_u32(q_full));
+                }
+                q_phase ^= 1;
+                __syncwarp();
+                for (int step = g.step0; step < g.step1 && ok; ++step) {
+                    const int next = step + 1 < g.step1 ? page_of(step + 1) : -1;
+                    const int have = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t full = smem_u32(&kv_full[stage]);
+                        if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(have * box * D * 2));
+                        __syncwarp();
+                        if (page >= 0) {
+                            const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile + lane * box * 128);
+                            const int tok = ps > kKeys ? step * kKeys % ps : 0;
+                            for (int d = 0; d < kSlabs; ++d)
+                                tma_load_4d(dst + d * kKeys * 128, kv ? &map_v : &map_k, d * 64, tok, g.h, page, full);
+                        }
+                        ring_waited |= 1u << stage;
+                        if (++stage == C::kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    page = next;
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------ MMAs
+            const uint32_t id_s = instr_desc(kM, kKeys), id_o = instr_desc(kM, D) | (1u << 16);
+            auto wait = [&](uint64_t *bar, uint32_t par) {
+                const bool r = mbar_wait(smem_u32(bar), par, wt);
+                ok = __all_sync(0xffffffffu, r);
+                return ok;
+            };
+            auto advance = [&](int &st, uint32_t &ph) {
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            auto issue_s = [&](int t, int st) {
+                const uint64_t qa = smem_desc(smem_u32(smem + t * C::kTile)), kb = smem_desc(smem_u32(smem + (2 + st) * C::kTile));
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks / 4) * (kM * 128 / 16) + (ks % 4) * 2;  // 16-byte units
+                    mma_bf16_warp(tmem + kColS + t * kKeys, qa + off, kb + off, id_s, ks > 0);
+                }
+                mma_commit_warp(smem_u32(&s_full[t]));
+            };
+            for (int k = 0; k < ns && ok; ++k) {
+                const Seg g = segs[k];
+                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                if (!wait(q_full, q_phase)) break;
+                q_phase ^= 1;
+                if (!wait(&kv_full[stage], phase)) break;
+                tc_fence_after();
+                int ks_stage = stage;  // the stage of the next K
+                for (int t = 0; t < g.tiles; ++t) issue_s(t, ks_stage);
+                mma_commit_warp(smem_u32(&kv_empty[ks_stage]));
+                advance(stage, phase);
+                if (g.step1 - g.step0 == 1) mma_commit_warp(smem_u32(q_empty));
+                for (int step = g.step0; step < g.step1 && ok; ++step) {
+                    const bool more = step + 1 < g.step1;
+                    const int v_stage = stage;
+                    if (!wait(&kv_full[v_stage], phase)) break;
+                    advance(stage, phase);
+                    // keys past the last that the item sees: their slots may hold anything (or were not
+                    // loaded), and 0 * NaN is NaN: zero the rows
+                    const int live = keys - step * kKeys;
+                    if (live < kKeys) {
+                        const int from = max(live, 0);
+                        const uint32_t vb = smem_u32(smem + (2 + v_stage) * C::kTile);
+                        for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
+#pragma unroll
+                            for (int d = 0; d < kSlabs; ++d)
+                                sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    for (int t = 0; t < g.tiles && ok; ++t) {
+                        if (step == g.step0) {  // O was read out by the previous segment's epilogue
+                            if (!wait(&o_empty[t], (oe_phase >> t) & 1)) break;
+                            oe_phase ^= 1u << t;
+                        }
+                        if (!wait(&p_full[t], (p_phase >> t) & 1)) break;
+                        p_phase ^= 1u << t;
+                        tc_fence_after();
+                        const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
+#pragma unroll
+                        for (int ks = 0; ks < kKeys / 16; ++ks)
+                            mma_bf16_tmem_warp(tmem + kColO + t * 128, tmem + kColS + t * kKeys + ks * 8,
+                                               vb + ks * (2048 / 16), id_o, step > g.step0 || ks > 0);
+                        if (!more) mma_commit_warp(smem_u32(&o_full[t]));
+                        if (more) {
+                            if (t == 0 && !wait(&kv_full[stage], phase)) break;
+                            issue_s(t, stage);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit_warp(smem_u32(&kv_empty[v_stage]));
+                    if (more) {
+                        mma_commit_warp(smem_u32(&kv_empty[stage]));
+                        advance(stage, phase);
+                        if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                    }
+                }
+            }
+        } else {
+            // ------------------------------------------------ softmax and epilogue, one row a thread
+            const int t = warp >> 2, r = tid & (kM - 1);
+            const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
+            const uint32_t ts = tmem + lanes + kColS + t * kKeys, to = tmem + lanes + kColO + t * 128;
+            const bool neg = a.scale < 0.f;
+            // a zero scale would make -inf * 0 of masked scores: any tiny factor gives the same result
+            const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+            for (int k = 0; k < ns && ok; ++k) {
+                const Seg g = segs[k];
+                if (t >= g.tiles) continue;
+                const int j = g.tok0 + t * int(tt) + r / int(G);  // this row's token in the chunk
+                const bool live = r < int(G * tt) && j < g.q_len;
+                const int past = g.kv_len - g.q_len;
+                const int seen = live ? max(past + j + 1, 0) : 0;
+                const int seen_all = past + g.tok0 + t * int(tt) + 1;  // keys that every row of the tile sees
+                float m = kNegInf, l = 0.f;
+                for (int step = g.step0; step < g.step1; ++step) {
+                    ok = mbar_wait(smem_u32(&s_full[t]), s_phase, wt);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    s_phase ^= 1;
+                    tc_fence_after();
+                    uint32_t x[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32_issue(ts + i * 32, x + i * 32);
+                    tmem_ld_done(x);
+                    if (neg) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
+                    }
+                    const int k0 = step * kKeys;
+                    if (k0 + kKeys > seen_all) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (k0 + i >= seen) x[i] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+                    for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4])));
+                    const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                    if (step == g.step0) {
+                        m = mn;
+                    } else if (__any_sync(0xffffffffu, (mn - m) * sl2 > kLag)) {
+                        // -inf - -inf is NaN and compares false: a row that has seen nothing stays
+                        const float f = mn == kNegInf ? 1.f : ex2((m - mn) * sl2);
+                        m = mn;
+                        l *= f;
+#pragma unroll
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + i, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(to + i, o);
+                        }
+                    }
+                    const float z = m == kNegInf ? 0.f : m * sl2;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 128; i += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float p = ex2(fmaf(__uint_as_float(x[i + e]), sl2, -z));
+                            x[i + e] = __float_as_uint(p);
+                            sum[e] += p;
+                        }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        x[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                    tmem_st64(ts, x);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&p_full[t]));
+                }
+                if (!ok) break;
+                ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                o_phase ^= 1;
+                tc_fence_after();
+                const int64_t tok = g.q0 + j;
+                const int head = g.h * int(G) + r % int(G);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const size_t prow = (size_t)max(g.slot, 0) * 2 * kM + t * kM + r;
+                uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D;
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + i, o);
+                    if (g.slot >= 0) {
+                        if (live) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(c.part_o + prow * D + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(o[e + q]) * inv;
+                            store8(dst + i + e, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&o_empty[t]));
+                if (live) {
+                    if (g.slot >= 0)
+                        c.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m * sl2, l);
+                    else if (a.lse)
+                        a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m * sl2 + log2f(l)) * kLn2;
+                }
+            }
+        }
+        // the segment list is free; a role that gave up ends the CTA
+        ok = !__syncthreads_or(!ok);
+    }
+
+    // ---------------------------------------------------------------- end
+    // an aborting CTA waits for its own copies and MMAs before it gives up its memory
+    if (warp == kLoadWarp && !ok) {
+        for (int i = 0; i < C::kStages; ++i) {
+            // the last fill of stage i was in the current phase if i < stage, else in the one before
+            const uint32_t par = i < stage ? phase : phase ^ 1;
+            if (ring_waited >> i & 1) mbar_wait_drain(smem_u32(&kv_full[i]), par, wt);
+        }
+        mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
+    }
+    if (warp == kMmaWarp) {  // every MMA and every arrival of its commits is over before the CTA ends
+        mma_commit_warp(smem_u32(drain));
+        mbar_wait_drain(smem_u32(drain), 0, wt);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Joins the parts of the items that were cut.  Block (cta, rows): the item that starts in the
+// share of `cta` and goes on, rows [16 y, 16 y + 16) of its 256; one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ Ctx c) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const Args &a = c.a;
+    const int *rp = reinterpret_cast<const int *>(c.rec + blockIdx.x);
+    const int n = ldp(rp);
+    if (n == 0) return;
+    const int h = ldp(rp + 1), tok0 = ldp(rp + 2), q0 = ldp(rp + 3), q_len = ldp(rp + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
+    const uint32_t cta = blockIdx.x;
+    auto slot_of = [&](int i) { return (size_t)(cta + i) * 2 + (i == 0 ? 1 : 0); };
+    for (int row = blockIdx.y * kJoinRows + warp; row < int(blockIdx.y + 1) * kJoinRows; row += 4) {
+        const int t = row / kM, r = row % kM, j = tok0 + t * int(c.tt) + r / G;
+        if (r >= G * int(c.tt) || j >= q_len) continue;
+        float m = kNegInf;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, ldp(&c.part_ml[slot_of(i) * 2 * kM + row].x));
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+        float l = 0.f;
+        constexpr int PER = D / 32;
+        float acc[PER] = {};
+        for (int i = 0; i < n; ++i) {
+            const size_t pr = slot_of(i) * 2 * kM + row;
+            const float pm = ldp(&c.part_ml[pr].x), pl = ldp(&c.part_ml[pr].y);
+            const float f = pm == kNegInf ? 0.f : ex2(pm - m);
+            l = fmaf(f, pl, l);
+            float v[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[e] = ldp(c.part_o + pr * D + e * 32 + lane);
+            if (f != 0.f) {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t tok = q0 + j;
+        const int head = h * G + r % G;
+        uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) dst[e * 32 + lane] = f32_to_bf16_bits(acc[e] * inv);
+        if (a.lse && lane == 0) a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    }
+}
+
+int64_t max_items(const moe_attn_shape &s) {
+    const int64_t tt2 = 2 * (kM / (s.n_heads / s.n_kv_heads));
+    return ((s.n_tokens + tt2 - 1) / tt2 + s.n_seqs) * s.n_kv_heads;
+}
+double max_steps(const moe_attn_shape &s) {
+    return double(max_items(s)) * ((double)s.max_pages * s.page_size / kKeys + 1);
+}
+// CTAs: no more than the steps there can be.
+int max_ctas(const moe_attn_shape &s) {
+    const double n = max_steps(s) / 2;
+    return n < 1 ? 1 : n < kMaxCtas ? int(n) : kMaxCtas;
+}
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int D>
+bool set_smem_attr() {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        if (cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
+            return false;
+        attr_set[dev] = true;
+    }
+    return true;
+}
+
+template <int D>
+cudaError_t launch_typed(const Ctx &c, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, int grid,
+                         cudaStream_t st) {
+    if (!set_smem_attr<D>()) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_pdl(chunk_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, mv, c);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * kM / kJoinRows), dim3(128), 0, st, c);
+}
+
+}  // namespace
+
+// bf16, head sizes 64 and 128, a group that fits a tile, pages that fill key steps (or that key
+// steps fill), and a line of steps that 32 bits count.
+bool chunk_supported(const moe_attn_shape &s) {
+    const int G = s.n_heads / s.n_kv_heads;
+    const bool pages = s.page_size >= 8 && (kKeys % s.page_size == 0 || s.page_size % kKeys == 0);
+    return s.dtype == MOE_DT_BF16 && (s.head_dim == 64 || s.head_dim == 128) && G <= kM && pages &&
+           max_steps(s) < 2147483648.0;
+}
+
+size_t chunk_ws_bytes(const moe_attn_shape &s) {
+    const size_t slots = 2 * (size_t)max_ctas(s);
+    return round256(kMaxCtas * sizeof(Rec)) + round256(slots * 2 * kM * sizeof(float2)) + slots * 2 * kM * s.head_dim * 4;
+}
+
+cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, cudaStream_t st) {
+    Ctx c{};
+    c.a = a;
+    c.tt = uint32_t(kM / a.group);
+    const int cap = max_ctas(s), grid = sms < cap ? sms : cap;
+    c.rec = reinterpret_cast<Rec *>(ws);
+    c.part_ml = reinterpret_cast<float2 *>(ws + round256(kMaxCtas * sizeof(Rec)));
+    c.part_o = reinterpret_cast<float *>(reinterpret_cast<char *>(c.part_ml) + round256((size_t)2 * cap * 2 * kM * sizeof(float2)));
+    c.wait_ns = wait_limit_ns();
+    c.extra_need = debug_extra_need();
+    const uint64_t D = s.head_dim;
+    CUtensorMap mq, mk, mv;
+    const uint64_t qd[3] = {D, (uint64_t)s.n_heads, (uint64_t)s.n_tokens}, qs[2] = {D * 2, (uint64_t)a.q_stride * 2};
+    const uint32_t qb[3] = {64, (uint32_t)a.group, c.tt};
+    // a dimension of one element is never stepped over: any legal stride stands in for its own
+    const uint64_t row = D * 2;
+    const uint64_t kd[4] = {D, (uint64_t)s.page_size, (uint64_t)s.n_kv_heads, (uint64_t)s.n_pages};
+    const uint64_t ks[3] = {(uint64_t)a.token_stride * 2, s.n_kv_heads > 1 ? (uint64_t)a.head_stride * 2 : row,
+                            s.n_pages > 1 ? (uint64_t)a.page_stride * 2 : row};
+    const uint32_t kb[4] = {64, (uint32_t)(s.page_size < kKeys ? s.page_size : kKeys), 1, 1};
+    if (!make_map_nd(&mq, a.q, 3, qd, qs, qb) || !make_map_nd(&mk, a.k, 4, kd, ks, kb) || !make_map_nd(&mv, a.v, 4, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    return D == 128 ? launch_typed<128>(c, mq, mk, mv, grid, st) : launch_typed<64>(c, mq, mk, mv, grid, st);
+}
+
+}  // namespace attn
+}  // namespace moe

@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     __shared__ uint32_t first[2];  // this CTA's first sequence and that sequence's first step
     __shared__ Seq first_seq;
     __shared__ int last_flag;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t G = a.group, Hkv = a.n_kv_heads;
 

@@ -45,8 +45,8 @@ template <typename T, int NJ>
 __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part, int tt) {
     extern __shared__ float4 smem4[];
     __shared__ int scratch[4 + kThreads / 32];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int D = a.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *Q = reinterpret_cast<float *>(smem4), *K = Q + kRows * D, *V = K + kKeys * (D + 4);
     float *P = V + kKeys * D + warp * kKeys * 4;  // [key][row] of this warp
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part
 // Joins the parts of a row, one warp a row: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int64_t rows = (int64_t)a.n_tokens * a.n_heads;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, D = a.head_dim;

@@ -24,10 +24,10 @@ constexpr int kAnyRows = 8;  // rows of x of one pass over the weights
 template <typename T>
 __global__ void __launch_bounds__(kAnyThreads) q4_any_kernel(Q4Args a) {
     __shared__ float book[16];
-    griddep_launch_dependents();
     if (threadIdx.x < 16) book[threadIdx.x] = a.codebook[threadIdx.x];
     __syncthreads();
     griddep_wait();
+    griddep_launch_dependents();
     const int n = blockIdx.x * (kAnyThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int t0 = blockIdx.y * kAnyRows, rows = min(kAnyRows, a.T - t0);
     if (n >= a.N) return;

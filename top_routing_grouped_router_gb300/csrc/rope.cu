@@ -30,8 +30,8 @@ template <typename T, int LG>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs r) {
     __shared__ float2 cs[kMaxPairs];
     __shared__ int where[2];  // the token's sequence, its place
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const attn::Args &a = r.a;
     const int t = blockIdx.x, tid = threadIdx.x;
     if (tid == 0) where[0] = -1;

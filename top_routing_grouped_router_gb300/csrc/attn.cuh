@@ -156,6 +156,7 @@ cudaError_t launch_combine(const Args &a, int dtype, const Partials &p, cudaStre
 cudaError_t launch_rope(const moe_attn_shape &s, const moe_rope &r, const attn::Args &a, const void *k, int64_t k_stride,
                         const void *v, int64_t v_stride, const int32_t *positions, cudaStream_t st);
 cudaError_t launch_q4_linear(const moe_q4_linear_shape &s, const void *x, int64_t x_stride, const moe_q4_weight &w,
-                             const void *res, int64_t res_stride, void *out, int64_t out_stride, cudaStream_t st);
+                             const void *res, int64_t res_stride, void *out, int64_t out_stride, int sms,
+                             cudaStream_t st);
 
 }  // namespace moe

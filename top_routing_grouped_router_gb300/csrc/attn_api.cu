@@ -204,7 +204,7 @@ int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64_t x_str
     if (x_stride % 8 || misaligned(x) || misaligned(out) || misaligned(weight->codes) || misaligned(weight->scales) ||
         misaligned(residual))
         return MOE_ERR_ALIGN;
-    return launch_rc(launch_q4_linear(s, x, x_stride, *weight, residual, residual_stride, out, out_stride,
+    return launch_rc(launch_q4_linear(s, x, x_stride, *weight, residual, residual_stride, out, out_stride, tc::sm_count(),
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -2,8 +2,9 @@
 // q_block inputs, a 16-entry codebook), for batches of few rows.  What bounds it is the read of
 // the codes, half a byte a weight, and next to it the instructions that unpack them.
 //
-// q4_mma_kernel: a CTA takes 16 outputs at a time.  Its eight warps split the inputs; each
-// streams its part of the 16 code rows through a cp.async ring of its own, 64 inputs a stage,
+// q4_mma_kernel: a CTA takes 16 outputs at a time (16 to 128 where there are many, "side").  Its
+// eight warps split the inputs; each
+// streams its part of the 16 code rows through a cp.async ring of its own, 128 inputs a stage,
 // unpacks the codes in registers to the A operand of mma.sync (m16n8k16, outputs x inputs) and
 // multiplies with the rows of x, which lie in shared memory in the order of the B fragments.
 // A block of inputs that shares a scale is summed by the MMA alone, then added to the fp32
@@ -14,7 +15,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <cstring>
 
 namespace moe {
 namespace {
@@ -87,25 +87,44 @@ cudaError_t launch_any(const Q4Args &a, int out_dtype, cudaStream_t st) {
                                    : launch_pdl(q4_any_kernel<uint16_t>, grid, block, 0, st, a);
 }
 
-// ---------------------------------------------------------------- tensor cores, q_block a multiple of 32
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kOut = 16;         // outputs of a tile
-constexpr int kIn = 64;          // inputs of a stage
-constexpr int kDepth = 8;        // stages of a warp's ring
-constexpr int kCodeBytes = kOut * kIn / 2, kScaleBytes = kOut * 2 * 4, kStageBytes = kCodeBytes + kScaleBytes;
-constexpr int kRingBytes = kWarps * kDepth * kStageBytes;
-constexpr int kLutBytes = 256 * 32 * 8;
+// ---------------------------------------------------------------- tensor cores
+constexpr int kStrip = 16;       // outputs of an MMA
+constexpr int kIn = 128;         // inputs of a stage, two halves of 64
 constexpr int kMaxSlices = 8;    // CTAs of a cluster that split the inputs
 constexpr int kMaxSmem = 232448;
+constexpr int kLutBytes = 256 * 32 * 8;
+
+// What a variant's shared memory holds.  NT: 8-row tiles of x; MT: strips of 16 outputs a warp works
+// on, 1 or 2: two read each fragment of x once, and share the cost of a stage's copies.
+template <int NT, int MT, bool kFine, bool kAffine>
+struct Var {
+    static constexpr int kWarps = MT == 2 ? 16 : 8, kThreads = kWarps * 32;
+    static constexpr int kDepth = MT == 2 || NT >= 2 ? 3 : 4;  // stages of a warp's ring
+    static constexpr int kOut = MT * kStrip;                 // outputs of a warp
+    static constexpr int kCols = NT * 8;                     // rows of x
+    static constexpr int kCodes = kOut * kIn / 2;            // code bytes of a stage
+    static constexpr int kScalesRow = kFine ? 4 : 2;         // scale words of an output
+    static constexpr int kStage = kCodes + kOut * kScalesRow * 4;
+    static constexpr int kRedStride = kOut + 4;              // padded column of sums: no bank conflicts
+    static constexpr int kRed = kWarps * kCols * kRedStride * 4;
+    static constexpr int kRing = kWarps * kDepth * kStage;
+    static constexpr int kFixed = kRed + kRing + (kAffine ? 0 : kLutBytes);
+    // 64 inputs of x: the fragments, and per block the start values (twice each, see below)
+    static constexpr int kHalf = NT * 1024 + (kAffine ? (kFine ? 2 : 1) * NT * 64 : 0);
+    static int part_bytes(int side) { return 2 * kCols * side * kOut * 4; }
+    static int max_stages() { return (kMaxSmem - kFixed) / (2 * kHalf); }                           // of one CTA
+    static int max_stages_sliced() { return (kMaxSmem - kFixed - part_bytes(kWarps)) / (2 * kHalf); }  // of a cluster's
+};
 
 struct MmaArgs {
     Q4Args a;
     int T0, rows;       // rows of x of this launch
     int slices;         // cluster size
-    int tiles;          // output tiles
-    int slice_stages;   // the most stages of 64 inputs that one CTA has
-    uint64_t per_block; // ceil(2^32 / m), q_block = 32 m: 32-input part j lies in block (j * per_block) >> 32
-    uint32_t centre;    // affine codebook: bf16x2 of 16 + j0
+    int side;           // output strips side by side in a CTA: its warps are side x (warps / side input parts)
+    int tiles;          // tiles of side strips
+    int slice_halves;   // the most 64-input halves that one CTA has
+    int shift;          // log2(q_block / 64) (not fine)
+    float centre;       // affine codebook: 16 + j0
     float step;         // affine codebook: its step; else 1
 };
 
@@ -138,70 +157,133 @@ __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with another addend: starts a sum.
+__device__ __forceinline__ void mma16816_from(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, const uint4 &z) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %11, %12, %13};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(__uint_as_float(z.x)),
+                   "f"(__uint_as_float(z.y)), "f"(__uint_as_float(z.z)), "f"(__uint_as_float(z.w)));
+}
 // (w & 0x00780078) | 0x41804180: two codes, already shifted to bits 3 .. 6 of each half, become
-// the bf16 pair 16 + j; minus 16 + j0 that is j - j0, every step exact.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask, uint32_t bias, uint32_t centre) {
+// the bf16 pair 16 + j, exactly.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask, uint32_t bias) {
     uint32_t r;
-    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, %2, %3, 0xEA;\n\tsub.rn.bf16x2 %0, t, %4;\n\t}"
-        : "=r"(r) : "r"(w), "r"(mask), "r"(bias), "r"(centre));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bias));
     return r;
 }
+// One 16-bit half of a word as a bf16 value: sel 0x1044 the low one, 0x3244 the high one.
+constexpr uint32_t kLow = 0x1044, kHigh = 0x3244;
+__device__ __forceinline__ float half_of(uint32_t w, uint32_t sel) { return __uint_as_float(__byte_perm(w, 0, sel)); }
 
-// NT: 8-row tiles of x.  kFine: scales may change every 32 inputs (else every 64 or more).
-// kAffine: codebook step * (j - j0); else a table in shared memory, each value as bf16 hi + lo.
-template <int NT, bool kFine, bool kAffine>
-__global__ void __launch_bounds__(kThreads) q4_mma_kernel(const __grid_constant__ MmaArgs m) {
+// NT: 8-row tiles of x.  kFine: q_block 32, four blocks a stage; else 64 times a power of two.
+// kAffine: codebook step * (j - j0).  The MMA multiplies the exact integers 16 + j, and each sum
+// starts at -(16 + j0) sum x of its block (fp32, found once a CTA), which leaves sum (j - j0) x: the
+// subtraction costs no instruction, and about a factor 5 of the fp32 sum's accuracy (16 + j
+// against j - j0).  Else a table in shared memory, each value as bf16 hi + lo.
+template <int NT, int MT, bool kFine, bool kAffine>
+__global__ void __launch_bounds__(Var<NT, MT, kFine, kAffine>::kThreads)
+q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     namespace cg = cooperative_groups;
-    constexpr int kCols = NT * 8;
-    constexpr int kRedBufs = NT <= 2 ? 2 : 1;
+    using V = Var<NT, MT, kFine, kAffine>;
+    constexpr int kWarps = V::kWarps, kThreads = V::kThreads, kDepth = V::kDepth, kOut = V::kOut, kCols = V::kCols;
+    constexpr int kStage = V::kStage, kRedStride = V::kRedStride, kRowBytes = kIn / 2;
     extern __shared__ __align__(128) unsigned char smem[];
     const Q4Args &a = m.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    float *red = reinterpret_cast<float *>(smem);                        // [kRedBufs][kWarps][kCols][kOut]
-    float *part = red + kRedBufs * kWarps * kCols * kOut;                // [2][kCols][kOut]
-    unsigned char *ring_base = reinterpret_cast<unsigned char *>(part + 2 * kCols * kOut);
-    unsigned char *lut = ring_base + kRingBytes;
-    unsigned char *xs = lut + (kAffine ? 0 : kLutBytes);                 // [stage][NT][2][32] x 16 bytes
-    const uint32_t ring = smem_addr(ring_base) + warp * kDepth * kStageBytes;
+    float *red = reinterpret_cast<float *>(smem);  // [kWarps][kCols][kRedStride]
+    unsigned char *ring_base = smem + V::kRed;
+    unsigned char *lut = ring_base + V::kRing;
+    unsigned char *xs = lut + (kAffine ? 0 : kLutBytes);  // [half][NT][2][32] x 16 bytes
+    unsigned char *starts = xs + (size_t)m.slice_halves * NT * 1024;  // [block][NT][4] x 16 bytes (affine)
+    float *part = reinterpret_cast<float *>(xs + (size_t)m.slice_halves * V::kHalf);  // [2][kCols][wide], slices > 1
+    const uint32_t ring = smem_addr(ring_base) + warp * kDepth * kStage;
 
     // this CTA's stages of the inputs, and this warp's
     const int stages = (a.K + kIn - 1) / kIn;
     const int slice = int(blockIdx.x) % m.slices, group = int(blockIdx.x) / m.slices, groups = int(gridDim.x) / m.slices;
     const int s0 = int((int64_t)stages * slice / m.slices), s1 = int((int64_t)stages * (slice + 1) / m.slices);
-    const int w0 = s0 + (s1 - s0) * warp / kWarps, w1 = s0 + (s1 - s0) * (warp + 1) / kWarps, mine = w1 - w0;
+    const int parts = kWarps / m.side, beside = warp % m.side, in_part = warp / m.side;
+    const int w0 = s0 + (s1 - s0) * in_part / parts, w1 = s0 + (s1 - s0) * (in_part + 1) / parts, mine = w1 - w0;
     const int my_tiles = (m.tiles - group + groups - 1) / groups;
-    const int total = mine * my_tiles;
+    const int wide = m.side * kOut, wide_log2 = __ffs(wide) - 1;
 
-    // the block of inputs [32 j, 32 j + 32)
-    auto block_of = [&](int j) { return uint32_t(uint64_t(j) * m.per_block >> 32); };
-
-    // the ring: copies run kDepth - 1 stages ahead, across tiles
-    const int blocks = a.K / a.q_block;
-    int p_tile = group, p_stage = 0;
-    const int crow = lane >> 1, chalf = lane & 1;
-    auto copy = [&](int i) {
-        if (i < total) {
-            const uint32_t dst = ring + (i % kDepth) * kStageBytes;
-            const int k = (w0 + p_stage) * kIn;
-            const int n = p_tile * kOut + crow;
-            const bool on = n < a.N && k + chalf * 32 < a.K;
-            cp16(dst + lane * 16, a.codes + (on ? (size_t)n * (a.K / 2) + k / 2 + chalf * 16 : 0), on ? 16 : 0);
-            // scales of the rows: one of each 32 inputs when they may differ there, else one a stage.
-            // 2 bytes each; the copy writes 4, the rest zero
-            if (kFine || chalf == 0) {
-                const size_t e = (size_t)n * blocks + block_of(k / 32 + chalf);
-                const size_t word = on ? e & ~size_t(1) : 0;
-                cp4(dst + kCodeBytes + lane * 4, a.scales + word, on ? ((e & 1) ? 4 : 2) : 0);
+    // The ring: copies run kDepth - 1 stages ahead, across tiles.  Piece (lane mod 4) of row lane / 4
+    // (+ 8 i) is 16 bytes; the pieces of a row are permuted so that the reads below have no bank
+    // conflicts.  The scales of row lane / 2 (+ 16 i), half lane % 2 are copied with the aligned word
+    // they lie in (2 bytes of it at the array's end), the reader picks the half by the index's parity.
+    const uint32_t blocks = uint32_t(a.K / a.q_block);
+    const size_t row_bytes = a.K / 2, row8 = 8 * row_bytes;
+    const int crow = lane >> 2, cpiece = lane & 3, srow = lane >> 1, shalf = lane & 1;
+    int p_n = group * wide + beside * kOut, p_stage = w0, left = mine * my_tiles;
+    const uint8_t *src = a.codes + (size_t)(p_n + crow) * row_bytes + (size_t)w0 * kRowBytes + cpiece * 16;
+    const size_t tile_skip = (size_t)groups * wide * row_bytes - (size_t)mine * kRowBytes;
+    uint32_t sbase = uint32_t(p_n + srow) * blocks;
+    const uint32_t ring_end = ring + kDepth * kStage;
+    uint32_t dst = ring;
+    const uint32_t code_at = crow * kRowBytes + ((cpiece ^ (crow >> 1 & 3)) * 16);  // row + 8: same permutation
+    const int K = a.K, N = a.N, shift = m.shift, tile_step = groups * wide;
+    // whole stages of whole tiles with one or two scales a half advance by constants; what is cut by
+    // the matrix's edge, or has wider blocks, is worked out
+    const bool simple = K % kIn == 0 && (kFine || shift == 0);
+    bool inside = simple && p_n + kOut <= N;
+    constexpr int kScaleStep = kFine ? 8 : 4;  // bytes of a row's scales in a stage
+    const char *scales = reinterpret_cast<const char *>(a.scales);
+    const size_t strip_scales = (size_t)kStrip * blocks * 2;
+    const uint32_t e0 = sbase + (kFine ? w0 * 4 + shalf * 2 : w0 * 2 + shalf);
+    const char *ssrc = scales + (size_t)(e0 & ~1u) * 2;
+    const size_t scale_skip = (size_t)tile_step * blocks * 2 - (size_t)mine * kScaleStep;
+    const int odd = e0 & 1;  // stages and tiles advance by even counts
+    auto copy = [&]() {
+        if (left > 0) {
+            if (inside) {
+                const uint8_t *s = src;
+#pragma unroll
+                for (int i = 0; i < kOut / 8; ++i, s += row8) cp16(dst + code_at + i * 8 * kRowBytes, s, 16);
+                const char *q = ssrc;
+#pragma unroll
+                for (int i = 0; i < MT; ++i, q += strip_scales) {
+                    const uint32_t to = dst + V::kCodes + (i * kStrip * 2 + lane) * (kFine ? 8 : 4);
+                    cp4(to, q, odd ? 4 : 2);
+                    if (kFine) cp4(to + 4, q + 4 * odd, odd ? 2 : 4);
+                }
+            } else {
+                const bool in = p_stage * kIn + cpiece * 32 < K;
+#pragma unroll
+                for (int i = 0; i < kOut / 8; ++i) {
+                    const bool ok = in && p_n + crow + i * 8 < N;
+                    cp16(dst + code_at + i * 8 * kRowBytes, ok ? src + i * row8 : a.codes, ok ? 16 : 0);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int wi = 0; wi < (kFine ? 2 : 1); ++wi) {
+                        const uint32_t e = sbase + i * kStrip * blocks +
+                                           (kFine ? p_stage * 4 + shalf * 2 + wi : (p_stage * 2 + shalf) >> shift);
+                        const bool ok = p_n + srow + i * kStrip < N && p_stage * kIn + shalf * 64 + wi * 32 < K;
+                        cp4(dst + V::kCodes + (i * kStrip * 2 + lane) * (kFine ? 8 : 4) + wi * 4,
+                            scales + (ok ? (size_t)(e & ~1u) * 2 : 0), ok ? 2 << (e & 1) : 0);
+                    }
             }
-            if (++p_stage == mine) {
-                p_stage = 0;
-                p_tile += groups;
+            src += kRowBytes;
+            ssrc += kScaleStep;
+            dst += kStage;
+            if (dst == ring_end) dst = ring;
+            --left;
+            if (++p_stage == w1) {
+                p_stage = w0;
+                p_n += tile_step;
+                src += tile_skip;
+                ssrc += scale_skip;
+                sbase += uint32_t(tile_step) * blocks;
+                inside = simple && p_n + kOut <= N;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) copy(i);  // weights: no kernel of the library writes them
+    for (int i = 0; i < kDepth - 1; ++i) copy();  // weights: no kernel of the library writes them
 
     if constexpr (!kAffine) {
         for (int v = warp; v < 256; v += kWarps) {
@@ -211,140 +293,207 @@ __global__ void __launch_bounds__(kThreads) q4_mma_kernel(const __grid_constant_
             *reinterpret_cast<uint2 *>(lut + v * 256 + lane * 8) = make_uint2(hi, attn::pack_bf16(l0, l1));
         }
     }
+    // x in the order of the B fragments: 8 inputs of one row are one 16-byte piece, for lane (row mod 8,
+    // t) of word wi of a 64-input half, inputs 32 wi + 8 t; the affine path unpacks codes i and i + 4
+    // together.  Rows past the last are zero.
+    const int n8 = (s1 - s0) * (kIn / 8);
+    auto put = [&](int c, int row, uint4 v) {
+        const int hf = c >> 3, wi = c >> 2 & 1, tt = c & 3;
+        *reinterpret_cast<uint4 *>(xs + ((((size_t)hf * NT + row / 8) * 2 + wi) * 32 + (row & 7) * 4 + tt) * 16) = v;
+    };
+    // start values in the order of the accumulators: lane t, columns 2 t, 2 t + 1, for both rows
+    constexpr int kPer = kFine ? 4 : 8;  // pieces of a block
+    auto put_start = [&](int block, int row, float v) {
+        float *z = reinterpret_cast<float *>(starts + ((size_t)block * NT + row / 8) * 64 + (row >> 1 & 3) * 16);
+        z[row & 1] = z[2 + (row & 1)] = v;
+    };
+    for (int i = m.rows * n8 + tid; i < n8 * kCols; i += kThreads) {
+        const int row = i / n8, c = i - row * n8;
+        put(c, row, make_uint4(0, 0, 0, 0));
+        if (kAffine && c % kPer == 0) put_start(c / kPer, row, 0.f);
+    }
     griddep_wait();
     griddep_launch_dependents();
-    // x into the order of the B fragments: 8 inputs of one row are one 16-byte piece, for lane
-    // (row mod 8, t) of word wi.  A lane's two code words hold inputs 16 t + 8 wi (one scale a
-    // stage) or 32 wi + 8 t (one each 32); the affine path unpacks codes i and i + 4 together.
-    const int n8 = (s1 - s0) * (kIn / 8);
-    for (int i = tid; i < n8 * kCols; i += kThreads) {
-        const int c = i % n8, row = i / n8;
-        const int k = s0 * kIn + c * 8, st = c / 8, o = c % 8;
-        const int wi = kFine ? o / 4 : o & 1, tt = kFine ? o & 3 : o / 2;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < m.rows && k < a.K) v = ldp16(a.x + (m.T0 + row) * a.x_stride + k);
-        if (kAffine)
-            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                           __byte_perm(v.y, v.w, 0x7632));
-        *reinterpret_cast<uint4 *>(xs + ((((size_t)st * NT + row / 8) * 2 + wi) * 32 + (row & 7) * 4 + tt) * 16) = v;
+    const int live = m.rows * n8;  // a multiple of 16: the lanes of a block stay together
+    constexpr int kBatch = 4;      // loads in flight a thread
+    for (int i0 = tid; i0 < live; i0 += kBatch * kThreads) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = min(i0 + b * kThreads, live - 1), row = i / n8, k = s0 * kIn + (i - row * n8) * 8;
+            v[b] = ldp16(a.x + (m.T0 + row) * a.x_stride + min(k, a.K - 8));
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads, row = i / n8, c = i - row * n8;
+            if (i >= live) break;  // whole groups of 16 lanes leave together
+            if (s0 * kIn + c * 8 >= a.K) v[b] = make_uint4(0, 0, 0, 0);
+            if (kAffine) {
+                float f[8];
+                attn::unpack8(v[b], f);
+                float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                const uint32_t group_mask = 0xffu << (lane & 24);
+#pragma unroll
+                for (int w = 1; w < kPer; w <<= 1) sum += __shfl_xor_sync(group_mask, sum, w);
+                if (c % kPer == 0) put_start(c / kPer, row, -m.centre * sum);
+                const uint4 u = v[b];
+                v[b] = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                                  __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+            }
+            put(c, row, v[b]);
+        }
     }
     __syncthreads();
 
-    const uint32_t xa = smem_addr(xs) + lane * 16, la = smem_addr(lut) + lane * 8;
-    const uint32_t mask = 0x00780078u, bias = 0x41804180u, centre = m.centre;
-    int i = 0;
+    const uint32_t x0 = smem_addr(xs) + lane * 16 + (w0 - s0) * NT * 2048, la = smem_addr(lut) + lane * 8;
+    const uint32_t z0 = smem_addr(starts) + (w0 - s0) * (kFine ? 4 : 2) * NT * 64 + t * 16;
+    const uint32_t mask = 0x00780078u, bias = 0x41804180u;
+    // word wi of half hf of row g (+ 8): piece 2 hf + wi, word t
+    uint32_t piece[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) piece[i] = g * kRowBytes + ((i ^ (g >> 1 & 3)) * 16) + t * 4;
+    // The half of the copied word that holds a scale: by the parity of its index, the same for rows
+    // g, g + 8, .. of every tile.
+    const uint32_t g_odd = uint32_t(g) * blocks;
+    uint32_t sel[2] = {g_odd & 1 ? kHigh : kLow, g_odd & 1 ? kLow : kHigh};  // q_block 32 or 64
+    uint32_t at = ring;
     for (int k = 0; k < my_tiles; ++k) {
-        const int tile = group + k * groups;
-        float acc[NT][4];
+        const int n0 = (group + k * groups) * wide;
+        float acc[MT][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-        for (int st = w0; st < w1; ++st, ++i) {
-            copy(i + kDepth - 1);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
+        uint32_t xa = x0, za = z0;
+        for (int st = w0; st < w1; ++st, xa += NT * 2048, za += (kFine ? 4 : 2) * NT * 64) {
+            copy();
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
             __syncwarp();
-            const uint32_t at = ring + (i % kDepth) * kStageBytes;
-            uint32_t w[2][2];  // [word][row g, g + 8]
-            float sc[2][2];    // [word][row g, g + 8]
-            if (kFine) {
+            if (!kFine && shift > 0) sel[0] = sel[1] = (g_odd + ((st * 2) >> shift)) & 1 ? kHigh : kLow;
+            float sc[MT][2][4];  // [strip][row g, g + 8][block of the stage]
 #pragma unroll
-                for (int wi = 0; wi < 2; ++wi)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) w[wi][r] = lds32(at + (g + 8 * r) * 32 + wi * 16 + t * 4);
-            } else {
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint2 v = lds64(at + (g + 8 * r) * 32 + t * 8);
-                    w[0][r] = v.x;
-                    w[1][r] = v.y;
+                    const uint32_t sa = at + V::kCodes + (i * kStrip + g + 8 * r) * V::kScalesRow * 4;
+                    if (kFine) {
+                        const uint4 v = lds128(sa);
+                        sc[i][r][0] = half_of(v.x, sel[0]);
+                        sc[i][r][1] = half_of(v.y, sel[1]);
+                        sc[i][r][2] = half_of(v.z, sel[0]);
+                        sc[i][r][3] = half_of(v.w, sel[1]);
+                    } else {
+                        const uint2 v = lds64(sa);
+                        sc[i][r][0] = half_of(v.x, sel[0]);
+                        sc[i][r][1] = half_of(v.y, sel[1]);
+                    }
                 }
-            }
+            float c[MT][NT][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int q = 0; q < 4; ++q) {  // 32 inputs: word q & 1 of half q / 2
+                const int block = kFine ? q : q / 2;
+                const bool first = kFine || (q & 1) == 0, last = kFine || (q & 1) == 1;
+                uint32_t p[MT][2][4], lo[MT][2][4];  // [strip][row][pair]; lo: the low parts of a table's values
 #pragma unroll
-                for (int wi = 0; wi < (kFine ? 2 : 1); ++wi) {
-                    const uint32_t word = lds32(at + kCodeBytes + ((g + 8 * r) * 2 + wi) * 4);
-                    // which half of the copied word: the parity of the scale's index
-                    const uint32_t e = uint32_t(tile * kOut + g + 8 * r) * uint32_t(blocks) + block_of(st * 2 + wi);
-                    sc[wi][r] = __uint_as_float((e & 1) ? word & 0xffff0000u : word << 16) * m.step;
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t v = lds32(at + piece[q] + (i * kStrip + 8 * r) * kRowBytes);
+                        if (kAffine) {
+                            p[i][r][0] = code_pair(v << 3, mask, bias);
+                            p[i][r][1] = code_pair(v >> 1, mask, bias);
+                            p[i][r][2] = code_pair(v >> 5, mask, bias);
+                            p[i][r][3] = code_pair(v >> 9, mask, bias);
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint2 h = lds64(la + ((v >> (8 * b)) & 255u) * 256);
+                                p[i][r][b] = h.x;
+                                lo[i][r][b] = h.y;
+                            }
+                        }
+                    }
+                uint4 x[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[n] = lds128(xa + (((q >> 1) * NT + n) * 2 + (q & 1)) * 512);
+                // products on one accumulator are kept apart: each waits for the one before
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                    if (kAffine && first) z = lds128(za + (block * NT + n) * 64);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        if (first)
+                            mma16816_from(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y, z);
+                        else
+                            mma16816(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y);
+                    }
                 }
-            float c[NT][4];
 #pragma unroll
-            for (int wi = 0; wi < 2; ++wi) {
-                if (wi == 0 || kFine) {
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma16816(c[i][n], p[i][0][2], p[i][1][2], p[i][0][3], p[i][1][3], x[n].z, x[n].w);
+                if (!kAffine) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) c[n][e] = 0.f;
+                        for (int i = 0; i < MT; ++i)
+                            mma16816(c[i][n], lo[i][0][0], lo[i][1][0], lo[i][0][1], lo[i][1][1], x[n].x, x[n].y);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            mma16816(c[i][n], lo[i][0][2], lo[i][1][2], lo[i][0][3], lo[i][1][3], x[n].z, x[n].w);
                 }
-                uint32_t p[2][4], q[2][4];  // [row][pair]; q: the low parts of a table's values
+                if (last) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t v = w[wi][r];
-                    if (kAffine) {
-                        p[r][0] = code_pair(v << 3, mask, bias, centre);
-                        p[r][1] = code_pair(v >> 1, mask, bias, centre);
-                        p[r][2] = code_pair(v >> 5, mask, bias, centre);
-                        p[r][3] = code_pair(v >> 9, mask, bias, centre);
-                    } else {
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint2 h = lds64(la + ((v >> (8 * b)) & 255u) * 256);
-                            p[r][b] = h.x;
-                            q[r][b] = h.y;
-                        }
-                    }
-                }
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 x = lds128(xa + (((st - s0) * NT + n) * 2 + wi) * 512);
-                    mma16816(c[n], p[0][0], p[1][0], p[0][1], p[1][1], x.x, x.y);
-                    mma16816(c[n], p[0][2], p[1][2], p[0][3], p[1][3], x.z, x.w);
-                    if (!kAffine) {
-                        mma16816(c[n], q[0][0], q[1][0], q[0][1], q[1][1], x.x, x.y);
-                        mma16816(c[n], q[0][2], q[1][2], q[0][3], q[1][3], x.z, x.w);
-                    }
-                }
-                if (kFine || wi == 1) {
-                    const float f0 = sc[kFine ? wi : 0][0], f1 = sc[kFine ? wi : 0][1];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[n][0] = fmaf(f0, c[n][0], acc[n][0]);
-                        acc[n][1] = fmaf(f0, c[n][1], acc[n][1]);
-                        acc[n][2] = fmaf(f1, c[n][2], acc[n][2]);
-                        acc[n][3] = fmaf(f1, c[n][3], acc[n][3]);
-                    }
+                            for (int e = 0; e < 4; ++e)
+                                acc[i][n][e] = fmaf(sc[i][e >> 1][block], c[i][n][e], acc[i][n][e]);
                 }
             }
+            at += kStage;
+            if (at == ring_end) at = ring;
             __syncwarp();  // the stage is read before the next copy lands in it
         }
         // the warps' sums, [column][output]; lane (g, t): outputs g and g + 8 of columns 2 t, 2 t + 1
-        float *rb = red + (kRedBufs == 2 ? (k & 1) * kWarps * kCols * kOut : 0);
-        if (kRedBufs == 1 && k > 0) __syncthreads();  // the tile before has been read
+        if (k > 0) __syncthreads();  // the tile before has been read
+        float *rb = red + (warp * kCols + 2 * t) * kRedStride + g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                rb[(warp * kCols + n * 8 + 2 * t + (e & 1)) * kOut + g + 8 * (e >> 1)] = acc[n][e];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    rb[(n * 8 + (e & 1)) * kRedStride + i * kStrip + 8 * (e >> 1)] = acc[i][n][e];
         __syncthreads();
-        float *pb = part + (k & 1) * kCols * kOut;
-        auto emit = [&](int idx, float y) {
-            const int row = idx / kOut, n = tile * kOut + idx % kOut;
-            if (row >= m.rows || n >= a.N) return;
+        float *pb = part + (k & 1) * kCols * wide;
+        auto emit = [&](int row, int n, float y) {
+            n += n0;
+            if (row >= m.rows || n >= N) return;
             const int64_t tr = m.T0 + row;
+            y *= m.step;
             if (a.res) y += bf16_bits_to_f32(ldp(a.res + tr * a.res_stride + n));
             if (a.out_f32)
                 static_cast<float *>(a.out)[tr * a.out_stride + n] = y;
             else
                 static_cast<uint16_t *>(a.out)[tr * a.out_stride + n] = f32_to_bf16_bits(y);
         };
-        for (int idx = tid; idx < kCols * kOut; idx += kThreads) {
-            float y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) y += rb[w * kCols * kOut + idx];
+        // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part
+        const int cols = m.slices == 1 ? min(kCols, m.rows) : kCols;
+        for (int idx = tid; idx < cols * wide; idx += kThreads) {
+            const int row = idx >> wide_log2, n = idx & (wide - 1);
+            const float *rr = red + (uint32_t(n) / kOut * kCols + row) * kRedStride + uint32_t(n) % kOut;
+            float y = rr[0];
+            for (int w = 1; w < parts; ++w) y += rr[w * m.side * kCols * kRedStride];
             if (m.slices == 1)
-                emit(idx, y);
+                emit(row, n, y);
             else
                 pb[idx] = y;
         }
@@ -353,64 +502,85 @@ __global__ void __launch_bounds__(kThreads) q4_mma_kernel(const __grid_constant_
             // other buffer is written meanwhile, so one barrier a tile is enough
             cg::cluster_group cl = cg::this_cluster();
             cl.sync();
-            for (int idx = slice * kThreads + tid; idx < kCols * kOut; idx += m.slices * kThreads) {
+            for (int idx = slice * kThreads + tid; idx < kCols * wide; idx += m.slices * kThreads) {
                 float y = 0.f;
                 for (int r = 0; r < m.slices; ++r) y += *cl.map_shared_rank(pb + idx, r);
-                emit(idx, y);
+                emit(idx >> wide_log2, idx & (wide - 1), y);
             }
         }
     }
     if (m.slices > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
 
-template <int NT, bool kFine, bool kAffine>
-int mma_smem(int slice_stages) {
-    const int red = (NT <= 2 ? 2 : 1) * kWarps * NT * 8 * kOut * 4, part = 2 * NT * 8 * kOut * 4;
-    return red + part + kRingBytes + (kAffine ? 0 : kLutBytes) + slice_stages * NT * 2 * 32 * 16;
-}
-
-template <int NT, bool kFine, bool kAffine>
-cudaError_t launch_mma(MmaArgs m, int sms, cudaStream_t st) {
+template <int NT, int MT, bool kFine, bool kAffine>
+cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
+    using V = Var<NT, MT, kFine, kAffine>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(q4_mma_kernel<NT, kFine, kAffine>,
+        const cudaError_t e = cudaFuncSetAttribute(q4_mma_kernel<NT, MT, kFine, kAffine>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int smem = mma_smem<NT, kFine, kAffine>(m.slice_stages);
-    const int per_sm = std::min(4, std::max(1, (kMaxSmem - 1024) / (smem + 1024)));
-    const int groups = std::max(1, std::min(m.tiles, sms * per_sm / m.slices));
+    const int strips = (m.a.N + V::kOut - 1) / V::kOut;
+    // slices: as many as x needs to fit; more while there are fewer CTAs than SMs and every warp
+    // keeps a stage
+    int slices = 1;
+    if (stages > V::max_stages()) slices = 2;
+    while (slices > 1 && (stages + slices - 1) / slices > V::max_stages_sliced()) slices *= 2;
+    while (slices < kMaxSlices && strips * slices * 2 <= sms * 2 && stages >= slices * 2 * V::kWarps) slices *= 2;
+    // strips side by side: when there are plenty, each warp takes a longer part of the inputs, and
+    // the sums over the parts cost less
+    m.slices = slices;
+    m.side = 1;
+    while (m.side < V::kWarps && strips * slices >= sms * 2 * m.side * 2 * (MT == 2 ? 2 : 1) && stages / slices < 4 * V::kWarps / m.side) m.side *= 2;
+    m.tiles = (strips + m.side - 1) / m.side;
+    m.slice_halves = 2 * ((stages + slices - 1) / slices);
+    const int smem = V::kFixed + m.slice_halves * V::kHalf + (slices > 1 ? V::part_bytes(m.side) : 0);
+    const int per_sm = std::min(MT == 2 || NT >= 8 ? 1 : NT == 4 ? 2 : 3, std::max(1, (kMaxSmem + 1024) / (smem + 1024)));
+    const int groups = std::max(1, std::min(m.tiles, sms * per_sm / slices));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(m.slices);
+    attr[1].val.clusterDim.x = unsigned(slices);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(groups * m.slices));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(unsigned(groups * slices));
+    cfg.blockDim = dim3(V::kThreads);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = m.slices > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, kFine, kAffine>, m);
+    cfg.numAttrs = slices > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, MT, kFine, kAffine>, m);
 }
 
-template <int NT>
-cudaError_t launch_nt(const MmaArgs &m, bool fine, bool affine, int sms, cudaStream_t st) {
-    if (affine) return fine ? launch_mma<NT, true, true>(m, sms, st) : launch_mma<NT, false, true>(m, sms, st);
-    return fine ? launch_mma<NT, true, false>(m, sms, st) : launch_mma<NT, false, false>(m, sms, st);
-}
-
-// The most stages of x that fit next to the rest for NT tiles of 8 rows.
-int max_stages(int nt, bool affine) {
-    const int fixed = (nt <= 2 ? 2 : 1) * kWarps * nt * 8 * kOut * 4 + 2 * nt * 8 * kOut * 4 + kRingBytes +
-                      (affine ? 0 : kLutBytes);
-    return (kMaxSmem - fixed) / (nt * 1024);
-}
+template <bool kFine, bool kAffine>
+struct Rows {  // the variants by rows of x
+    static bool fits(int nt, int stages) {
+        const int s = (stages + kMaxSlices - 1) / kMaxSlices;
+        return s <= (nt == 1   ? Var<1, 1, kFine, kAffine>::max_stages_sliced()
+                     : nt == 2 ? Var<2, 1, kFine, kAffine>::max_stages_sliced()
+                     : nt == 4 ? Var<4, 1, kFine, kAffine>::max_stages_sliced()
+                               : Var<8, 1, kFine, kAffine>::max_stages_sliced());
+    }
+    static cudaError_t launch(int nt, const MmaArgs &m, int stages, int sms, cudaStream_t st) {
+        // two strips a warp: when every SM gets at least eight such pairs and x fits one CTA
+        const bool two = m.a.N >= sms * 8 * 2 * kStrip;
+        if (nt == 1)
+            return two && stages <= Var<1, 2, kFine, kAffine>::max_stages()
+                       ? launch_mma<1, 2, kFine, kAffine>(m, stages, sms, st)
+                       : launch_mma<1, 1, kFine, kAffine>(m, stages, sms, st);
+        if (nt == 2)
+            return two && stages <= Var<2, 2, kFine, kAffine>::max_stages()
+                       ? launch_mma<2, 2, kFine, kAffine>(m, stages, sms, st)
+                       : launch_mma<2, 1, kFine, kAffine>(m, stages, sms, st);
+        return nt == 4 ? launch_mma<4, 1, kFine, kAffine>(m, stages, sms, st)
+                       : launch_mma<8, 1, kFine, kAffine>(m, stages, sms, st);
+    }
+};
 
 // The rows in passes of up to 64 (fewer when x would not fit even split over a cluster); false
 // if not even 8 rows fit.
@@ -418,37 +588,29 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     float step = 1.f;
     int twice = 0;
     const bool affine = q4_codebook_affine(a.codebook, &step, &twice);
-    const bool fine = a.q_block % kIn != 0;
-    const int stages = (a.K + kIn - 1) / kIn, tiles = (a.N + kOut - 1) / kOut;
+    const bool fine = a.q_block == 32;
+    const int stages = (a.K + kIn - 1) / kIn;
+    // counted in 32 bits in the kernel
+    if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
+    auto fits = [&](int nt) {
+        return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
+                      : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
+    };
     int nt_max = 8;
-    while (nt_max > 0 && (stages + kMaxSlices - 1) / kMaxSlices > max_stages(nt_max, affine)) nt_max /= 2;
+    while (nt_max > 0 && !fits(nt_max)) nt_max /= 2;
     if (nt_max == 0) return false;
     MmaArgs m{};
     m.a = a;
-    m.tiles = tiles;
     m.step = affine ? step : 1.f;
-    const uint32_t per = uint32_t(a.q_block / 32);
-    m.per_block = ((uint64_t(1) << 32) + per - 1) / per;
-    const float c = 16.f + 0.5f * float(twice);  // 6 significant bits: exact in bf16
-    uint32_t bits;
-    memcpy(&bits, &c, 4);
-    m.centre = (bits & 0xffff0000u) | bits >> 16;
+    while (!fine && (64 << m.shift) < a.q_block) ++m.shift;
+    m.centre = 16.f + 0.5f * float(twice);
     *err = cudaSuccess;
     for (int t0 = 0; t0 < a.T && *err == cudaSuccess; t0 += nt_max * 8) {
         m.T0 = t0;
         m.rows = std::min(a.T - t0, nt_max * 8);
         const int nt = m.rows <= 8 ? 1 : m.rows <= 16 ? 2 : m.rows <= 32 ? 4 : 8;
-        // slices: as many as x needs to fit; more while there are fewer CTAs than SMs and every
-        // warp keeps two stages
-        int slices = 1;
-        while ((stages + slices - 1) / slices > max_stages(nt, affine)) slices *= 2;
-        while (slices < kMaxSlices && tiles * slices * 2 <= sms * 2 && stages >= slices * 2 * 2 * kWarps) slices *= 2;
-        m.slices = slices;
-        m.slice_stages = (stages + slices - 1) / slices;
-        *err = nt == 1   ? launch_nt<1>(m, fine, affine, sms, st)
-               : nt == 2 ? launch_nt<2>(m, fine, affine, sms, st)
-               : nt == 4 ? launch_nt<4>(m, fine, affine, sms, st)
-                         : launch_nt<8>(m, fine, affine, sms, st);
+        *err = affine ? (fine ? Rows<true, true>::launch(nt, m, stages, sms, st) : Rows<false, true>::launch(nt, m, stages, sms, st))
+                      : (fine ? Rows<true, false>::launch(nt, m, stages, sms, st) : Rows<false, false>::launch(nt, m, stages, sms, st));
     }
     return true;
 }
@@ -472,12 +634,10 @@ cudaError_t launch_q4_linear(const moe_q4_linear_shape &s, const void *x, int64_
     a.q_block = s.q_block;
     a.out_f32 = s.out_dtype == MOE_DT_F32;
     for (int i = 0; i < 16; ++i) a.codebook[i] = w.codebook[i];
-    // code rows in 16-byte pieces, blocks that cover whole halves of a stage, 32-bit counts and an
-    // exact division by the block's size (j m < 2^32)
+    // q_block 32, or 64 times a power of two (a shift finds an input's block)
+    const int q = s.q_block;
     cudaError_t err;
-    if (s.q_block % 32 == 0 && (uint64_t)(s.K / 32) * (s.q_block / 32) < (uint64_t(1) << 32) && (int64_t)((s.N + kOut - 1) / kOut) * ((s.K + kIn - 1) / kIn) < INT32_MAX &&
-        run_mma(a, sms, st, &err))
-        return err;
+    if ((q == 32 || (q % 64 == 0 && (q & (q - 1)) == 0)) && run_mma(a, sms, st, &err)) return err;
     return launch_any(a, s.out_dtype, st);
 }
 

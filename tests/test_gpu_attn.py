@@ -260,6 +260,8 @@ ROPE = {
     "widest interleaved": ("f32", 3, 3, 256, 7, [5, 3], [5, 50], 240, True, True, "none", 1.0, None),
     "cut short": ("bf16", 8, 2, 64, 16, [6, 4], [2, 0], 64, False, False, "none", 1.0, 50),
     "negative positions": ("f32", 2, 2, 32, 16, [6], [9], 32, False, False, "none", 1.0, -20),
+    "many tokens": ("bf16", 5, 1, 64, 16, [1, 900, 0, 2047], [4, 900, 3, 2100], 32, False, True, "none", 1.0, None),
+    "many tokens fp32": ("f32", 3, 1, 24, 3, [1300, 1, 1200], [1300, 1, 1201], 16, True, False, "none", 1.0, 7),
     "many sequences": ("bf16", 4, 2, 64, 16, [i % 3 for i in range(600)], [i % 3 + i % 7 for i in range(600)], 64, True,
                        False, "none", 1.0, None),
 }

@@ -441,19 +441,41 @@ def _row_stride(t, what):
     return st[0]
 
 
+def _head_rows(t, dim, what):
+    """_row_stride of a [rows][heads][dim] tensor, quick where the heads follow one another."""
+    row, head, elem = t.stride()
+    return row if elem == 1 and head == dim else _row_stride(t, what)
+
+
+def _current_stream():
+    """The raw handle of torch's current stream on the current device."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    _current_stream = lambda: raw(device())  # noqa: E731 -- a fraction of a microsecond; the Stream object costs several
+    return _current_stream()
+
+
 def moe_attn_workspace_size(shape: MoEAttnShape) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().moe_attn_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_attn_workspace_size")
     return n.value
 
 
+# These calls are made several times a layer and step: structs pass by their addresses and
+# nothing is looked up twice, so that the host keeps ahead of kernels of a few microseconds.
+
 def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, workspace=None, stream=None):
     """q_out = rotated q; rotated k and v into their cache slots.  q, q_out [N][heads][dim], k, v [N][kv heads][dim]
     (rows may be slices of a wider tensor)."""
-    rc = lib().moe_rope_append(ctypes.byref(shape), ctypes.byref(rope), q.data_ptr(), _row_stride(q, "q"),
-                               k.data_ptr(), _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"),
-                               ctypes.byref(cache), ctypes.byref(batch), _ptr(positions), q_out.data_ptr(),
-                               _row_stride(q_out, "q_out"), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    ref, dim = ctypes.byref, shape.head_dim
+    rc = (_lib or lib()).moe_rope_append(
+        ref(shape), ref(rope), q.data_ptr(), _head_rows(q, dim, "q"), k.data_ptr(), _head_rows(k, dim, "k"),
+        v.data_ptr(), _head_rows(v, dim, "v"), ref(cache), ref(batch), None if positions is None else _ptr(positions),
+        q_out.data_ptr(), _head_rows(q_out, dim, "q_out"), workspace.data_ptr(), workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_rope_append")
 
@@ -462,18 +484,21 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
     """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5."""
     if lse is not None and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    rc = lib().moe_paged_attention(ctypes.byref(shape), q.data_ptr(), _row_stride(q, "q"), ctypes.byref(cache),
-                                   ctypes.byref(batch), shape.head_dim ** -0.5 if scale is None else scale,
-                                   out.data_ptr(), _row_stride(out, "out"), _ptr(lse), _ptr(workspace),
-                                   _nbytes(workspace), _stream(stream))
+    ref, dim = ctypes.byref, shape.head_dim
+    rc = (_lib or lib()).moe_paged_attention(
+        ref(shape), q.data_ptr(), _head_rows(q, dim, "q"), ref(cache), ref(batch), dim ** -0.5 if scale is None else scale,
+        out.data_ptr(), _head_rows(out, dim, "out"), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_paged_attention")
 
 
 def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
     """out = x . W^T (+ residual) with a 4-bit weight (make_q4_weight)."""
-    rc = lib().moe_q4_linear(ctypes.byref(shape), x.data_ptr(), _row_stride(x, "x"), ctypes.byref(weight),
-                             _ptr(residual), 0 if residual is None else _row_stride(residual, "residual"),
-                             out.data_ptr(), _row_stride(out, "out"), _stream(stream))
+    ref = ctypes.byref
+    rc = (_lib or lib()).moe_q4_linear(
+        ref(shape), x.data_ptr(), _row_stride(x, "x"), ref(weight), None if residual is None else residual.data_ptr(),
+        0 if residual is None else _row_stride(residual, "residual"), out.data_ptr(), _row_stride(out, "out"),
+        _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_q4_linear")

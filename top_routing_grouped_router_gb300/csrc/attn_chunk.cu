@@ -140,6 +140,82 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// The MMAs of one product in one block of assembly: one election, and descriptors that differ by
+// constants, so that the issuing warp needs few of the issue slots that the softmax warps fill.
+// (Written as separate calls an MMA took 147 cycles to issue next to them, 64 to run.)
+// S: D / 16 MMAs over the 64-element slabs of Q and K (128 rows x 128 bytes each), then a commit.
+template <int D>
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, uint32_t bar) {
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred e, z;\n\t.reg .b64 q, k;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 z, %3, %3;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\tsetp.eq.b32 z, %3, %3;\n\t"
+            "add.s64 q, %1, 2;\n\tadd.s64 k, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 4;\n\tadd.s64 k, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 6;\n\tadd.s64 k, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 1024;\n\tadd.s64 k, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 1026;\n\tadd.s64 k, %2, 1026;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 1028;\n\tadd.s64 k, %2, 1028;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 1030;\n\tadd.s64 k, %2, 1030;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}"
+            ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(bar)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred e, z;\n\t.reg .b64 q, k;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 z, %3, %3;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\tsetp.eq.b32 z, %3, %3;\n\t"
+            "add.s64 q, %1, 2;\n\tadd.s64 k, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 4;\n\tadd.s64 k, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "add.s64 q, %1, 6;\n\tadd.s64 k, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %3, z;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}"
+            ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(bar)
+            : "memory");
+    }
+}
+// O (+)= P V over 128 keys: 8 MMAs, P at TMEM columns p + 8 i, V 2048 bytes (16 keys) further each.
+__device__ __forceinline__ void mma_o(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, z;\n\t.reg .b64 v;\n\t.reg .b32 p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 z, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, z;\n\tsetp.eq.b32 z, %3, %3;\n\t"
+        "add.s32 p, %1, 8;\n\tadd.s64 v, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 16;\n\tadd.s64 v, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 24;\n\tadd.s64 v, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 32;\n\tadd.s64 v, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 40;\n\tadd.s64 v, %2, 640;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 48;\n\tadd.s64 v, %2, 768;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
+        "add.s32 p, %1, 56;\n\tadd.s64 v, %2, 896;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t}"
+        ::"r"(d), "r"(p), "l"(v), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Two floats in one 64-bit register, for the paired fp32 instructions.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 struct Ctx {
     Args a;
     uint32_t tt;        // tokens of a tile
@@ -415,12 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             auto issue_s = [&](int t, int st) {
                 const uint64_t qa = smem_desc(smem_u32(smem + t * C::kTile)), kb = smem_desc(smem_u32(smem + (2 + st) * C::kTile));
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks / 4) * (kM * 128 / 16) + (ks % 4) * 2;  // 16-byte units
-                    mma_bf16_warp(tmem + kColS + t * kKeys, qa + off, kb + off, id_s, ks > 0);
-                }
-                mma_commit_warp(smem_u32(&s_full[t]));
+                mma_s<D>(tmem + kColS + t * kKeys, qa, kb, id_s, smem_u32(&s_full[t]));
             };
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
@@ -461,10 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         p_phase ^= 1u << t;
                         tc_fence_after();
                         const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
-#pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            mma_bf16_tmem_warp(tmem + kColO + t * 128, tmem + kColS + t * kKeys + ks * 8,
-                                               vb + ks * (2048 / 16), id_o, step > g.step0 || ks > 0);
+                        mma_o(tmem + kColO + t * 128, tmem + kColS + t * kKeys, vb, id_o, step > g.step0);
                         if (!more) mma_commit_warp(smem_u32(&o_full[t]));
                         if (more) {
                             if (t == 0 && !wait(&kv_full[stage], phase)) break;
@@ -521,12 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                     float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
 #pragma unroll
                     for (int i = 8; i < 128; i += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4])));
+                            mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
                     const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
                     if (step == g.step0) {
                         m = mn;
@@ -536,29 +604,32 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         m = mn;
                         l *= f;
 #pragma unroll
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + i, o);
+                        for (int i = 0; i < D; i += 16) {
+                            float o[16];
+                            uint32_t w[16];
+                            tmem_ld16(to + i, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(to + i, o);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+                            tmem_st16(to + i, w);
                         }
                     }
                     const float z = m == kNegInf ? 0.f : m * sl2;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int i = 0; i < 128; i += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float p = ex2(fmaf(__uint_as_float(x[i + e]), sl2, -z));
-                            x[i + e] = __float_as_uint(p);
-                            sum[e] += p;
-                        }
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        x[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                    tmem_st64(ts, x);
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    for (int i = 0; i < 128; i += 2) {
+                        float p0, p1;
+                        unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2p, zp), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair(p0, p1));
+                        x[i / 2] = pack_bf16(p0, p1);
+                        if (i == 62) tmem_st32(ts, x);
+                    }
+                    tmem_st32(ts + 32, x + 32);
+                    float s0, s1;
+                    unpair(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(smem_u32(&p_full[t]));

@@ -52,19 +52,20 @@ struct Rec {
     int n, h, tok0, q0, q_len, last;  // n: parts (0: none); last: the last CTA
 };
 
-// sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0, by the Euclid-like recursion.
-__device__ __forceinline__ uint64_t floor_sum(uint64_t n, uint32_t m, uint32_t a, uint64_t b) {
-    uint64_t sum = 0;
+// sum_{i < n} floor((a i + b) / m), m > 0, by the Euclid-like recursion; the sum and a n + m fit
+// 32 bits.
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    uint32_t sum = 0;
     while (n > 0) {
         if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
+            sum += uint32_t(uint64_t(n) * (n - 1) / 2) * (a / m);
             a %= m;
         }
         if (b >= m) {
             sum += n * (b / m);
             b %= m;
         }
-        const uint64_t y = (uint64_t)a * n + b;
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
@@ -91,9 +92,17 @@ __device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, uint3
     const int64_t past = (int64_t)s.kv_len - s.q_len;
     // items that see no key have one step each
     uint32_t none = 0;
-    if (past < 0) none = min((uint64_t)full, (uint64_t)(-past) / tt2);
-    const uint64_t b = uint64_t(past + (int64_t)(none + 1) * tt2 + kKeys - 1);  // > kKeys - 1
-    return none + uint32_t(floor_sum(full - none, kKeys, tt2, b)) + last;
+    if (past < 0) none = min(full, uint32_t(-past) / tt2);
+    const uint32_t b = uint32_t(past + (int64_t)(none + 1) * tt2 + kKeys - 1);  // > kKeys - 1
+    return none + floor_sum(full - none, kKeys, tt2, b) + last;
+}
+
+// On the line of all steps an item takes kSetup places more than its steps, at its front: what
+// starting and ending an item costs, about two steps' time (a mixed batch of short and long
+// items: 85 us with none, the slowest CTA 1.45 times the mean).
+constexpr uint32_t kSetup = 2;
+__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, uint32_t tt2) {
+    return steps_before(s, i, tt2) + i * kSetup;
 }
 
 struct Shares {
@@ -301,34 +310,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *sum = total;
         return before + incl - n;
     };
-    auto seq_steps = [&](const Seq &s) { return steps_before(s, items_of(s, tt2), tt2); };
-    uint32_t total = 0;
+    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, tt2), tt2); };
+    uint32_t total = 0, n0 = 0, before0 = 0;
+    Seq s0{};
     for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
         uint32_t n = 0, sum;
-        if (b0 + tid < a.n_seqs) n = seq_steps(load_seq(a, b0 + tid)) * Hkv;
-        scan_block(n, &sum);
+        Seq s{};
+        if (b0 + tid < a.n_seqs) {
+            s = load_seq(a, b0 + tid);
+            n = seq_places(s) * Hkv;
+        }
+        const uint32_t before = scan_block(n, &sum);
+        if (b0 == 0) {
+            n0 = n;
+            before0 = before;
+            s0 = s;
+        }
         total += sum;
     }
-    const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, total / 2));
+    const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, total / (kSetup + 2)));
     const Shares sh{total / ctas, total % ctas};
     const uint32_t u_begin = cta < ctas ? sh.begin(cta) : 0, u_end = cta < ctas ? sh.begin(cta + 1) : 0;
     if (tid == 0) c.rec[cta].n = 0;
     if (u_begin < u_end) {
-        uint32_t base = 0;
-        for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-            uint32_t n = 0, sum;
-            Seq s{};
-            if (b0 + tid < a.n_seqs) {
-                s = load_seq(a, b0 + tid);
-                n = seq_steps(s) * Hkv;
-            }
-            const uint32_t before = base + scan_block(n, &sum);
+        auto found = [&](int b, uint32_t before, uint32_t n, const Seq &s) {
             if (u_begin >= before && u_begin - before < n) {
-                cursor[0] = b0 + tid;
+                cursor[0] = b;
                 cursor[1] = before;
                 cursor[2] = n / Hkv;
                 *cur_seq = s;
             }
+        };
+        found(tid, before0, n0, s0);
+        uint32_t base = 0;
+        for (int b0 = 0; a.n_seqs > kThreads && b0 < a.n_seqs; b0 += kThreads) {
+            uint32_t n = 0, sum;
+            Seq s{};
+            if (b0 + tid < a.n_seqs) {
+                s = load_seq(a, b0 + tid);
+                n = seq_places(s) * Hkv;
+            }
+            const uint32_t before = base + scan_block(n, &sum);
+            found(b0 + tid, before, n, s);
             base += sum;
             if (u_begin < base) break;
         }
@@ -358,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     while (w - first >= per_head * Hkv) {  // the next sequence with a chunk
                         first += per_head * Hkv;
                         s = load_seq(a, ++b);
-                        per_head = seq_steps(s);
+                        per_head = seq_places(s);
                     }
                     h = (w - first) / per_head;
                     const uint32_t rem = w - first - h * per_head;
@@ -367,40 +390,44 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     while (n > 1) {
                         const uint32_t each = (n + 31) / 32;
                         const uint32_t cand = lo + lane * each;
-                        const bool at = lane * each < n && steps_before(s, cand, tt2) <= rem;
+                        const bool at = lane * each < n && places_before(s, cand, tt2) <= rem;
                         const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, at));
                         lo += last * each;
                         n = min(each, n - last * each);
                     }
                     i = lo;
-                    item0 = first + h * per_head + steps_before(s, i, tt2);
+                    item0 = first + h * per_head + places_before(s, i, tt2);
                     located = true;
                 }
-                const uint32_t steps = item_steps(s, i, tt2);
-                const uint32_t end = min(item0 + steps, u_end);
-                const bool whole = w == item0 && end == item0 + steps;
-                if (lane == 0) {
-                    Seg g;
-                    g.b = b;
-                    g.h = int(h);
-                    g.tok0 = int(i * tt2);
-                    g.q0 = s.q0;
-                    g.q_len = s.q_len;
-                    g.kv_len = s.kv_len;
-                    g.step0 = int(w - item0);
-                    g.step1 = int(end - item0);
-                    g.slot = whole ? -1 : int(cta * 2 + (w == item0 ? 1 : 0));
-                    g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
-                    segs[k] = g;
-                    if (!whole && w == item0) {
-                        const int last = int(sh.owner(item0 + steps - 1));
-                        c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len, last};
+                const uint32_t places = item_steps(s, i, tt2) + kSetup;
+                const uint32_t end = min(item0 + places, u_end);
+                // steps begin after the item's setup; a share that ends within it leaves the item to the next
+                const uint32_t from = max(w, item0 + kSetup);
+                const bool starts = from == item0 + kSetup, whole = starts && end == item0 + places;
+                if (from < end) {
+                    if (lane == 0) {
+                        Seg g;
+                        g.b = b;
+                        g.h = int(h);
+                        g.tok0 = int(i * tt2);
+                        g.q0 = s.q0;
+                        g.q_len = s.q_len;
+                        g.kv_len = s.kv_len;
+                        g.step0 = int(from - item0 - kSetup);
+                        g.step1 = int(end - item0 - kSetup);
+                        g.slot = whole ? -1 : int(cta * 2 + (starts ? 1 : 0));
+                        g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
+                        segs[k] = g;
+                        if (!whole && starts) {
+                            const int last = int(sh.owner(item0 + places - 1));
+                            c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len, last};
+                        }
                     }
+                    ++k;
                 }
-                ++k;
                 w = end;
-                if (end == item0 + steps) {
-                    item0 += steps;
+                if (end == item0 + places) {
+                    item0 += places;
                     if (++i == items_of(s, tt2)) {
                         i = 0;
                         ++h;
@@ -755,12 +782,12 @@ int64_t max_items(const moe_attn_shape &s) {
     const int64_t tt2 = 2 * (kM / (s.n_heads / s.n_kv_heads));
     return ((s.n_tokens + tt2 - 1) / tt2 + s.n_seqs) * s.n_kv_heads;
 }
-double max_steps(const moe_attn_shape &s) {
-    return double(max_items(s)) * ((double)s.max_pages * s.page_size / kKeys + 1);
+// The longest that the line of all steps can be.
+double max_places(const moe_attn_shape &s) {
+    return double(max_items(s)) * ((double)s.max_pages * s.page_size / kKeys + 1 + kSetup);
 }
-// CTAs: no more than the steps there can be.
 int max_ctas(const moe_attn_shape &s) {
-    const double n = max_steps(s) / 2;
+    const double n = max_places(s) / (kSetup + 2);
     return n < 1 ? 1 : n < kMaxCtas ? int(n) : kMaxCtas;
 }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -795,7 +822,7 @@ bool chunk_supported(const moe_attn_shape &s) {
     const int G = s.n_heads / s.n_kv_heads;
     const bool pages = s.page_size >= 8 && (kKeys % s.page_size == 0 || s.page_size % kKeys == 0);
     return s.dtype == MOE_DT_BF16 && (s.head_dim == 64 || s.head_dim == 128) && G <= kM && pages &&
-           max_steps(s) < 2147483648.0;
+           max_places(s) < 2147483648.0;
 }
 
 size_t chunk_ws_bytes(const moe_attn_shape &s) {

@@ -13,7 +13,7 @@ constexpr int kThreads = 128;
 constexpr int kRows = 16;      // query rows (token, head of the group) of a block: 4 a warp
 constexpr int kKeys = 32;      // keys of a tile: one a lane
 constexpr int kMaxParts = 32;
-constexpr int kTargetBlocks = 304;  // two blocks on each of 152 SMs
+constexpr int kTargetBlocks = 1216;  // eight blocks of four warps on each of 152 SMs
 
 int tokens_per_tile(int group) { return group >= kRows ? 1 : kRows / group; }
 // A group wider than a tile is split into head slices of kRows.
@@ -26,13 +26,13 @@ int64_t max_tiles(const moe_attn_shape &s) {
     return ragged < s.n_tokens ? ragged : s.n_tokens;  // a tile holds at least one token
 }
 
-// Parts that each tile's keys are split into: enough blocks for the machine, at least four
-// key tiles a part of the longest sequence that the block table allows.
+// Parts that each tile's keys are split into: enough blocks for the machine, at least two key
+// tiles a part of the longest sequence that the block table allows.
 int parts(const moe_attn_shape &s) {
     const int64_t blocks = max_tiles(s) * s.n_kv_heads * head_slices(s.n_heads / s.n_kv_heads);
     const int64_t keys = (int64_t)s.max_pages * s.page_size;
     int64_t p = blocks > 0 ? kTargetBlocks / blocks : 1;
-    const int64_t most = (keys + 4 * kKeys - 1) / (4 * kKeys);
+    const int64_t most = (keys + 2 * kKeys - 1) / (2 * kKeys);
     if (p > most) p = most;
     if (p > kMaxParts) p = kMaxParts;
     return p < 1 ? 1 : int(p);

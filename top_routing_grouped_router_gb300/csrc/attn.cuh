@@ -14,6 +14,7 @@ struct Args {
     int64_t page_stride, head_stride, token_stride;  // elements
     int32_t n_tokens, n_seqs, n_heads, n_kv_heads, head_dim, group;
     int32_t page_size, n_pages, max_pages, max_q;
+    int32_t page_shift;  // log2(page_size), -1 if it is no power of two
     const void *q;
     void *out;
     float *lse;

@@ -78,6 +78,9 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache &c, const moe_a
     a.n_pages = s.n_pages;
     a.max_pages = s.max_pages;
     a.max_q = s.max_q;
+    a.page_shift = -1;
+    if ((s.page_size & (s.page_size - 1)) == 0)
+        for (a.page_shift = 0; (1 << a.page_shift) < s.page_size;) ++a.page_shift;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;

@@ -8,9 +8,11 @@
 // 16-byte pieces into a ring of its own (no barrier between warps), rows swizzled so that
 // ldmatrix reads without bank conflicts.
 //
-// All (sequence, key head) pairs are laid end to end as steps of 16 keys, and every CTA takes
-// an equal share of that line, whatever the lengths.  A pair that a CTA holds whole is written
-// out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
+// All (sequence, key head) pairs are laid end to end as steps of 16 keys.  Where the pairs are few,
+// each is cut into parts of about the same number of steps, one part a CTA.  Where they are many,
+// every CTA takes an equal share of the line, whatever the lengths, and may end one pair and
+// begin the next: the shares are even, but a CTA pays the start and end of each piece (about
+// kPiece steps' time).  A pair that a CTA holds whole is written out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
 // arrive last join them in the order of the keys, so the bits do not depend on timing.
 #include "attn.cuh"
 
@@ -98,6 +100,8 @@ struct Shares {
         return step < edge ? step / (each + 1) : more + (step - edge) / each;
     }
 };
+
+constexpr uint32_t kPiece = 10;
 
 // Partial results in the workspace.  A CTA leaves at most two: of the pair that its share
 // begins inside (slot 2 cta) and of the pair that begins in its share and goes on (slot
@@ -214,102 +218,159 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t G = a.group, Hkv = a.n_kv_heads;
 
-    // this CTA's share of all steps
-    uint32_t n0 = 0, before0 = 0, total = 0;
+    // the line of all steps, and how it is cut
+    uint32_t n0 = 0, before0 = 0, total = 0, pairs = 0;
     Seq s{};
     for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
         uint32_t n = 0, sum;
         if (b0 + tid < a.n_seqs) {
             const Seq x = load_seq(a, b0 + tid);
-            n = steps_of(x) * Hkv;
+            n = steps_of(x);
             if (b0 == 0) s = x;
         }
-        const uint32_t before = block_scan(n, &sum, scratch);
+        pairs += uint32_t(__syncthreads_count(n > 0)) * Hkv;
+        const uint32_t before = block_scan(n * Hkv, &sum, scratch);
         if (b0 == 0) {
             n0 = n;
             before0 = before;
         }
         total += sum;
     }
+    const uint32_t cta = blockIdx.x, grid = gridDim.x;
+    // parts of at most `part` steps make at most total / part + pairs <= grid CTAs; each warp keeps
+    // two steps
+    const uint32_t part = pairs < grid ? max(2u * kWarps, (total + grid - pairs - 1) / (grid - pairs)) : 0u;
+    const bool aligned = part > 0 && part <= max(2u * kWarps, total / grid + kPiece);
     // no more CTAs than leave every warp two steps: fewer parts to join
-    const uint32_t ctas = max(1u, min(gridDim.x, total / (2 * kWarps))), cta = blockIdx.x;
+    const uint32_t ctas = max(1u, min(grid, total / (2 * kWarps)));
     const Shares sh{total / ctas, total % ctas};
-    if (cta >= ctas) return;
-    uint32_t u = sh.begin(cta);
-    const uint32_t u_end = sh.begin(cta + 1);
-    if (u >= u_end) return;
-    if (u >= before0 && u - before0 < n0) {
-        first[0] = tid;
-        first[1] = before0;
-        first_seq = s;
+    uint32_t u = 0, u_end = 0;  // the share on the line (not aligned)
+    if (!aligned) {
+        if (cta >= ctas) return;
+        u = sh.begin(cta);
+        u_end = sh.begin(cta + 1);
+        if (u >= u_end) return;
     }
-    if (a.n_seqs > kThreads) {
-        uint32_t base = 0;
+    // places of a sequence: its parts (aligned), or its steps, of all heads
+    auto places_of = [&](uint32_t n) { return (aligned ? (n + part - 1) / part : n) * Hkv; };
+    const uint32_t at = aligned ? cta : u;
+    if (tid == 0) first[0] = ~0u;
+    auto found = [&](uint32_t b, uint32_t before, uint32_t n, const Seq &x) {
+        if (at >= before && at - before < n) {
+            first[0] = b;
+            first[1] = before;
+            first_seq = x;
+        }
+    };
+    uint32_t base = 0;
+    if (a.n_seqs <= kThreads) {
+        uint32_t sum;
+        const uint32_t n = places_of(n0), before = aligned ? block_scan(n, &sum, scratch) : before0;
+        __syncthreads();
+        found(tid, before, n, s);
+    } else {
         for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
             uint32_t n = 0, sum;
             Seq x{};
             if (b0 + tid < a.n_seqs) {
                 x = load_seq(a, b0 + tid);
-                n = steps_of(x) * Hkv;
+                n = places_of(steps_of(x));
             }
             const uint32_t before = base + block_scan(n, &sum, scratch);
-            if (u >= before && u - before < n) {
-                first[0] = b0 + tid;
-                first[1] = before;
-                first_seq = x;
-            }
+            found(b0 + tid, before, n, x);
             base += sum;
-            if (u < base) break;
+            if (at < base) break;
         }
     }
     __syncthreads();
+    if (first[0] == ~0u) return;  // past the last part
     int b = int(first[0]);
-    uint32_t base = first[1];
+    base = first[1];
     s = first_seq;
     uint32_t steps = steps_of(s);
 
     const uint32_t ring = smem_addr(smem) + warp * C::kRing;
     const float sl2 = a.scale * kLog2e;
 
-    while (u < u_end) {
-        while (u - base >= steps * Hkv) {  // the next sequence with a chunk
-            base += steps * Hkv;
-            s = load_seq(a, ++b);
-            steps = steps_of(s);
+    for (bool more = true; more;) {
+        uint32_t h, c0, n_parts, step0, step1, item = 0;
+        if (aligned) {
+            const uint32_t per = (steps + part - 1) / part;
+            h = (at - base) / per;
+            const uint32_t i = at - base - h * per;
+            // even parts of the pair
+            const Shares even{steps / per, steps % per};
+            step0 = even.begin(i);
+            step1 = even.begin(i + 1);
+            c0 = cta - i;
+            n_parts = per;
+            more = false;
+        } else {
+            while (u - base >= steps * Hkv) {  // the next sequence with a chunk
+                base += steps * Hkv;
+                s = load_seq(a, ++b);
+                steps = steps_of(s);
+            }
+            h = (u - base) / steps;
+            item = base + h * steps;  // its first step
+            step0 = u - item;
+            step1 = min(steps, u_end - item);
+            c0 = step0 == 0 ? cta : sh.owner(item);
+            n_parts = (step1 == steps ? cta : sh.owner(item + steps - 1)) - c0 + 1;
+            u = item + step1;
+            more = u < u_end;
         }
-        const uint32_t h = (u - base) / steps;
-        const uint32_t item = base + h * steps;  // its first step
-        const int step0 = int(u - item), step1 = int(min(steps, u_end - item));
         const int rows = min(s.q_len * int(G), kRows), past = s.kv_len - s.q_len;
 
-        // the warp's keys: steps step0 + warp, + kWarps, ...  Lane r < 16 finds the cache offset of
-        // key row r, one step before it is copied.
-        const int mine = step1 - step0 > warp ? (step1 - step0 - warp + kWarps - 1) / kWarps : 0;
+        // the warp's keys: steps step0 + warp, + kWarps, ...  The cache offset of lane r's key row (r <
+        // 16), or of the first row where a step lies within a page, is found a step before the copy.
+        const int mine = step1 - step0 > uint32_t(warp) ? int(step1 - step0 - warp + kWarps - 1) / kWarps : 0;
+        const bool in_page = a.page_size % kStep == 0;
         auto find_row = [&](int i) -> int64_t {
-            const int p = (step0 + warp + i * kWarps) * kStep + (lane & 15);
+            const int p = int(step0 + warp + i * kWarps) * kStep + (in_page ? 0 : lane & 15);
             if (i >= mine || p >= s.kv_len) return -1;
-            const int pi = p / a.page_size;
+            const int pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
             return load_page(a, b, pi) * a.page_stride + (int64_t)(p - pi * a.page_size) * a.token_stride;
         };
-        const uint16_t *kc = static_cast<const uint16_t *>(a.k) + h * a.head_stride;
-        const uint16_t *vc = static_cast<const uint16_t *>(a.v) + h * a.head_stride;
+        const uint16_t *kc = static_cast<const uint16_t *>(a.k) + h * a.head_stride + lane % CH * 8;
+        const uint16_t *vc = static_cast<const uint16_t *>(a.v) + h * a.head_stride + lane % CH * 8;
+        const int64_t lane_row = (int64_t)(lane / CH) * a.token_stride, next_row = (int64_t)RPI * a.token_stride;
+        // rows it * RPI + lane / CH: the swizzle's row bits repeat every 8 rows
         auto copy = [&](int i, int64_t row_off) {
             if (i < mine) {
-                const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes;
+                const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes + lane / CH * (D * 2);
+                const int p = int(step0 + warp + i * kWarps) * kStep;
+                if (in_page && p + kStep <= s.kv_len) {
+                    const uint16_t *ks = kc + row_off + lane_row, *vs = vc + row_off + lane_row;
 #pragma unroll
-                for (int it = 0; it < kStep / RPI; ++it) {
-                    const int r = it * RPI + lane / CH, c = lane % CH;
-                    const int64_t off = __shfl_sync(0xffffffffu, row_off, r);
-                    const uint32_t at = dst + r * (D * 2) + ((c ^ (r & 7)) * 16);
-                    const int n = off >= 0 ? 16 : 0;
-                    cp16(at, kc + (n ? off + c * 8 : 0), n);
-                    cp16(at + kStep * D * 2, vc + (n ? off + c * 8 : 0), n);
+                    for (int it = 0; it < kStep / RPI; ++it, ks += next_row, vs += next_row) {
+                        const uint32_t to = dst + it * RPI * (D * 2) + (((lane % CH) ^ ((it * RPI + lane / CH) & 7)) * 16);
+                        cp16(to, ks, 16);
+                        cp16(to + kStep * D * 2, vs, 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int it = 0; it < kStep / RPI; ++it) {
+                        const int r = it * RPI + lane / CH;
+                        int64_t off = __shfl_sync(0xffffffffu, row_off, in_page ? 0 : r);
+                        if (in_page) off += r * a.token_stride;
+                        const int n = p + r < s.kv_len ? 16 : 0;  // rows past the last key: zeros, nothing is read
+                        const uint32_t to = dst + it * RPI * (D * 2) + (((lane % CH) ^ (r & 7)) * 16);
+                        cp16(to, kc + (n ? off : 0), n);
+                        cp16(to + kStep * D * 2, vc + (n ? off : 0), n);
+                    }
                 }
             }
             cp_commit();
         };
         int64_t next = find_row(0);
 
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            const int64_t cur = next;
+            next = find_row(i + 1);
+            copy(i, cur);
+        }
         // Q as A fragments: rows g and g + 8, columns 16 ks + 2 t4 (+1) and + 8; a row past the
         // last reads the first one's and is zeroed, so that all loads go out together
         uint32_t q[KS][4];
@@ -322,12 +383,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 q[ks][e] = ldp(reinterpret_cast<const uint32_t *>(((e & 1) ? q1 : q0) + ks * 16 + (e >> 1) * 8));
-#pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) {
-            const int64_t cur = next;
-            next = find_row(i + 1);
-            copy(i, cur);
-        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -359,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                     mma16816(sc[1], q[ks], kf[2], kf[3]);
                 }
             }
-            const int key0 = (step0 + warp + i * kWarps) * kStep;
+            const int key0 = int(step0 + warp + i * kWarps) * kStep;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -454,8 +509,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             *reinterpret_cast<float4 *>(parts.o + (slot * kRows + r) * D + d) = v;
             if (d == 0) parts.ml[slot * kRows + r] = make_float2(m, l);
         };
-        const bool whole = step0 == 0 && step1 == int(steps);
-        const uint32_t c0 = step0 == 0 ? cta : sh.owner(item);
+        const bool whole = n_parts == 1;
         const size_t slot = (size_t)cta * 2 + (cta == c0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -480,8 +534,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                 write_part(slot, r, d, acc, m, l);
         }
         if (!whole) {
-            const uint32_t c1 = step1 == int(steps) ? cta : sh.owner(item + steps - 1);
-            const uint32_t n = c1 - c0 + 1, groups = (n + kGroup - 1) / kGroup, k = (cta - c0) / kGroup;
+            const uint32_t n = n_parts, groups = (n + kGroup - 1) / kGroup, k = (cta - c0) / kGroup;
             const uint32_t first_cta = c0 + k * kGroup, members = min(kGroup, n - k * kGroup);
             auto slot_of = [&](uint32_t i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };  // i-th CTA of the pair
             float *sm = reinterpret_cast<float *>(smem);
@@ -499,7 +552,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             }
         }
         __syncthreads();  // the join's buffers become the ring again
-        u = item + step1;
     }
 }
 

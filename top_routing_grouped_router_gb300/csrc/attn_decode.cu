@@ -133,11 +133,11 @@ __device__ __forceinline__ bool arrive_last(uint32_t *word, int shift, uint32_t 
     return *flag != 0;
 }
 
-// Joins parts [0, n) (their slots from slot_of) of `rows` rows; emit(row, d, float4, m, l).
-// sm: float2 [kJoinBatch][kRows] per batch of parts, then per-row results.
-template <int D, typename SlotOf, typename Emit>
-__device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows, float *sm, SlotOf slot_of, Emit emit) {
-    constexpr int PER = kRows * D / 4 / kThreads;  // float4 positions of a thread
+// Joins parts [0, n) (their slots from slot_of) of `rows` <= kMost rows; emit(row, d, float4, m, l).
+// sm: float2 [kJoinBatch][kRows].
+template <int D, int kMost, typename SlotOf, typename Emit>
+__device__ __forceinline__ void join_rows(const Parts &p, uint32_t n, int rows, float *sm, SlotOf slot_of, Emit emit) {
+    constexpr int PER = kMost * D / 4 / kThreads;  // float4 positions of a thread
     const int tid = threadIdx.x;
     const int mr = tid & (kRows - 1), mi = tid / kRows;  // (row, part) whose (max, sum) the thread reads
     float4 acc[PER];
@@ -199,6 +199,14 @@ __device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows,
         const int i = e * kThreads + tid;
         if (i < rows * (D / 4)) emit(i / (D / 4), i % (D / 4) * 4, acc[e], m[e], l[e]);
     }
+}
+
+template <int D, typename SlotOf, typename Emit>
+__device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows, float *sm, SlotOf slot_of, Emit emit) {
+    if (rows <= 8)
+        join_rows<D, 8>(p, n, rows, sm, slot_of, emit);
+    else
+        join_rows<D, 16>(p, n, rows, sm, slot_of, emit);
 }
 
 template <int D>
@@ -365,12 +373,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         };
         int64_t next = find_row(0);
 
-#pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) {
-            const int64_t cur = next;
-            next = find_row(i + 1);
-            copy(i, cur);
-        }
         // Q as A fragments: rows g and g + 8, columns 16 ks + 2 t4 (+1) and + 8; a row past the
         // last reads the first one's and is zeroed, so that all loads go out together
         uint32_t q[KS][4];
@@ -383,6 +385,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 q[ks][e] = ldp(reinterpret_cast<const uint32_t *>(((e & 1) ? q1 : q0) + ks * 16 + (e >> 1) * 8));
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            const int64_t cur = next;
+            next = find_row(i + 1);
+            copy(i, cur);
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

@@ -611,6 +611,15 @@ MOE_API int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64
                           const moe_q4_weight *weight, const void *residual, int64_t residual_stride, void *out,
                           int64_t out_stride, moe_stream_t stream);
 
+/*
+ * Reads and clears the error word of moe_q4_linear on the current device
+ * (MOE_ERR_DEVICE if a bounded wait of its tensor-core kernel ran out, which no
+ * healthy call does; that call's results are unspecified).  Synchronises
+ * `stream`.  Returns MOE_ERR_NULLPTR for a NULL code, MOE_ERR_LAUNCH if the copy
+ * failed.
+ */
+MOE_API int moe_q4_linear_read_error(int32_t *code, moe_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 MOE_API const char *moe_status_string(int status);
 

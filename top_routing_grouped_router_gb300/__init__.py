@@ -23,6 +23,7 @@ __all__ = [
     "moe_debug_set_waits", "MoEAttnShape", "MoEAttnBatch", "MoEKVCache", "MoERope", "MoEQ4LinearShape", "MoEQ4Weight",
     "make_attn_shape", "make_attn_batch", "make_kv_cache", "make_rope", "make_q4_linear_shape", "make_q4_weight",
     "moe_attn_workspace_size", "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear",
+    "moe_q4_linear_read_error",
 ]
 
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_Q4 = 0, 1, 2
@@ -36,7 +37,8 @@ EXPORTED_SYMBOLS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_group
                     "moe_forward_static_scratch", "moe_forward_rmsnorm", "moe_forward_lora", "moe_graph_buckets", "moe_graphs_arena_size", "moe_graphs_create",
                     "moe_graphs_bucket", "moe_graphs_run", "moe_graphs_destroy", "moe_lora_pack_size", "moe_lora_pack",
                     "moe_static_scratch_read_error", "moe_debug_set_waits", "moe_attn_workspace_size",
-                    "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear")
+                    "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear",
+                    "moe_q4_linear_read_error")
 
 
 class MoEError(RuntimeError):
@@ -133,6 +135,7 @@ def lib() -> ctypes.CDLL:
             "moe_rope_append": [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp],
             "moe_paged_attention": [vp, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
             "moe_q4_linear": [vp, vp, i64, vp, vp, i64, vp, i64, vp],
+            "moe_q4_linear_read_error": [ctypes.POINTER(ctypes.c_int32), vp],
         }
         for name, argtypes in sig.items():
             f = getattr(L, name)
@@ -502,3 +505,10 @@ def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
         _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_q4_linear")
+
+
+def moe_q4_linear_read_error(stream=None) -> int:
+    """Reads and clears the 4-bit linear's device error word (synchronises the stream)."""
+    code = ctypes.c_int32(0)
+    _check(lib().moe_q4_linear_read_error(ctypes.byref(code), _stream(stream)), "moe_q4_linear_read_error")
+    return code.value

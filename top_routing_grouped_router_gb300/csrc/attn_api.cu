@@ -1,6 +1,7 @@
 // attn_api.cu -- the extern "C" entry points of the attention half of a decoder layer:
 // host-side validation, workspace sizes and the choice of kernel.
 #include "attn.cuh"
+#include "q4_linear.cuh"
 #include "tc_common.cuh"
 
 #include <cmath>
@@ -209,6 +210,11 @@ int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64_t x_str
         return MOE_ERR_ALIGN;
     return launch_rc(launch_q4_linear(s, x, x_stride, *weight, residual, residual_stride, out, out_stride, tc::sm_count(),
                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_q4_linear_read_error(int32_t *code, moe_stream_t stream) {
+    if (!code) return MOE_ERR_NULLPTR;
+    return launch_rc(q4::read_error(code, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

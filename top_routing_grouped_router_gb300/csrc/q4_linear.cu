@@ -10,25 +10,15 @@
 // A block of inputs that shares a scale is summed by the MMA alone, then added to the fp32
 // result with the scale: the scales cost one multiply-add an output and block, and no weight is
 // rounded.  The warps' sums are added in a fixed order.
-#include "attn.cuh"
+#include "q4_linear.cuh"
 
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
 namespace moe {
+namespace q4 {
 namespace {
-
-struct Q4Args {
-    const uint16_t *x;
-    const uint8_t *codes;
-    const uint16_t *scales;
-    const uint16_t *res;
-    void *out;
-    int64_t x_stride, res_stride, out_stride;
-    int T, K, N, q_block, out_f32;
-    float codebook[16];
-};
 
 // ---------------------------------------------------------------- any q_block
 constexpr int kAnyThreads = 128;
@@ -135,24 +125,20 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int src_byte
 __device__ __forceinline__ void cp4(uint32_t dst, const void *src, int src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
+// Plain loads and MMAs without `volatile`: the compiler may move them past one another (the waits
+// for copies are barriers to it), so that a warp's loads, unpacking and products overlap.
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+    return *reinterpret_cast<const uint32_t *>(__cvta_shared_to_generic(addr));
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
+    return *reinterpret_cast<const uint2 *>(__cvta_shared_to_generic(addr));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
+    return *reinterpret_cast<const uint4 *>(__cvta_shared_to_generic(addr));
 }
 __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -160,23 +146,12 @@ __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uin
 // The same with another addend: starts a sum.
 __device__ __forceinline__ void mma16816_from(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1, const uint4 &z) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%10, %11, %12, %13};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(__uint_as_float(z.x)),
                    "f"(__uint_as_float(z.y)), "f"(__uint_as_float(z.z)), "f"(__uint_as_float(z.w)));
 }
-// (w & 0x00780078) | 0x41804180: two codes, already shifted to bits 3 .. 6 of each half, become
-// the bf16 pair 16 + j, exactly.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask, uint32_t bias) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bias));
-    return r;
-}
-// One 16-bit half of a word as a bf16 value: sel 0x1044 the low one, 0x3244 the high one.
-constexpr uint32_t kLow = 0x1044, kHigh = 0x3244;
-__device__ __forceinline__ float half_of(uint32_t w, uint32_t sel) { return __uint_as_float(__byte_perm(w, 0, sel)); }
-
 // NT: 8-row tiles of x.  kFine: q_block 32, four blocks a stage; else 64 times a power of two.
 // kAffine: codebook step * (j - j0).  The MMA multiplies the exact integers 16 + j, and each sum
 // starts at -(16 + j0) sum x of its block (fp32, found once a CTA), which leaves sum (j - j0) x: the
@@ -307,40 +282,44 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         float *z = reinterpret_cast<float *>(starts + ((size_t)block * NT + row / 8) * 64 + (row >> 1 & 3) * 16);
         z[row & 1] = z[2 + (row & 1)] = v;
     };
-    for (int i = m.rows * n8 + tid; i < n8 * kCols; i += kThreads) {
-        const int row = i / n8, c = i - row * n8;
-        put(c, row, make_uint4(0, 0, 0, 0));
-        if (kAffine && c % kPer == 0) put_start(c / kPer, row, 0.f);
-    }
+    for (int row = m.rows + warp; row < kCols; row += kWarps)
+        for (int c = lane; c < n8; c += 32) {
+            put(c, row, make_uint4(0, 0, 0, 0));
+            if (kAffine && c % kPer == 0) put_start(c / kPer, row, 0.f);
+        }
     griddep_wait();
     griddep_launch_dependents();
-    const int live = m.rows * n8;  // a multiple of 16: the lanes of a block stay together
-    constexpr int kBatch = 4;      // loads in flight a thread
-    for (int i0 = tid; i0 < live; i0 += kBatch * kThreads) {
-        uint4 v[kBatch];
+    // the warps take the rows in turn, or where those are few, pieces of one: n8 is a multiple of 16,
+    // so the lanes of a block stay together
+    constexpr int kBatch = 4;  // loads in flight a thread
+    const int beside_rows = m.rows < kWarps ? kWarps / m.rows : 1;  // warps on a row
+    const int row_step = kWarps / beside_rows, c_step = beside_rows * 32;
+    for (int row = warp / beside_rows; row < m.rows && warp < row_step * beside_rows; row += row_step) {
+        const uint16_t *xr = a.x + (m.T0 + row) * a.x_stride + (int64_t)s0 * kIn;
+        const int most = a.K - 8 - s0 * kIn;  // the last whole piece of the row
+        for (int c0 = (warp % beside_rows) * 32 + lane; c0 < n8; c0 += kBatch * c_step) {
+            uint4 v[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = min(i0 + b * kThreads, live - 1), row = i / n8, k = s0 * kIn + (i - row * n8) * 8;
-            v[b] = ldp16(a.x + (m.T0 + row) * a.x_stride + min(k, a.K - 8));
-        }
+            for (int b = 0; b < kBatch; ++b) v[b] = ldp16(xr + min((c0 + b * c_step) * 8, most));
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * kThreads, row = i / n8, c = i - row * n8;
-            if (i >= live) break;  // whole groups of 16 lanes leave together
-            if (s0 * kIn + c * 8 >= a.K) v[b] = make_uint4(0, 0, 0, 0);
-            if (kAffine) {
-                float f[8];
-                attn::unpack8(v[b], f);
-                float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-                const uint32_t group_mask = 0xffu << (lane & 24);
+            for (int b = 0; b < kBatch; ++b) {
+                const int c = c0 + b * c_step;
+                if (c >= n8) break;  // whole groups of 16 lanes leave together
+                if (c * 8 > most) v[b] = make_uint4(0, 0, 0, 0);
+                if (kAffine) {
+                    float f[8];
+                    attn::unpack8(v[b], f);
+                    float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                    const uint32_t group_mask = 0xffu << (lane & 24);
 #pragma unroll
-                for (int w = 1; w < kPer; w <<= 1) sum += __shfl_xor_sync(group_mask, sum, w);
-                if (c % kPer == 0) put_start(c / kPer, row, -m.centre * sum);
-                const uint4 u = v[b];
-                v[b] = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
-                                  __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+                    for (int w = 1; w < kPer; w <<= 1) sum += __shfl_xor_sync(group_mask, sum, w);
+                    if (c % kPer == 0) put_start(c / kPer, row, -m.centre * sum);
+                    const uint4 u = v[b];
+                    v[b] = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                                      __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+                }
+                put(c, row, v[b]);
             }
-            put(c, row, v[b]);
         }
     }
     __syncthreads();
@@ -476,26 +455,23 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         float *pb = part + (k & 1) * kCols * wide;
         auto emit = [&](int row, int n, float y) {
             n += n0;
-            if (row >= m.rows || n >= N) return;
-            const int64_t tr = m.T0 + row;
-            y *= m.step;
-            if (a.res) y += bf16_bits_to_f32(ldp(a.res + tr * a.res_stride + n));
-            if (a.out_f32)
-                static_cast<float *>(a.out)[tr * a.out_stride + n] = y;
-            else
-                static_cast<uint16_t *>(a.out)[tr * a.out_stride + n] = f32_to_bf16_bits(y);
+            if (row < m.rows && n < N) q4_emit(a, m.T0 + row, n, y * m.step);
         };
-        // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part
-        const int cols = m.slices == 1 ? min(kCols, m.rows) : kCols;
-        for (int idx = tid; idx < cols * wide; idx += kThreads) {
-            const int row = idx >> wide_log2, n = idx & (wide - 1);
-            const float *rr = red + (uint32_t(n) / kOut * kCols + row) * kRedStride + uint32_t(n) % kOut;
-            float y = rr[0];
-            for (int w = 1; w < parts; ++w) y += rr[w * m.side * kCols * kRedStride];
-            if (m.slices == 1)
-                emit(row, n, y);
-            else
-                pb[idx] = y;
+        // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part.
+        // Threads are a multiple of the tile's outputs: a thread keeps its output, rows go by.
+        {
+            const uint32_t n = tid & (wide - 1), rows_step = kThreads >> wide_log2;
+            const int cols = m.slices == 1 ? m.rows : kCols;
+            const float *rr = red + (n / kOut * kCols) * kRedStride + n % kOut;
+            const int part_step = m.side * kCols * kRedStride;
+            for (int row = tid >> wide_log2; row < cols; row += rows_step) {
+                float y = rr[row * kRedStride];
+                for (int w = 1; w < parts; ++w) y += rr[row * kRedStride + w * part_step];
+                if (m.slices == 1)
+                    emit(row, int(n), y);
+                else
+                    pb[row * wide + n] = y;
+            }
         }
         if (m.slices > 1) {
             // each CTA of the cluster adds the slices of its part of the outputs, in order; the
@@ -592,6 +568,7 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
+    if (affine && !fine && a.T > 8 && run_tc(a, step, twice, sms, st, err)) return true;
     auto fits = [&](int nt) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
@@ -616,10 +593,11 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
 }
 
 }  // namespace
+}  // namespace q4
 
 cudaError_t launch_q4_linear(const moe_q4_linear_shape &s, const void *x, int64_t x_stride, const moe_q4_weight &w,
                              const void *res, int64_t res_stride, void *out, int64_t out_stride, int sms, cudaStream_t st) {
-    Q4Args a{};
+    q4::Q4Args a{};
     a.x = static_cast<const uint16_t *>(x);
     a.codes = static_cast<const uint8_t *>(w.codes);
     a.scales = static_cast<const uint16_t *>(w.scales);
@@ -637,8 +615,8 @@ cudaError_t launch_q4_linear(const moe_q4_linear_shape &s, const void *x, int64_
     // q_block 32, or 64 times a power of two (a shift finds an input's block)
     const int q = s.q_block;
     cudaError_t err;
-    if ((q == 32 || (q % 64 == 0 && (q & (q - 1)) == 0)) && run_mma(a, sms, st, &err)) return err;
-    return launch_any(a, s.out_dtype, st);
+    if ((q == 32 || (q % 64 == 0 && (q & (q - 1)) == 0)) && q4::run_mma(a, sms, st, &err)) return err;
+    return q4::launch_any(a, s.out_dtype, st);
 }
 
 }  // namespace moe

@@ -89,7 +89,7 @@ constexpr int kLutBytes = 256 * 32 * 8;
 template <int NT, int MT, bool kFine, bool kAffine>
 struct Var {
     static constexpr int kWarps = MT == 2 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kDepth = MT == 2 || NT >= 2 ? 3 : 4;  // stages of a warp's ring
+    static constexpr int kDepth = MT == 2 || NT == 2 ? 3 : 4;  // stages of a warp's ring
     static constexpr int kOut = MT * kStrip;                 // outputs of a warp
     static constexpr int kCols = NT * 8;                     // rows of x
     static constexpr int kCodes = kOut * kIn / 2;            // code bytes of a stage
@@ -105,6 +105,8 @@ struct Var {
     static int max_stages() { return (kMaxSmem - kFixed) / (2 * kHalf); }                           // of one CTA
     static int max_stages_sliced() { return (kMaxSmem - kFixed - part_bytes(kWarps)) / (2 * kHalf); }  // of a cluster's
 };
+
+constexpr int kMmaRows = 16;     // rows of x of a pass
 
 struct MmaArgs {
     Q4Args a;
@@ -515,7 +517,7 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     m.tiles = (strips + m.side - 1) / m.side;
     m.slice_halves = 2 * ((stages + slices - 1) / slices);
     const int smem = V::kFixed + m.slice_halves * V::kHalf + (slices > 1 ? V::part_bytes(m.side) : 0);
-    const int per_sm = std::min(MT == 2 || NT >= 8 ? 1 : NT == 4 ? 2 : 3, std::max(1, (kMaxSmem + 1024) / (smem + 1024)));
+    const int per_sm = std::min(MT == 2 ? 1 : 3, std::max(1, (kMaxSmem + 1024) / (smem + 1024)));
     const int groups = std::max(1, std::min(m.tiles, sms * per_sm / slices));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -537,29 +539,21 @@ template <bool kFine, bool kAffine>
 struct Rows {  // the variants by rows of x
     static bool fits(int nt, int stages) {
         const int s = (stages + kMaxSlices - 1) / kMaxSlices;
-        return s <= (nt == 1   ? Var<1, 1, kFine, kAffine>::max_stages_sliced()
-                     : nt == 2 ? Var<2, 1, kFine, kAffine>::max_stages_sliced()
-                     : nt == 4 ? Var<4, 1, kFine, kAffine>::max_stages_sliced()
-                               : Var<8, 1, kFine, kAffine>::max_stages_sliced());
+        return s <= (nt == 1 ? Var<1, 1, kFine, kAffine>::max_stages_sliced() : Var<2, 1, kFine, kAffine>::max_stages_sliced());
     }
-    static cudaError_t launch(int nt, const MmaArgs &m, int stages, int sms, cudaStream_t st) {
+    template <int NT>
+    static cudaError_t launch_nt(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
         // two strips a warp: when every SM gets at least eight such pairs and x fits one CTA
-        const bool two = m.a.N >= sms * 8 * 2 * kStrip;
-        if (nt == 1)
-            return two && stages <= Var<1, 2, kFine, kAffine>::max_stages()
-                       ? launch_mma<1, 2, kFine, kAffine>(m, stages, sms, st)
-                       : launch_mma<1, 1, kFine, kAffine>(m, stages, sms, st);
-        if (nt == 2)
-            return two && stages <= Var<2, 2, kFine, kAffine>::max_stages()
-                       ? launch_mma<2, 2, kFine, kAffine>(m, stages, sms, st)
-                       : launch_mma<2, 1, kFine, kAffine>(m, stages, sms, st);
-        return nt == 4 ? launch_mma<4, 1, kFine, kAffine>(m, stages, sms, st)
-                       : launch_mma<8, 1, kFine, kAffine>(m, stages, sms, st);
+        const bool two = m.a.N >= sms * 8 * 2 * kStrip && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
+        return two ? launch_mma<NT, 2, kFine, kAffine>(m, stages, sms, st) : launch_mma<NT, 1, kFine, kAffine>(m, stages, sms, st);
+    }
+    static cudaError_t launch(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
+        return m.rows <= 8 ? launch_nt<1>(m, stages, sms, st) : launch_nt<2>(m, stages, sms, st);
     }
 };
 
-// The rows in passes of up to 64 (fewer when x would not fit even split over a cluster); false
-// if not even 8 rows fit.
+// The rows in passes of 16 (8 when x would not fit even split over a cluster); false if not even
+// 8 rows fit.
 bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     float step = 1.f;
     int twice = 0;
@@ -568,12 +562,14 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
-    if (affine && !fine && a.T > 8 && run_tc(a, step, twice, sms, st, err)) return true;
+    // tcgen05 from the second pass of 16 rows on, and where the weights are large enough that its
+    // longer start does not count (16 x 4096 x 5120: 13.8 us against 18.9; 12 x 2048 x 2048: 13.7, 7.6)
+    if (affine && !fine && (a.T > kMmaRows || (a.T > 8 && (int64_t)a.N * a.K >= (1 << 24))) && run_tc(a, step, twice, sms, st, err)) return true;
     auto fits = [&](int nt) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
     };
-    int nt_max = 8;
+    int nt_max = 2;
     while (nt_max > 0 && !fits(nt_max)) nt_max /= 2;
     if (nt_max == 0) return false;
     MmaArgs m{};
@@ -585,9 +581,8 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     for (int t0 = 0; t0 < a.T && *err == cudaSuccess; t0 += nt_max * 8) {
         m.T0 = t0;
         m.rows = std::min(a.T - t0, nt_max * 8);
-        const int nt = m.rows <= 8 ? 1 : m.rows <= 16 ? 2 : m.rows <= 32 ? 4 : 8;
-        *err = affine ? (fine ? Rows<true, true>::launch(nt, m, stages, sms, st) : Rows<false, true>::launch(nt, m, stages, sms, st))
-                      : (fine ? Rows<true, false>::launch(nt, m, stages, sms, st) : Rows<false, false>::launch(nt, m, stages, sms, st));
+        *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
+                      : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));
     }
     return true;
 }

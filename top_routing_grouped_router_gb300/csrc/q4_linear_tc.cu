@@ -14,6 +14,7 @@
 #include "tc_common.cuh"
 
 #include <algorithm>
+#include <cmath>
 #include <cooperative_groups.h>
 
 #include "q4_linear.cuh"
@@ -26,7 +27,9 @@ using namespace tc;
 
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kUnpack0 = 2, kAdd0 = 10, kThreads = 18 * 32;
 constexpr int kOut = 128, kIn = 128;
-constexpr int kRing = 6;                              // stages of codes and scales
+// Stages of codes and scales: what fits next to x, from kMinRing to kMaxRing.  A stage lands 1.5 us
+// after it is asked for under load: 6 stages (48 KB) held a 16 x 2048 x 131072 product at 61 us.
+constexpr int kMinRing = 6, kMaxRing = 16;
 constexpr int kCodeBytes = kOut * kIn / 2, kScaleBytes = kOut * 2 * 4, kStage = kCodeBytes + kScaleBytes;
 constexpr int kA = 4;                                 // A operands in TMEM, 64 columns each
 constexpr uint32_t kColD = kA * 64;
@@ -38,7 +41,7 @@ __device__ int32_t g_err;
 struct TcArgs {
     Q4Args a;
     int T0, rows;
-    int slices, tiles, slice_stages, shift;
+    int slices, tiles, slice_stages, shift, ring;
     float centre, step;
     unsigned long long wait_ns;
     int extra_need;
@@ -51,16 +54,26 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void *src, int src_bytes
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// D = A B over 64 inputs: four MMAs, A at TMEM columns a + 8 i, B 32 bytes further each.
-__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+// A stage's products, D = A B over its first 64 inputs and over the others (four MMAs each, A at
+// TMEM columns a + 8 i, B 32 bytes further each; the second half of B at b2, of D at d2), and the
+// commits to the two barriers: one election, one block of assembly, since the issuing warp shares
+// its scheduler with warps that unpack and add.
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t d2, uint32_t a, uint64_t b, uint64_t b2, uint32_t idesc,
+                                          uint32_t bar_d, uint32_t bar_a) {
     asm volatile(
-        "{\n\t.reg .pred e, z;\n\t.reg .b64 v;\n\t.reg .b32 p;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 z, %3, %3;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, z;\n\tsetp.eq.b32 z, %3, %3;\n\t"
-        "add.s32 p, %1, 8;\n\tadd.s64 v, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
-        "add.s32 p, %1, 16;\n\tadd.s64 v, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t"
-        "add.s32 p, %1, 24;\n\tadd.s64 v, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %3, z;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc)
+        "{\n\t.reg .pred e, z, o;\n\t.reg .b64 v;\n\t.reg .b32 p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 z, %5, %5;\n\tsetp.eq.b32 o, %5, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %3, %5, z;\n\t"
+        "add.s32 p, %2, 8;\n\tadd.s64 v, %3, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %5, o;\n\t"
+        "add.s32 p, %2, 16;\n\tadd.s64 v, %3, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %5, o;\n\t"
+        "add.s32 p, %2, 24;\n\tadd.s64 v, %3, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [p], v, %5, o;\n\t"
+        "add.s32 p, %2, 32;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%1], [p], %4, %5, z;\n\t"
+        "add.s32 p, %2, 40;\n\tadd.s64 v, %4, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%1], [p], v, %5, o;\n\t"
+        "add.s32 p, %2, 48;\n\tadd.s64 v, %4, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%1], [p], v, %5, o;\n\t"
+        "add.s32 p, %2, 56;\n\tadd.s64 v, %4, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%1], [p], v, %5, o;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}"
+        ::"r"(d), "r"(d2), "r"(a), "l"(b), "l"(b2), "r"(idesc), "r"(bar_d), "r"(bar_a)
         : "memory");
 }
 template <int N>
@@ -97,14 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     extern __shared__ __align__(1024) uint8_t smem[];
     const Q4Args &a = m.a;
     uint8_t *xs = smem;                                             // [64 inputs][COLS][128 bytes]
-    uint8_t *ring = xs + (size_t)m.slice_stages * 2 * COLS * 128;   // [kRing][codes, scales]
-    float *starts = reinterpret_cast<float *>(ring + kRing * kStage);  // [64 inputs][COLS]: -(16 + j0) sum x
-    uint64_t *cf = reinterpret_cast<uint64_t *>(starts + (size_t)m.slice_stages * 2 * COLS);  // [kRing]
-    uint64_t *ce = cf + kRing, *af = ce + kRing, *ae = af + kA, *df = ae + kA, *de = df + kD, *xf = de + kD;
+    uint8_t *ring = xs + (size_t)m.slice_stages * 2 * COLS * 128;   // [m.ring][codes, scales]
+    float *starts = reinterpret_cast<float *>(ring + m.ring * kStage);  // [64 inputs][COLS]: -(16 + j0) sum x
+    uint64_t *cf = reinterpret_cast<uint64_t *>(starts + (size_t)m.slice_stages * 2 * COLS);  // [kMaxRing]
+    uint64_t *ce = cf + kMaxRing, *af = ce + kMaxRing, *ae = af + kA, *df = ae + kA, *de = df + kD, *xf = de + kD;
     uint64_t *drain = xf + 1;
     volatile int *abort = reinterpret_cast<volatile int *>(drain + 1);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1) + 1;
-    static_assert((2 * kRing + 2 * kA + 2 * 4 + 2) * 8 + 8 <= kCtrl, "");
+    static_assert((2 * kMaxRing + 2 * kA + 2 * 4 + 2) * 8 + 8 <= kCtrl, "");
     const Waits wt{&g_err, abort, m.wait_ns, smem_u32(const_cast<int *>(abort))};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {  // not seen: shared memory starts on such a boundary
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     const int my_tiles = (m.tiles - group + groups - 1) / groups;
 
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < m.ring; ++i) {
             mbar_init(smem_u32(&cf[i]), 33);      // the TMA's arrival and 32 lanes' scales
             mbar_init(smem_u32(&ce[i]), 4 + 8);   // unpacking and adding warps
         }
@@ -177,21 +190,22 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
                 }
                 cp_arrive(bar);
                 ++filled;
-                if (++slot == kRing) {
+                if (++slot == m.ring) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
         }
         if (!ok) {  // the copies in flight land before the CTA gives up its memory
-            for (int i = max(0, filled - kRing); i < filled; ++i)
-                mbar_wait_drain(smem_u32(&cf[i % kRing]), (i / kRing) & 1, wt);
+            for (int i = max(0, filled - m.ring); i < filled; ++i)
+                mbar_wait_drain(smem_u32(&cf[i % m.ring]), (i / m.ring) & 1, wt);
         }
     } else if (warp == kMmaWarp) {
         const uint32_t idesc = instr_desc(kOut, COLS);
         int i = 0;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(xf), 0, wt));
-        for (int k = 0; k < my_tiles && ok; ++k)
+        for (int k = 0; k < my_tiles && ok; ++k) {
+            uint64_t b_desc = smem_desc(smem_u32(xs));
             for (int st = s0; st < s1; ++st, ++i) {
                 ok = mbar_wait(smem_u32(&de[i % kD]), ((i / kD) & 1) ^ 1, wt) &&
                      mbar_wait(smem_u32(&af[i % kA]), (i / kA) & 1, wt);
@@ -200,13 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
                     break;
                 }
                 tc_fence_after();
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    mma_block(tmem + kColD + ((i % kD) * 2 + b) * COLS, tmem + (i % kA) * 64 + b * 32,
-                              smem_desc(smem_u32(xs + (size_t)((st - s0) * 2 + b) * COLS * 128)), idesc);
-                mma_commit_warp(smem_u32(&df[i % kD]));
-                mma_commit_warp(smem_u32(&ae[i % kA]));
+                const uint32_t d = tmem + kColD + (i % kD) * 2 * COLS;
+                mma_stage(d, d + COLS, tmem + (i % kA) * 64, b_desc, b_desc + COLS * 8, idesc, smem_u32(&df[i % kD]),
+                          smem_u32(&ae[i % kA]));
+                b_desc += 2 * COLS * 8;
             }
+        }
         // every MMA and every arrival of its commits is over before the CTA ends
         mma_commit_warp(smem_u32(drain));
         mbar_wait_drain(smem_u32(drain), 0, wt);
@@ -215,10 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
         const uint32_t mask = 0x00780078u, bias = 0x41804180u, ta = tmem + (uint32_t(q) << 21);
         const uint32_t row_at = row * 64, swz = (row >> 1) & 3;
         const int total = my_tiles * (s1 - s0);
+        int slot = set;
+        uint32_t phase = 0;
         for (int i = set; i < total; i += 2) {
-            ok = mbar_wait(smem_u32(&cf[i % kRing]), (i / kRing) & 1, wt);
+            ok = mbar_wait(smem_u32(&cf[slot]), phase, wt);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const uint32_t at = smem_u32(ring + (i % kRing) * kStage) + row_at;
+            const uint32_t at = smem_u32(ring + slot * kStage) + row_at;
             uint32_t w[16], v[64];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -236,7 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
                 v[4 * c + 3] = code_pair(w[c] >> 9, mask, bias);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ce[i % kRing]));
+            if (lane == 0) mbar_arrive(smem_u32(&ce[slot]));
+            if ((slot += 2) >= m.ring) {
+                slot -= m.ring;
+                phase ^= 1;
+            }
             ok = mbar_wait(smem_u32(&ae[i % kA]), ((i / kA) & 1) ^ 1, wt);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -260,29 +279,30 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
             }
         griddep_wait();
         griddep_launch_dependents();
-        constexpr int kBatch = 4;  // loads in flight a thread
+        constexpr int kBatch = 8;  // loads in flight a thread
         const int most = a.K - 8 - s0 * kIn, beside = m.rows < 8 ? 8 / m.rows : 1, mine = warp - kAdd0;
         for (int r = mine / beside; r < m.rows && mine < 8 / beside * beside; r += 8 / beside) {
             const uint16_t *xr = a.x + (m.T0 + r) * a.x_stride + (int64_t)s0 * kIn;
-            for (int c0 = (mine % beside) * 32 + lane; c0 < n8; c0 += kBatch * beside * 32) {
+            for (int w0 = mine % beside * 32; w0 < n8; w0 += kBatch * beside * 32) {
+                const int c0 = w0 + lane;
                 uint4 v[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) v[b] = ldp16(xr + min((c0 + b * beside * 32) * 8, most));
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     const int c = c0 + b * beside * 32;
-                    if (c >= n8) break;  // n8 is a multiple of 16: whole groups of 16 lanes leave together
                     if (c * 8 > most) v[b] = make_uint4(0, 0, 0, 0);
                     float f[8];
                     attn::unpack8(v[b], f);
                     float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-                    const uint32_t lanes = 0xffu << (lane & 24);
 #pragma unroll
-                    for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(lanes, sum, w);
-                    if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = -m.centre * sum;
+                    for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
                     const uint4 u = v[b];
-                    put(c, r, make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
-                                         __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632)));
+                    if (c < n8) {
+                        if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = -m.centre * sum;
+                        put(c, r, make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                                             __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632)));
+                    }
                 }
             }
         }
@@ -293,19 +313,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
         const int set = (warp - kAdd0) >> 2, q = warp & 3, row = q * 32 + lane;
         const uint32_t ta = tmem + (uint32_t(q) << 21) + kColD + set * kHalf;
         const uint32_t odd = uint32_t(row) * blocks;  // tiles start on even rows: the same parity in all
-        int i = 0;
+        int i = 0, slot = 0;
+        uint32_t phase = 0;
         for (int k = 0; k < my_tiles && ok; ++k) {
 #pragma unroll
             for (int n = 0; n < kHalf; ++n) acc[n] = 0.f;
             for (int st = s0; st < s1; ++st, ++i) {
-                ok = mbar_wait(smem_u32(&cf[i % kRing]), (i / kRing) & 1, wt) &&
+                ok = mbar_wait(smem_u32(&cf[slot]), phase, wt) &&
                      mbar_wait(smem_u32(&df[i % kD]), (i / kD) & 1, wt);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint2 words = lds_v2(smem_u32(ring + (i % kRing) * kStage) + kCodeBytes + row * 8);
+                const uint2 words = lds_v2(smem_u32(ring + slot * kStage) + kCodeBytes + row * 8);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const float sc = half_of(b ? words.y : words.x, (odd + ((st * 2 + b) >> m.shift)) & 1 ? kHigh : kLow);
@@ -330,7 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&de[i % kD]));
-                    mbar_arrive(smem_u32(&ce[i % kRing]));
+                    mbar_arrive(smem_u32(&ce[slot]));
+                }
+                if (++slot == m.ring) {
+                    slot = 0;
+                    phase ^= 1;
                 }
             }
             if (!ok || m.slices > 1) break;  // sliced: one tile a CTA, joined below
@@ -375,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
 }
 
 template <int COLS>
-int smem_bytes(int slice_stages) {
-    return slice_stages * 2 * COLS * (128 + 4) + kRing * kStage + kCtrl;
+int smem_bytes(int slice_stages, int ring) {
+    return slice_stages * 2 * COLS * (128 + 4) + ring * kStage + kCtrl;
 }
 
 template <int COLS>
@@ -390,6 +415,7 @@ cudaError_t launch(const CUtensorMap &map, TcArgs m, int stages, int sms, cudaSt
         attr_set[dev] = true;
     }
     m.slice_stages = (stages + m.slices - 1) / m.slices;
+    m.ring = std::min(kMaxRing, (kMaxSmem - smem_bytes<COLS>(m.slice_stages, 0)) / kStage);
     const int groups = m.slices > 1 ? m.tiles : std::min(m.tiles, sms);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -400,7 +426,7 @@ cudaError_t launch(const CUtensorMap &map, TcArgs m, int stages, int sms, cudaSt
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(groups * m.slices));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(smem_bytes<COLS>(m.slice_stages));
+    cfg.dynamicSmemBytes = size_t(smem_bytes<COLS>(m.slice_stages, m.ring));
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = m.slices > 1 ? 2 : 1;
@@ -408,7 +434,7 @@ cudaError_t launch(const CUtensorMap &map, TcArgs m, int stages, int sms, cudaSt
 }
 
 template <int COLS>
-bool fits(int stages, int slices) { return smem_bytes<COLS>((stages + slices - 1) / slices) <= kMaxSmem; }
+bool fits(int stages, int slices) { return smem_bytes<COLS>((stages + slices - 1) / slices, kMinRing) <= kMaxSmem; }
 
 }  // namespace
 
@@ -424,15 +450,29 @@ bool run_tc(const Q4Args &a, float step, int twice_j0, int sms, cudaStream_t st,
     m.step = step;
     m.wait_ns = wait_limit_ns();
     m.extra_need = debug_extra_need();
-    // slices: while all CTAs of a single round fit the machine; a slice keeps two stages
-    int slices = 1;
-    while (slices < kMaxSlices && tiles * slices * 2 <= sms && stages >= slices * 4) slices *= 2;
-    m.slices = slices;
+    // Rows of a pass and slices of the inputs, by the time they should take (us, measured at 2048
+    // inputs): a stage 0.45, 0.5 or 0.7 for 16, 32 or 64 columns, 4 to bring 32768 elements of x into
+    // place, 6 to start and end a CTA.  Unsliced CTAs go through several tiles with one x; sliced ones
+    // hold one tile, and clusters of 8 and 4 find places for fewer CTAs than there are SMs.
+    int cols_max = 0;
+    double best = 1e30;
+    for (int cols = 16; cols <= 64; cols *= 2)
+        for (int slices = 1; slices <= kMaxSlices && (slices == 1 || stages >= 2 * slices); slices *= 2) {
+            const bool ok = cols == 64 ? fits<64>(stages, slices) : cols == 32 ? fits<32>(stages, slices) : fits<16>(stages, slices);
+            if (!ok || (cols > 16 && cols / 2 >= a.T)) continue;
+            const double stage = cols == 64 ? 0.7 : cols == 32 ? 0.5 : 0.45;
+            const double part = double((stages + slices - 1) / slices), x = 4.0 * cols * part * kIn / 32768;
+            const int places = slices == 8 ? 96 : slices == 4 ? 128 : sms;
+            const double rounds = std::ceil(double(tiles) * slices / places);
+            const double t = std::ceil(double(a.T) / cols) * (slices == 1 ? rounds * part * stage + x + 6 : rounds * (part * stage + x + 6));
+            if (t < best) {
+                best = t;
+                cols_max = cols;
+                m.slices = slices;
+            }
+        }
+    if (cols_max == 0) return false;
     CUtensorMap map;
-    int cols_max = 64;
-    while (cols_max >= 16 && !(cols_max == 64 ? fits<64>(stages, slices) : cols_max == 32 ? fits<32>(stages, slices) : fits<16>(stages, slices)))
-        cols_max /= 2;
-    if (cols_max < 16) return false;
     if (!make_map(&map, a.codes, (uint64_t)a.N, (uint64_t)a.K / 2, kOut, kIn / 2, true, true)) return false;
     *err = cudaSuccess;
     for (int t0 = 0; t0 < a.T && *err == cudaSuccess; t0 += cols_max) {

@@ -535,6 +535,9 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, MT, kFine, kAffine>, m);
 }
 
+// Outputs from which every SM gets at least eight pairs of strips.
+int two_strips_from(int sms) { return sms * 8 * 2 * kStrip; }
+
 template <bool kFine, bool kAffine>
 struct Rows {  // the variants by rows of x
     static bool fits(int nt, int stages) {
@@ -543,8 +546,8 @@ struct Rows {  // the variants by rows of x
     }
     template <int NT>
     static cudaError_t launch_nt(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
-        // two strips a warp: when every SM gets at least eight such pairs and x fits one CTA
-        const bool two = m.a.N >= sms * 8 * 2 * kStrip && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
+        // two strips a warp where there are plenty and x fits one CTA
+        const bool two = m.a.N >= two_strips_from(sms) && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
         return two ? launch_mma<NT, 2, kFine, kAffine>(m, stages, sms, st) : launch_mma<NT, 1, kFine, kAffine>(m, stages, sms, st);
     }
     static cudaError_t launch(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
@@ -562,9 +565,12 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
-    // tcgen05 from the second pass of 16 rows on, and where the weights are large enough that its
-    // longer start does not count (16 x 4096 x 5120: 13.8 us against 18.9; 12 x 2048 x 2048: 13.7, 7.6)
-    if (affine && !fine && (a.T > kMmaRows || (a.T > 8 && (int64_t)a.N * a.K >= (1 << 24))) && run_tc(a, step, twice, sms, st, err)) return true;
+    // tcgen05 from the second pass of 16 rows on.  For 9 to 16 rows also where the weights are large
+    // enough that its longer start does not count, but not so many that mma.sync takes two strips a
+    // warp (16 x 4096 x 5120: 13.8 us against 18.9; 12 x 2048 x 2048: 13.7, 7.6; 16 x 2048 x 131072:
+    // 58.6, 54.1)
+    const bool large = (int64_t)a.N * a.K >= (1 << 24) && a.N < two_strips_from(sms);
+    if (affine && !fine && (a.T > kMmaRows || (a.T > 8 && large)) && run_tc(a, step, twice, sms, st, err)) return true;
     auto fits = [&](int nt) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));

@@ -7,7 +7,7 @@
 //             a LOP3 for two of them), written to TMEM as the A operand
 //   MMA       A (TMEM, outputs x inputs) times x (shared memory, rows x inputs), one fp32 product
 //             P = sum (16 + j) x for each 64 inputs
-//   add       eight warps: result += scale (P - (16 + j0) sum x), in fp32 registers
+//   add       eight warps, half the columns each: result += scale (P - (16 + j0) sum x), in fp32 registers
 // No weight is rounded.  x lies in shared memory whole (or the CTA's share of the inputs, where a
 // cluster splits them), in the order in which the codes are unpacked.
 #include "attn.cuh"
@@ -26,6 +26,7 @@ namespace {
 using namespace tc;
 
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kUnpack0 = 2, kAdd0 = 10, kThreads = 18 * 32;
+constexpr int kStagers = kThreads / 32 - kUnpack0;  // warps that bring x into place
 constexpr int kOut = 128, kIn = 128;
 // Stages of codes and scales: what fits next to x, from kMinRing to kMaxRing.  A stage lands 1.5 us
 // after it is asked for under load: 6 stages (48 KB) held a 16 x 2048 x 131072 product at 61 us.
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < m.ring; ++i) {
             mbar_init(smem_u32(&cf[i]), 33);      // the TMA's arrival and 32 lanes' scales
-            mbar_init(smem_u32(&ce[i]), 4 + 8);   // unpacking and adding warps
+            mbar_init(smem_u32(&ce[i]), 4 + 8);  // unpacking and adding warps
         }
         for (int i = 0; i < kA; ++i) {
             mbar_init(smem_u32(&af[i]), 4 + m.extra_need);
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
             mbar_init(smem_u32(&df[i]), 1);
             mbar_init(smem_u32(&de[i]), 8);
         }
-        mbar_init(smem_u32(xf), 8);
+        mbar_init(smem_u32(xf), kStagers);
         mbar_init(smem_u32(drain), 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -161,7 +162,52 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     float acc[kHalf];  // adding warps: this output's sums
 
     // Codes and scales are weights, which no kernel of the library writes: they stream while the
-    // kernel before this one ends.  Only the adding warps touch what it may have written.
+    // kernel before this one ends.
+    if (warp >= kUnpack0) {
+            // x, by the unpacking and adding warps before they have anything to do
+        const int n8 = (s1 - s0) * (kIn / 8);
+        auto put = [&](int c, int r, uint4 v) {  // 16-byte piece c of a row: 128-byte swizzle within 64 inputs
+            *reinterpret_cast<uint4 *>(xs + ((size_t)(c >> 3) * COLS + r) * 128 + (((c & 7) ^ (r & 7)) * 16)) = v;
+        };
+        for (int r = m.rows + warp - kUnpack0; r < COLS; r += kStagers)  // rows past the last are zero
+            for (int c = lane; c < n8; c += 32) {
+                put(c, r, make_uint4(0, 0, 0, 0));
+                if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = 0.f;
+            }
+        griddep_wait();
+        griddep_launch_dependents();
+        constexpr int kBatch = 8;  // loads in flight a thread
+        const int most = a.K - 8 - s0 * kIn, beside = m.rows < kStagers ? kStagers / m.rows : 1, mine = warp - kUnpack0;
+        for (int r = mine / beside; r < m.rows && mine < kStagers / beside * beside; r += kStagers / beside) {
+            const uint16_t *xr = a.x + (m.T0 + r) * a.x_stride + (int64_t)s0 * kIn;
+            for (int w0 = mine % beside * 32; w0 < n8; w0 += kBatch * beside * 32) {
+                const int c0 = w0 + lane;
+                uint4 v[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) v[b] = ldp16(xr + min((c0 + b * beside * 32) * 8, most));
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int c = c0 + b * beside * 32;
+                    if (c * 8 > most) v[b] = make_uint4(0, 0, 0, 0);
+                    float f[8];
+                    attn::unpack8(v[b], f);
+                    float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+#pragma unroll
+                    for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                    const uint4 u = v[b];
+                    if (c < n8) {
+                        if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = -m.centre * sum;
+                        put(c, r, make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
+                                             __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632)));
+                    }
+                }
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read x
+        asm volatile("bar.sync 1, %0;" ::"n"(kStagers * 32) : "memory");  // the adding warps read others' start values
+        if (lane == 0) mbar_arrive(smem_u32(xf));
+    }
+
     if (warp == kLoadWarp) {
         int filled = 0;  // stages filled so far
         const int srow = lane >> 1, shalf = lane & 1;
@@ -267,49 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
         }
         ok = __all_sync(0xffffffffu, ok);
     } else {
-        // x, by the adding warps before they have anything to add
-        const int n8 = (s1 - s0) * (kIn / 8);
-        auto put = [&](int c, int r, uint4 v) {  // 16-byte piece c of a row: 128-byte swizzle within 64 inputs
-            *reinterpret_cast<uint4 *>(xs + ((size_t)(c >> 3) * COLS + r) * 128 + (((c & 7) ^ (r & 7)) * 16)) = v;
-        };
-        for (int r = m.rows + warp - kAdd0; r < COLS; r += 8)  // rows past the last are zero
-            for (int c = lane; c < n8; c += 32) {
-                put(c, r, make_uint4(0, 0, 0, 0));
-                if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = 0.f;
-            }
-        griddep_wait();
-        griddep_launch_dependents();
-        constexpr int kBatch = 8;  // loads in flight a thread
-        const int most = a.K - 8 - s0 * kIn, beside = m.rows < 8 ? 8 / m.rows : 1, mine = warp - kAdd0;
-        for (int r = mine / beside; r < m.rows && mine < 8 / beside * beside; r += 8 / beside) {
-            const uint16_t *xr = a.x + (m.T0 + r) * a.x_stride + (int64_t)s0 * kIn;
-            for (int w0 = mine % beside * 32; w0 < n8; w0 += kBatch * beside * 32) {
-                const int c0 = w0 + lane;
-                uint4 v[kBatch];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) v[b] = ldp16(xr + min((c0 + b * beside * 32) * 8, most));
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int c = c0 + b * beside * 32;
-                    if (c * 8 > most) v[b] = make_uint4(0, 0, 0, 0);
-                    float f[8];
-                    attn::unpack8(v[b], f);
-                    float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-#pragma unroll
-                    for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                    const uint4 u = v[b];
-                    if (c < n8) {
-                        if ((c & 7) == 0) starts[(c >> 3) * COLS + r] = -m.centre * sum;
-                        put(c, r, make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
-                                             __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632)));
-                    }
-                }
-            }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read x
-        asm volatile("bar.sync 1, 256;" ::: "memory");                // the adding warps read each other's start values
-        if (lane == 0) mbar_arrive(smem_u32(xf));
-
         const int set = (warp - kAdd0) >> 2, q = warp & 3, row = q * 32 + lane;
         const uint32_t ta = tmem + (uint32_t(q) << 21) + kColD + set * kHalf;
         const uint32_t odd = uint32_t(row) * blocks;  // tiles start on even rows: the same parity in all

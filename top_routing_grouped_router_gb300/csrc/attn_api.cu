@@ -31,7 +31,7 @@ int64_t elem_bytes(const moe_attn_shape &s) { return s.dtype == MOE_DT_F32 ? 4 :
 
 // A row stride in elements: a multiple of 16 bytes that does not overlap rows.
 int check_stride(const moe_attn_shape &s, int64_t stride, int heads) {
-    if (stride < (int64_t)heads * s.head_dim) return MOE_ERR_SHAPE;
+    if (stride < (int64_t)heads * s.head_dim || stride > INT32_MAX) return MOE_ERR_SHAPE;
     return (stride * elem_bytes(s)) % 16 ? MOE_ERR_ALIGN : MOE_OK;
 }
 

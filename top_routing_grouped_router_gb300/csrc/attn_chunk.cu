@@ -49,7 +49,7 @@ struct Seg {
 };
 // What the join kernel needs of an item that starts in a CTA's share and goes on past it.
 struct Rec {
-    int n, h, tok0, q0, q_len, last;  // n: parts (0: none); last: the last CTA
+    int n, h, tok0, q0, q_len;  // n: parts (0: none)
 };
 
 // sum_{i < n} floor((a i + b) / m), m > 0, by the Euclid-like recursion; the sum and a n + m fit
@@ -200,25 +200,6 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t p, uint64_t v, uint32
         : "memory");
 }
 
-// Two floats in one 64-bit register, for the paired fp32 instructions.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -420,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         segs[k] = g;
                         if (!whole && starts) {
                             const int last = int(sh.owner(item0 + places - 1));
-                            c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len, last};
+                            c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len};
                         }
                     }
                     ++k;

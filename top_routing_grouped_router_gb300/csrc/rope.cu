@@ -29,7 +29,7 @@ struct RopeArgs {
     float mscale, eps;
 };
 
-// Eight elements as loaded.
+// Eight elements as loaded; get: as four pairs of floats.
 template <typename T>
 struct Raw;
 template <>
@@ -37,7 +37,11 @@ struct Raw<uint16_t> {
     uint4 v;
     __device__ __forceinline__ void load(const uint16_t *p) { v = ldp16(p); }
     __device__ __forceinline__ void load_const(const uint16_t *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float *f) const { attn::unpack8(v, f); }
+    __device__ __forceinline__ void get(uint64_t *f) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = attn::pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
 };
 template <>
 struct Raw<float> {
@@ -50,10 +54,18 @@ struct Raw<float> {
         a = __ldg(reinterpret_cast<const float4 *>(p));
         b = __ldg(reinterpret_cast<const float4 *>(p + 4));
     }
-    __device__ __forceinline__ void get(float *f) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void get(uint64_t *f) const {
+        f[0] = attn::pair(a.x, a.y);
+        f[1] = attn::pair(a.z, a.w);
+        f[2] = attn::pair(b.x, b.y);
+        f[3] = attn::pair(b.z, b.w);
     }
 };
+
+// The 16-byte place of cosines and sines of pairs 2 q and 2 q + 1: rotated within eight places by
+// q / 8, so that lanes eight (half layout: four places apart) or four pairs apart fall in
+// different banks.
+__device__ __forceinline__ int place_of(int q) { return (q & ~7) | ((q + (q >> 3)) & 7); }
 
 // A group of LG lanes (a power of two that covers head_dim / 16) holds one head, two pieces of
 // eight elements a lane: lane l < rot_dim / 16 pieces l and l + rot_dim / 16, the others the
@@ -61,7 +73,7 @@ struct Raw<float> {
 // its TB tokens.
 template <typename T, int LG, int TB>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs r) {
-    __shared__ __align__(16) float2 cs[TB][kMaxPairs];
+    __shared__ float4 cs[TB][kMaxPairs / 2];  // (cos, cos, sin, sin) of two pairs at place_of(pair / 2)
     __shared__ int seq[TB], where[TB];     // the tokens' sequences (-1: none) and places
     __shared__ int64_t slots[TB];          // element offset of a token's slot of head 0, -1 if it has none
     const attn::Args &a = r.a;
@@ -70,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const bool turned = l < half;
     const int da = (turned ? l : 2 * l) * 8, db = (turned ? l + half : 2 * l + 1) * 8;  // the lane's elements
     const bool on_a = da < D, on_b = db < D;
-    const int heads = a.n_heads + 2 * a.n_kv_heads, q_heads = a.n_heads, qk_heads = a.n_heads + a.n_kv_heads;
+    const int q_heads = a.n_heads;
     const int t0 = blockIdx.x * TB, tokens = min(TB, a.n_tokens - t0);
     constexpr int kGroups = kThreads / LG;
 
@@ -85,27 +97,49 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     griddep_wait();
     griddep_launch_dependents();
 
-    Raw<T> xa, xb, na, nb;
-    auto load = [&](int tk, int h) {
-        if (tk >= tokens) return;
-        const int64_t t = t0 + tk;
-        const T *src = h < q_heads    ? static_cast<const T *>(a.q) + t * a.q_stride + h * D
-                       : h < qk_heads ? static_cast<const T *>(r.k_in) + t * r.k_stride + (h - q_heads) * D
-                                      : static_cast<const T *>(r.v_in) + t * r.v_stride + (h - qk_heads) * D;
+    // Row i of the block: first the tokens' q heads, then their k and v heads.  A group takes rows
+    // group, group + kGroups, ..; its place among a token's heads moves on without a division.
+    Raw<T> na, nb;
+    struct At {
+        int tk, h;
+    };
+    const int group = tid / LG;
+    auto start = [&](int per_token) {
+        At at{0, group};
+        for (; at.h >= per_token; at.h -= per_token) ++at.tk;
+        return at;
+    };
+    auto next = [&](At at, int per_token) {
+        for (at.h += kGroups; at.h >= per_token; at.h -= per_token) ++at.tk;
+        return at;
+    };
+    const int kv_heads = 2 * a.n_kv_heads;
+    auto load = [&](const T *src) {
         if (on_a) na.load(src + da);
         if (on_b) nb.load(src + db);
     };
-    int tk = 0, h = tid / LG;
-    auto next = [&](int &k, int &g) {
-        for (g += kGroups; g >= heads; g -= heads) ++k;
+    const T *q_in = static_cast<const T *>(a.q) + (int64_t)t0 * a.q_stride;
+    const T *k_in = static_cast<const T *>(r.k_in) + (int64_t)t0 * r.k_stride;
+    const T *v_in = static_cast<const T *>(r.v_in) + (int64_t)t0 * r.v_stride;
+    const int q_row = int(a.q_stride), k_row = int(r.k_stride), v_row = int(r.v_stride), out_row = int(a.out_stride);
+    auto load_q = [&](At at) {
+        if (at.tk < tokens) load(q_in + (int64_t)at.tk * q_row + at.h * D);
     };
-    for (; h >= heads; h -= heads) ++tk;
-    load(tk, h);
+    auto load_kv = [&](At at) {
+        if (at.tk < tokens)
+            load(at.h < a.n_kv_heads ? k_in + (int64_t)at.tk * k_row + at.h * D
+                                     : v_in + (int64_t)at.tk * v_row + (at.h - a.n_kv_heads) * D);
+    };
+    At at_q = start(q_heads);
+    load_q(at_q);
 
     auto angles = [&](int i, int at, int k, int64_t pos) {
         float s, c;
         sincospif(__ll2float_rn(int64_t(turn[i] * uint64_t(pos))) * 0x1p-63f, &s, &c);  // half turns: 2 * frac / 2^64
-        cs[k][at - k * pairs] = make_float2(c * r.mscale, s * r.mscale);
+        const int p = at - k * pairs;
+        float *to = reinterpret_cast<float *>(&cs[k][place_of(p >> 1)]) + (p & 1);
+        to[0] = c * r.mscale;
+        to[2] = s * r.mscale;
     };
     int32_t given[kTurns];
     if (r.positions) {
@@ -163,84 +197,95 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     __syncthreads();
 
     const float inv_d = 1.f / float(D);
-    const bool norm = r.gq || r.gk;
-    // every group makes the same number of turns: all lanes take part in the shuffles
-    for (int left = (tokens * heads + kGroups - 1) / kGroups; left > 0; --left) {
-        xa = na;
-        xb = nb;
-        int tk2 = tk, h2 = h;
-        next(tk2, h2);
-        load(tk2, h2);
-        const bool on = tk < tokens && seq[tk < tokens ? tk : 0] >= 0;
-        const bool is_q = h < q_heads, is_v = h >= qk_heads;
-        float f[16] = {};
-        if (on && on_a) xa.get(f);
-        if (on && on_b) xb.get(f + 8);
-        if (norm) {
-            float s0 = 0.f, s1 = 0.f;
+    // One row: the norm (gamma not null), the rotation, the store.  All lanes take part.
+    auto row = [&](bool on, const T *gamma, bool rotate, const float4 *ct, T *dst) {
+        uint64_t f[8] = {};
+        if (on && on_a) na.get(f);
+        if (on && on_b) nb.get(f + 4);
+        return [=]() mutable {
+            if (r.gq || r.gk) {
+                uint64_t s2 = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s0 = fmaf(f[e], f[e], s0);
-                s1 = fmaf(f[8 + e], f[8 + e], s1);
-            }
-            float ss = s0 + s1;
+                for (int e = 0; e < 8; ++e) s2 = attn::fma2(f[e], f[e], s2);
+                float lo, hi;
+                attn::unpair(s2, lo, hi);
+                float ss = lo + hi;
 #pragma unroll
-            for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rs = rsqrtf(ss * inv_d + r.eps);
-            const T *gamma = static_cast<const T *>(is_q ? r.gq : is_v ? nullptr : r.gk);
-            if (gamma) {
-                float g[8];
-                Raw<T> w;
-                if (on_a) {
-                    w.load_const(gamma + da);
-                    w.get(g);
+                for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (gamma) {
+                    const float rs = rsqrtf(ss * inv_d + r.eps);
+                    const uint64_t rs2 = attn::pair(rs, rs);
+                    uint64_t g[4];
+                    Raw<T> w;
+                    if (on_a) {
+                        w.load_const(gamma + da);
+                        w.get(g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = f[e] * rs * g[e];
-                }
-                if (on_b) {
-                    w.load_const(gamma + db);
-                    w.get(g);
+                        for (int e = 0; e < 4; ++e) f[e] = attn::mul2(attn::mul2(f[e], rs2), g[e]);
+                    }
+                    if (on_b) {
+                        w.load_const(gamma + db);
+                        w.get(g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[8 + e] = f[8 + e] * rs * g[e];
+                        for (int e = 0; e < 4; ++e) f[4 + e] = attn::mul2(attn::mul2(f[4 + e], rs2), g[e]);
+                    }
                 }
             }
-        }
-        if (turned && !is_v) {
-            const float2 *ct = cs[tk < tokens ? tk : 0];
-            if (r.interleaved) {  // pairs da / 2 .. + 3 and db / 2 .. + 3
+            if (rotate) {
+                const uint64_t minus = attn::pair(-1.f, -1.f);
+                if (r.interleaved) {  // pairs da / 2 .. + 3 and db / 2 .. + 3
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 c = *reinterpret_cast<const float4 *>(ct + ((e < 8 ? da : db) + (e & 7)) / 2);
-                    const float u0 = f[e], w0 = f[e + 1], u1 = f[e + 2], w1 = f[e + 3];
-                    f[e] = u0 * c.x - w0 * c.y;
-                    f[e + 1] = w0 * c.x + u0 * c.y;
-                    f[e + 2] = u1 * c.z - w1 * c.w;
-                    f[e + 3] = w1 * c.z + u1 * c.w;
-                }
-            } else {  // element da + e pairs with db + e
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 c = ct[place_of(((e < 4 ? da : db) + 2 * (e & 3)) / 4)];
+                        float u0, w0, u1, w1;
+                        attn::unpair(f[e], u0, w0);
+                        attn::unpair(f[e + 1], u1, w1);
+                        f[e] = attn::pair(u0 * c.x - w0 * c.z, w0 * c.x + u0 * c.z);
+                        f[e + 1] = attn::pair(u1 * c.y - w1 * c.w, w1 * c.y + u1 * c.w);
+                    }
+                } else {  // element da + e pairs with db + e
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 c = *reinterpret_cast<const float4 *>(ct + da + e);
-                    const float u0 = f[e], w0 = f[8 + e], u1 = f[e + 1], w1 = f[9 + e];
-                    f[e] = u0 * c.x - w0 * c.y;
-                    f[8 + e] = w0 * c.x + u0 * c.y;
-                    f[e + 1] = u1 * c.z - w1 * c.w;
-                    f[9 + e] = w1 * c.z + u1 * c.w;
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 c = ct[place_of(da / 2 + e)];
+                        const uint64_t co = attn::pair(c.x, c.y), si = attn::pair(c.z, c.w), u = f[e], w = f[4 + e];
+                        f[e] = attn::fma2(w, attn::mul2(si, minus), attn::mul2(u, co));
+                        f[4 + e] = attn::fma2(u, si, attn::mul2(w, co));
+                    }
                 }
             }
-        }
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) attn::unpair(f[e], y[2 * e], y[2 * e + 1]);
+            if (dst && on_a) attn::store8(dst + da, y);
+            if (dst && on_b) attn::store8(dst + db, y + 8);
+        };
+    };
+    // every group makes the same number of turns: all lanes take part in the shuffles.  The next row
+    // is requested before a row is worked on.
+    At at_kv = start(kv_heads);
+    T *out = static_cast<T *>(a.out) + (int64_t)t0 * a.out_stride;
+    for (int left = (tokens * q_heads + kGroups - 1) / kGroups; left > 0; --left) {
+        const int tk = at_q.tk < tokens ? at_q.tk : 0;
+        const bool on = at_q.tk < tokens && seq[tk] >= 0;
+        auto work = row(on, static_cast<const T *>(r.gq), turned, cs[tk], on ? out + (int64_t)tk * out_row + at_q.h * D : nullptr);
+        at_q = next(at_q, q_heads);
+        if (left > 1)
+            load_q(at_q);
+        else
+            load_kv(at_kv);
+        work();
+    }
+    for (int left = (tokens * kv_heads + kGroups - 1) / kGroups; left > 0; --left) {
+        const int tk = at_kv.tk < tokens ? at_kv.tk : 0;
+        const bool on = at_kv.tk < tokens && seq[tk] >= 0, is_v = at_kv.h >= a.n_kv_heads;
         T *dst = nullptr;
-        if (on) {
-            if (is_q)
-                dst = static_cast<T *>(a.out) + (int64_t)(t0 + tk) * a.out_stride + h * D;
-            else if (slots[tk] >= 0)
-                dst = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k)) + slots[tk] +
-                      (int64_t)(is_v ? h - qk_heads : h - q_heads) * a.head_stride;
-        }
-        if (dst && on_a) attn::store8(dst + da, f);
-        if (dst && on_b) attn::store8(dst + db, f + 8);
-        tk = tk2;
-        h = h2;
+        if (on && slots[tk] >= 0)
+            dst = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k)) + slots[tk] +
+                  (int64_t)(is_v ? at_kv.h - a.n_kv_heads : at_kv.h) * a.head_stride;
+        auto work = row(on, static_cast<const T *>(is_v ? nullptr : r.gk), turned && !is_v, cs[tk], dst);
+        at_kv = next(at_kv, kv_heads);
+        if (left > 1) load_kv(at_kv);
+        work();
     }
 }
 

@@ -89,23 +89,42 @@ __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part
     for (int64_t kb = k_begin; kb < k_end; kb += kKeys) {
         __syncthreads();
         const int k0 = int(kb);
-        for (int i = tid; i < kKeys * (D / 8); i += kThreads) {
-            const int kk = i / (D / 8), c = i % (D / 8) * 8, p = k0 + kk;
-            float kv[8] = {}, vv[8] = {};
-            if (p < keys) {  // slots past the last visible key are not read: they may hold anything
-                const int pi = p / a.page_size;
-                const int64_t off = load_page(a, at.b, pi) * a.page_stride + hk * a.head_stride +
-                                    (int64_t)(p - pi * a.page_size) * a.token_stride + c;
-                ldp8(static_cast<const T *>(a.k) + off, kv);
-                ldp8(static_cast<const T *>(a.v) + off, vv);
+        // the cache offset of key lane, in every warp; slots past the last visible key are not read:
+        // they may hold anything
+        int64_t key_off = -1;
+        if (k0 + lane < keys) {
+            const int p = k0 + lane, pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
+            key_off = load_page(a, at.b, pi) * a.page_stride + hk * a.head_stride +
+                      (int64_t)(p - pi * a.page_size) * a.token_stride;
+        }
+        // pieces of eight elements, two rounds' loads in flight
+        constexpr int kRounds = (kKeys * NJ * 4 + kThreads - 1) / kThreads, kFly = kRounds < 2 ? kRounds : 2;
+        const int pieces = D / 8;
+#pragma unroll
+        for (int i0 = 0; i0 < kRounds; i0 += kFly) {
+            float kv[kFly][8], vv[kFly][8];
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
+                const int64_t off = __shfl_sync(0xffffffffu, key_off, kk & 31);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) kv[i][e] = vv[i][e] = 0.f;
+                if (kk < kKeys && off >= 0) {
+                    ldp8(static_cast<const T *>(a.k) + off + c, kv[i]);
+                    ldp8(static_cast<const T *>(a.v) + off + c, vv[i]);
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                K[kk * (D + 4) + c + e] = kv[e];
-                V[kk * D + c + e] = vv[e];
+            for (int i = 0; i < kFly; ++i) {
+                const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
+                if (kk >= kKeys) continue;
+                // K rows are D + 4 floats apart, V rows D: both multiples of 16 bytes
+                store8(K + kk * (D + 4) + c, kv[i]);
+                store8(V + kk * D + c, vv[i]);
             }
         }
         __syncthreads();
+        if (warp * 4 >= rows) continue;  // this warp only helps to load
         float sc[4] = {0.f, 0.f, 0.f, 0.f};
         for (int d = 0; d < D; d += 4) {
             const float4 k4 = *reinterpret_cast<const float4 *>(K + lane * (D + 4) + d);
@@ -194,20 +213,24 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part
     const float l = warp_sum(ml.y * f);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T *dst = static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D;
+    constexpr int kFly = 8;  // parts requested together; every part holds finite values (zeros for no keys)
     for (int d0 = 0; d0 < D; d0 += 128) {
-        const int d = d0 + lane * 4;
+        const int d = min(d0 + lane * 4, D - 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < part.parts; ++p) {
-            const float fp = __shfl_sync(0xffffffffu, f, p);
-            if (fp != 0.f && d < D) {
-                const float4 v = ldp16f(part.o + (p * rows + row) * D + d);
-                acc.x = fmaf(fp, v.x, acc.x);
-                acc.y = fmaf(fp, v.y, acc.y);
-                acc.z = fmaf(fp, v.z, acc.z);
-                acc.w = fmaf(fp, v.w, acc.w);
+        for (int p0 = 0; p0 < part.parts; p0 += kFly) {
+            float4 v[kFly];
+#pragma unroll
+            for (int p = 0; p < kFly; ++p) v[p] = ldp16f(part.o + (min(p0 + p, part.parts - 1) * rows + row) * D + d);
+#pragma unroll
+            for (int p = 0; p < kFly; ++p) {
+                const float fp = p0 + p < 32 ? __shfl_sync(0xffffffffu, f, (p0 + p) & 31) : 0.f;  // 0 past the last
+                acc.x = fmaf(fp, v[p].x, acc.x);
+                acc.y = fmaf(fp, v[p].y, acc.y);
+                acc.z = fmaf(fp, v[p].z, acc.z);
+                acc.w = fmaf(fp, v[p].w, acc.w);
             }
         }
-        if (d >= D) continue;
+        if (d0 + lane * 4 >= D) continue;
         from_f32(acc.x * inv, dst + d);
         from_f32(acc.y * inv, dst + d + 1);
         from_f32(acc.z * inv, dst + d + 2);

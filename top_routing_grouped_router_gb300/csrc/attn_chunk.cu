@@ -712,51 +712,70 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
 }
 
-// Joins the parts of the items that were cut.  Block (cta, rows): the item that starts in the
-// share of `cta` and goes on, rows [16 y, 16 y + 16) of its 256; one warp a row.
+// Joins the parts of the items that were cut.  Block (cta, y): the item that starts in the share of
+// `cta` and goes on, rows [16 y, 16 y + 16) of its 256; 16 threads a row.  Four parts are requested
+// together, their maxima and sums with their outputs (one warp a row, part by part, took 19 us
+// for a mixed batch's 150 cut items).
+constexpr int kJoinThreads = kJoinRows * 16;
 template <int D>
-__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ Ctx c) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ Ctx c) {
     griddep_wait();
     griddep_launch_dependents();
     const Args &a = c.a;
     const int *rp = reinterpret_cast<const int *>(c.rec + blockIdx.x);
-    const int n = ldp(rp);
+    const int n = ldp(rp), h = ldp(rp + 1), tok0 = ldp(rp + 2), q0 = ldp(rp + 3), q_len = ldp(rp + 4);
     if (n == 0) return;
-    const int h = ldp(rp + 1), tok0 = ldp(rp + 2), q0 = ldp(rp + 3), q_len = ldp(rp + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
-    const uint32_t cta = blockIdx.x;
-    auto slot_of = [&](int i) { return (size_t)(cta + i) * 2 + (i == 0 ? 1 : 0); };
-    for (int row = blockIdx.y * kJoinRows + warp; row < int(blockIdx.y + 1) * kJoinRows; row += 4) {
-        const int t = row / kM, r = row % kM, j = tok0 + t * int(c.tt) + r / G;
-        if (r >= G * int(c.tt) || j >= q_len) continue;
-        float m = kNegInf;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, ldp(&c.part_ml[slot_of(i) * 2 * kM + row].x));
+    const int G = a.group, row = blockIdx.y * kJoinRows + threadIdx.x / 16, t = row / kM, r = row % kM;
+    const int rt = r / G, j = tok0 + t * int(c.tt) + rt;
+    if (r >= G * int(c.tt) || j >= q_len) return;
+    constexpr int kFly = 4, E = D / 64;  // float4 pieces of a thread: 16 apart
+    const int d0 = threadIdx.x % 16 * 4;
+    float m = kNegInf, l = 0.f;
+    float4 acc[E];
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-        float l = 0.f;
-        constexpr int PER = D / 32;
-        float acc[PER] = {};
-        for (int i = 0; i < n; ++i) {
-            const size_t pr = slot_of(i) * 2 * kM + row;
-            const float pm = ldp(&c.part_ml[pr].x), pl = ldp(&c.part_ml[pr].y);
-            const float f = pm == kNegInf ? 0.f : ex2(pm - m);
-            l = fmaf(f, pl, l);
-            float v[PER];
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < n; p0 += kFly) {
+        float pm[kFly], pl[kFly];
+        float4 v[kFly][E];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) v[e] = ldp(c.part_o + pr * D + e * 32 + lane);
-            if (f != 0.f) {
+        for (int p = 0; p < kFly; ++p) {
+            const int i = min(p0 + p, n - 1);
+            const size_t pr = ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * 2 * kM + row;
+            asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(pm[p]), "=f"(pl[p]) : "l"(c.part_ml + pr));
 #pragma unroll
-                for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+            for (int e = 0; e < E; ++e) v[p][e] = ldp16f(c.part_o + pr * D + e * 64 + d0);
+        }
+        float mn = m;
+#pragma unroll
+        for (int p = 0; p < kFly; ++p) mn = fmaxf(mn, pm[p]);
+        const float f0 = m == kNegInf ? 0.f : ex2(m - mn);
+        m = mn;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * f0, acc[e].y * f0, acc[e].z * f0, acc[e].w * f0);
+#pragma unroll
+        for (int p = 0; p < kFly; ++p) {
+            if (p0 + p >= n || pm[p] == kNegInf) continue;
+            const float f = ex2(pm[p] - mn);
+            l = fmaf(f, pl[p], l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                acc[e].x = fmaf(f, v[p][e].x, acc[e].x);
+                acc[e].y = fmaf(f, v[p][e].y, acc[e].y);
+                acc[e].z = fmaf(f, v[p][e].z, acc[e].z);
+                acc[e].w = fmaf(f, v[p][e].w, acc[e].w);
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t tok = q0 + j;
-        const int head = h * G + r % G;
-        uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) dst[e * 32 + lane] = f32_to_bf16_bits(acc[e] * inv);
-        if (a.lse && lane == 0) a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = q0 + j;
+    const int head = h * G + (r - rt * G);
+    uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D + d0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        *reinterpret_cast<uint2 *>(dst + e * 64) =
+            make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+    if (a.lse && d0 == 0) a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 
 int64_t max_items(const moe_attn_shape &s) {
@@ -792,7 +811,7 @@ cudaError_t launch_typed(const Ctx &c, const CUtensorMap &mq, const CUtensorMap 
     if (!set_smem_attr<D>()) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(chunk_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, mv, c);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * kM / kJoinRows), dim3(128), 0, st, c);
+    return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * kM / kJoinRows), dim3(kJoinThreads), 0, st, c);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
 // share's end leave fp32 partial results that a second kernel joins.
 #include "attn.cuh"
-#include "tc_common.cuh"
+#include "tma_nd.cuh"
 
 namespace moe {
 namespace attn {

@@ -1,7 +1,7 @@
 // tc_common.cu -- host side of the tensor-core kernels: the driver's tensor-map encoder
 // (looked up once through the runtime, so the library does not link libcuda) and the SM
 // count per device.
-#include "tc_common.cuh"
+#include "tma_nd.cuh"
 
 #include <atomic>
 #include <mutex>

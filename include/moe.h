@@ -463,8 +463,8 @@ MOE_API int moe_graphs_destroy(moe_graphs *graphs);
  * among those a sequence uses, a chunk longer than max_q, a kv_len outside
  * [0, max_pages * page_size] or a cu_q that falls or leaves [0, n_tokens]
  * records MOE_ERR_DEVICE in the workspace's error word (moe_read_device_error).
- * Nothing outside the arrays is touched then; that sequence's results are
- * unspecified.
+ * Nothing outside the arrays is touched then; that sequence's results (with a
+ * wrong cu_q, the whole call's) are unspecified.
  */
 typedef struct {
     int32_t n_tokens, n_seqs;
@@ -546,7 +546,8 @@ typedef struct {
  * Computed in fp32, rounded once.
  *   q [n_tokens][n_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim]:
  *     token rows q_stride / k_stride / v_stride elements apart (multiples of 16
- *     bytes: slices of one projection's output), heads contiguous in a row
+ *     bytes below 2^31 elements: slices of one projection's output), heads
+ *     contiguous in a row
  *   positions [n_tokens] int32 or NULL: the position of each token's rotation
  *     (NULL: its place in the sequence)
  *   q_out [n_tokens][n_heads][head_dim], rows q_out_stride apart; may be q itself
@@ -570,7 +571,7 @@ MOE_API int moe_rope_append(const moe_attn_shape *shape, const moe_rope *rope, c
  * for the product with v.  Results do not depend on timing (bitwise
  * deterministic).
  *   q, out [n_tokens][n_heads][head_dim], token rows q_stride / out_stride
- *     elements apart (multiples of 16 bytes)
+ *     elements apart (multiples of 16 bytes below 2^31 elements)
  *   lse [n_tokens][n_heads] fp32 or NULL: natural log of the sum of
  *     exp(scale * q . k_p)
  *   scale: finite, else MOE_ERR_SHAPE

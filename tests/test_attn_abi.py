@@ -81,7 +81,7 @@ def _attn(L, **kw):
     (dict(q=None), NULLPTR), (dict(out=None), NULLPTR), (dict(k=None), NULLPTR), (dict(v=None), NULLPTR),
     (dict(cu=None), NULLPTR), (dict(kv=None), NULLPTR), (dict(tb=None), NULLPTR), (dict(scale=math.nan), SHAPE),
     (dict(scale=math.inf), SHAPE), (dict(qs=504), SHAPE), (dict(os=8), SHAPE), (dict(ts=56), SHAPE),
-    (dict(hs=32), SHAPE), (dict(ps=-2048), SHAPE), (dict(qs=516), ALIGN), (dict(os=513), ALIGN), (dict(ps=2052), ALIGN),
+    (dict(hs=32), SHAPE), (dict(ps=-2048), SHAPE), (dict(qs=1 << 31), SHAPE), (dict(os=1 << 40), SHAPE), (dict(qs=516), ALIGN), (dict(os=513), ALIGN), (dict(ps=2052), ALIGN),
     (dict(ts=68), ALIGN), (dict(q=FAKE + 8), ALIGN), (dict(out=FAKE + 2), ALIGN), (dict(k=FAKE + 4), ALIGN),
     (dict(v=FAKE + 8), ALIGN), (dict(cu=FAKE + 2), ALIGN), (dict(lse=FAKE + 1), ALIGN), (dict(ws=None), WORKSPACE),
     (dict(need=2047), WORKSPACE), (dict(ws=FAKE + 64), ALIGN)])

@@ -178,6 +178,28 @@ def test_attention_bad_data_is_recorded(name):
         assert moe.moe_read_device_error(d.ws) == 0  # read and cleared
 
 
+@pytest.mark.parametrize("name", ["decode ragged", "chunk over cache", "chunk ragged", "odd pages"])
+@pytest.mark.parametrize("what", ["falls", "leaves", "negative"])
+def test_attention_bad_rows_are_recorded(name, what):
+    # a cu_q that falls or leaves the rows: recorded, nothing outside the arrays is touched, and the
+    # next call with the right one is right
+    bt = make_batch(*ATTN[name], seed=12)
+    d = Dev(bt, pad_rows=2)
+    good = d.cu_q.clone()
+    if what == "falls":
+        d.cu_q[-1] = -5 if len(bt.q_len) == 1 else int(good[-2]) - 1
+    elif what == "leaves":
+        d.cu_q[-1] = bt.tokens + 1000
+    else:
+        d.cu_q[0] = -1000
+    assert d.attend(0.1) == -7
+    d.cu_q.copy_(good)
+    d.out.fill_(7.0)
+    assert d.attend(0.1) == 0
+    out, _, tol, _ = attention(bt, 0.1)
+    assert ((d.out[:bt.tokens].cpu().double() - out).abs() <= tol).all() and (d.out[bt.tokens:] == 7).all()
+
+
 def test_attention_graph_and_streams():
     # replays of a captured graph see new lengths and new data; two streams with their own
     # workspaces do not disturb each other
@@ -326,6 +348,18 @@ def test_rope_append(name):
 @pytest.mark.parametrize("in_place,layout", [(True, "slots"), (False, "joint")])
 def test_rope_append_in_place_and_layouts(name, in_place, layout):
     _rope_case(name, in_place, layout)
+
+
+@pytest.mark.parametrize("cu", [[0, 9, 4], [0, 3, 5000], [-7, 3, 6]])
+def test_rope_append_bad_rows_are_recorded(cu):
+    bt = make_batch("bf16", 4, 2, 64, 16, [3, 3], [3, 20], seed=1, fill=5.0)
+    d = Dev(bt)
+    d.cu_q.copy_(torch.tensor(cu, dtype=torch.int32))
+    x = torch.randn(bt.tokens, 4, 64, device="cuda").bfloat16()
+    moe.moe_rope_append(d.shape, moe.make_rope(64), x, x[:, :2].contiguous(), x[:, 2:].contiguous(), d.cache, d.batch,
+                        d.out, workspace=d.ws)
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_error(d.ws) == -7
 
 
 def test_rope_append_bad_page_is_recorded_and_skipped():

@@ -27,6 +27,7 @@ struct Seq {
     int q0;      // first row of the chunk
     int q_len;   // rows
     int kv_len;  // keys, the chunk's own included
+    bool rows_ok;  // cu_q rises within [0, n_tokens] here
 };
 
 // Sequence b, forced into the arrays' bounds; a value that had to be forced is recorded.
@@ -37,7 +38,8 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int b) {
     s.q0 = min(max(c0, 0), a.n_tokens);
     s.q_len = max(min(max(c1, 0), a.n_tokens) - s.q0, 0);
     s.kv_len = int(min((int64_t)max(kv, 0), (int64_t)a.max_pages * a.page_size));
-    if (c0 != s.q0 || c1 != s.q0 + s.q_len || kv != s.kv_len || s.q_len > a.max_q) record_error(a.err, MOE_ERR_DEVICE);
+    s.rows_ok = c0 == s.q0 && c1 == s.q0 + s.q_len;
+    if (!s.rows_ok || kv != s.kv_len || s.q_len > a.max_q) record_error(a.err, MOE_ERR_DEVICE);
     return s;
 }
 

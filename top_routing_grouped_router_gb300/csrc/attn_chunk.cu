@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     };
     auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, tt2), tt2); };
     uint32_t total = 0, n0 = 0, before0 = 0;
+    bool rows_ok = true;
     Seq s0{};
     for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
         uint32_t n = 0, sum;
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (b0 + tid < a.n_seqs) {
             s = load_seq(a, b0 + tid);
             n = seq_places(s) * Hkv;
+            rows_ok = rows_ok && s.rows_ok;
         }
         const uint32_t before = scan_block(n, &sum);
         if (b0 == 0) {
@@ -309,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         total += sum;
     }
+    // chunks that overlap could make a line longer than 32 bits count: such a call does nothing (the
+    // error is recorded)
+    if (__syncthreads_or(!rows_ok)) total = 0;
     const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, total / (kSetup + 2)));
     const Shares sh{total / ctas, total % ctas};
     const uint32_t u_begin = cta < ctas ? sh.begin(cta) : 0, u_end = cta < ctas ? sh.begin(cta + 1) : 0;
@@ -361,8 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (!located) {
                     while (w - first >= per_head * Hkv) {  // the next sequence with a chunk
                         first += per_head * Hkv;
-                        s = load_seq(a, ++b);
+                        if (++b >= a.n_seqs) break;  // not seen: the line ends with the last sequence
+                        s = load_seq(a, b);
                         per_head = seq_places(s);
+                    }
+                    if (b >= a.n_seqs) {
+                        w = u_end;
+                        break;
                     }
                     h = (w - first) / per_head;
                     const uint32_t rem = w - first - h * per_head;

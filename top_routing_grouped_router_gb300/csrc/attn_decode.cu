@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         } else {
             while (u - base >= steps * Hkv) {  // the next sequence with a chunk
                 base += steps * Hkv;
-                s = load_seq(a, ++b);
+                if (++b >= a.n_seqs) return;  // not seen: the line ends with the last sequence
+                s = load_seq(a, b);
                 steps = steps_of(s);
             }
             h = (u - base) / steps;
@@ -565,8 +566,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 
 template <int D>
 cudaError_t launch_typed(const Args &a, char *hdr, char *ws, int grid, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-    if (e != cudaSuccess) return e;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
     float *o = reinterpret_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(o + (size_t)kMaxGrid * 2 * kRows * D);
     const Parts p{reinterpret_cast<uint32_t *>(hdr + kCounters), o, ml};

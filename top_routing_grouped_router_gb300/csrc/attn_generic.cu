@@ -241,9 +241,15 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part
 
 template <typename T, int NJ>
 cudaError_t launch_typed(const Args &a, const Partials &p, dim3 grid, int tt, cudaStream_t st) {
-    static const cudaError_t set = cudaFuncSetAttribute(generic_kernel<T, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                        smem_bytes(32 * NJ));
-    if (set != cudaSuccess) return set;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(generic_kernel<T, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   smem_bytes(32 * NJ));
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
     return launch_pdl(generic_kernel<T, NJ>, grid, dim3(kThreads), smem_bytes(a.head_dim), st, a, p, tt);
 }
 

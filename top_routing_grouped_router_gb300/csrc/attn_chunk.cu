@@ -101,9 +101,12 @@ __device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, uint3
 // starting and ending an item costs, about two steps' time (a mixed batch of short and long
 // items: 85 us with none, the slowest CTA 1.45 times the mean).
 constexpr uint32_t kSetup = 2;
-__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, uint32_t tt2) {
-    return steps_before(s, i, tt2) + i * kSetup;
+__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, uint32_t tt2, bool whole) {
+    return whole ? i : steps_before(s, i, tt2) + i * kSetup;
 }
+// Where no sequence can hold more keys than this, items are not cut (each takes one place on the
+// line), and the join is not launched.
+constexpr int kWholeKeys = 512;
 
 struct Shares {
     uint32_t each, more;
@@ -214,6 +217,7 @@ struct Ctx {
     Rec *rec;           // [kMaxCtas]
     unsigned long long wait_ns;
     int extra_need;
+    bool whole;         // items are not cut
 };
 
 template <int D>
@@ -243,6 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const Waits wt{a.err, abort, c.wait_ns, smem_u32(const_cast<int *>(abort))};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t tt = c.tt, tt2 = 2 * tt, G = a.group, Hkv = a.n_kv_heads;
+    if (tid == kLoadWarp * 32) {
+        for (const CUtensorMap *p : {&map_q, &map_k, &map_v})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(p)) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&kv_full[i]), 1);
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *sum = total;
         return before + incl - n;
     };
-    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, tt2), tt2); };
+    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, tt2), tt2, c.whole); };
     uint32_t total = 0, n0 = 0, before0 = 0;
     bool rows_ok = true;
     Seq s0{};
@@ -314,10 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // chunks that overlap could make a line longer than 32 bits count: such a call does nothing (the
     // error is recorded)
     if (__syncthreads_or(!rows_ok)) total = 0;
-    const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, total / (kSetup + 2)));
+    const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, c.whole ? total : total / (kSetup + 2)));
     const Shares sh{total / ctas, total % ctas};
     const uint32_t u_begin = cta < ctas ? sh.begin(cta) : 0, u_end = cta < ctas ? sh.begin(cta + 1) : 0;
-    if (tid == 0) c.rec[cta].n = 0;
+    if (tid == 0 && !c.whole) c.rec[cta].n = 0;
     if (u_begin < u_end) {
         auto found = [&](int b, uint32_t before, uint32_t n, const Seq &s) {
             if (u_begin >= before && u_begin - before < n) {
@@ -381,20 +389,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     while (n > 1) {
                         const uint32_t each = (n + 31) / 32;
                         const uint32_t cand = lo + lane * each;
-                        const bool at = lane * each < n && places_before(s, cand, tt2) <= rem;
+                        const bool at = lane * each < n && places_before(s, cand, tt2, c.whole) <= rem;
                         const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, at));
                         lo += last * each;
                         n = min(each, n - last * each);
                     }
                     i = lo;
-                    item0 = first + h * per_head + places_before(s, i, tt2);
+                    item0 = first + h * per_head + places_before(s, i, tt2, c.whole);
                     located = true;
                 }
-                const uint32_t places = item_steps(s, i, tt2) + kSetup;
-                const uint32_t end = min(item0 + places, u_end);
+                const uint32_t steps = item_steps(s, i, tt2), setup = c.whole ? 0 : kSetup;
+                const uint32_t places = c.whole ? 1 : steps + kSetup, end = min(item0 + places, u_end);
                 // steps begin after the item's setup; a share that ends within it leaves the item to the next
-                const uint32_t from = max(w, item0 + kSetup);
-                const bool starts = from == item0 + kSetup, whole = starts && end == item0 + places;
+                const uint32_t from = max(w, item0 + setup);
+                const bool starts = from == item0 + setup, whole = starts && end == item0 + places;
                 if (from < end) {
                     if (lane == 0) {
                         Seg g;
@@ -404,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         g.q0 = s.q0;
                         g.q_len = s.q_len;
                         g.kv_len = s.kv_len;
-                        g.step0 = int(from - item0 - kSetup);
-                        g.step1 = int(end - item0 - kSetup);
+                        g.step0 = int(from - item0 - setup);
+                        g.step1 = c.whole ? int(steps) : int(end - item0 - setup);
                         g.slot = whole ? -1 : int(cta * 2 + (starts ? 1 : 0));
                         g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
                         segs[k] = g;
@@ -796,8 +804,9 @@ int64_t max_items(const moe_attn_shape &s) {
 double max_places(const moe_attn_shape &s) {
     return double(max_items(s)) * ((double)s.max_pages * s.page_size / kKeys + 1 + kSetup);
 }
+bool not_cut(const moe_attn_shape &s) { return (int64_t)s.max_pages * s.page_size <= kWholeKeys; }
 int max_ctas(const moe_attn_shape &s) {
-    const double n = max_places(s) / (kSetup + 2);
+    const double n = not_cut(s) ? double(max_items(s)) : max_places(s) / (kSetup + 2);
     return n < 1 ? 1 : n < kMaxCtas ? int(n) : kMaxCtas;
 }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -820,7 +829,7 @@ cudaError_t launch_typed(const Ctx &c, const CUtensorMap &mq, const CUtensorMap 
                          cudaStream_t st) {
     if (!set_smem_attr<D>()) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(chunk_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, mv, c);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || c.whole) return e;
     return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * kM / kJoinRows), dim3(kJoinThreads), 0, st, c);
 }
 
@@ -850,6 +859,7 @@ cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int s
     c.part_o = reinterpret_cast<float *>(reinterpret_cast<char *>(c.part_ml) + round256((size_t)2 * cap * 2 * kM * sizeof(float2)));
     c.wait_ns = wait_limit_ns();
     c.extra_need = debug_extra_need();
+    c.whole = not_cut(s);
     const uint64_t D = s.head_dim;
     CUtensorMap mq, mk, mv;
     const uint64_t qd[3] = {D, (uint64_t)s.n_heads, (uint64_t)s.n_tokens}, qs[2] = {D * 2, (uint64_t)a.q_stride * 2};

@@ -110,7 +110,7 @@ constexpr int kMmaRows = 16;     // rows of x of a pass
 
 struct MmaArgs {
     Q4Args a;
-    int T0, rows;       // rows of x of this launch
+    int pass_rows;      // rows of x of a pass: grid.y passes read the weights side by side
     int slices;         // cluster size
     int side;           // output strips side by side in a CTA: its warps are side x (warps / side input parts)
     int tiles;          // tiles of side strips
@@ -176,6 +176,8 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     unsigned char *starts = xs + (size_t)m.slice_halves * NT * 1024;  // [block][NT][4] x 16 bytes (affine)
     float *part = reinterpret_cast<float *>(xs + (size_t)m.slice_halves * V::kHalf);  // [2][kCols][wide], slices > 1
     const uint32_t ring = smem_addr(ring_base) + warp * kDepth * kStage;
+
+    const int T0 = blockIdx.y * m.pass_rows, rows = min(a.T - T0, m.pass_rows);
 
     // this CTA's stages of the inputs, and this warp's
     const int stages = (a.K + kIn - 1) / kIn;
@@ -284,7 +286,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         float *z = reinterpret_cast<float *>(starts + ((size_t)block * NT + row / 8) * 64 + (row >> 1 & 3) * 16);
         z[row & 1] = z[2 + (row & 1)] = v;
     };
-    for (int row = m.rows + warp; row < kCols; row += kWarps)
+    for (int row = rows + warp; row < kCols; row += kWarps)
         for (int c = lane; c < n8; c += 32) {
             put(c, row, make_uint4(0, 0, 0, 0));
             if (kAffine && c % kPer == 0) put_start(c / kPer, row, 0.f);
@@ -294,10 +296,10 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     // the warps take the rows in turn, or where those are few, pieces of one: n8 is a multiple of 16,
     // so the lanes of a block stay together
     constexpr int kBatch = 4;  // loads in flight a thread
-    const int beside_rows = m.rows < kWarps ? kWarps / m.rows : 1;  // warps on a row
+    const int beside_rows = rows < kWarps ? kWarps / rows : 1;  // warps on a row
     const int row_step = kWarps / beside_rows, c_step = beside_rows * 32;
-    for (int row = warp / beside_rows; row < m.rows && warp < row_step * beside_rows; row += row_step) {
-        const uint16_t *xr = a.x + (m.T0 + row) * a.x_stride + (int64_t)s0 * kIn;
+    for (int row = warp / beside_rows; row < rows && warp < row_step * beside_rows; row += row_step) {
+        const uint16_t *xr = a.x + (int64_t)(T0 + row) * a.x_stride + (int64_t)s0 * kIn;
         const int most = a.K - 8 - s0 * kIn;  // the last whole piece of the row
         for (int c0 = (warp % beside_rows) * 32 + lane; c0 < n8; c0 += kBatch * c_step) {
             uint4 v[kBatch];
@@ -457,13 +459,13 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         float *pb = part + (k & 1) * kCols * wide;
         auto emit = [&](int row, int n, float y) {
             n += n0;
-            if (row < m.rows && n < N) q4_emit(a, m.T0 + row, n, y * m.step);
+            if (row < rows && n < N) q4_emit(a, T0 + row, n, y * m.step);
         };
         // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part.
         // Threads are a multiple of the tile's outputs: a thread keeps its output, rows go by.
         {
             const uint32_t n = tid & (wide - 1), rows_step = kThreads >> wide_log2;
-            const int cols = m.slices == 1 ? m.rows : kCols;
+            const int cols = m.slices == 1 ? rows : kCols;
             const float *rr = red + (n / kOut * kCols) * kRedStride + n % kOut;
             const int part_step = m.side * kCols * kRedStride;
             for (int row = tid >> wide_log2; row < cols; row += rows_step) {
@@ -508,7 +510,8 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     int slices = 1;
     if (stages > V::max_stages()) slices = 2;
     while (slices > 1 && (stages + slices - 1) / slices > V::max_stages_sliced()) slices *= 2;
-    while (slices < kMaxSlices && strips * slices * 2 <= sms * 2 && stages >= slices * 2 * V::kWarps) slices *= 2;
+    const int passes = (m.a.T + m.pass_rows - 1) / m.pass_rows;
+    while (slices < kMaxSlices && (int64_t)strips * passes * slices * 2 <= sms * 2 && stages >= slices * 2 * V::kWarps) slices *= 2;
     // strips side by side: when there are plenty, each warp takes a longer part of the inputs, and
     // the sums over the parts cost less
     m.slices = slices;
@@ -518,7 +521,7 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     m.slice_halves = 2 * ((stages + slices - 1) / slices);
     const int smem = V::kFixed + m.slice_halves * V::kHalf + (slices > 1 ? V::part_bytes(m.side) : 0);
     const int per_sm = std::min(MT == 2 ? 1 : 3, std::max(1, (kMaxSmem + 1024) / (smem + 1024)));
-    const int groups = std::max(1, std::min(m.tiles, sms * per_sm / slices));
+    const int groups = std::max(1, std::min(m.tiles, sms * per_sm / slices / std::min(passes, 4)));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -526,7 +529,7 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.x = unsigned(slices);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(groups * slices));
+    cfg.gridDim = dim3(unsigned(groups * slices), unsigned(passes));
     cfg.blockDim = dim3(V::kThreads);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
@@ -551,12 +554,12 @@ struct Rows {  // the variants by rows of x
         return two ? launch_mma<NT, 2, kFine, kAffine>(m, stages, sms, st) : launch_mma<NT, 1, kFine, kAffine>(m, stages, sms, st);
     }
     static cudaError_t launch(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
-        return m.rows <= 8 ? launch_nt<1>(m, stages, sms, st) : launch_nt<2>(m, stages, sms, st);
+        return m.pass_rows <= 8 ? launch_nt<1>(m, stages, sms, st) : launch_nt<2>(m, stages, sms, st);
     }
 };
 
-// The rows in passes of 16 (8 when x would not fit even split over a cluster); false if not even
-// 8 rows fit.
+// The rows in passes of 16 (8 when x would not fit even split over a cluster), all in one launch;
+// false if not even 8 rows fit.
 bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     float step = 1.f;
     int twice = 0;
@@ -583,13 +586,9 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     m.step = affine ? step : 1.f;
     while (!fine && (64 << m.shift) < a.q_block) ++m.shift;
     m.centre = 16.f + 0.5f * float(twice);
-    *err = cudaSuccess;
-    for (int t0 = 0; t0 < a.T && *err == cudaSuccess; t0 += nt_max * 8) {
-        m.T0 = t0;
-        m.rows = std::min(a.T - t0, nt_max * 8);
-        *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
-                      : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));
-    }
+    m.pass_rows = a.T <= 8 ? 8 : nt_max * 8;
+    *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
+                  : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));
     return true;
 }
 

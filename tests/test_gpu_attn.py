@@ -393,6 +393,7 @@ SHIFTED = [0.25 * (j - 3) for j in range(16)]
 @pytest.mark.parametrize("T,K,N,q_block", [
     (1, 64, 1, 64), (1, 2048, 640, 64), (8, 512, 129, 64), (3, 96, 17, 32), (7, 4064, 515, 32), (16, 1024, 256, 128),
     (17, 768, 100, 64), (33, 640, 65, 128), (64, 2048, 200, 64), (65, 256, 48, 32), (130, 512, 33, 64), (2, 8, 5, 2),
+    (20, 2112, 4100, 64), (70, 4224, 2050, 128), (33, 512, 140000, 64), (9, 8192, 1030, 64), (64, 8192, 1100, 256),
     (20, 192, 40000, 64), (3, 320, 20001, 64), (40, 96, 19999, 32), (11, 4160, 130, 64), (16, 8192, 300, 512),
     (5, 240, 31, 48), (9, 176, 40, 16), (4, 8192, 24, 256), (1, 5632, 2047, 128), (12, 32, 64, 32)])
 def test_q4_linear(T, K, N, q_block, out, book):
@@ -427,11 +428,11 @@ def test_q4_linear_wait_that_runs_out():
     # the tensor-core kernel's operands can never be complete: the wait ends after its limit with an
     # error recorded, and the next ordinary call is right
     g = torch.Generator().manual_seed(2)
-    codes = torch.randint(0, 256, (300, 256), generator=g).to(torch.uint8)
-    scales = (torch.rand(300, 8, generator=g) + 0.25).bfloat16()
-    x = torch.randn(20, 512, generator=g).bfloat16()
-    shape, weight = moe.make_q4_linear_shape(20, 512, 300, "f32"), moe.make_q4_weight(codes.cuda(), scales.cuda(), UNIFORM)
-    out = torch.empty(20, 300, device="cuda")
+    codes = torch.randint(0, 256, (4100, 1024), generator=g).to(torch.uint8)
+    scales = (torch.rand(4100, 32, generator=g) + 0.25).bfloat16()
+    x = torch.randn(20, 2048, generator=g).bfloat16()
+    shape, weight = moe.make_q4_linear_shape(20, 2048, 4100, "f32"), moe.make_q4_weight(codes.cuda(), scales.cuda(), UNIFORM)
+    out = torch.empty(20, 4100, device="cuda")
     moe.moe_debug_set_waits(1_000_000, 1)
     try:
         moe.moe_q4_linear(shape, x.cuda(), weight, out)
@@ -441,7 +442,7 @@ def test_q4_linear_wait_that_runs_out():
     moe.moe_q4_linear(shape, x.cuda(), weight, out)
     assert moe.moe_q4_linear_read_error() == 0
     want = x.double() @ q4_dense(codes, scales, UNIFORM, 64).T
-    assert (out.cpu().double() - want).abs().max() <= 1e-3
+    assert (out.cpu().double() - want).abs().max() <= 2e-3
 
 
 def test_q4_linear_residual_in_place():

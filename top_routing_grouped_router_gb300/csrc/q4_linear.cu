@@ -568,12 +568,15 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
-    // tcgen05 from the second pass of 16 rows on.  For 9 to 16 rows also where the weights are large
-    // enough that its longer start does not count, but not so many that mma.sync takes two strips a
-    // warp (16 x 4096 x 5120: 13.8 us against 18.9; 12 x 2048 x 2048: 13.7, 7.6; 16 x 2048 x 131072:
-    // 58.6, 54.1)
-    const bool large = (int64_t)a.N * a.K >= (1 << 24) && a.N < two_strips_from(sms);
-    if (affine && !fine && (a.T > kMmaRows || (a.T > 8 && large)) && run_tc(a, step, twice, sms, st, err)) return true;
+    // tcgen05 for more than 8 rows where the weights are large enough that its longer start does not
+    // count (us, tcgen05 and mma.sync): 12 x 2048 x 2048 7.7, 7.7; 64 x 2048 x 2048 14.6, 11.6; 40 x 512 x
+    // 20000 18.0, 15.1; 16 x 4096 x 5120 13.9, 18.7; 32 x 4096 x 5120 17.3, 25.0; 64 x 4096 x 10240 54, 69.  Up to
+    // 16 rows not where mma.sync takes two strips a warp: 16 x 2048 x 131072 57, 54.
+    const int64_t weights = (int64_t)a.N * a.K;
+    const bool large = (a.K >= 2048 && weights >= (1 << 23)) || weights >= (1 << 26);
+    if (affine && !fine && large && a.T > 8 && (a.T > kMmaRows || a.N < two_strips_from(sms)) &&
+        run_tc(a, step, twice, sms, st, err))
+        return true;
     auto fits = [&](int nt) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));

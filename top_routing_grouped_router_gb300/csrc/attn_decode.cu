@@ -226,10 +226,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t G = a.group, Hkv = a.n_kv_heads;
 
-    // the line of all steps, and how it is cut
+    // the line of all steps, and how it is cut.  Up to 32 sequences every warp scans by itself, without
+    // barriers.
+    const bool few = a.n_seqs <= 32;
     uint32_t n0 = 0, before0 = 0, total = 0, pairs = 0;
     Seq s{};
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+    auto warp_scan = [&](uint32_t n, uint32_t *sum) {
+        uint32_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        *sum = __shfl_sync(0xffffffffu, incl, 31);
+        return incl - n;
+    };
+    if (few) {
+        if (lane < a.n_seqs) {
+            s = load_seq(a, lane);
+            n0 = steps_of(s);
+        }
+        pairs = __popc(__ballot_sync(0xffffffffu, n0 > 0)) * Hkv;
+        before0 = warp_scan(n0 * Hkv, &total);
+    }
+    for (int b0 = 0; !few && b0 < a.n_seqs; b0 += kThreads) {
         uint32_t n = 0, sum;
         if (b0 + tid < a.n_seqs) {
             const Seq x = load_seq(a, b0 + tid);
@@ -262,39 +282,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     // places of a sequence: its parts (aligned), or its steps, of all heads
     auto places_of = [&](uint32_t n) { return (aligned ? (n + part - 1) / part : n) * Hkv; };
     const uint32_t at = aligned ? cta : u;
-    if (tid == 0) first[0] = ~0u;
-    auto found = [&](uint32_t b, uint32_t before, uint32_t n, const Seq &x) {
-        if (at >= before && at - before < n) {
-            first[0] = b;
-            first[1] = before;
-            first_seq = x;
-        }
-    };
+    int b;
     uint32_t base = 0;
-    if (a.n_seqs <= kThreads) {
+    if (few) {
         uint32_t sum;
-        const uint32_t n = places_of(n0), before = aligned ? block_scan(n, &sum, scratch) : before0;
-        __syncthreads();
-        found(tid, before, n, s);
+        const uint32_t n = places_of(n0), before = aligned ? warp_scan(n, &sum) : before0;
+        const uint32_t here = __ballot_sync(0xffffffffu, at >= before && at - before < n);
+        if (here == 0) return;  // past the last part: every warp of the block
+        b = __ffs(here) - 1;
+        base = __shfl_sync(0xffffffffu, before, b);
+        s.q0 = __shfl_sync(0xffffffffu, s.q0, b);
+        s.q_len = __shfl_sync(0xffffffffu, s.q_len, b);
+        s.kv_len = __shfl_sync(0xffffffffu, s.kv_len, b);
     } else {
-        for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-            uint32_t n = 0, sum;
-            Seq x{};
-            if (b0 + tid < a.n_seqs) {
-                x = load_seq(a, b0 + tid);
-                n = places_of(steps_of(x));
+        if (tid == 0) first[0] = ~0u;
+        auto found = [&](uint32_t i, uint32_t before, uint32_t n, const Seq &x) {
+            if (at >= before && at - before < n) {
+                first[0] = i;
+                first[1] = before;
+                first_seq = x;
             }
-            const uint32_t before = base + block_scan(n, &sum, scratch);
-            found(b0 + tid, before, n, x);
-            base += sum;
-            if (at < base) break;
+        };
+        if (a.n_seqs <= kThreads) {
+            uint32_t sum;
+            const uint32_t n = places_of(n0), before = aligned ? block_scan(n, &sum, scratch) : before0;
+            __syncthreads();
+            found(tid, before, n, s);
+        } else {
+            for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+                uint32_t n = 0, sum;
+                Seq x{};
+                if (b0 + tid < a.n_seqs) {
+                    x = load_seq(a, b0 + tid);
+                    n = places_of(steps_of(x));
+                }
+                const uint32_t before = base + block_scan(n, &sum, scratch);
+                found(b0 + tid, before, n, x);
+                base += sum;
+                if (at < base) break;
+            }
         }
+        __syncthreads();
+        if (first[0] == ~0u) return;  // past the last part
+        b = int(first[0]);
+        base = first[1];
+        s = first_seq;
     }
-    __syncthreads();
-    if (first[0] == ~0u) return;  // past the last part
-    int b = int(first[0]);
-    base = first[1];
-    s = first_seq;
     uint32_t steps = steps_of(s);
 
     const uint32_t ring = smem_addr(smem) + warp * C::kRing;
@@ -382,10 +415,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         const uint32_t r0 = on0 ? g : 0, r1 = on1 ? g + 8 : 0, j0 = r0 / G, j1 = r1 / G;
         const uint16_t *q0 = qp + j0 * a.q_stride + (r0 - j0 * G) * D, *q1 = qp + j1 * a.q_stride + (r1 - j1 * G) * D;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks) {
+            q[ks][0] = ldp(reinterpret_cast<const uint32_t *>(q0 + ks * 16));
+            q[ks][2] = ldp(reinterpret_cast<const uint32_t *>(q0 + ks * 16 + 8));
+        }
+        if (rows > 8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                q[ks][e] = ldp(reinterpret_cast<const uint32_t *>(((e & 1) ? q1 : q0) + ks * 16 + (e >> 1) * 8));
+            for (int ks = 0; ks < KS; ++ks) {
+                q[ks][1] = ldp(reinterpret_cast<const uint32_t *>(q1 + ks * 16));
+                q[ks][3] = ldp(reinterpret_cast<const uint32_t *>(q1 + ks * 16 + 8));
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) q[ks][1] = q[ks][3] = 0u;
+        }
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) {
             const int64_t cur = next;
@@ -415,13 +458,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             float sc[2][4] = {};
             {
                 const int r = (lane & 7) + (lane >> 4) * 8;  // matrices: keys 0-7 (two pieces), keys 8-15
+                float odd[2][4] = {};  // a second chain of dependent products, half as long each
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     uint32_t kf[4];
                     ldsm4(kb + r * (D * 2) + (((2 * ks + ((lane >> 3) & 1)) ^ (r & 7)) * 16), kf);
-                    mma16816(sc[0], q[ks], kf[0], kf[1]);
-                    mma16816(sc[1], q[ks], kf[2], kf[3]);
+                    mma16816(ks & 1 ? odd[0] : sc[0], q[ks], kf[0], kf[1]);
+                    mma16816(ks & 1 ? odd[1] : sc[1], q[ks], kf[2], kf[3]);
                 }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][e] += odd[n][e];
             }
             const int key0 = int(step0 + warp + i * kWarps) * kStep;
 #pragma unroll

@@ -14,7 +14,13 @@
 // begin the next: the shares are even, but a CTA pays the start and end of each piece (about
 // kPiece steps' time).  A pair that a CTA holds whole is written out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
 // arrive last join them in the order of the keys, so the bits do not depend on timing.
+//
+// Where the host sees that the pairs are few and no sequence can be long, a cluster of eight CTAs
+// takes each pair: nothing is scheduled on the device, and the parts meet in shared memory
+// (8 sequences of 150 to 1100 keys, 4 key heads: @@ us, 9.3 through the workspace).
 #include "attn.cuh"
+
+#include <cooperative_groups.h>
 
 namespace moe {
 namespace attn {
@@ -209,9 +215,17 @@ __device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows,
         join_rows<D, 16>(p, n, rows, sm, slot_of, emit);
 }
 
-template <int D>
+constexpr int kCluster = 8;          // CTAs of a pair
+constexpr int kClusterPairs = 32;    // clusters of 8 that the machine holds at two CTAs an SM
+constexpr int kClusterKeys = 4096;   // keys up to which a cluster's CTAs are enough for a pair
+
+template <int D, bool kClustered>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Parts parts) {
+    namespace cg = cooperative_groups;
     using C = Cfg<D>;
+    // the join's buffers: [warp][row][D], [warp][row] (max, sum); clustered, after them [row][D], [row]
+    constexpr int kJoinFloats = kWarps * kRows * (D + 2);
+    static_assert((kJoinFloats + kRows * (D + 2)) * 4 <= C::kSmem, "");
     constexpr int NT = D / 8;        // 8-column tiles of O
     constexpr int KS = D / 16;       // 16-element steps of the head dimension
     constexpr int CH = D / 8;        // 16-byte pieces of a row
@@ -226,116 +240,132 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t G = a.group, Hkv = a.n_kv_heads;
 
-    // the line of all steps, and how it is cut.  Up to 32 sequences every warp scans by itself, without
-    // barriers.
-    const bool few = a.n_seqs <= 32;
-    uint32_t n0 = 0, before0 = 0, total = 0, pairs = 0;
+    int b = 0;
+    uint32_t base = 0, steps = 0, part = 0, at = 0, u = 0, u_end = 0;
+    bool aligned = false;
+    Shares sh{};
     Seq s{};
-    auto warp_scan = [&](uint32_t n, uint32_t *sum) {
-        uint32_t incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        *sum = __shfl_sync(0xffffffffu, incl, 31);
-        return incl - n;
-    };
-    if (few) {
-        if (lane < a.n_seqs) {
-            s = load_seq(a, lane);
-            n0 = steps_of(s);
-        }
-        pairs = __popc(__ballot_sync(0xffffffffu, n0 > 0)) * Hkv;
-        before0 = warp_scan(n0 * Hkv, &total);
-    }
-    for (int b0 = 0; !few && b0 < a.n_seqs; b0 += kThreads) {
-        uint32_t n = 0, sum;
-        if (b0 + tid < a.n_seqs) {
-            const Seq x = load_seq(a, b0 + tid);
-            n = steps_of(x);
-            if (b0 == 0) s = x;
-        }
-        pairs += uint32_t(__syncthreads_count(n > 0)) * Hkv;
-        const uint32_t before = block_scan(n * Hkv, &sum, scratch);
-        if (b0 == 0) {
-            n0 = n;
-            before0 = before;
-        }
-        total += sum;
-    }
-    const uint32_t cta = blockIdx.x, grid = gridDim.x;
-    // parts of at most `part` steps make at most total / part + pairs <= grid CTAs; each warp keeps
-    // two steps
-    const uint32_t part = pairs < grid ? max(2u * kWarps, (total + grid - pairs - 1) / (grid - pairs)) : 0u;
-    const bool aligned = part > 0 && part <= max(2u * kWarps, total / grid + kPiece);
-    // no more CTAs than leave every warp two steps: fewer parts to join
-    const uint32_t ctas = max(1u, min(grid, total / (2 * kWarps)));
-    const Shares sh{total / ctas, total % ctas};
-    uint32_t u = 0, u_end = 0;  // the share on the line (not aligned)
-    if (!aligned) {
-        if (cta >= ctas) return;
-        u = sh.begin(cta);
-        u_end = sh.begin(cta + 1);
-        if (u >= u_end) return;
-    }
-    // places of a sequence: its parts (aligned), or its steps, of all heads
-    auto places_of = [&](uint32_t n) { return (aligned ? (n + part - 1) / part : n) * Hkv; };
-    const uint32_t at = aligned ? cta : u;
-    int b;
-    uint32_t base = 0;
-    if (few) {
-        uint32_t sum;
-        const uint32_t n = places_of(n0), before = aligned ? warp_scan(n, &sum) : before0;
-        const uint32_t here = __ballot_sync(0xffffffffu, at >= before && at - before < n);
-        if (here == 0) return;  // past the last part: every warp of the block
-        b = __ffs(here) - 1;
-        base = __shfl_sync(0xffffffffu, before, b);
-        s.q0 = __shfl_sync(0xffffffffu, s.q0, b);
-        s.q_len = __shfl_sync(0xffffffffu, s.q_len, b);
-        s.kv_len = __shfl_sync(0xffffffffu, s.kv_len, b);
+    const uint32_t cta = blockIdx.x;
+    if constexpr (kClustered) {
+        b = int(cta / kCluster / Hkv);
+        s = load_seq(a, b);
+        if (s.q_len == 0) return;  // the whole cluster
+        steps = steps_of(s);
     } else {
-        if (tid == 0) first[0] = ~0u;
-        auto found = [&](uint32_t i, uint32_t before, uint32_t n, const Seq &x) {
-            if (at >= before && at - before < n) {
-                first[0] = i;
-                first[1] = before;
-                first_seq = x;
+        // the line of all steps, and how it is cut.  Up to 32 sequences every warp scans by itself, without
+        // barriers.
+        const bool few = a.n_seqs <= 32;
+        uint32_t n0 = 0, before0 = 0, total = 0, pairs = 0;
+        auto warp_scan = [&](uint32_t n, uint32_t *sum) {
+            uint32_t incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
             }
+            *sum = __shfl_sync(0xffffffffu, incl, 31);
+            return incl - n;
         };
-        if (a.n_seqs <= kThreads) {
-            uint32_t sum;
-            const uint32_t n = places_of(n0), before = aligned ? block_scan(n, &sum, scratch) : before0;
-            __syncthreads();
-            found(tid, before, n, s);
-        } else {
-            for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-                uint32_t n = 0, sum;
-                Seq x{};
-                if (b0 + tid < a.n_seqs) {
-                    x = load_seq(a, b0 + tid);
-                    n = places_of(steps_of(x));
-                }
-                const uint32_t before = base + block_scan(n, &sum, scratch);
-                found(b0 + tid, before, n, x);
-                base += sum;
-                if (at < base) break;
+        if (few) {
+            if (lane < a.n_seqs) {
+                s = load_seq(a, lane);
+                n0 = steps_of(s);
             }
+            pairs = __popc(__ballot_sync(0xffffffffu, n0 > 0)) * Hkv;
+            before0 = warp_scan(n0 * Hkv, &total);
         }
-        __syncthreads();
-        if (first[0] == ~0u) return;  // past the last part
-        b = int(first[0]);
-        base = first[1];
-        s = first_seq;
+        for (int b0 = 0; !few && b0 < a.n_seqs; b0 += kThreads) {
+            uint32_t n = 0, sum;
+            if (b0 + tid < a.n_seqs) {
+                const Seq x = load_seq(a, b0 + tid);
+                n = steps_of(x);
+                if (b0 == 0) s = x;
+            }
+            pairs += uint32_t(__syncthreads_count(n > 0)) * Hkv;
+            const uint32_t before = block_scan(n * Hkv, &sum, scratch);
+            if (b0 == 0) {
+                n0 = n;
+                before0 = before;
+            }
+            total += sum;
+        }
+        const uint32_t grid = gridDim.x;
+        // parts of at most `part` steps make at most total / part + pairs <= grid CTAs; each warp keeps
+        // two steps
+        part = pairs < grid ? max(2u * kWarps, (total + grid - pairs - 1) / (grid - pairs)) : 0u;
+        aligned = part > 0 && part <= max(2u * kWarps, total / grid + kPiece);
+        // no more CTAs than leave every warp two steps: fewer parts to join
+        const uint32_t ctas = max(1u, min(grid, total / (2 * kWarps)));
+        sh = Shares{total / ctas, total % ctas};
+        if (!aligned) {
+            if (cta >= ctas) return;
+            u = sh.begin(cta);
+            u_end = sh.begin(cta + 1);
+            if (u >= u_end) return;
+        }
+        // places of a sequence: its parts (aligned), or its steps, of all heads
+        auto places_of = [&](uint32_t n) { return (aligned ? (n + part - 1) / part : n) * Hkv; };
+        at = aligned ? cta : u;  // its place on the line of parts or steps
+        if (few) {
+            uint32_t sum;
+            const uint32_t n = places_of(n0), before = aligned ? warp_scan(n, &sum) : before0;
+            const uint32_t here = __ballot_sync(0xffffffffu, at >= before && at - before < n);
+            if (here == 0) return;  // past the last part: every warp of the block
+            b = __ffs(here) - 1;
+            base = __shfl_sync(0xffffffffu, before, b);
+            s.q0 = __shfl_sync(0xffffffffu, s.q0, b);
+            s.q_len = __shfl_sync(0xffffffffu, s.q_len, b);
+            s.kv_len = __shfl_sync(0xffffffffu, s.kv_len, b);
+        } else {
+            if (tid == 0) first[0] = ~0u;
+            auto found = [&](uint32_t i, uint32_t before, uint32_t n, const Seq &x) {
+                if (at >= before && at - before < n) {
+                    first[0] = i;
+                    first[1] = before;
+                    first_seq = x;
+                }
+            };
+            if (a.n_seqs <= kThreads) {
+                uint32_t sum;
+                const uint32_t n = places_of(n0), before = aligned ? block_scan(n, &sum, scratch) : before0;
+                __syncthreads();
+                found(tid, before, n, s);
+            } else {
+                for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+                    uint32_t n = 0, sum;
+                    Seq x{};
+                    if (b0 + tid < a.n_seqs) {
+                        x = load_seq(a, b0 + tid);
+                        n = places_of(steps_of(x));
+                    }
+                    const uint32_t before = base + block_scan(n, &sum, scratch);
+                    found(b0 + tid, before, n, x);
+                    base += sum;
+                    if (at < base) break;
+                }
+            }
+            __syncthreads();
+            if (first[0] == ~0u) return;  // past the last part
+            b = int(first[0]);
+            base = first[1];
+            s = first_seq;
+        }
+        steps = steps_of(s);
     }
-    uint32_t steps = steps_of(s);
 
     const uint32_t ring = smem_addr(smem) + warp * C::kRing;
     const float sl2 = a.scale * kLog2e;
 
     for (bool more = true; more;) {
-        uint32_t h, c0, n_parts, step0, step1, item = 0;
-        if (aligned) {
+        uint32_t h, c0 = 0, n_parts = 1, step0, step1, item = 0;
+        if (kClustered) {
+            h = cta / kCluster % Hkv;
+            const uint32_t rank = cta % kCluster;
+            const Shares even{steps / kCluster, steps % kCluster};
+            step0 = even.begin(rank);
+            step1 = even.begin(rank + 1);
+            more = false;
+        } else if (aligned) {
             const uint32_t per = (steps + part - 1) / part;
             h = (at - base) / per;
             const uint32_t i = at - base - h * per;
@@ -567,6 +597,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             if (d == 0) parts.ml[slot * kRows + r] = make_float2(m, l);
         };
         const bool whole = n_parts == 1;
+        float *cj = jo + kJoinFloats;  // clustered: this CTA's part for the others
+        float2 *cm = reinterpret_cast<float2 *>(cj + kRows * D);
         const size_t slot = (size_t)cta * 2 + (cta == c0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -585,10 +617,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            if (whole)
+            if (kClustered) {
+                *reinterpret_cast<float4 *>(cj + r * D + d) = acc;
+                if (d == 0) cm[r] = make_float2(m, l);
+            } else if (whole) {
                 write_out(r, d, acc, m, l);
-            else
+            } else {
                 write_part(slot, r, d, acc, m, l);
+            }
+        }
+        if constexpr (kClustered) {
+            // each CTA joins an eighth of the outputs, the parts in the order of the keys
+            cg::cluster_group cl = cg::this_cluster();
+            cl.sync();
+            const int all = rows * (D / 4), each = (all + kCluster - 1) / kCluster, i = int(cta % kCluster) * each + tid;
+            if (tid < each && i < all) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                float2 ml[kCluster];
+                float4 v[kCluster];
+                float m = kNegInf, l = 0.f;
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    ml[k] = *cl.map_shared_rank(cm + r, k);
+                    v[k] = *cl.map_shared_rank(reinterpret_cast<float4 *>(cj + r * D + d), k);
+                }
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) m = fmaxf(m, ml[k].x);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    const float f = ml[k].x == kNegInf ? 0.f : ex2(ml[k].x - m);
+                    l = fmaf(f, ml[k].y, l);
+                    acc.x = fmaf(f, v[k].x, acc.x);
+                    acc.y = fmaf(f, v[k].y, acc.y);
+                    acc.z = fmaf(f, v[k].z, acc.z);
+                    acc.w = fmaf(f, v[k].w, acc.w);
+                }
+                write_out(r, d, acc, m, l);
+            }
+            cl.sync();  // no CTA leaves while another reads its part
+            return;
         }
         if (!whole) {
             const uint32_t n = n_parts, groups = (n + kGroup - 1) / kGroup, k = (cta - c0) / kGroup;
@@ -612,20 +680,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     }
 }
 
-template <int D>
-cudaError_t launch_typed(const Args &a, char *hdr, char *ws, int grid, cudaStream_t st) {
+// Few pairs, and no sequence with more keys than a cluster's CTAs go through quickly.
+bool clustered(const moe_attn_shape &s) {
+    return (int64_t)s.n_seqs * s.n_kv_heads <= kClusterPairs && (int64_t)s.max_pages * s.page_size <= kClusterKeys;
+}
+
+template <int D, bool kClustered>
+cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int grid, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kClustered>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
     float *o = reinterpret_cast<float *>(ws);
     float2 *ml = reinterpret_cast<float2 *>(o + (size_t)kMaxGrid * 2 * kRows * D);
     const Parts p{reinterpret_cast<uint32_t *>(hdr + kCounters), o, ml};
-    return launch_pdl(decode_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, a, p);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kClustered ? unsigned(s.n_seqs * s.n_kv_heads * kCluster) : unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = kClustered ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kClustered>, a, p);
 }
 
 }  // namespace
@@ -641,7 +728,11 @@ size_t decode_ws_bytes(const moe_attn_shape &s) { return (size_t)kMaxGrid * 2 * 
 
 cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st) {
     const int grid = sms * kCtasPerSm < kMaxGrid ? sms * kCtasPerSm : kMaxGrid;
-    return s.head_dim == 128 ? launch_typed<128>(a, hdr, ws, grid, st) : launch_typed<64>(a, hdr, ws, grid, st);
+    if (clustered(s))
+        return s.head_dim == 128 ? launch_typed<128, true>(a, s, hdr, ws, grid, st)
+                                 : launch_typed<64, true>(a, s, hdr, ws, grid, st);
+    return s.head_dim == 128 ? launch_typed<128, false>(a, s, hdr, ws, grid, st)
+                             : launch_typed<64, false>(a, s, hdr, ws, grid, st);
 }
 
 }  // namespace attn

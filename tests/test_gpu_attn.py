@@ -90,6 +90,11 @@ ATTN = {
     "decode long": ("bf16", 8, 1, 128, 64, [1], [9000]),
     "decode empty caches": ("bf16", 8, 2, 128, 16, [1, 1, 1, 1], [0, 40, 0, 1]),
     "idle sequences": ("bf16", 8, 2, 128, 16, [0, 1, 0, 1, 0], [20, 30, 0, 1, 7]),
+    "decode 40 pairs": ("bf16", 16, 4, 128, 16, [1, 0, 1, 2, 1, 1, 1, 1, 1, 2], [700, 30, 0, 1, 1900, 65, 512, 513, 2, 40]),
+    "decode 120 pairs": ("bf16", 24, 8, 64, 32, [1] * 15, [1 + 67 * i for i in range(15)]),
+    "decode 200 pairs": ("bf16", 16, 8, 64, 16, [1, 2, 0, 1, 1] * 5, [(i * 41) % 500 for i in range(25)]),
+    "decode 400 pairs": ("bf16", 8, 8, 128, 16, [1] * 50, [(i * 29) % 300 for i in range(50)]),
+    "decode one pair long table": ("bf16", 16, 1, 64, 64, [1], [4096]),
     "few tokens": ("bf16", 8, 4, 128, 16, [3, 1, 5, 2], [3, 200, 97, 64]),
     "few tokens group 8": ("bf16", 16, 2, 64, 32, [2, 2, 1], [2, 100, 513]),
     "few tokens cut short": ("bf16", 8, 4, 128, 16, [4, 4, 4], [2, 0, 4]),

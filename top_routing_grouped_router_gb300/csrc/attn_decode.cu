@@ -15,9 +15,10 @@
 // kPiece steps' time).  A pair that a CTA holds whole is written out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
 // arrive last join them in the order of the keys, so the bits do not depend on timing.
 //
-// Where the host sees that the pairs are few and no sequence can be long, a cluster of eight CTAs
-// takes each pair: nothing is scheduled on the device, and the parts meet in shared memory
-// (8 sequences of 150 to 1100 keys, 4 key heads: @@ us, 9.3 through the workspace).
+// Where the host sees that the pairs are few and no sequence can be long, a cluster of eight, four
+// or two CTAs (or one CTA) takes each pair: nothing is scheduled on the device, and the parts meet
+// in shared memory (8 sequences of 150 to 1100 keys, 4 key heads: 7.5 us, 9.3 through the
+// workspace; one sequence of 2000 keys 7.1 us, 9.3).
 #include "attn.cuh"
 
 #include <cooperative_groups.h>
@@ -215,14 +216,13 @@ __device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows,
         join_rows<D, 16>(p, n, rows, sm, slot_of, emit);
 }
 
-constexpr int kCluster = 8;          // CTAs of a pair
-constexpr int kClusterPairs = 32;    // clusters of 8 that the machine holds at two CTAs an SM
-constexpr int kClusterKeys = 4096;   // keys up to which a cluster's CTAs are enough for a pair
-
-template <int D, bool kClustered>
+// kCluster: CTAs of a pair, 0 where the work is scheduled on the device.
+template <int D, int kCluster>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Parts parts) {
     namespace cg = cooperative_groups;
     using C = Cfg<D>;
+    constexpr bool kClustered = kCluster > 0;
+    constexpr int kC = kClustered ? kCluster : 1;
     // the join's buffers: [warp][row][D], [warp][row] (max, sum); clustered, after them [row][D], [row]
     constexpr int kJoinFloats = kWarps * kRows * (D + 2);
     static_assert((kJoinFloats + kRows * (D + 2)) * 4 <= C::kSmem, "");
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     Seq s{};
     const uint32_t cta = blockIdx.x;
     if constexpr (kClustered) {
-        b = int(cta / kCluster / Hkv);
+        b = int(cta / kC / Hkv);
         s = load_seq(a, b);
         if (s.q_len == 0) return;  // the whole cluster
         steps = steps_of(s);
@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     for (bool more = true; more;) {
         uint32_t h, c0 = 0, n_parts = 1, step0, step1, item = 0;
         if (kClustered) {
-            h = cta / kCluster % Hkv;
-            const uint32_t rank = cta % kCluster;
-            const Shares even{steps / kCluster, steps % kCluster};
+            h = cta / kC % Hkv;
+            const uint32_t rank = cta % kC;
+            const Shares even{steps / kC, steps % kC};
             step0 = even.begin(rank);
             step1 = even.begin(rank + 1);
             more = false;
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            if (kClustered) {
+            if (kC > 1) {
                 *reinterpret_cast<float4 *>(cj + r * D + d) = acc;
                 if (d == 0) cm[r] = make_float2(m, l);
             } else if (whole) {
@@ -626,26 +626,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                 write_part(slot, r, d, acc, m, l);
             }
         }
-        if constexpr (kClustered) {
-            // each CTA joins an eighth of the outputs, the parts in the order of the keys
+        if constexpr (kC > 1) {
+            // each CTA joins its share of the outputs, the parts in the order of the keys
             cg::cluster_group cl = cg::this_cluster();
             cl.sync();
-            const int all = rows * (D / 4), each = (all + kCluster - 1) / kCluster, i = int(cta % kCluster) * each + tid;
+            const int all = rows * (D / 4), each = (all + kC - 1) / kC, i = int(cta % kC) * each + tid;
             if (tid < each && i < all) {
                 const int r = i / (D / 4), d = i % (D / 4) * 4;
-                float2 ml[kCluster];
-                float4 v[kCluster];
+                float2 ml[kC];
+                float4 v[kC];
                 float m = kNegInf, l = 0.f;
 #pragma unroll
-                for (int k = 0; k < kCluster; ++k) {
+                for (int k = 0; k < kC; ++k) {
                     ml[k] = *cl.map_shared_rank(cm + r, k);
                     v[k] = *cl.map_shared_rank(reinterpret_cast<float4 *>(cj + r * D + d), k);
                 }
 #pragma unroll
-                for (int k = 0; k < kCluster; ++k) m = fmaxf(m, ml[k].x);
+                for (int k = 0; k < kC; ++k) m = fmaxf(m, ml[k].x);
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < kCluster; ++k) {
+                for (int k = 0; k < kC; ++k) {
                     const float f = ml[k].x == kNegInf ? 0.f : ex2(ml[k].x - m);
                     l = fmaf(f, ml[k].y, l);
                     acc.x = fmaf(f, v[k].x, acc.x);
@@ -680,18 +680,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
     }
 }
 
-// Few pairs, and no sequence with more keys than a cluster's CTAs go through quickly.
-bool clustered(const moe_attn_shape &s) {
-    return (int64_t)s.n_seqs * s.n_kv_heads <= kClusterPairs && (int64_t)s.max_pages * s.page_size <= kClusterKeys;
+// CTAs of a pair's cluster, or 0: as many clusters as the machine holds at two CTAs an SM (a little
+// fewer than their number says: eight CTAs find places within one part of the chip only), and no
+// sequence with more than 8 steps a warp (104 pairs of up to 1819 keys, 14 steps: 13.8 us with
+// clusters of two, 12.2 scheduled; 40 pairs of up to 1989, clusters of four: 9.3, 9.6).
+int cluster_of(const moe_attn_shape &s) {
+    const int64_t pairs = (int64_t)s.n_seqs * s.n_kv_heads, keys = (int64_t)s.max_pages * s.page_size;
+    const int sizes[4] = {8, 4, 2, 1}, most[4] = {32, 72, 152, 304};
+    for (int i = 0; i < 4; ++i)
+        if (pairs <= most[i]) return keys <= 8 * kWarps * kStep * sizes[i] ? sizes[i] : 0;
+    return 0;
 }
 
-template <int D, bool kClustered>
+template <int D, int kCluster>
 cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int grid, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kClustered>,
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kCluster>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
@@ -703,16 +710,22 @@ cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.x = kCluster > 0 ? kCluster : 1;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kClustered ? unsigned(s.n_seqs * s.n_kv_heads * kCluster) : unsigned(grid));
+    cfg.gridDim = dim3(kCluster > 0 ? unsigned(s.n_seqs * s.n_kv_heads * kCluster) : unsigned(grid));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Cfg<D>::kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = kClustered ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kClustered>, a, p);
+    cfg.numAttrs = kCluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kCluster>, a, p);
+}
+
+template <int kCluster>
+cudaError_t launch_dim(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int grid, cudaStream_t st) {
+    return s.head_dim == 128 ? launch_typed<128, kCluster>(a, s, hdr, ws, grid, st)
+                             : launch_typed<64, kCluster>(a, s, hdr, ws, grid, st);
 }
 
 }  // namespace
@@ -728,11 +741,13 @@ size_t decode_ws_bytes(const moe_attn_shape &s) { return (size_t)kMaxGrid * 2 * 
 
 cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st) {
     const int grid = sms * kCtasPerSm < kMaxGrid ? sms * kCtasPerSm : kMaxGrid;
-    if (clustered(s))
-        return s.head_dim == 128 ? launch_typed<128, true>(a, s, hdr, ws, grid, st)
-                                 : launch_typed<64, true>(a, s, hdr, ws, grid, st);
-    return s.head_dim == 128 ? launch_typed<128, false>(a, s, hdr, ws, grid, st)
-                             : launch_typed<64, false>(a, s, hdr, ws, grid, st);
+    switch (cluster_of(s)) {
+    case 8: return launch_dim<8>(a, s, hdr, ws, grid, st);
+    case 4: return launch_dim<4>(a, s, hdr, ws, grid, st);
+    case 2: return launch_dim<2>(a, s, hdr, ws, grid, st);
+    case 1: return launch_dim<1>(a, s, hdr, ws, grid, st);
+    default: return launch_dim<0>(a, s, hdr, ws, grid, st);
+    }
 }
 
 }  // namespace attn

@@ -76,33 +76,56 @@ __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a
     return sum;
 }
 
-// Steps of item i of a chunk: the keys that its last token sees, at least one step.
-__device__ __forceinline__ uint32_t item_steps(const Seq &s, uint32_t i, uint32_t tt2) {
-    const int64_t keys = min((int64_t)s.kv_len - s.q_len + (int64_t)(i + 1) * tt2, (int64_t)s.kv_len);
-    return keys <= kKeys ? 1u : uint32_t((keys + kKeys - 1) / kKeys);
+// Tokens of an item, and their logarithm (-1 if they are no power of two).
+struct Item {
+    uint32_t tokens;
+    int shift;
+    __device__ __forceinline__ uint32_t div(uint32_t x) const { return shift >= 0 ? x >> shift : x / tokens; }
+};
+
+// sum_{i < n} floor((tokens i + b) / kKeys).  Tokens that are a power of two need no division: below
+// kKeys, floor((i + floor(b / tokens)) / p) with p = kKeys / tokens.
+__device__ __forceinline__ uint32_t step_sum(uint32_t n, Item it, uint32_t b) {
+    constexpr int kLog = 7;
+    static_assert(kKeys == 1 << kLog, "");
+    if (it.shift < 0) return floor_sum(n, kKeys, it.tokens, b);
+    if (n == 0) return 0;
+    if (it.shift >= kLog) return (uint32_t((uint64_t)n * (n - 1) / 2) << (it.shift - kLog)) + n * (b >> kLog);
+    const int lp = kLog - it.shift;
+    const uint32_t b1 = b >> it.shift;
+    auto f = [lp](uint32_t x) {  // sum_{j < x} floor(j / p)
+        const uint32_t q = x >> lp;
+        return ((q * (q - 1) / 2) << lp) + q * (x - (q << lp));
+    };
+    return f(b1 + n) - f(b1);
 }
-__device__ __forceinline__ uint32_t items_of(const Seq &s, uint32_t tt2) { return (s.q_len + tt2 - 1) / tt2; }
+
+// Steps of item i of a chunk: the keys that its last token sees, at least one step.
+__device__ __forceinline__ uint32_t item_steps(const Seq &s, uint32_t i, Item it) {
+    const int64_t keys = min((int64_t)s.kv_len - s.q_len + (int64_t)(i + 1) * it.tokens, (int64_t)s.kv_len);
+    return keys <= kKeys ? 1u : (uint32_t(keys) + kKeys - 1) / kKeys;
+}
+__device__ __forceinline__ uint32_t items_of(const Seq &s, Item it) { return it.div(s.q_len + it.tokens - 1); }
 
 // Steps of items [0, i) of a chunk.
-__device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, uint32_t tt2) {
+__device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, Item it) {
     if (i == 0) return 0;
-    const uint32_t n = items_of(s, tt2);
-    const uint32_t last = i == n ? item_steps(s, n - 1, tt2) : 0;
-    const uint32_t full = i == n ? n - 1 : i;  // items that hold tt2 tokens
+    const uint32_t n = items_of(s, it);
+    const uint32_t last = i == n ? item_steps(s, n - 1, it) : 0;
+    const uint32_t full = i == n ? n - 1 : i;  // items that hold all their tokens
     const int64_t past = (int64_t)s.kv_len - s.q_len;
     // items that see no key have one step each
-    uint32_t none = 0;
-    if (past < 0) none = min(full, uint32_t(-past) / tt2);
-    const uint32_t b = uint32_t(past + (int64_t)(none + 1) * tt2 + kKeys - 1);  // > kKeys - 1
-    return none + floor_sum(full - none, kKeys, tt2, b) + last;
+    const uint32_t none = past < 0 ? min(full, it.div(uint32_t(-past))) : 0;
+    const uint32_t b = uint32_t(past + (int64_t)(none + 1) * it.tokens + kKeys - 1);  // > kKeys - 1
+    return none + step_sum(full - none, it, b) + last;
 }
 
 // On the line of all steps an item takes kSetup places more than its steps, at its front: what
 // starting and ending an item costs, about two steps' time (a mixed batch of short and long
 // items: 85 us with none, the slowest CTA 1.45 times the mean).
 constexpr uint32_t kSetup = 2;
-__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, uint32_t tt2, bool whole) {
-    return whole ? i : steps_before(s, i, tt2) + i * kSetup;
+__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, Item it, bool whole) {
+    return whole ? i : steps_before(s, i, it) + i * kSetup;
 }
 // Where no sequence can hold more keys than this, items are not cut (each takes one place on the
 // line), and the join is not launched.
@@ -212,7 +235,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct Ctx {
     Args a;
     uint32_t tt;        // tokens of a tile
-    float *part_o;      // [slot][2 * kM][D]
+    int item_shift;     // log2(2 tt), -1 if that is no power of two
+    float *part_o;      // [slot][D / 4][2 * kM][4]: a warp's rows side by side
     float2 *part_ml;    // [slot][2 * kM]
     Rec *rec;           // [kMaxCtas]
     unsigned long long wait_ns;
@@ -247,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const Waits wt{a.err, abort, c.wait_ns, smem_u32(const_cast<int *>(abort))};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t tt = c.tt, tt2 = 2 * tt, G = a.group, Hkv = a.n_kv_heads;
+    const Item it{tt2, c.item_shift};
     if (tid == kLoadWarp * 32) {
         for (const CUtensorMap *p : {&map_q, &map_k, &map_v})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(p)) : "memory");
@@ -299,29 +324,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *sum = total;
         return before + incl - n;
     };
-    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, tt2), tt2, c.whole); };
+    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, it), it, c.whole); };
     uint32_t total = 0, n0 = 0, before0 = 0;
     bool rows_ok = true;
     Seq s0{};
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
-        uint32_t n = 0, sum;
-        Seq s{};
-        if (b0 + tid < a.n_seqs) {
-            s = load_seq(a, b0 + tid);
-            n = seq_places(s) * Hkv;
-            rows_ok = rows_ok && s.rows_ok;
+    const bool few = a.n_seqs <= 32;  // every warp scans by itself, without barriers
+    if (few) {
+        if (lane < a.n_seqs) {
+            s0 = load_seq(a, lane);
+            n0 = seq_places(s0) * Hkv;
+            rows_ok = s0.rows_ok;
         }
-        const uint32_t before = scan_block(n, &sum);
-        if (b0 == 0) {
-            n0 = n;
-            before0 = before;
-            s0 = s;
+        uint32_t incl = n0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
         }
-        total += sum;
+        before0 = incl - n0;
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        rows_ok = __all_sync(0xffffffffu, rows_ok);
+    } else {
+        for (int b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
+            uint32_t n = 0, sum;
+            Seq s{};
+            if (b0 + tid < a.n_seqs) {
+                s = load_seq(a, b0 + tid);
+                n = seq_places(s) * Hkv;
+                rows_ok = rows_ok && s.rows_ok;
+            }
+            const uint32_t before = scan_block(n, &sum);
+            if (b0 == 0) {
+                n0 = n;
+                before0 = before;
+                s0 = s;
+            }
+            total += sum;
+        }
+        rows_ok = !__syncthreads_or(!rows_ok);
     }
     // chunks that overlap could make a line longer than 32 bits count: such a call does nothing (the
     // error is recorded)
-    if (__syncthreads_or(!rows_ok)) total = 0;
+    if (!rows_ok) total = 0;
     const uint32_t cta = blockIdx.x, ctas = max(1u, min(gridDim.x, c.whole ? total : total / (kSetup + 2)));
     const Shares sh{total / ctas, total % ctas};
     const uint32_t u_begin = cta < ctas ? sh.begin(cta) : 0, u_end = cta < ctas ? sh.begin(cta + 1) : 0;
@@ -335,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 *cur_seq = s;
             }
         };
-        found(tid, before0, n0, s0);
+        if (!few || warp == 0) found(few ? lane : tid, before0, n0, s0);
         uint32_t base = 0;
         for (int b0 = 0; a.n_seqs > kThreads && b0 < a.n_seqs; b0 += kThreads) {
             uint32_t n = 0, sum;
@@ -385,20 +429,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     h = (w - first) / per_head;
                     const uint32_t rem = w - first - h * per_head;
                     // the last item that begins at or before rem: 32 candidates a round
-                    uint32_t lo = 0, n = items_of(s, tt2);
+                    uint32_t lo = 0, n = items_of(s, it), at_lo = 0;
                     while (n > 1) {
-                        const uint32_t each = (n + 31) / 32;
-                        const uint32_t cand = lo + lane * each;
-                        const bool at = lane * each < n && places_before(s, cand, tt2, c.whole) <= rem;
-                        const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, at));
+                        const uint32_t each = (n + 31) / 32, cand = lo + lane * each;
+                        const uint32_t before = lane * each < n ? places_before(s, cand, it, c.whole) : ~0u;
+                        const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, before <= rem));
+                        at_lo = __shfl_sync(0xffffffffu, before, last);
                         lo += last * each;
                         n = min(each, n - last * each);
                     }
                     i = lo;
-                    item0 = first + h * per_head + places_before(s, i, tt2, c.whole);
+                    item0 = first + h * per_head + at_lo;
                     located = true;
                 }
-                const uint32_t steps = item_steps(s, i, tt2), setup = c.whole ? 0 : kSetup;
+                const uint32_t steps = item_steps(s, i, it), setup = c.whole ? 0 : kSetup;
                 const uint32_t places = c.whole ? 1 : steps + kSetup, end = min(item0 + places, u_end);
                 // steps begin after the item's setup; a share that ends within it leaves the item to the next
                 const uint32_t from = max(w, item0 + setup);
@@ -427,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 w = end;
                 if (end == item0 + places) {
                     item0 += places;
-                    if (++i == items_of(s, tt2)) {
+                    if (++i == items_of(s, it)) {
                         i = 0;
                         ++h;
                         if (h == Hkv) located = false;  // the next sequence
@@ -679,9 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     tmem_ld32(to + i, o);
                     if (g.slot >= 0) {
                         if (live) {
+                            uint4 *to = reinterpret_cast<uint4 *>(c.part_o) + ((size_t)g.slot * (D / 4) + i / 4) * 2 * kM + t * kM + r;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(c.part_o + prow * D + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            for (int e = 0; e < 8; ++e)
+                                to[e * 2 * kM] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     } else if (live) {
 #pragma unroll
@@ -743,11 +788,11 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     const int *rp = reinterpret_cast<const int *>(c.rec + blockIdx.x);
     const int n = ldp(rp), h = ldp(rp + 1), tok0 = ldp(rp + 2), q0 = ldp(rp + 3), q_len = ldp(rp + 4);
     if (n == 0) return;
-    const int G = a.group, row = blockIdx.y * kJoinRows + threadIdx.x / 16, t = row / kM, r = row % kM;
+    const int G = a.group, row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, t = row / kM, r = row % kM;
     const int rt = r / G, j = tok0 + t * int(c.tt) + rt;
     if (r >= G * int(c.tt) || j >= q_len) return;
-    constexpr int kFly = 4, E = D / 64;  // float4 pieces of a thread: 16 apart
-    const int d0 = threadIdx.x % 16 * 4;
+    constexpr int kFly = 4, E = D / 64;  // float4 pieces of a thread: neighbours
+    const int d0 = threadIdx.x / kJoinRows * (4 * E);
     float m = kNegInf, l = 0.f;
     float4 acc[E];
 #pragma unroll
@@ -758,10 +803,11 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 #pragma unroll
         for (int p = 0; p < kFly; ++p) {
             const int i = min(p0 + p, n - 1);
-            const size_t pr = ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * 2 * kM + row;
-            asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(pm[p]), "=f"(pl[p]) : "l"(c.part_ml + pr));
+            const size_t slot = (size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0);
+            asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(pm[p]), "=f"(pl[p]) : "l"(c.part_ml + slot * 2 * kM + row));
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[p][e] = ldp16f(c.part_o + pr * D + e * 64 + d0);
+            for (int e = 0; e < E; ++e)
+                v[p][e] = ldp16f(c.part_o + ((slot * (D / 4) + d0 / 4 + e) * 2 * kM + row) * 4);
         }
         float mn = m;
 #pragma unroll
@@ -791,7 +837,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D + d0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        *reinterpret_cast<uint2 *>(dst + e * 64) =
+        *reinterpret_cast<uint2 *>(dst + e * 4) =
             make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
     if (a.lse && d0 == 0) a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
@@ -853,6 +899,9 @@ cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int s
     Ctx c{};
     c.a = a;
     c.tt = uint32_t(kM / a.group);
+    c.item_shift = -1;
+    if ((c.tt & (c.tt - 1)) == 0)
+        for (c.item_shift = 0; (1u << c.item_shift) < 2 * c.tt;) ++c.item_shift;
     const int cap = max_ctas(s), grid = sms < cap ? sms : cap;
     c.rec = reinterpret_cast<Rec *>(ws);
     c.part_ml = reinterpret_cast<float2 *>(ws + round256(kMaxCtas * sizeof(Rec)));

@@ -96,7 +96,7 @@ struct Var {
     static constexpr int kScalesRow = kFine ? 4 : 2;         // scale words of an output
     static constexpr int kStage = kCodes + kOut * kScalesRow * 4;
     static constexpr int kRedStride = kOut + 4;              // padded column of sums: no bank conflicts
-    static constexpr int kRed = kWarps * kCols * kRedStride * 4;
+    static constexpr int kRed = MT == 2 ? kWarps * MT * NT * 512 : kWarps * kCols * kRedStride * 4;
     static constexpr int kRing = kWarps * kDepth * kStage;
     static constexpr int kFixed = kRed + kRing + (kAffine ? 0 : kLutBytes);
     // 64 inputs of x: the fragments, and per block the start values (twice each, see below)
@@ -179,14 +179,21 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
 
     const int T0 = blockIdx.y * m.pass_rows, rows = min(a.T - T0, m.pass_rows);
 
-    // this CTA's stages of the inputs, and this warp's
     const int stages = (a.K + kIn - 1) / kIn;
+    // MT 1: this CTA's stages of the inputs, and this warp's, the same in each of the CTA's tiles.
     const int slice = int(blockIdx.x) % m.slices, group = int(blockIdx.x) / m.slices, groups = int(gridDim.x) / m.slices;
     const int s0 = int((int64_t)stages * slice / m.slices), s1 = int((int64_t)stages * (slice + 1) / m.slices);
     const int parts = kWarps / m.side, beside = warp % m.side, in_part = warp / m.side;
-    const int w0 = s0 + (s1 - s0) * in_part / parts, w1 = s0 + (s1 - s0) * (in_part + 1) / parts, mine = w1 - w0;
-    const int my_tiles = (m.tiles - group + groups - 1) / groups;
     const int wide = m.side * kOut, wide_log2 = __ffs(wide) - 1;
+    // MT 2: the CTA's pairs of strips are a line of stages, and each warp takes an equal piece of it.
+    // Its first pair may have been begun by the warps before, its last be ended by those after.
+    const int pair0 = int((int64_t)m.tiles * blockIdx.x / gridDim.x);
+    const int line = (int((int64_t)m.tiles * (blockIdx.x + 1) / gridDim.x) - pair0) * stages;
+    auto line_at = [&](int w) { return int((int64_t)line * w / kWarps); };
+    const int u0 = line_at(warp), u1 = line_at(warp + 1);
+    const int w0 = MT == 2 ? u0 % stages : s0 + (s1 - s0) * in_part / parts;
+    const int w1 = MT == 2 ? stages : s0 + (s1 - s0) * (in_part + 1) / parts, mine = w1 - w0;
+    const int my_tiles = (m.tiles - group + groups - 1) / groups;
 
     // The ring: copies run kDepth - 1 stages ahead, across tiles.  Piece (lane mod 4) of row lane / 4
     // (+ 8 i) is 16 bytes; the pieces of a row are permuted so that the reads below have no bank
@@ -195,14 +202,16 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     const uint32_t blocks = uint32_t(a.K / a.q_block);
     const size_t row_bytes = a.K / 2, row8 = 8 * row_bytes;
     const int crow = lane >> 2, cpiece = lane & 3, srow = lane >> 1, shalf = lane & 1;
-    int p_n = group * wide + beside * kOut, p_stage = w0, left = mine * my_tiles;
+    int p_n = MT == 2 ? (pair0 + u0 / stages) * kOut : group * wide + beside * kOut;
+    int p_stage = w0, left = MT == 2 ? u1 - u0 : mine * my_tiles;
     const uint8_t *src = a.codes + (size_t)(p_n + crow) * row_bytes + (size_t)w0 * kRowBytes + cpiece * 16;
-    const size_t tile_skip = (size_t)groups * wide * row_bytes - (size_t)mine * kRowBytes;
+    const int tile_step = MT == 2 ? kOut : groups * wide, again = MT == 2 ? stages : mine;
+    const size_t tile_skip = (size_t)tile_step * row_bytes - (size_t)again * kRowBytes;
     uint32_t sbase = uint32_t(p_n + srow) * blocks;
     const uint32_t ring_end = ring + kDepth * kStage;
     uint32_t dst = ring;
     const uint32_t code_at = crow * kRowBytes + ((cpiece ^ (crow >> 1 & 3)) * 16);  // row + 8: same permutation
-    const int K = a.K, N = a.N, shift = m.shift, tile_step = groups * wide;
+    const int K = a.K, N = a.N, shift = m.shift;
     // whole stages of whole tiles with one or two scales a half advance by constants; what is cut by
     // the matrix's edge, or has wider blocks, is worked out
     const bool simple = K % kIn == 0 && (kFine || shift == 0);
@@ -212,7 +221,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     const size_t strip_scales = (size_t)kStrip * blocks * 2;
     const uint32_t e0 = sbase + (kFine ? w0 * 4 + shalf * 2 : w0 * 2 + shalf);
     const char *ssrc = scales + (size_t)(e0 & ~1u) * 2;
-    const size_t scale_skip = (size_t)tile_step * blocks * 2 - (size_t)mine * kScaleStep;
+    const size_t scale_skip = (size_t)tile_step * blocks * 2 - (size_t)again * kScaleStep;
     const int odd = e0 & 1;  // stages and tiles advance by even counts
     auto copy = [&]() {
         if (left > 0) {
@@ -251,7 +260,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
             if (dst == ring_end) dst = ring;
             --left;
             if (++p_stage == w1) {
-                p_stage = w0;
+                p_stage = MT == 2 ? 0 : w0;
                 p_n += tile_step;
                 src += tile_skip;
                 ssrc += scale_skip;
@@ -328,8 +337,8 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     }
     __syncthreads();
 
-    const uint32_t x0 = smem_addr(xs) + lane * 16 + (w0 - s0) * NT * 2048, la = smem_addr(lut) + lane * 8;
-    const uint32_t z0 = smem_addr(starts) + (w0 - s0) * (kFine ? 4 : 2) * NT * 64 + t * 16;
+    const uint32_t x0 = smem_addr(xs) + lane * 16, la = smem_addr(lut) + lane * 8;
+    const uint32_t z0 = smem_addr(starts) + t * 16;
     const uint32_t mask = 0x00780078u, bias = 0x41804180u;
     // word wi of half hf of row g (+ 8): piece 2 hf + wi, word t
     uint32_t piece[4];
@@ -340,156 +349,219 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     const uint32_t g_odd = uint32_t(g) * blocks;
     uint32_t sel[2] = {g_odd & 1 ? kHigh : kLow, g_odd & 1 ? kLow : kHigh};  // q_block 32 or 64
     uint32_t at = ring;
-    for (int k = 0; k < my_tiles; ++k) {
-        const int n0 = (group + k * groups) * wide;
-        float acc[MT][NT][4];
+    // Adds stage st (counted from the row's start) of the outputs in hand.
+    auto stage = [&](int st, float (&acc)[MT][NT][4]) {
+        const uint32_t xa = x0 + (st - s0) * (NT * 2048), za = z0 + (st - s0) * ((kFine ? 4 : 2) * NT * 64);
+        copy();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        __syncwarp();
+        if (!kFine && shift > 0) sel[0] = sel[1] = (g_odd + ((st * 2) >> shift)) & 1 ? kHigh : kLow;
+        float sc[MT][2][4];  // [strip][row g, g + 8][block of the stage]
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t sa = at + V::kCodes + (i * kStrip + g + 8 * r) * V::kScalesRow * 4;
+                if (kFine) {
+                    const uint4 v = lds128(sa);
+                    sc[i][r][0] = half_of(v.x, sel[0]);
+                    sc[i][r][1] = half_of(v.y, sel[1]);
+                    sc[i][r][2] = half_of(v.z, sel[0]);
+                    sc[i][r][3] = half_of(v.w, sel[1]);
+                } else {
+                    const uint2 v = lds64(sa);
+                    sc[i][r][0] = half_of(v.x, sel[0]);
+                    sc[i][r][1] = half_of(v.y, sel[1]);
+                }
+            }
+        float c[MT][NT][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // 32 inputs: word q & 1 of half q / 2
+            const int block = kFine ? q : q / 2;
+            const bool first = kFine || (q & 1) == 0, last = kFine || (q & 1) == 1;
+            uint32_t p[MT][2][4], lo[MT][2][4];  // [strip][row][pair]; lo: the low parts of a table's values
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t v = lds32(at + piece[q] + (i * kStrip + 8 * r) * kRowBytes);
+                    if (kAffine) {
+                        p[i][r][0] = code_pair(v << 3, mask, bias);
+                        p[i][r][1] = code_pair(v >> 1, mask, bias);
+                        p[i][r][2] = code_pair(v >> 5, mask, bias);
+                        p[i][r][3] = code_pair(v >> 9, mask, bias);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint2 h = lds64(la + ((v >> (8 * b)) & 255u) * 256);
+                            p[i][r][b] = h.x;
+                            lo[i][r][b] = h.y;
+                        }
+                    }
+                }
+            uint4 x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] = lds128(xa + (((q >> 1) * NT + n) * 2 + (q & 1)) * 512);
+            // products on one accumulator are kept apart: each waits for the one before
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                if (kAffine && first) z = lds128(za + (block * NT + n) * 64);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if (first)
+                        mma16816_from(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y, z);
+                    else
+                        mma16816(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    mma16816(c[i][n], p[i][0][2], p[i][1][2], p[i][0][3], p[i][1][3], x[n].z, x[n].w);
+            if (!kAffine) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma16816(c[i][n], lo[i][0][0], lo[i][1][0], lo[i][0][1], lo[i][1][1], x[n].x, x[n].y);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma16816(c[i][n], lo[i][0][2], lo[i][1][2], lo[i][0][3], lo[i][1][3], x[n].z, x[n].w);
+            }
+            if (last) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][n][e] = fmaf(sc[i][e >> 1][block], c[i][n][e], acc[i][n][e]);
+            }
+        }
+        at += kStage;
+        if (at == ring_end) at = ring;
+        __syncwarp();  // the stage is read before the next copy lands in it
+    };
+    auto clear = [](float (&acc)[MT][NT][4]) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
-        uint32_t xa = x0, za = z0;
-        for (int st = w0; st < w1; ++st, xa += NT * 2048, za += (kFine ? 4 : 2) * NT * 64) {
-            copy();
-            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-            __syncwarp();
-            if (!kFine && shift > 0) sel[0] = sel[1] = (g_odd + ((st * 2) >> shift)) & 1 ? kHigh : kLow;
-            float sc[MT][2][4];  // [strip][row g, g + 8][block of the stage]
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t sa = at + V::kCodes + (i * kStrip + g + 8 * r) * V::kScalesRow * 4;
-                    if (kFine) {
-                        const uint4 v = lds128(sa);
-                        sc[i][r][0] = half_of(v.x, sel[0]);
-                        sc[i][r][1] = half_of(v.y, sel[1]);
-                        sc[i][r][2] = half_of(v.z, sel[0]);
-                        sc[i][r][3] = half_of(v.w, sel[1]);
-                    } else {
-                        const uint2 v = lds64(sa);
-                        sc[i][r][0] = half_of(v.x, sel[0]);
-                        sc[i][r][1] = half_of(v.y, sel[1]);
-                    }
-                }
-            float c[MT][NT][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 32 inputs: word q & 1 of half q / 2
-                const int block = kFine ? q : q / 2;
-                const bool first = kFine || (q & 1) == 0, last = kFine || (q & 1) == 1;
-                uint32_t p[MT][2][4], lo[MT][2][4];  // [strip][row][pair]; lo: the low parts of a table's values
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t v = lds32(at + piece[q] + (i * kStrip + 8 * r) * kRowBytes);
-                        if (kAffine) {
-                            p[i][r][0] = code_pair(v << 3, mask, bias);
-                            p[i][r][1] = code_pair(v >> 1, mask, bias);
-                            p[i][r][2] = code_pair(v >> 5, mask, bias);
-                            p[i][r][3] = code_pair(v >> 9, mask, bias);
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const uint2 h = lds64(la + ((v >> (8 * b)) & 255u) * 256);
-                                p[i][r][b] = h.x;
-                                lo[i][r][b] = h.y;
-                            }
-                        }
-                    }
-                uint4 x[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) x[n] = lds128(xa + (((q >> 1) * NT + n) * 2 + (q & 1)) * 512);
-                // products on one accumulator are kept apart: each waits for the one before
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    if (kAffine && first) z = lds128(za + (block * NT + n) * 64);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        if (first)
-                            mma16816_from(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y, z);
-                        else
-                            mma16816(c[i][n], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], x[n].x, x[n].y);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        mma16816(c[i][n], p[i][0][2], p[i][1][2], p[i][0][3], p[i][1][3], x[n].z, x[n].w);
-                if (!kAffine) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            mma16816(c[i][n], lo[i][0][0], lo[i][1][0], lo[i][0][1], lo[i][1][1], x[n].x, x[n].y);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            mma16816(c[i][n], lo[i][0][2], lo[i][1][2], lo[i][0][3], lo[i][1][3], x[n].z, x[n].w);
-                }
-                if (last) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[i][n][e] = fmaf(sc[i][e >> 1][block], c[i][n][e], acc[i][n][e]);
-                }
-            }
-            at += kStage;
-            if (at == ring_end) at = ring;
-            __syncwarp();  // the stage is read before the next copy lands in it
-        }
-        // the warps' sums, [column][output]; lane (g, t): outputs g and g + 8 of columns 2 t, 2 t + 1
-        if (k > 0) __syncthreads();  // the tile before has been read
-        float *rb = red + (warp * kCols + 2 * t) * kRedStride + g;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
+    };
+    if constexpr (MT == 2) {
+        // A pair that one warp has whole goes out from its registers.  Of a pair that several share,
+        // the one that begins it keeps its sums (they are its last), the others leave theirs in
+        // `red`, and it adds those in order after the CTA's only barrier.
+        float acc[MT][NT][4];
+        auto emit_pair = [&](int n0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    rb[(n * 8 + (e & 1)) * kRedStride + i * kStrip + 8 * (e >> 1)] = acc[i][n][e];
-        __syncthreads();
-        float *pb = part + (k & 1) * kCols * wide;
-        auto emit = [&](int row, int n, float y) {
-            n += n0;
-            if (row < rows && n < N) q4_emit(a, T0 + row, n, y * m.step);
+                for (int c = 0; c < 2; ++c) {
+                    const int row = n * 8 + 2 * t + c;
+                    if (row >= rows) continue;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int o = n0 + i * kStrip + 8 * r + g;
+                            if (o < N) q4_emit(a, T0 + row, o, acc[i][n][2 * r + c] * m.step);
+                        }
+                }
         };
-        // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part.
-        // Threads are a multiple of the tile's outputs: a thread keeps its output, rows go by.
-        {
-            const uint32_t n = tid & (wide - 1), rows_step = kThreads >> wide_log2;
-            const int cols = m.slices == 1 ? rows : kCols;
-            const float *rr = red + (n / kOut * kCols) * kRedStride + n % kOut;
-            const int part_step = m.side * kCols * kRedStride;
-            for (int row = tid >> wide_log2; row < cols; row += rows_step) {
-                float y = rr[row * kRedStride];
-                for (int w = 1; w < parts; ++w) y += rr[row * kRedStride + w * part_step];
-                if (m.slices == 1)
-                    emit(row, int(n), y);
-                else
-                    pb[row * wide + n] = y;
+        int pending = -1, done = 0;  // the pair begun and not ended, and its stages
+        for (int u = u0; u < u1;) {
+            const int pair = u / stages, st0 = u - pair * stages, st1 = min(stages, st0 + u1 - u);
+            clear(acc);
+            for (int st = st0; st < st1; ++st) stage(st, acc);
+            if (st0 > 0) {
+                float4 *to = reinterpret_cast<float4 *>(red) + warp * (MT * NT * 32) + lane;
+#pragma unroll
+                for (int i = 0; i < MT * NT; ++i) {
+                    const float *v = acc[i / NT][i % NT];
+                    to[i * 32] = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            } else if (st1 == stages) {
+                emit_pair((pair0 + pair) * kOut);
+            } else {
+                pending = pair;
+                done = st1;
+            }
+            u += st1 - st0;
+        }
+        __syncthreads();
+        if (pending < 0) return;
+        for (int w = warp + 1; done < stages; ++w) {
+            const int theirs = line_at(w + 1) - line_at(w);
+            if (theirs == 0) continue;
+            const float4 *from = reinterpret_cast<const float4 *>(red) + w * (MT * NT * 32) + lane;
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) {
+                const float4 v = from[i * 32];
+                float *to = acc[i / NT][i % NT];
+                to[0] += v.x, to[1] += v.y, to[2] += v.z, to[3] += v.w;
+            }
+            done += theirs;
+        }
+        emit_pair((pair0 + pending) * kOut);
+    } else {
+        for (int k = 0; k < my_tiles; ++k) {
+            const int n0 = (group + k * groups) * wide;
+            float acc[MT][NT][4];
+            clear(acc);
+            for (int st = w0; st < w1; ++st) stage(st, acc);
+            // the warps' sums, [column][output]; lane (g, t): outputs g and g + 8 of columns 2 t, 2 t + 1
+            if (k > 0) __syncthreads();  // the tile before has been read
+            float *rb = red + (warp * kCols + 2 * t) * kRedStride + g;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        rb[(n * 8 + (e & 1)) * kRedStride + i * kStrip + 8 * (e >> 1)] = acc[i][n][e];
+            __syncthreads();
+            float *pb = part + (k & 1) * kCols * wide;
+            auto emit = [&](int row, int n, float y) {
+                n += n0;
+                if (row < rows && n < N) q4_emit(a, T0 + row, n, y * m.step);
+            };
+            // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part.
+            // Threads are a multiple of the tile's outputs: a thread keeps its output, rows go by.
+            {
+                const uint32_t n = tid & (wide - 1), rows_step = kThreads >> wide_log2;
+                const int cols = m.slices == 1 ? rows : kCols;
+                const float *rr = red + (n / kOut * kCols) * kRedStride + n % kOut;
+                const int part_step = m.side * kCols * kRedStride;
+                for (int row = tid >> wide_log2; row < cols; row += rows_step) {
+                    float y = rr[row * kRedStride];
+                    for (int w = 1; w < parts; ++w) y += rr[row * kRedStride + w * part_step];
+                    if (m.slices == 1)
+                        emit(row, int(n), y);
+                    else
+                        pb[row * wide + n] = y;
+                }
+            }
+            if (m.slices > 1) {
+                // each CTA of the cluster adds the slices of its part of the outputs, in order; the
+                // other buffer is written meanwhile, so one barrier a tile is enough
+                cg::cluster_group cl = cg::this_cluster();
+                cl.sync();
+                for (int idx = slice * kThreads + tid; idx < kCols * wide; idx += m.slices * kThreads) {
+                    float y = 0.f;
+                    for (int r = 0; r < m.slices; ++r) y += *cl.map_shared_rank(pb + idx, r);
+                    emit(idx >> wide_log2, idx & (wide - 1), y);
+                }
             }
         }
-        if (m.slices > 1) {
-            // each CTA of the cluster adds the slices of its part of the outputs, in order; the
-            // other buffer is written meanwhile, so one barrier a tile is enough
-            cg::cluster_group cl = cg::this_cluster();
-            cl.sync();
-            for (int idx = slice * kThreads + tid; idx < kCols * wide; idx += m.slices * kThreads) {
-                float y = 0.f;
-                for (int r = 0; r < m.slices; ++r) y += *cl.map_shared_rank(pb + idx, r);
-                emit(idx >> wide_log2, idx & (wide - 1), y);
-            }
-        }
+        if (m.slices > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
     }
-    if (m.slices > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
 
 template <int NT, int MT, bool kFine, bool kAffine>
@@ -511,12 +583,14 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     if (stages > V::max_stages()) slices = 2;
     while (slices > 1 && (stages + slices - 1) / slices > V::max_stages_sliced()) slices *= 2;
     const int passes = (m.a.T + m.pass_rows - 1) / m.pass_rows;
-    while (slices < kMaxSlices && (int64_t)strips * passes * slices * 2 <= sms * 2 && stages >= slices * 2 * V::kWarps) slices *= 2;
-    // strips side by side: when there are plenty, each warp takes a longer part of the inputs, and
-    // the sums over the parts cost less
-    m.slices = slices;
     m.side = 1;
-    while (m.side < V::kWarps && strips * slices >= sms * 2 * m.side * 2 * (MT == 2 ? 2 : 1) && stages / slices < 4 * V::kWarps / m.side) m.side *= 2;
+    if (MT == 1) {
+        while (slices < kMaxSlices && (int64_t)strips * passes * slices * 2 <= sms * 2 && stages >= slices * 2 * V::kWarps) slices *= 2;
+        // strips side by side: when there are plenty, each warp takes a longer part of the inputs, and
+        // the sums over the parts cost less
+        while (m.side < V::kWarps && strips * slices >= sms * 2 * m.side * 2 && stages / slices < 4 * V::kWarps / m.side) m.side *= 2;
+    }
+    m.slices = slices;
     m.tiles = (strips + m.side - 1) / m.side;
     m.slice_halves = 2 * ((stages + slices - 1) / slices);
     const int smem = V::kFixed + m.slice_halves * V::kHalf + (slices > 1 ? V::part_bytes(m.side) : 0);

@@ -62,6 +62,21 @@ struct TileAt {
 };
 __device__ __forceinline__ TileAt find_tile(const Args &a, int tile, int tokens_per_tile, int *scratch) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarp = (blockDim.x + 31) >> 5;
+    if (a.n_seqs <= 32) {  // every warp for itself, without barriers
+        int n = 0;
+        if (lane < a.n_seqs) {
+            const int c0 = min(max(ldp(a.cu_q + lane), 0), a.n_tokens), c1 = min(max(ldp(a.cu_q + lane + 1), 0), a.n_tokens);
+            n = (max(c1 - c0, 0) + tokens_per_tile - 1) / tokens_per_tile;
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const int b = __ffs(__ballot_sync(0xffffffffu, tile < incl)) - 1;
+        return {b, tile - __shfl_sync(0xffffffffu, incl - n, max(b, 0))};
+    }
     if (tid == 0) scratch[0] = -1;
     int base = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += blockDim.x) {

@@ -42,7 +42,7 @@ int smem_bytes(int D) { return (kRows * D + kKeys * (D + 4) + kKeys * D + 4 * kK
 
 // NJ: output elements of a lane, head_dim <= 32 NJ.
 template <typename T, int NJ>
-__global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part, int tt) {
+__global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args a, Partials part, int tt) {
     extern __shared__ float4 smem4[];
     __shared__ int scratch[4 + kThreads / 32];
     griddep_wait();
@@ -59,15 +59,6 @@ __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part
     const int gw = min(a.group - g0, kRows);  // heads of the group in this block
     const int j0 = at.tile * tt, nj = min(tt, s.q_len - j0), rows = nj * gw;
     const int past = s.kv_len - s.q_len;
-
-    for (int i = tid; i < rows * (D / 8); i += kThreads) {
-        const int r = i / (D / 8), c = i % (D / 8) * 8;
-        float v[8];
-        ldp8(static_cast<const T *>(a.q) + (s.q0 + j0 + r / gw) * a.q_stride + (int64_t)(hk * a.group + g0 + r % gw) * D + c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) Q[r * D + c + e] = v[e] * (a.scale * kLog2e);
-    }
-    for (int i = rows * D + tid; i < kRows * D; i += kThreads) Q[i] = 0.f;
 
     // keys seen by each of the warp's rows, and by the block
     int seen[4];
@@ -86,44 +77,71 @@ __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part
     const int64_t k_begin = (int64_t)blockIdx.z * per;
     const int k_end = int(min(k_begin + per, (int64_t)keys));
 
+    // Tiles of keys: pieces of eight elements.  Small heads request the next tile before they work on
+    // the one in hand, larger ones (which would not have the registers) two rounds of a tile at a time.
+    constexpr int kRounds = (kKeys * NJ * 4 + kThreads - 1) / kThreads, kFly = kRounds < 2 ? kRounds : 2;
+    constexpr bool kAhead = kFly == kRounds;
+    const int pieces = D / 8;
+    float kv[kFly][8], vv[kFly][8];
+    // the cache offset of key lane, in every warp; slots past the last visible key are not read: they
+    // may hold anything
+    auto find_key = [&](int64_t k0) {
+        const int64_t p = k0 + lane;
+        if (p >= keys) return (int64_t)-1;
+        const int pi = a.page_shift >= 0 ? int(p) >> a.page_shift : int(p) / a.page_size;
+        return load_page(a, at.b, pi) * a.page_stride + hk * a.head_stride + (int64_t)(int(p) - pi * a.page_size) * a.token_stride;
+    };
+    auto load = [&](int64_t key_off, int i0) {
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
+            const int64_t off = __shfl_sync(0xffffffffu, key_off, kk & 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kv[i][e] = vv[i][e] = 0.f;
+            if (kk < kKeys && off >= 0) {
+                ldp8(static_cast<const T *>(a.k) + off + c, kv[i]);
+                ldp8(static_cast<const T *>(a.v) + off + c, vv[i]);
+            }
+        }
+    };
+    auto store = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
+            if (kk >= kKeys) continue;
+            // K rows are D + 4 floats apart, V rows D: both multiples of 16 bytes
+            store8(K + kk * (D + 4) + c, kv[i]);
+            store8(V + kk * D + c, vv[i]);
+        }
+    };
+    if (kAhead && k_begin < k_end) load(find_key(k_begin), 0);
+
+    // the rows of q, scaled, while those loads are in flight
+    for (int i = tid; i < rows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8) * 8;
+        float v[8];
+        ldp8(static_cast<const T *>(a.q) + (s.q0 + j0 + r / gw) * a.q_stride + (int64_t)(hk * a.group + g0 + r % gw) * D + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) Q[r * D + c + e] = v[e] * (a.scale * kLog2e);
+    }
+    for (int i = rows * D + tid; i < kRows * D; i += kThreads) Q[i] = 0.f;
+
     for (int64_t kb = k_begin; kb < k_end; kb += kKeys) {
-        __syncthreads();
         const int k0 = int(kb);
-        // the cache offset of key lane, in every warp; slots past the last visible key are not read:
-        // they may hold anything
-        int64_t key_off = -1;
-        if (k0 + lane < keys) {
-            const int p = k0 + lane, pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
-            key_off = load_page(a, at.b, pi) * a.page_stride + hk * a.head_stride +
-                      (int64_t)(p - pi * a.page_size) * a.token_stride;
-        }
-        // pieces of eight elements, two rounds' loads in flight
-        constexpr int kRounds = (kKeys * NJ * 4 + kThreads - 1) / kThreads, kFly = kRounds < 2 ? kRounds : 2;
-        const int pieces = D / 8;
+        if (kAhead) {
+            __syncthreads();  // the tile before has been read
+            store(0);
+        } else {
+            const int64_t key_off = find_key(kb);
+            __syncthreads();
 #pragma unroll
-        for (int i0 = 0; i0 < kRounds; i0 += kFly) {
-            float kv[kFly][8], vv[kFly][8];
-#pragma unroll
-            for (int i = 0; i < kFly; ++i) {
-                const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
-                const int64_t off = __shfl_sync(0xffffffffu, key_off, kk & 31);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) kv[i][e] = vv[i][e] = 0.f;
-                if (kk < kKeys && off >= 0) {
-                    ldp8(static_cast<const T *>(a.k) + off + c, kv[i]);
-                    ldp8(static_cast<const T *>(a.v) + off + c, vv[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kFly; ++i) {
-                const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
-                if (kk >= kKeys) continue;
-                // K rows are D + 4 floats apart, V rows D: both multiples of 16 bytes
-                store8(K + kk * (D + 4) + c, kv[i]);
-                store8(V + kk * D + c, vv[i]);
+            for (int i0 = 0; i0 < kRounds; i0 += kFly) {
+                load(key_off, i0);
+                store(i0);
             }
         }
         __syncthreads();
+        if (kAhead && kb + kKeys < k_end) load(find_key(kb + kKeys), 0);
         if (warp * 4 >= rows) continue;  // this warp only helps to load
         float sc[4] = {0.f, 0.f, 0.f, 0.f};
         for (int d = 0; d < D; d += 4) {
@@ -152,6 +170,7 @@ __global__ void __launch_bounds__(kThreads) generic_kernel(Args a, Partials part
         }
         *reinterpret_cast<float4 *>(P + lane * 4) = make_float4(pr[0], pr[1], pr[2], pr[3]);
         __syncwarp();
+#pragma unroll 8
         for (int kk = 0; kk < kKeys; ++kk) {
             const float4 p4 = *reinterpret_cast<const float4 *>(P + kk * 4);
 #pragma unroll
@@ -201,11 +220,18 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part
     if (row >= rows) return;
     const int t = int(row / a.n_heads), head = int(row % a.n_heads);
     if (t < ldp(a.cu_q) || t >= ldp(a.cu_q + a.n_seqs)) return;  // a padding row
+    constexpr int kFly = 8;  // parts requested together; every part holds finite values (zeros for no keys)
+    float4 v[kFly];
+    auto load = [&](int d, int p0) {
+#pragma unroll
+        for (int p = 0; p < kFly; ++p) v[p] = ldp16f(part.o + (min(p0 + p, part.parts - 1) * rows + row) * D + d);
+    };
     float2 ml = make_float2(kNegInf, 0.f);  // lane p: part p (at most 32)
     if (lane < part.parts) {
         const float *p = reinterpret_cast<const float *>(part.ml + lane * rows + row);
         ml = make_float2(ldp(p), ldp(p + 1));
     }
+    load(min(lane * 4, D - 4), 0);
     float m = ml.x;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
@@ -213,14 +239,11 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part
     const float l = warp_sum(ml.y * f);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T *dst = static_cast<T *>(a.out) + t * a.out_stride + (int64_t)head * D;
-    constexpr int kFly = 8;  // parts requested together; every part holds finite values (zeros for no keys)
     for (int d0 = 0; d0 < D; d0 += 128) {
         const int d = min(d0 + lane * 4, D - 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p0 = 0; p0 < part.parts; p0 += kFly) {
-            float4 v[kFly];
-#pragma unroll
-            for (int p = 0; p < kFly; ++p) v[p] = ldp16f(part.o + (min(p0 + p, part.parts - 1) * rows + row) * D + d);
+            if (d0 + p0 > 0) load(d, p0);
 #pragma unroll
             for (int p = 0; p < kFly; ++p) {
                 const float fp = p0 + p < 32 ? __shfl_sync(0xffffffffu, f, (p0 + p) & 31) : 0.f;  // 0 past the last

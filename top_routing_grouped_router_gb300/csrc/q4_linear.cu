@@ -621,6 +621,7 @@ struct Rows {  // the variants by rows of x
         const int s = (stages + kMaxSlices - 1) / kMaxSlices;
         return s <= (nt == 1 ? Var<1, 1, kFine, kAffine>::max_stages_sliced() : Var<2, 1, kFine, kAffine>::max_stages_sliced());
     }
+    static int two_fit(int nt) { return nt == 1 ? Var<1, 2, kFine, kAffine>::max_stages() : Var<2, 2, kFine, kAffine>::max_stages(); }
     template <int NT>
     static cudaError_t launch_nt(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
         // two strips a warp where there are plenty and x fits one CTA
@@ -655,6 +656,10 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
     };
+    auto two_fit = [&](int nt) {  // the most stages of two strips a warp
+        return affine ? (fine ? Rows<true, true>::two_fit(nt) : Rows<false, true>::two_fit(nt))
+                      : (fine ? Rows<true, false>::two_fit(nt) : Rows<false, false>::two_fit(nt));
+    };
     int nt_max = 2;
     while (nt_max > 0 && !fits(nt_max)) nt_max /= 2;
     if (nt_max == 0) return false;
@@ -663,6 +668,9 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     m.step = affine ? step : 1.f;
     while (!fine && (64 << m.shift) < a.q_block) ++m.shift;
     m.centre = 16.f + 0.5f * float(twice);
+    // where only 8 rows of x leave room for two strips a warp, passes of 8 (16 x 2048 x 131072 with a
+    // general codebook: 102 us, 128 in one pass)
+    if (nt_max == 2 && a.N >= two_strips_from(sms) && two_fit(2) < stages && two_fit(1) >= stages) nt_max = 1;
     m.pass_rows = a.T <= 8 ? 8 : nt_max * 8;
     *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
                   : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));

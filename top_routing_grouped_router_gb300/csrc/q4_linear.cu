@@ -612,8 +612,10 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, MT, kFine, kAffine>, m);
 }
 
-// Outputs from which every SM gets at least eight pairs of strips.
-int two_strips_from(int sms) { return sms * 8 * 2 * kStrip; }
+// Whether warps take two strips: outputs for so many that every SM gets four pairs, or two where x has
+// more than 8 rows (us with one strip and with two: 1 x 4096 x 10240 11.6, 13.5; 1 x 2048 x 20480 11.6,
+// 10.2; 8 x 2048 x 20480 13.7, 10.5; 16 x 2048 x 10240 13.5, 10.6).
+bool many(int64_t outputs, int sms, int nt) { return outputs >= (int64_t)sms * (nt == 2 ? 2 : 4) * 2 * kStrip; }
 
 template <bool kFine, bool kAffine>
 struct Rows {  // the variants by rows of x
@@ -625,7 +627,8 @@ struct Rows {  // the variants by rows of x
     template <int NT>
     static cudaError_t launch_nt(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
         // two strips a warp where there are plenty and x fits one CTA
-        const bool two = m.a.N >= two_strips_from(sms) && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
+        const int passes = (m.a.T + m.pass_rows - 1) / m.pass_rows;
+        const bool two = many((int64_t)m.a.N * passes, sms, NT) && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
         return two ? launch_mma<NT, 2, kFine, kAffine>(m, stages, sms, st) : launch_mma<NT, 1, kFine, kAffine>(m, stages, sms, st);
     }
     static cudaError_t launch(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
@@ -643,22 +646,26 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
-    // tcgen05 for more than 8 rows where the weights are large enough that its longer start does not
-    // count (us, tcgen05 and mma.sync): 12 x 2048 x 2048 7.7, 7.7; 64 x 2048 x 2048 14.6, 11.6; 40 x 512 x
-    // 20000 18.0, 15.1; 16 x 4096 x 5120 13.9, 18.7; 32 x 4096 x 5120 17.3, 25.0; 64 x 4096 x 10240 54, 69.  Up to
-    // 16 rows not where mma.sync takes two strips a warp: 16 x 2048 x 131072 57, 54.
+    auto two_fit = [&](int nt) {  // the most stages of two strips a warp
+        return affine ? (fine ? Rows<true, true>::two_fit(nt) : Rows<false, true>::two_fit(nt))
+                      : (fine ? Rows<true, false>::two_fit(nt) : Rows<false, false>::two_fit(nt));
+    };
+    // where only 8 rows of x leave room for two strips a warp, passes of 8 (us in one pass and in two: 16 x
+    // 4096 x 10240 24.9, 18.7; 16 x 2048 x 131072 with a general codebook 128, 102)
+    const bool eights = a.T > 8 && two_fit(2) < stages && two_fit(1) >= stages && many((int64_t)a.N * ((a.T + 7) / 8), sms, 1);
+    // tcgen05 for more rows than one pass where the weights are large enough that its longer start does
+    // not count (us, tcgen05 and mma.sync): 64 x 2048 x 2048 14.6, 11.6; 40 x 512 x 20000 18.0, 15.1; 32 x 4096 x
+    // 5120 17.3, 25.0; 64 x 4096 x 10240 54, 69.  For one pass of more than 8 rows only where neither side
+    // of it has room for two strips: 16 x 2048 x 5120 10.2, 10.1; 16 x 4096 x 5120 13.9, 18.5; 16 x 8192 x 10240
+    // 42, 52.
     const int64_t weights = (int64_t)a.N * a.K;
     const bool large = (a.K >= 2048 && weights >= (1 << 23)) || weights >= (1 << 26);
-    if (affine && !fine && large && a.T > 8 && (a.T > kMmaRows || a.N < two_strips_from(sms)) &&
+    if (affine && !fine && large && (a.T > kMmaRows || (a.T > 8 && two_fit(2) < stages && !eights)) &&
         run_tc(a, step, twice, sms, st, err))
         return true;
     auto fits = [&](int nt) {
         return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
                       : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
-    };
-    auto two_fit = [&](int nt) {  // the most stages of two strips a warp
-        return affine ? (fine ? Rows<true, true>::two_fit(nt) : Rows<false, true>::two_fit(nt))
-                      : (fine ? Rows<true, false>::two_fit(nt) : Rows<false, false>::two_fit(nt));
     };
     int nt_max = 2;
     while (nt_max > 0 && !fits(nt_max)) nt_max /= 2;
@@ -668,9 +675,7 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     m.step = affine ? step : 1.f;
     while (!fine && (64 << m.shift) < a.q_block) ++m.shift;
     m.centre = 16.f + 0.5f * float(twice);
-    // where only 8 rows of x leave room for two strips a warp, passes of 8 (16 x 2048 x 131072 with a
-    // general codebook: 102 us, 128 in one pass)
-    if (nt_max == 2 && a.N >= two_strips_from(sms) && two_fit(2) < stages && two_fit(1) >= stages) nt_max = 1;
+    if (eights) nt_max = std::min(nt_max, 1);
     m.pass_rows = a.T <= 8 ? 8 : nt_max * 8;
     *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
                   : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));

@@ -24,8 +24,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 320;   // warps 0-3, 4-7: softmax of tile 0, 1; warp 8: MMA; warp 9: loads
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMA, loads, the list of segments, one
+// spare.  It gives up registers that the softmax takes: 8 x 32 x 208 + 4 x 32 x 72 is within the launch's
+// 12 x 32 x 168.
+constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 72;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "");
 constexpr int kM = 128, kKeys = 128;
 constexpr int kMaxCtas = 160;   // one per SM (152)
 constexpr int kMaxSegs = 16;    // segments prepared at a time
@@ -226,6 +230,16 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t p, uint64_t v, uint32
         : "memory");
 }
 
+// The block's barrier where its warps are in different code, and its form that ORs a value.
+__device__ __forceinline__ void meet() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ bool meet_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(uint32_t(v)), "n"(kThreads) : "memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -398,227 +412,250 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
 
     // ---------------------------------------------------------------- roles
-    int stage = 0;                      // ring position: load and MMA warps
-    uint32_t phase = 0;
-    uint32_t q_phase = 0, s_phase = 0, o_phase = 0;
-    uint32_t p_phase = 0, oe_phase = 3;  // bit t: tile t
-    uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
-    bool ok = true;
-
-    for (uint32_t u = u_begin; u < u_end && ok;) {
-        // up to kMaxSegs segments, found by warp 0
-        if (warp == 0) {
-            int b = int(cursor[0]);
-            uint32_t first = cursor[1], per_head = cursor[2], w = cursor[3];
-            Seq s = *cur_seq;
-            int k = 0;
-            uint32_t h = 0, i = 0, item0 = 0;
-            bool located = false;
-            while (w < u_end && k < kMaxSegs) {
-                if (!located) {
-                    while (w - first >= per_head * Hkv) {  // the next sequence with a chunk
-                        first += per_head * Hkv;
-                        if (++b >= a.n_seqs) break;  // not seen: the line ends with the last sequence
-                        s = load_seq(a, b);
-                        per_head = seq_places(s);
-                    }
-                    if (b >= a.n_seqs) {
-                        w = u_end;
-                        break;
-                    }
-                    h = (w - first) / per_head;
-                    const uint32_t rem = w - first - h * per_head;
-                    // the last item that begins at or before rem: 32 candidates a round
-                    uint32_t lo = 0, n = items_of(s, it), at_lo = 0;
-                    while (n > 1) {
-                        const uint32_t each = (n + 31) / 32, cand = lo + lane * each;
-                        const uint32_t before = lane * each < n ? places_before(s, cand, it, c.whole) : ~0u;
-                        const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, before <= rem));
-                        at_lo = __shfl_sync(0xffffffffu, before, last);
-                        lo += last * each;
-                        n = min(each, n - last * each);
-                    }
-                    i = lo;
-                    item0 = first + h * per_head + at_lo;
-                    located = true;
+    // the next segments, up to kMaxSegs, by one warp
+    auto list = [&]() {
+        int b = int(cursor[0]);
+        uint32_t first = cursor[1], per_head = cursor[2], w = cursor[3];
+        Seq s = *cur_seq;
+        int k = 0;
+        uint32_t h = 0, i = 0, item0 = 0;
+        bool located = false;
+        while (w < u_end && k < kMaxSegs) {
+            if (!located) {
+                while (w - first >= per_head * Hkv) {  // the next sequence with a chunk
+                    first += per_head * Hkv;
+                    if (++b >= a.n_seqs) break;  // not seen: the line ends with the last sequence
+                    s = load_seq(a, b);
+                    per_head = seq_places(s);
                 }
-                const uint32_t steps = item_steps(s, i, it), setup = c.whole ? 0 : kSetup;
-                const uint32_t places = c.whole ? 1 : steps + kSetup, end = min(item0 + places, u_end);
-                // steps begin after the item's setup; a share that ends within it leaves the item to the next
-                const uint32_t from = max(w, item0 + setup);
-                const bool starts = from == item0 + setup, whole = starts && end == item0 + places;
-                if (from < end) {
-                    if (lane == 0) {
-                        Seg g;
-                        g.b = b;
-                        g.h = int(h);
-                        g.tok0 = int(i * tt2);
-                        g.q0 = s.q0;
-                        g.q_len = s.q_len;
-                        g.kv_len = s.kv_len;
-                        g.step0 = int(from - item0 - setup);
-                        g.step1 = c.whole ? int(steps) : int(end - item0 - setup);
-                        g.slot = whole ? -1 : int(cta * 2 + (starts ? 1 : 0));
-                        g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
-                        segs[k] = g;
-                        if (!whole && starts) {
-                            const int last = int(sh.owner(item0 + places - 1));
-                            c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len};
-                        }
-                    }
-                    ++k;
-                }
-                w = end;
-                if (end == item0 + places) {
-                    item0 += places;
-                    if (++i == items_of(s, it)) {
-                        i = 0;
-                        ++h;
-                        if (h == Hkv) located = false;  // the next sequence
-                    }
-                }
-            }
-            if (lane == 0) {
-                *nseg = k;
-                cursor[0] = b;
-                cursor[1] = first;
-                cursor[2] = per_head;
-                cursor[3] = w;
-                *cur_seq = s;
-            }
-        }
-        __syncthreads();
-        const int ns = *nseg;
-        u = cursor[3];
-
-        if (warp == kLoadWarp) {
-            // ------------------------------------------------ loads
-            const int ps = a.page_size, box = min(ps, kKeys);
-            for (int k = 0; k < ns && ok; ++k) {
-                const Seg g = segs[k];
-                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
-                const int boxes_max = kKeys / box;
-                auto page_of = [&](int step) {  // lane i: the page of box i of the step
-                    const int p = step * kKeys + lane * box;
-                    return lane < boxes_max && p < keys ? load_page(a, g.b, p / ps) : -1;
-                };
-                int page = page_of(g.step0);
-                ok = mbar_wait(smem_u32(q_empty), q_phase ^ 1, wt);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
+                if (b >= a.n_seqs) {
+                    w = u_end;
                     break;
                 }
+                h = (w - first) / per_head;
+                const uint32_t rem = w - first - h * per_head;
+                // the last item that begins at or before rem: 32 candidates a round
+                uint32_t lo = 0, n = items_of(s, it), at_lo = 0;
+                while (n > 1) {
+                    const uint32_t each = (n + 31) / 32, cand = lo + lane * each;
+                    const uint32_t before = lane * each < n ? places_before(s, cand, it, c.whole) : ~0u;
+                    const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, before <= rem));
+                    at_lo = __shfl_sync(0xffffffffu, before, last);
+                    lo += last * each;
+                    n = min(each, n - last * each);
+                }
+                i = lo;
+                item0 = first + h * per_head + at_lo;
+                located = true;
+            }
+            const uint32_t steps = item_steps(s, i, it), setup = c.whole ? 0 : kSetup;
+            const uint32_t places = c.whole ? 1 : steps + kSetup, end = min(item0 + places, u_end);
+            // steps begin after the item's setup; a share that ends within it leaves the item to the next
+            const uint32_t from = max(w, item0 + setup);
+            const bool starts = from == item0 + setup, whole = starts && end == item0 + places;
+            if (from < end) {
                 if (lane == 0) {
-                    const int rows = int(G * tt);
-                    mbar_arrive_expect_tx(smem_u32(q_full), uint32_t(g.tiles * rows * D * 2));
-                    for (int t = 0; t < g.tiles; ++t)
-                        for (int d = 0; d < kSlabs; ++d)
-                            tma_load_3d(smem_u32(smem + t * C::kTile + d * kM * 128), &map_q, d * 64, int(g.h * G),
-                                        g.q0 + g.tok0 + t * int(tt), smem_u32(q_full));
-                }
-                q_phase ^= 1;
-                __syncwarp();
-                for (int step = g.step0; step < g.step1 && ok; ++step) {
-                    const int next = step + 1 < g.step1 ? page_of(step + 1) : -1;
-                    const int have = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t full = smem_u32(&kv_full[stage]);
-                        if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(have * box * D * 2));
-                        __syncwarp();
-                        if (page >= 0) {
-                            const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile + lane * box * 128);
-                            const int tok = ps > kKeys ? step * kKeys % ps : 0;
-                            for (int d = 0; d < kSlabs; ++d)
-                                tma_load_4d(dst + d * kKeys * 128, kv ? &map_v : &map_k, d * 64, tok, g.h, page, full);
-                        }
-                        ring_waited |= 1u << stage;
-                        if (++stage == C::kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                    Seg g;
+                    g.b = b;
+                    g.h = int(h);
+                    g.tok0 = int(i * tt2);
+                    g.q0 = s.q0;
+                    g.q_len = s.q_len;
+                    g.kv_len = s.kv_len;
+                    g.step0 = int(from - item0 - setup);
+                    g.step1 = c.whole ? int(steps) : int(end - item0 - setup);
+                    g.slot = whole ? -1 : int(cta * 2 + (starts ? 1 : 0));
+                    g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
+                    segs[k] = g;
+                    if (!whole && starts) {
+                        const int last = int(sh.owner(item0 + places - 1));
+                        c.rec[cta] = Rec{last - int(cta) + 1, g.h, g.tok0, g.q0, g.q_len};
                     }
-                    page = next;
+                }
+                ++k;
+            }
+            w = end;
+            if (end == item0 + places) {
+                item0 += places;
+                if (++i == items_of(s, it)) {
+                    i = 0;
+                    ++h;
+                    if (h == Hkv) located = false;  // the next sequence
                 }
             }
-        } else if (warp == kMmaWarp) {
-            // ------------------------------------------------ MMAs
-            const uint32_t id_s = instr_desc(kM, kKeys), id_o = instr_desc(kM, D) | (1u << 16);
-            auto wait = [&](uint64_t *bar, uint32_t par) {
-                const bool r = mbar_wait(smem_u32(bar), par, wt);
-                ok = __all_sync(0xffffffffu, r);
-                return ok;
-            };
-            auto advance = [&](int &st, uint32_t &ph) {
-                if (++st == C::kStages) {
-                    st = 0;
-                    ph ^= 1;
+        }
+        if (lane == 0) {
+            *nseg = k;
+            cursor[0] = b;
+            cursor[1] = first;
+            cursor[2] = per_head;
+            cursor[3] = w;
+            *cur_seq = s;
+        }
+    };
+    bool ok = true;
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        int stage = 0;                      // ring position
+        uint32_t phase = 0, q_phase = 0;
+        uint32_t p_phase = 0, oe_phase = 3;  // bit t: tile t
+        uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
+        for (uint32_t u = u_begin; u < u_end && ok;) {
+            if (warp == kListWarp) list();
+            meet();
+            const int ns = *nseg;
+            u = cursor[3];
+            if (warp == kLoadWarp) {
+                // ------------------------------------------------ loads
+                const int ps = a.page_size, box = min(ps, kKeys);
+                for (int k = 0; k < ns && ok; ++k) {
+                    const Seg g = segs[k];
+                    const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                    const int boxes_max = kKeys / box;
+                    auto page_of = [&](int step) {  // lane i: the page of box i of the step
+                        const int p = step * kKeys + lane * box;
+                        return lane < boxes_max && p < keys ? load_page(a, g.b, p / ps) : -1;
+                    };
+                    int page = page_of(g.step0);
+                    ok = mbar_wait(smem_u32(q_empty), q_phase ^ 1, wt);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const int rows = int(G * tt);
+                        mbar_arrive_expect_tx(smem_u32(q_full), uint32_t(g.tiles * rows * D * 2));
+                        for (int t = 0; t < g.tiles; ++t)
+                            for (int d = 0; d < kSlabs; ++d)
+                                tma_load_3d(smem_u32(smem + t * C::kTile + d * kM * 128), &map_q, d * 64, int(g.h * G),
+                                            g.q0 + g.tok0 + t * int(tt), smem_u32(q_full));
+                    }
+                    q_phase ^= 1;
+                    __syncwarp();
+                    for (int step = g.step0; step < g.step1 && ok; ++step) {
+                        const int next = step + 1 < g.step1 ? page_of(step + 1) : -1;
+                        const int have = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                        for (int kv = 0; kv < 2; ++kv) {
+                            ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t full = smem_u32(&kv_full[stage]);
+                            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(have * box * D * 2));
+                            __syncwarp();
+                            if (page >= 0) {
+                                const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile + lane * box * 128);
+                                const int tok = ps > kKeys ? step * kKeys % ps : 0;
+                                for (int d = 0; d < kSlabs; ++d)
+                                    tma_load_4d(dst + d * kKeys * 128, kv ? &map_v : &map_k, d * 64, tok, g.h, page, full);
+                            }
+                            ring_waited |= 1u << stage;
+                            if (++stage == C::kStages) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        page = next;
+                    }
                 }
-            };
-            auto issue_s = [&](int t, int st) {
-                const uint64_t qa = smem_desc(smem_u32(smem + t * C::kTile)), kb = smem_desc(smem_u32(smem + (2 + st) * C::kTile));
-                mma_s<D>(tmem + kColS + t * kKeys, qa, kb, id_s, smem_u32(&s_full[t]));
-            };
-            for (int k = 0; k < ns && ok; ++k) {
-                const Seg g = segs[k];
-                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
-                if (!wait(q_full, q_phase)) break;
-                q_phase ^= 1;
-                if (!wait(&kv_full[stage], phase)) break;
-                tc_fence_after();
-                int ks_stage = stage;  // the stage of the next K
-                for (int t = 0; t < g.tiles; ++t) issue_s(t, ks_stage);
-                mma_commit_warp(smem_u32(&kv_empty[ks_stage]));
-                advance(stage, phase);
-                if (g.step1 - g.step0 == 1) mma_commit_warp(smem_u32(q_empty));
-                for (int step = g.step0; step < g.step1 && ok; ++step) {
-                    const bool more = step + 1 < g.step1;
-                    const int v_stage = stage;
-                    if (!wait(&kv_full[v_stage], phase)) break;
+            } else if (warp == kMmaWarp) {
+                // ------------------------------------------------ MMAs
+                const uint32_t id_s = instr_desc(kM, kKeys), id_o = instr_desc(kM, D) | (1u << 16);
+                auto wait = [&](uint64_t *bar, uint32_t par) {
+                    const bool r = mbar_wait(smem_u32(bar), par, wt);
+                    ok = __all_sync(0xffffffffu, r);
+                    return ok;
+                };
+                auto advance = [&](int &st, uint32_t &ph) {
+                    if (++st == C::kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                };
+                auto issue_s = [&](int t, int st) {
+                    const uint64_t qa = smem_desc(smem_u32(smem + t * C::kTile)), kb = smem_desc(smem_u32(smem + (2 + st) * C::kTile));
+                    mma_s<D>(tmem + kColS + t * kKeys, qa, kb, id_s, smem_u32(&s_full[t]));
+                };
+                for (int k = 0; k < ns && ok; ++k) {
+                    const Seg g = segs[k];
+                    const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                    if (!wait(q_full, q_phase)) break;
+                    q_phase ^= 1;
+                    if (!wait(&kv_full[stage], phase)) break;
+                    tc_fence_after();
+                    int ks_stage = stage;  // the stage of the next K
+                    for (int t = 0; t < g.tiles; ++t) issue_s(t, ks_stage);
+                    mma_commit_warp(smem_u32(&kv_empty[ks_stage]));
                     advance(stage, phase);
-                    // keys past the last that the item sees: their slots may hold anything (or were not
-                    // loaded), and 0 * NaN is NaN: zero the rows
-                    const int live = keys - step * kKeys;
-                    if (live < kKeys) {
-                        const int from = max(live, 0);
-                        const uint32_t vb = smem_u32(smem + (2 + v_stage) * C::kTile);
-                        for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
-#pragma unroll
-                            for (int d = 0; d < kSlabs; ++d)
-                                sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                    for (int t = 0; t < g.tiles && ok; ++t) {
-                        if (step == g.step0) {  // O was read out by the previous segment's epilogue
-                            if (!wait(&o_empty[t], (oe_phase >> t) & 1)) break;
-                            oe_phase ^= 1u << t;
-                        }
-                        if (!wait(&p_full[t], (p_phase >> t) & 1)) break;
-                        p_phase ^= 1u << t;
-                        tc_fence_after();
-                        const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
-                        mma_o(tmem + kColO + t * 128, tmem + kColS + t * kKeys, vb, id_o, step > g.step0);
-                        if (!more) mma_commit_warp(smem_u32(&o_full[t]));
-                        if (more) {
-                            if (t == 0 && !wait(&kv_full[stage], phase)) break;
-                            issue_s(t, stage);
-                        }
-                    }
-                    if (!ok) break;
-                    mma_commit_warp(smem_u32(&kv_empty[v_stage]));
-                    if (more) {
-                        mma_commit_warp(smem_u32(&kv_empty[stage]));
+                    if (g.step1 - g.step0 == 1) mma_commit_warp(smem_u32(q_empty));
+                    for (int step = g.step0; step < g.step1 && ok; ++step) {
+                        const bool more = step + 1 < g.step1;
+                        const int v_stage = stage;
+                        if (!wait(&kv_full[v_stage], phase)) break;
                         advance(stage, phase);
-                        if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                        // keys past the last that the item sees: their slots may hold anything (or were not
+                        // loaded), and 0 * NaN is NaN: zero the rows
+                        const int live = keys - step * kKeys;
+                        if (live < kKeys) {
+                            const int from = max(live, 0);
+                            const uint32_t vb = smem_u32(smem + (2 + v_stage) * C::kTile);
+                            for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
+#pragma unroll
+                                for (int d = 0; d < kSlabs; ++d)
+                                    sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
+                        for (int t = 0; t < g.tiles && ok; ++t) {
+                            if (step == g.step0) {  // O was read out by the previous segment's epilogue
+                                if (!wait(&o_empty[t], (oe_phase >> t) & 1)) break;
+                                oe_phase ^= 1u << t;
+                            }
+                            if (!wait(&p_full[t], (p_phase >> t) & 1)) break;
+                            p_phase ^= 1u << t;
+                            tc_fence_after();
+                            const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
+                            mma_o(tmem + kColO + t * 128, tmem + kColS + t * kKeys, vb, id_o, step > g.step0);
+                            if (!more) mma_commit_warp(smem_u32(&o_full[t]));
+                            if (more) {
+                                if (t == 0 && !wait(&kv_full[stage], phase)) break;
+                                issue_s(t, stage);
+                            }
+                        }
+                        if (!ok) break;
+                        mma_commit_warp(smem_u32(&kv_empty[v_stage]));
+                        if (more) {
+                            mma_commit_warp(smem_u32(&kv_empty[stage]));
+                            advance(stage, phase);
+                            if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                        }
                     }
                 }
             }
-        } else {
+            // the segment list is free; a role that gave up ends the CTA
+            ok = !meet_any(!ok);
+        }
+        // an aborting CTA waits for its own copies and MMAs before it gives up its memory
+        if (warp == kLoadWarp && !ok) {
+            for (int i = 0; i < C::kStages; ++i) {
+                // the last fill of stage i was in the current phase if i < stage, else in the one before
+                const uint32_t par = i < stage ? phase : phase ^ 1;
+                if (ring_waited >> i & 1) mbar_wait_drain(smem_u32(&kv_full[i]), par, wt);
+            }
+            mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
+        }
+        if (warp == kMmaWarp) {  // every MMA and every arrival of its commits is over before the CTA ends
+            mma_commit_warp(smem_u32(drain));
+            mbar_wait_drain(smem_u32(drain), 0, wt);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        uint32_t s_phase = 0, o_phase = 0;
+        for (uint32_t u = u_begin; u < u_end && ok;) {
+            meet();
+            const int ns = *nseg;
+            u = cursor[3];
             // ------------------------------------------------ softmax and epilogue, one row a thread
             const int t = warp >> 2, r = tid & (kM - 1);
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
@@ -747,25 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m * sl2 + log2f(l)) * kLn2;
                 }
             }
+            ok = !meet_any(!ok);
         }
-        // the segment list is free; a role that gave up ends the CTA
-        ok = !__syncthreads_or(!ok);
     }
 
-    // ---------------------------------------------------------------- end
-    // an aborting CTA waits for its own copies and MMAs before it gives up its memory
-    if (warp == kLoadWarp && !ok) {
-        for (int i = 0; i < C::kStages; ++i) {
-            // the last fill of stage i was in the current phase if i < stage, else in the one before
-            const uint32_t par = i < stage ? phase : phase ^ 1;
-            if (ring_waited >> i & 1) mbar_wait_drain(smem_u32(&kv_full[i]), par, wt);
-        }
-        mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
-    }
-    if (warp == kMmaWarp) {  // every MMA and every arrival of its commits is over before the CTA ends
-        mma_commit_warp(smem_u32(drain));
-        mbar_wait_drain(smem_u32(drain), 0, wt);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -865,6 +887,9 @@ bool set_smem_attr() {
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
         if (cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
             return false;
+        // the softmax's registers come from the launch's: fewer, and the kernel would wait for them for ever
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, chunk_kernel<D>) != cudaSuccess || fa.numRegs < kLaunchRegs) return false;
         attr_set[dev] = true;
     }
     return true;

@@ -42,6 +42,12 @@ struct Cfg {
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 2048;
     static_assert(kSmem <= 232448, "");
+    // TMEM columns of tile t: S at 128 t, P and O here.  Heads of 64 leave room for P beside S: the scores
+    // of the next step are computed while the softmax works on this one's, which the softmax holds in
+    // registers.  Heads of 128 do not: P takes the place of S.
+    static constexpr bool kEarly = D == 64;
+    static constexpr uint32_t col_p(int t) { return kEarly ? 256 + 64 * t : 128 * t; }
+    static constexpr uint32_t col_o(int t) { return kEarly ? 384 + 64 * t : 256 + 128 * t; }
 };
 
 // One item, or the part of it in this CTA's share.
@@ -144,8 +150,6 @@ struct Shares {
     }
 };
 
-// TMEM columns.
-constexpr uint32_t kColS = 0, kColO = 256;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     uint64_t *kv_full = reinterpret_cast<uint64_t *>(ctrl);  // [kStages]
     uint64_t *kv_empty = kv_full + C::kStages;               // [kStages]
     uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
-    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
+    uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
     uint64_t *drain = o_empty + 2;
     Seg *segs = reinterpret_cast<Seg *>(drain + 1);  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
@@ -283,7 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
     const Args &a = c.a;
     const Waits wt{a.err, abort, c.wait_ns, smem_u32(const_cast<int *>(abort))};
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number from one lane: the compiler then knows it to be the same in all of them, and the
+    // MMA warp's addresses and descriptors stay in the uniform registers that its instructions take
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t tt = c.tt, tt2 = 2 * tt, G = a.group, Hkv = a.n_kv_heads;
     const Item it{tt2, c.item_shift};
     if (tid == kLoadWarp * 32) {
@@ -299,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         mbar_init(smem_u32(q_empty), 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&s_full[t]), 1);
+            mbar_init(smem_u32(&s_empty[t]), kM);
             mbar_init(smem_u32(&p_full[t]), kM + c.extra_need);
             mbar_init(smem_u32(&o_full[t]), 1);
             mbar_init(smem_u32(&o_empty[t]), kM);
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     griddep_wait();
     griddep_launch_dependents();
 
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         int stage = 0;                      // ring position
         uint32_t phase = 0, q_phase = 0;
-        uint32_t p_phase = 0, oe_phase = 3;  // bit t: tile t
+        uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
         uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
         for (uint32_t u = u_begin; u < u_end && ok;) {
             if (warp == kListWarp) list();
@@ -575,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 };
                 auto issue_s = [&](int t, int st) {
                     const uint64_t qa = smem_desc(smem_u32(smem + t * C::kTile)), kb = smem_desc(smem_u32(smem + (2 + st) * C::kTile));
-                    mma_s<D>(tmem + kColS + t * kKeys, qa, kb, id_s, smem_u32(&s_full[t]));
+                    mma_s<D>(tmem + t * kKeys, qa, kb, id_s, smem_u32(&s_full[t]));
                 };
                 for (int k = 0; k < ns && ok; ++k) {
                     const Seg g = segs[k];
@@ -592,8 +599,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     for (int step = g.step0; step < g.step1 && ok; ++step) {
                         const bool more = step + 1 < g.step1;
                         const int v_stage = stage;
-                        if (!wait(&kv_full[v_stage], phase)) break;
+                        const uint32_t v_phase = phase;
                         advance(stage, phase);
+                        if (C::kEarly && more) {  // the next scores, once the softmax has these
+                            if (!wait(&kv_full[stage], phase)) break;
+                            for (int t = 0; t < g.tiles && ok; ++t) {
+                                if (!wait(&s_empty[t], (se_phase >> t) & 1)) break;
+                                se_phase ^= 1u << t;
+                                tc_fence_after();
+                                issue_s(t, stage);
+                            }
+                            if (!ok) break;
+                            mma_commit_warp(smem_u32(&kv_empty[stage]));
+                            advance(stage, phase);
+                            if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                        }
+                        if (!wait(&kv_full[v_stage], v_phase)) break;
                         // keys past the last that the item sees: their slots may hold anything (or were not
                         // loaded), and 0 * NaN is NaN: zero the rows
                         const int live = keys - step * kKeys;
@@ -616,20 +637,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             p_phase ^= 1u << t;
                             tc_fence_after();
                             const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
-                            mma_o(tmem + kColO + t * 128, tmem + kColS + t * kKeys, vb, id_o, step > g.step0);
-                            if (!more) mma_commit_warp(smem_u32(&o_full[t]));
-                            if (more) {
+                            mma_o(tmem + C::col_o(t), tmem + C::col_p(t), vb, id_o, step > g.step0);
+                            if (C::kEarly || !more) mma_commit_warp(smem_u32(&o_full[t]));
+                            if (!C::kEarly && more) {
                                 if (t == 0 && !wait(&kv_full[stage], phase)) break;
                                 issue_s(t, stage);
                             }
                         }
                         if (!ok) break;
                         mma_commit_warp(smem_u32(&kv_empty[v_stage]));
-                        if (more) {
+                        if (!C::kEarly && more) {
                             mma_commit_warp(smem_u32(&kv_empty[stage]));
                             advance(stage, phase);
                             if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
                         }
+                        if (C::kEarly && !more) se_phase ^= g.tiles == 2 ? 3u : 1u;  // the segment's last: past, with its P
                     }
                 }
             }
@@ -659,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // ------------------------------------------------ softmax and epilogue, one row a thread
             const int t = warp >> 2, r = tid & (kM - 1);
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
-            const uint32_t ts = tmem + lanes + kColS + t * kKeys, to = tmem + lanes + kColO + t * 128;
+            const uint32_t ts = tmem + lanes + t * kKeys, tp = tmem + lanes + C::col_p(t), to = tmem + lanes + C::col_o(t);
             const bool neg = a.scale < 0.f;
             // a zero scale would make -inf * 0 of masked scores: any tiny factor gives the same result
             const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
@@ -684,6 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld32_issue(ts + i * 32, x + i * 32);
                     tmem_ld_done(x);
+                    if (C::kEarly) {
+                        tc_fence_before();
+                        mbar_arrive(smem_u32(&s_empty[t]));
+                    }
                     if (neg) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
@@ -703,6 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         for (int e = 0; e < 4; ++e)
                             mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
                     const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                    if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
+                        ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        o_phase ^= 1;
+                        tc_fence_after();
+                    }
                     if (step == g.step0) {
                         m = mn;
                     } else if (__any_sync(0xffffffffu, (mn - m) * sl2 > kLag)) {
@@ -731,9 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         p1 = ex2(p1);
                         sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair(p0, p1));
                         x[i / 2] = pack_bf16(p0, p1);
-                        if (i == 62) tmem_st32(ts, x);
+                        if (i == 62) tmem_st32(tp, x);
                     }
-                    tmem_st32(ts + 32, x + 32);
+                    tmem_st32(tp + 32, x + 32);
                     float s0, s1;
                     unpair(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;

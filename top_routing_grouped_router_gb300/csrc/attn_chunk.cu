@@ -24,11 +24,11 @@ namespace {
 
 using namespace tc;
 
-// Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMA, loads, the list of segments, one
-// spare.  It gives up registers that the softmax takes: 8 x 32 x 208 + 4 x 32 x 72 is within the launch's
+// Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMAs, loads, the list of
+// segments, and with heads of 64 the MMAs of tile 1.  It gives up registers that the softmax takes: 8 x 32 x 208 + 4 x 32 x 80 is within the launch's
 // 12 x 32 x 168.
-constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 72;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10;
+constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 80;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "");
 constexpr int kM = 128, kKeys = 128;
 constexpr int kMaxCtas = 160;   // one per SM (152)
@@ -46,6 +46,10 @@ struct Cfg {
     // of the next step are computed while the softmax works on this one's, which the softmax holds in
     // registers.  Heads of 128 do not: P takes the place of S.
     static constexpr bool kEarly = D == 64;
+    // Warps that issue MMAs, each for its tiles.  With heads of 128 one, in the order of the tiles, which
+    // keeps one tile's products beside the other's softmax (two: 420 us for a chunk of 2048, one: 341);
+    // with heads of 64, whose products are half as long, two (a mixed batch 48.4 us, with one 51).
+    static constexpr int kMmaWarps = D == 64 ? 2 : 1;
     static constexpr uint32_t col_p(int t) { return kEarly ? 256 + 64 * t : 128 * t; }
     static constexpr uint32_t col_o(int t) { return kEarly ? 384 + 64 * t : 256 + 128 * t; }
 };
@@ -276,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     uint64_t *kv_empty = kv_full + C::kStages;               // [kStages]
     uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
-    uint64_t *drain = o_empty + 2;
-    Seg *segs = reinterpret_cast<Seg *>(drain + 1);  // [kMaxSegs]
+    uint64_t *v_zero = o_empty + 2, *drain = v_zero + C::kStages;  // [kStages], [2]
+    Seg *segs = reinterpret_cast<Seg *>(drain + 2);  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
     int *nseg = reinterpret_cast<int *>(scan + 16);
     volatile int *abort = nseg + 1;
@@ -299,10 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&kv_full[i]), 1);
-            mbar_init(smem_u32(&kv_empty[i]), 1);
+            mbar_init(smem_u32(&kv_empty[i]), C::kMmaWarps);
+            mbar_init(smem_u32(&v_zero[i]), 1);
         }
         mbar_init(smem_u32(q_full), 1);
-        mbar_init(smem_u32(q_empty), 1);
+        mbar_init(smem_u32(q_empty), C::kMmaWarps);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&s_full[t]), 1);
             mbar_init(smem_u32(&s_empty[t]), kM);
@@ -310,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(smem_u32(&o_full[t]), 1);
             mbar_init(smem_u32(&o_empty[t]), kM);
         }
-        mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(&drain[0]), 1);
+        mbar_init(smem_u32(&drain[1]), 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -506,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         int stage = 0;                      // ring position
         uint32_t phase = 0, q_phase = 0;
         uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
+        uint32_t z_phase = 0;               // bit i: stage i
         uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
         for (uint32_t u = u_begin; u < u_end && ok;) {
             if (warp == kListWarp) list();
@@ -566,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         page = next;
                     }
                 }
-            } else if (warp == kMmaWarp) {
-                // ------------------------------------------------ MMAs
+            } else if (warp == kMmaWarp || (C::kMmaWarps == 2 && warp == kMma1Warp)) {
+                // ------------------------------------------------ MMAs of tiles t0 .. t1 - 1
+                const int t0 = warp == kMmaWarp ? 0 : 1, t_end = C::kMmaWarps == 2 ? t0 + 1 : 2;
                 const uint32_t id_s = instr_desc(kM, kKeys), id_o = instr_desc(kM, D) | (1u << 16);
                 auto wait = [&](uint64_t *bar, uint32_t par) {
                     const bool r = mbar_wait(smem_u32(bar), par, wt);
@@ -587,13 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int k = 0; k < ns && ok; ++k) {
                     const Seg g = segs[k];
                     const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                    const int t1 = min(t_end, g.tiles);  // none: the warp only keeps step with the ring
                     if (!wait(q_full, q_phase)) break;
                     q_phase ^= 1;
                     if (!wait(&kv_full[stage], phase)) break;
                     tc_fence_after();
-                    int ks_stage = stage;  // the stage of the next K
-                    for (int t = 0; t < g.tiles; ++t) issue_s(t, ks_stage);
-                    mma_commit_warp(smem_u32(&kv_empty[ks_stage]));
+                    for (int t = t0; t < t1; ++t) issue_s(t, stage);
+                    mma_commit_warp(smem_u32(&kv_empty[stage]));
                     advance(stage, phase);
                     if (g.step1 - g.step0 == 1) mma_commit_warp(smem_u32(q_empty));
                     for (int step = g.step0; step < g.step1 && ok; ++step) {
@@ -601,24 +609,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         const int v_stage = stage;
                         const uint32_t v_phase = phase;
                         advance(stage, phase);
+                        auto release_k = [&]() {
+                            mma_commit_warp(smem_u32(&kv_empty[stage]));
+                            advance(stage, phase);
+                            if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                        };
                         if (C::kEarly && more) {  // the next scores, once the softmax has these
                             if (!wait(&kv_full[stage], phase)) break;
-                            for (int t = 0; t < g.tiles && ok; ++t) {
+                            for (int t = t0; t < t1 && ok; ++t) {
                                 if (!wait(&s_empty[t], (se_phase >> t) & 1)) break;
                                 se_phase ^= 1u << t;
                                 tc_fence_after();
                                 issue_s(t, stage);
                             }
                             if (!ok) break;
-                            mma_commit_warp(smem_u32(&kv_empty[stage]));
-                            advance(stage, phase);
-                            if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
+                            release_k();
                         }
                         if (!wait(&kv_full[v_stage], v_phase)) break;
                         // keys past the last that the item sees: their slots may hold anything (or were not
-                        // loaded), and 0 * NaN is NaN: zero the rows
+                        // loaded), and 0 * NaN is NaN: the first warp zeroes the rows
                         const int live = keys - step * kKeys;
-                        if (live < kKeys) {
+                        if (live < kKeys && t0 == 0) {
                             const int from = max(live, 0);
                             const uint32_t vb = smem_u32(smem + (2 + v_stage) * C::kTile);
                             for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
@@ -627,8 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                     sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
+                            if (C::kMmaWarps == 2 && lane == 0) mbar_arrive(smem_u32(&v_zero[v_stage]));
+                        } else if (live < kKeys) {
+                            if (!wait(&v_zero[v_stage], z_phase >> v_stage & 1)) break;
+                            z_phase ^= 1u << v_stage;
                         }
-                        for (int t = 0; t < g.tiles && ok; ++t) {
+                        for (int t = t0; t < t1 && ok; ++t) {
                             if (step == g.step0) {  // O was read out by the previous segment's epilogue
                                 if (!wait(&o_empty[t], (oe_phase >> t) & 1)) break;
                                 oe_phase ^= 1u << t;
@@ -639,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             const uint64_t vb = v_desc(smem_u32(smem + (2 + v_stage) * C::kTile));
                             mma_o(tmem + C::col_o(t), tmem + C::col_p(t), vb, id_o, step > g.step0);
                             if (C::kEarly || !more) mma_commit_warp(smem_u32(&o_full[t]));
+                            if (C::kEarly && !more) se_phase ^= 1u << t;  // the segment's last scores: past, with its P
                             if (!C::kEarly && more) {
                                 if (t == 0 && !wait(&kv_full[stage], phase)) break;
                                 issue_s(t, stage);
@@ -646,12 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         }
                         if (!ok) break;
                         mma_commit_warp(smem_u32(&kv_empty[v_stage]));
-                        if (!C::kEarly && more) {
-                            mma_commit_warp(smem_u32(&kv_empty[stage]));
-                            advance(stage, phase);
-                            if (step + 2 == g.step1) mma_commit_warp(smem_u32(q_empty));
-                        }
-                        if (C::kEarly && !more) se_phase ^= g.tiles == 2 ? 3u : 1u;  // the segment's last: past, with its P
+                        if (!C::kEarly && more) release_k();
                     }
                 }
             }
@@ -667,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
         }
-        if (warp == kMmaWarp) {  // every MMA and every arrival of its commits is over before the CTA ends
-            mma_commit_warp(smem_u32(drain));
-            mbar_wait_drain(smem_u32(drain), 0, wt);
+        if (warp == kMmaWarp || warp == kMma1Warp) {  // every MMA and every arrival of its commits is over before the CTA ends
+            const uint32_t bar = smem_u32(&drain[warp == kMmaWarp ? 0 : 1]);
+            mma_commit_warp(bar);
+            mbar_wait_drain(bar, 0, wt);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));

@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1) + 1;
     static_assert((2 * kMaxRing + 2 * kA + 2 * 4 + 2) * 8 + 8 <= kCtrl, "");
     const Waits wt{&g_err, abort, m.wait_ns, smem_u32(const_cast<int *>(abort))};
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number from one lane: known to be the same in all of them, so that the MMA warp's operands
+    // stay in uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (smem_u32(smem) & 1023u) {  // not seen: shared memory starts on such a boundary
         if (tid == 0) record_error(&g_err, MOE_ERR_DEVICE);
         return;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t blocks = uint32_t(a.K / a.q_block);
     bool ok = true;
     float acc[kHalf];  // adding warps: this output's sums

@@ -466,6 +466,20 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
                 for (int c = 0; c < 2; ++c) {
                     const int row = n * 8 + 2 * t + c;
                     if (row >= rows) continue;
+                    if (!a.res && n0 + kOut <= N) {  // the usual case: one address a row
+                        const int64_t at_out = (T0 + row) * a.out_stride + n0 + g;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float y = acc[i][n][2 * r + c] * m.step;
+                                if (a.out_f32)
+                                    static_cast<float *>(a.out)[at_out + i * kStrip + 8 * r] = y;
+                                else
+                                    static_cast<uint16_t *>(a.out)[at_out + i * kStrip + 8 * r] = f32_to_bf16_bits(y);
+                            }
+                        continue;
+                    }
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll

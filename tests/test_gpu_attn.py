@@ -125,6 +125,15 @@ def test_attention(name):
     check(make_batch(*ATTN[name], seed=len(name)))
 
 
+@pytest.mark.parametrize("seqs", [1, 6, 14, 34, 70, 90])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,most", [(8, 5), (32, 2), (60, 1), (4, 16)])
+def test_attention_rows_of_a_pair(seqs, dim, heads, most):
+    # up to 16 query rows a key head, for every number of CTAs that a pair can get
+    q_len = [most - i % 2 if most > 1 else 1 for i in range(seqs)]
+    check(make_batch("bf16", heads, 4, dim, 32, q_len, [q_len[i] + (i * 19) % 44 for i in range(seqs)], seed=seqs))
+
+
 @pytest.mark.parametrize("name", ["decode ragged", "few tokens", "chunk ragged", "chunk fp32"])
 @pytest.mark.parametrize("layout", ["slots", "joint"])
 def test_attention_layouts(name, layout):

@@ -630,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             // each CTA joins its share of the outputs, the parts in the order of the keys
             cg::cluster_group cl = cg::this_cluster();
             cl.sync();
-            const int all = rows * (D / 4), each = (all + kC - 1) / kC, i = int(cta % kC) * each + tid;
-            if (tid < each && i < all) {
+            const int all = rows * (D / 4), each = (all + kC - 1) / kC, from = int(cta % kC) * each;
+            for (int i = from + tid; i < min(from + each, all); i += kThreads) {
                 const int r = i / (D / 4), d = i % (D / 4) * 4;
                 float2 ml[kC];
                 float4 v[kC];

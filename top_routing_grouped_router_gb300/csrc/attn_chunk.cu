@@ -5,12 +5,18 @@
 // rows.  A CTA works on two tiles at a time ("item": a sequence, a key head, 2 x 128 rows) and
 // goes over the keys in steps of 128:
 //   S_t = Q_t K^T      M = 128, N = 128, into TMEM
-//   P_t = 2^(S_t - m)  by four warps per tile, one row a thread, written over S_t as bf16
+//   P_t = 2^(S_t - m)  by four warps per tile, one row a thread, to TMEM as bf16
 //   O_t += P_t V       A = P_t from TMEM, V as it lies in the cache (keys x head: N-major)
-// The MMA warp issues P0 V, S0', P1 V, S1': while one tile's softmax runs, the tensor cores work
-// on the other's products.  The running maximum m may lag behind: only when a row's maximum
-// grows by more than 2^8 is O rescaled (by the softmax warps, in TMEM); until then the larger
-// probabilities are exact in bf16 terms all the same, since the scale of a row cancels.
+// Heads of 128: P_t takes the place of S_t (TMEM is full), and one warp issues P0 V, S0', P1 V, S1':
+// while one tile's softmax runs, the tensor cores work on the other's products.  What bounds it is
+// that chain: 1400 cycles of softmax and 1024 of products a tile, 2890 a step of both tiles where the
+// products alone are 2048 (2048 tokens over 16384 keys, 32 heads: 339 us, 1520 TFLOP/s).  Multiplying the
+// first half of P while the softmax works on the second made it slower (371 us).
+// Heads of 64: P_t lies beside S_t, the next scores are computed while the softmax works, and each
+// tile has an MMA warp of its own.
+// The running maximum m may lag behind: only when a row's maximum grows by more than 2^8 is O
+// rescaled (by the softmax warps, in TMEM); until then the larger probabilities are exact in bf16
+// terms all the same, since the scale of a row cancels.
 //
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a

@@ -2,9 +2,11 @@
 // q_block inputs, a 16-entry codebook), for batches of few rows.  What bounds it is the read of
 // the codes, half a byte a weight, and next to it the instructions that unpack them.
 //
-// q4_mma_kernel: a CTA takes 16 outputs at a time (16 to 128 where there are many, "side").  Its
-// eight warps split the inputs; each
-// streams its part of the 16 code rows through a cp.async ring of its own, 128 inputs a stage,
+// q4_mma_kernel: a CTA takes 16 outputs at a time (16 to 128 where there are more, "side").  Its
+// eight warps split the inputs; where there are many outputs, sixteen warps take pairs of 16 instead,
+// each an equal piece of the line of all the CTA's pairs (16 rows x 2048 x 131072: 39 us; tiles whose inputs
+// the warps split, with a barrier and a sum each, 54).  Each warp
+// streams its part of the code rows through a cp.async ring of its own, 128 inputs a stage,
 // unpacks the codes in registers to the A operand of mma.sync (m16n8k16, outputs x inputs) and
 // multiplies with the rows of x, which lie in shared memory in the order of the B fragments.
 // A block of inputs that shares a scale is summed by the MMA alone, then added to the fp32
@@ -669,9 +671,9 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const bool eights = a.T > 8 && two_fit(2) < stages && two_fit(1) >= stages && many((int64_t)a.N * ((a.T + 7) / 8), sms, 1);
     // tcgen05 for more rows than one pass where the weights are large enough that its longer start does
     // not count (us, tcgen05 and mma.sync): 64 x 2048 x 2048 14.6, 11.6; 40 x 512 x 20000 18.0, 15.1; 32 x 4096 x
-    // 5120 17.3, 25.0; 64 x 4096 x 10240 54, 69.  For one pass of more than 8 rows only where neither side
-    // of it has room for two strips: 16 x 2048 x 5120 10.2, 10.1; 16 x 4096 x 5120 13.9, 18.5; 16 x 8192 x 10240
-    // 42, 52.
+    // 5120 16.0, 25.0; 64 x 4096 x 10240 51, 69.  For one pass of more than 8 rows only where neither side
+    // of it has room for two strips: 16 x 2048 x 5120 10.2, 10.1; 16 x 4096 x 5120 12.1, 18.5; 16 x 8192 x 10240
+    // 37, 52.
     const int64_t weights = (int64_t)a.N * a.K;
     const bool large = (a.K >= 2048 && weights >= (1 << 23)) || weights >= (1 << 26);
     if (affine && !fine && large && (a.T > kMmaRows || (a.T > 8 && two_fit(2) < stages && !eights)) &&

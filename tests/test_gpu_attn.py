@@ -470,3 +470,21 @@ def test_q4_linear_residual_in_place():
     moe.moe_q4_linear(shape, x, weight, b, residual=b)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,K,N,q_block", [(7, 512, 300, 64), (16, 192, 2000, 32), (33, 640, 40000, 64), (40, 96, 70, 32)])
+def test_q4_linear_keeps_fp32_values(T, K, N, q_block):
+    # rows of x with a single one: each result is one weight, codebook value times scale.  Its value is
+    # held to 24 bits (three roundings of its parts' sum), the product with the scale rounds once more;
+    # the start of the sum and the empty blocks add zeros.
+    g = torch.Generator().manual_seed(K)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g).to(torch.uint8)
+    scales = (torch.rand(N, K // q_block, generator=g) + 0.25).bfloat16()
+    x = torch.zeros(T, K)
+    x[torch.arange(T), torch.randperm(K, generator=g)[:T]] = 1.0
+    book = [float(torch.tensor(b).float()) for b in NORMAL]
+    want = x.double() @ q4_dense(codes, scales, book, q_block).T
+    shape, weight = moe.make_q4_linear_shape(T, K, N, "f32", q_block), moe.make_q4_weight(codes.cuda(), scales.cuda(), NORMAL)
+    out = torch.empty(T, N, device="cuda")
+    moe.moe_q4_linear(shape, x.bfloat16().cuda(), weight, out)
+    assert ((out.cpu().double() - want).abs() <= 6 * FP32 * want.abs()).all()

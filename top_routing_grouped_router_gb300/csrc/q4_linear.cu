@@ -84,12 +84,13 @@ constexpr int kStrip = 16;       // outputs of an MMA
 constexpr int kIn = 128;         // inputs of a stage, two halves of 64
 constexpr int kMaxSlices = 8;    // CTAs of a cluster that split the inputs
 constexpr int kMaxSmem = 232448;
-constexpr int kLutBytes = 256 * 32 * 8;
+constexpr int kLutBytes = 256 * 32 * 8, kThirdBytes = 256 * 32 * 4;
 
 // What a variant's shared memory holds.  NT: 8-row tiles of x; MT: strips of 16 outputs a warp works
 // on, 1 or 2: two read each fragment of x once, and share the cost of a stage's copies.
-template <int NT, int MT, bool kFine, bool kAffine>
+template <int NT, int MT, bool kFine, int kParts>
 struct Var {
+    static constexpr bool kAffine = kParts == 0;
     static constexpr int kWarps = MT == 2 ? 16 : 8, kThreads = kWarps * 32;
     static constexpr int kDepth = MT == 2 || NT == 2 ? 3 : 4;  // stages of a warp's ring
     static constexpr int kOut = MT * kStrip;                 // outputs of a warp
@@ -100,7 +101,8 @@ struct Var {
     static constexpr int kRedStride = kOut + 4;              // padded column of sums: no bank conflicts
     static constexpr int kRed = MT == 2 ? kWarps * MT * NT * 512 : kWarps * kCols * kRedStride * 4;
     static constexpr int kRing = kWarps * kDepth * kStage;
-    static constexpr int kFixed = kRed + kRing + (kAffine ? 0 : kLutBytes);
+    static constexpr int kLut = kAffine ? 0 : kLutBytes + (kParts == 3 ? kThirdBytes : 0);
+    static constexpr int kFixed = kRed + kRing + kLut;
     // 64 inputs of x: the fragments, and per block the start values (twice each, see below)
     static constexpr int kHalf = NT * 1024 + (kAffine ? (kFine ? 2 : 1) * NT * 64 : 0);
     static int part_bytes(int side) { return 2 * kCols * side * kOut * 4; }
@@ -157,15 +159,17 @@ __device__ __forceinline__ void mma16816_from(float *c, uint32_t a0, uint32_t a1
                    "f"(__uint_as_float(z.y)), "f"(__uint_as_float(z.z)), "f"(__uint_as_float(z.w)));
 }
 // NT: 8-row tiles of x.  kFine: q_block 32, four blocks a stage; else 64 times a power of two.
-// kAffine: codebook step * (j - j0).  The MMA multiplies the exact integers 16 + j, and each sum
+// kParts 0, affine: codebook step * (j - j0).  The MMA multiplies the exact integers 16 + j, and each sum
 // starts at -(16 + j0) sum x of its block (fp32, found once a CTA), which leaves sum (j - j0) x: the
 // subtraction costs no instruction, and about a factor 5 of the fp32 sum's accuracy (16 + j
-// against j - j0).  Else a table in shared memory, each value as bf16 hi + lo.
-template <int NT, int MT, bool kFine, bool kAffine>
-__global__ void __launch_bounds__(Var<NT, MT, kFine, kAffine>::kThreads)
+// against j - j0).  Else a table in shared memory, each value as kParts bf16 that add up to it: two
+// (16 bits, 2^-17 of a value, for results that are rounded to bf16's 2^-9) or three (24 bits, for fp32).
+template <int NT, int MT, bool kFine, int kParts>
+__global__ void __launch_bounds__(Var<NT, MT, kFine, kParts>::kThreads)
 q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     namespace cg = cooperative_groups;
-    using V = Var<NT, MT, kFine, kAffine>;
+    using V = Var<NT, MT, kFine, kParts>;
+    constexpr bool kAffine = V::kAffine;
     constexpr int kWarps = V::kWarps, kThreads = V::kThreads, kDepth = V::kDepth, kOut = V::kOut, kCols = V::kCols;
     constexpr int kStage = V::kStage, kRedStride = V::kRedStride, kRowBytes = kIn / 2;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -174,7 +178,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     float *red = reinterpret_cast<float *>(smem);  // [kWarps][kCols][kRedStride]
     unsigned char *ring_base = smem + V::kRed;
     unsigned char *lut = ring_base + V::kRing;
-    unsigned char *xs = lut + (kAffine ? 0 : kLutBytes);  // [half][NT][2][32] x 16 bytes
+    unsigned char *xs = lut + V::kLut;  // [half][NT][2][32] x 16 bytes
     unsigned char *starts = xs + (size_t)m.slice_halves * NT * 1024;  // [block][NT][4] x 16 bytes (affine)
     float *part = reinterpret_cast<float *>(xs + (size_t)m.slice_halves * V::kHalf);  // [2][kCols][wide], slices > 1
     const uint32_t ring = smem_addr(ring_base) + warp * kDepth * kStage;
@@ -280,7 +284,11 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
             const float c0 = a.codebook[v & 15], c1 = a.codebook[v >> 4];
             const uint32_t hi = attn::pack_bf16(c0, c1);
             const float l0 = c0 - __uint_as_float(hi << 16), l1 = c1 - __uint_as_float(hi & 0xffff0000u);
-            *reinterpret_cast<uint2 *>(lut + v * 256 + lane * 8) = make_uint2(hi, attn::pack_bf16(l0, l1));
+            const uint32_t lo = attn::pack_bf16(l0, l1);
+            *reinterpret_cast<uint2 *>(lut + v * 256 + lane * 8) = make_uint2(hi, lo);
+            if (kParts == 3)
+                *reinterpret_cast<uint32_t *>(lut + kLutBytes + v * 128 + lane * 4) =
+                    attn::pack_bf16(l0 - __uint_as_float(lo << 16), l1 - __uint_as_float(lo & 0xffff0000u));
         }
     }
     // x in the order of the B fragments: 8 inputs of one row are one 16-byte piece, for lane (row mod 8,
@@ -339,7 +347,8 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     }
     __syncthreads();
 
-    const uint32_t x0 = smem_addr(xs) + lane * 16, la = smem_addr(lut) + lane * 8;
+    const uint32_t x0 = smem_addr(xs) + lane * 16, la = smem_addr(lut) + lane * 8,
+                   l3 = smem_addr(lut) + kLutBytes + lane * 4;
     const uint32_t z0 = smem_addr(starts) + t * 16;
     const uint32_t mask = 0x00780078u, bias = 0x41804180u;
     // word wi of half hf of row g (+ 8): piece 2 hf + wi, word t
@@ -381,7 +390,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         for (int q = 0; q < 4; ++q) {  // 32 inputs: word q & 1 of half q / 2
             const int block = kFine ? q : q / 2;
             const bool first = kFine || (q & 1) == 0, last = kFine || (q & 1) == 1;
-            uint32_t p[MT][2][4], lo[MT][2][4];  // [strip][row][pair]; lo: the low parts of a table's values
+            uint32_t p[MT][2][4], lo[MT][2][4], rest[MT][2][4];  // [strip][row][pair]; lo, rest: of a table's values
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -398,6 +407,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
                             const uint2 h = lds64(la + ((v >> (8 * b)) & 255u) * 256);
                             p[i][r][b] = h.x;
                             lo[i][r][b] = h.y;
+                            if (kParts == 3) rest[i][r][b] = lds32(l3 + ((v >> (8 * b)) & 255u) * 128);
                         }
                     }
                 }
@@ -433,6 +443,18 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
                         mma16816(c[i][n], lo[i][0][2], lo[i][1][2], lo[i][0][3], lo[i][1][3], x[n].z, x[n].w);
+            }
+            if (kParts == 3) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma16816(c[i][n], rest[i][0][0], rest[i][1][0], rest[i][0][1], rest[i][1][1], x[n].x, x[n].y);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma16816(c[i][n], rest[i][0][2], rest[i][1][2], rest[i][0][3], rest[i][1][3], x[n].z, x[n].w);
             }
             if (last) {
 #pragma unroll
@@ -580,14 +602,14 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
     }
 }
 
-template <int NT, int MT, bool kFine, bool kAffine>
+template <int NT, int MT, bool kFine, int kParts>
 cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
-    using V = Var<NT, MT, kFine, kAffine>;
+    using V = Var<NT, MT, kFine, kParts>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(q4_mma_kernel<NT, MT, kFine, kAffine>,
+        const cudaError_t e = cudaFuncSetAttribute(q4_mma_kernel<NT, MT, kFine, kParts>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
@@ -625,7 +647,7 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = slices > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, MT, kFine, kAffine>, m);
+    return cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, MT, kFine, kParts>, m);
 }
 
 // Whether warps take two strips: outputs for so many that every SM gets four pairs, or two where x has
@@ -633,19 +655,25 @@ cudaError_t launch_mma(MmaArgs m, int stages, int sms, cudaStream_t st) {
 // 10.2; 8 x 2048 x 20480 13.7, 10.5; 16 x 2048 x 10240 13.5, 10.6).
 bool many(int64_t outputs, int sms, int nt) { return outputs >= (int64_t)sms * (nt == 2 ? 2 : 4) * 2 * kStrip; }
 
-template <bool kFine, bool kAffine>
+template <bool kFine, int kParts>
 struct Rows {  // the variants by rows of x
     static bool fits(int nt, int stages) {
         const int s = (stages + kMaxSlices - 1) / kMaxSlices;
-        return s <= (nt == 1 ? Var<1, 1, kFine, kAffine>::max_stages_sliced() : Var<2, 1, kFine, kAffine>::max_stages_sliced());
+        return s <= (nt == 1 ? Var<1, 1, kFine, kParts>::max_stages_sliced() : Var<2, 1, kFine, kParts>::max_stages_sliced());
     }
-    static int two_fit(int nt) { return nt == 1 ? Var<1, 2, kFine, kAffine>::max_stages() : Var<2, 2, kFine, kAffine>::max_stages(); }
+    static int two_fit(int nt) {
+        if (kParts == 3) return 0;  // one strip a warp: two would not have the registers
+        return nt == 1 ? Var<1, 2, kFine, kParts>::max_stages() : Var<2, 2, kFine, kParts>::max_stages();
+    }
     template <int NT>
     static cudaError_t launch_nt(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
         // two strips a warp where there are plenty and x fits one CTA
         const int passes = (m.a.T + m.pass_rows - 1) / m.pass_rows;
-        const bool two = many((int64_t)m.a.N * passes, sms, NT) && stages <= Var<NT, 2, kFine, kAffine>::max_stages();
-        return two ? launch_mma<NT, 2, kFine, kAffine>(m, stages, sms, st) : launch_mma<NT, 1, kFine, kAffine>(m, stages, sms, st);
+        if constexpr (kParts != 3) {
+            if (many((int64_t)m.a.N * passes, sms, NT) && stages <= Var<NT, 2, kFine, kParts>::max_stages())
+                return launch_mma<NT, 2, kFine, kParts>(m, stages, sms, st);
+        }
+        return launch_mma<NT, 1, kFine, kParts>(m, stages, sms, st);
     }
     static cudaError_t launch(const MmaArgs &m, int stages, int sms, cudaStream_t st) {
         return m.pass_rows <= 8 ? launch_nt<1>(m, stages, sms, st) : launch_nt<2>(m, stages, sms, st);
@@ -662,12 +690,17 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel
     if ((int64_t)(a.N + (1 << 20)) * (a.K / a.q_block) > UINT32_MAX || (int64_t)a.N * stages > INT32_MAX) return false;
+    const int values = affine ? 0 : a.out_f32 ? 3 : 2;
+    auto pick = [&](auto f) {
+        if (values == 0) return fine ? f(Rows<true, 0>{}) : f(Rows<false, 0>{});
+        if (values == 2) return fine ? f(Rows<true, 2>{}) : f(Rows<false, 2>{});
+        return fine ? f(Rows<true, 3>{}) : f(Rows<false, 3>{});
+    };
     auto two_fit = [&](int nt) {  // the most stages of two strips a warp
-        return affine ? (fine ? Rows<true, true>::two_fit(nt) : Rows<false, true>::two_fit(nt))
-                      : (fine ? Rows<true, false>::two_fit(nt) : Rows<false, false>::two_fit(nt));
+        return pick([&](auto v) { return decltype(v)::two_fit(nt); });
     };
     // where only 8 rows of x leave room for two strips a warp, passes of 8 (us in one pass and in two: 16 x
-    // 4096 x 10240 24.9, 18.7; 16 x 2048 x 131072 with a general codebook 128, 102)
+    // 4096 x 10240 24.9, 18.7; 16 x 2048 x 131072 with a general codebook in two parts 128, 102)
     const bool eights = a.T > 8 && two_fit(2) < stages && two_fit(1) >= stages && many((int64_t)a.N * ((a.T + 7) / 8), sms, 1);
     // tcgen05 for more rows than one pass where the weights are large enough that its longer start does
     // not count (us, tcgen05 and mma.sync): 64 x 2048 x 2048 14.6, 11.6; 40 x 512 x 20000 18.0, 15.1; 32 x 4096 x
@@ -680,8 +713,7 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
         run_tc(a, step, twice, sms, st, err))
         return true;
     auto fits = [&](int nt) {
-        return affine ? (fine ? Rows<true, true>::fits(nt, stages) : Rows<false, true>::fits(nt, stages))
-                      : (fine ? Rows<true, false>::fits(nt, stages) : Rows<false, false>::fits(nt, stages));
+        return pick([&](auto v) { return decltype(v)::fits(nt, stages); });
     };
     int nt_max = 2;
     while (nt_max > 0 && !fits(nt_max)) nt_max /= 2;
@@ -693,8 +725,7 @@ bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     m.centre = 16.f + 0.5f * float(twice);
     if (eights) nt_max = std::min(nt_max, 1);
     m.pass_rows = a.T <= 8 ? 8 : nt_max * 8;
-    *err = affine ? (fine ? Rows<true, true>::launch(m, stages, sms, st) : Rows<false, true>::launch(m, stages, sms, st))
-                  : (fine ? Rows<true, false>::launch(m, stages, sms, st) : Rows<false, false>::launch(m, stages, sms, st));
+    *err = pick([&](auto v) { return decltype(v)::launch(m, stages, sms, st); });
     return true;
 }
 

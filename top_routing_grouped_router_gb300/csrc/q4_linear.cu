@@ -41,11 +41,11 @@ __global__ void __launch_bounds__(kAnyThreads) q4_any_kernel(Q4Args a) {
     const uint16_t *scales = a.scales + (size_t)n * (a.K / a.q_block);
     float acc[kAnyRows] = {};
     for (int w = lane; w < a.K / 8; w += 32) {
-        const uint32_t c = __ldg(codes + w);
+        const uint32_t c = codes[w];
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {  // q_block is even: a pair shares its scale
-            const float s = bf16_bits_to_f32(__ldg(scales + (w * 8 + e) / a.q_block));
+            const float s = bf16_bits_to_f32(scales[(w * 8 + e) / a.q_block]);
             v[e] = book[(c >> (4 * e)) & 15] * s;
             v[e + 1] = book[(c >> (4 * e + 4)) & 15] * s;
         }
@@ -276,9 +276,6 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) copy();  // weights: no kernel of the library writes them
-
     if constexpr (!kAffine) {
         for (int v = warp; v < 256; v += kWarps) {
             const float c0 = a.codebook[v & 15], c1 = a.codebook[v >> 4];
@@ -310,8 +307,11 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
             put(c, row, make_uint4(0, 0, 0, 0));
             if (kAffine && c % kPer == 0) put_start(c / kPer, row, 0.f);
         }
+    // codes and scales too may be what the kernel before this one writes (a quantisation, a copy)
     griddep_wait();
     griddep_launch_dependents();
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) copy();
     // the warps take the rows in turn, or where those are few, pieces of one: n8 is a multiple of 16,
     // so the lanes of a block stay together
     constexpr int kBatch = 4;  // loads in flight a thread

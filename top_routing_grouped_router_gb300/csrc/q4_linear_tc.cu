@@ -163,10 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     bool ok = true;
     float acc[kHalf];  // adding warps: this output's sums
 
-    // Codes and scales are weights, which no kernel of the library writes: they stream while the
-    // kernel before this one ends.
+    // Codes and scales, as much as x, may be what the kernel before this one writes: every warp that
+    // reads an array waits for that kernel first.
     if (warp >= kUnpack0) {
-            // x, by the unpacking and adding warps before they have anything to do
+        // x, by the unpacking and adding warps before they have anything to do
         const int n8 = (s1 - s0) * (kIn / 8);
         auto put = [&](int c, int r, uint4 v) {  // 16-byte piece c of a row: 128-byte swizzle within 64 inputs
             *reinterpret_cast<uint4 *>(xs + ((size_t)(c >> 3) * COLS + r) * 128 + (((c & 7) ^ (r & 7)) * 16)) = v;
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
     }
 
     if (warp == kLoadWarp) {
+        griddep_wait();
         int filled = 0;  // stages filled so far
         const int srow = lane >> 1, shalf = lane & 1;
         int slot = 0;

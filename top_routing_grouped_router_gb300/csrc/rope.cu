@@ -36,7 +36,10 @@ template <>
 struct Raw<uint16_t> {
     uint4 v;
     __device__ __forceinline__ void load(const uint16_t *p) { v = ldp16(p); }
-    __device__ __forceinline__ void load_const(const uint16_t *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    // through L1: weights that every row of the block reads (plain C++ loads: 1583 fp32 tokens 7.5 us, 6.6)
+    __device__ __forceinline__ void load_cached(const uint16_t *p) {
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    }
     __device__ __forceinline__ void get(uint64_t *f) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -50,9 +53,9 @@ struct Raw<float> {
         a = ldp16f(p);
         b = ldp16f(p + 4);
     }
-    __device__ __forceinline__ void load_const(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p + 4));
+    __device__ __forceinline__ void load_cached(const float *p) {
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "l"(p));
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w) : "l"(p + 4));
     }
     __device__ __forceinline__ void get(uint64_t *f) const {
         f[0] = attn::pair(a.x, a.y);
@@ -86,16 +89,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int t0 = blockIdx.x * TB, tokens = min(TB, a.n_tokens - t0);
     constexpr int kGroups = kThreads / LG;
 
-    // weights: no kernel of the library writes them
+    // the table and the norms' weights too may be what the kernel before this one writes
+    griddep_wait();
+    griddep_launch_dependents();
     constexpr int kTurns = (TB * kMaxPairs + kThreads - 1) / kThreads;
     uint64_t turn[kTurns];
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
         const int at = tid + i * kThreads;
-        if (at < TB * pairs) turn[i] = __ldg(reinterpret_cast<const unsigned long long *>(r.turns) + at % pairs);
+        if (at < TB * pairs) turn[i] = r.turns[at % pairs];
     }
-    griddep_wait();
-    griddep_launch_dependents();
 
     // Row i of the block: first the tokens' q heads, then their k and v heads.  A group takes rows
     // group, group + kGroups, ..; its place among a token's heads moves on without a division.
@@ -218,13 +221,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     uint64_t g[4];
                     Raw<T> w;
                     if (on_a) {
-                        w.load_const(gamma + da);
+                        w.load_cached(gamma + da);
                         w.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[e] = attn::mul2(attn::mul2(f[e], rs2), g[e]);
                     }
                     if (on_b) {
-                        w.load_const(gamma + db);
+                        w.load_cached(gamma + db);
                         w.get(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[4 + e] = attn::mul2(attn::mul2(f[4 + e], rs2), g[e]);

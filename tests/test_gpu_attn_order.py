@@ -99,3 +99,36 @@ def test_rope_append_reads_what_the_kernel_before_wrote(what, tokens, graph):
     target = {"turns": rope.tensors[0].view(torch.float32)[:8], "gamma": gamma[:8], "q": x.view(-1)[:8]}[what]
     _reads_what_was_written(target, lambda: moe.moe_rope_append(d.shape, rope, x, k, v, d.cache, d.batch, d.out,
                                                                 workspace=d.ws), lambda: d.out, graph)
+
+
+@pytest.mark.parametrize("T,K,N", [(33, 2048, 20000), (20, 4096, 2112)])
+def test_q4_linear_wait_limit_starts_after_the_kernel_before(T, K, N):
+    # the waits of the tensor-core kernel are limited in time; the time that the kernel before it still
+    # runs does not count
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.rand(N, K // 64, generator=g, device="cuda").add_(0.5).bfloat16()
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    out, want = (torch.empty(T, N, device="cuda") for _ in range(2))
+    shape, weight = moe.make_q4_linear_shape(T, K, N, "f32"), moe.make_q4_weight(codes, scales, UNIFORM)
+    write = Writer(x.view(-1)[:8])
+    for _ in range(2):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        write()
+        end.record()
+    moe.moe_q4_linear(shape, x, weight, want)
+    torch.cuda.synchronize()
+    limit = int(start.elapsed_time(end) * 1e6) // 4
+    assert limit > 300_000  # ns: far above any wait of the call itself
+    moe.moe_debug_set_waits(limit)
+    try:
+        for _ in range(3):
+            write()
+            moe.moe_q4_linear(shape, x, weight, out)
+            assert moe.moe_q4_linear_read_error() == 0
+            assert torch.equal(out, want)
+            out.zero_()
+    finally:
+        moe.moe_debug_set_waits()

@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
                 mbar_wait_drain(smem_u32(&cf[i % m.ring]), (i / m.ring) & 1, wt);
         }
     } else if (warp == kMmaWarp) {
+        griddep_wait();  // or the limit of its first wait would count the time that the kernel before still runs
         const uint32_t idesc = instr_desc(kOut, COLS);
         int i = 0;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(xf), 0, wt));

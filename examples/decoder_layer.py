@@ -104,8 +104,10 @@ class DecoderLayer:
         return p["y"]
 
     def errors(self, p):
-        """Device-side error codes of the plan's workspaces (0: none); synchronises."""
-        return moe.moe_read_device_error(p["attn_ws"]), moe.moe_read_device_error(p["moe_ws"])
+        """Device-side error codes of the attention half (its projections, then the plan's workspace) and of the MoE
+        half (0: none); synchronises.  The projections' word is one for all streams of the device."""
+        linear, attn = moe.moe_q4_linear_read_error(), moe.moe_read_device_error(p["attn_ws"])
+        return linear or attn, moe.moe_read_device_error(p["moe_ws"])
 
 
 def main():

@@ -615,9 +615,11 @@ MOE_API int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64
 /*
  * Reads and clears the error word of moe_q4_linear on the current device
  * (MOE_ERR_DEVICE if a bounded wait of its tensor-core kernel ran out, which no
- * healthy call does; that call's results are unspecified).  Synchronises
- * `stream`.  Returns MOE_ERR_NULLPTR for a NULL code, MOE_ERR_LAUNCH if the copy
- * failed.
+ * healthy call does; that call's results are unspecified).  The call has no
+ * workspace: the word is one for all its calls on the device, whatever their
+ * stream, so whoever reads it learns of (and clears) the errors of every stream's
+ * calls that have ended.  Synchronises `stream`.  Returns MOE_ERR_NULLPTR for a
+ * NULL code, MOE_ERR_LAUNCH if the copy failed.
  */
 MOE_API int moe_q4_linear_read_error(int32_t *code, moe_stream_t stream);
 

@@ -91,3 +91,20 @@ def test_a_full_cache_is_refused(example):
     layer = example.DecoderLayer(**SIZES)
     with pytest.raises(RuntimeError):
         layer.plan({0: SIZES["page_size"] * SIZES["max_pages"] + 1})
+
+
+def test_a_failed_projection_is_an_error(example):
+    # a projection whose tensor-core kernel gave up (its operands can never be complete) shows in errors()
+    import top_routing_grouped_router_gb300 as moe
+    layer = example.DecoderLayer()
+    p = layer.plan({0: 20})
+    x = torch.zeros(20, layer.hidden, dtype=torch.bfloat16, device="cuda")
+    moe.moe_debug_set_waits(1_000_000, 1)
+    try:
+        moe.moe_q4_linear(p["in"], x, layer.w_qkv, p["qkv"])
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_debug_set_waits()
+    assert layer.errors(p) == (-7, 0)
+    layer.step(p, x)
+    assert layer.errors(p) == (0, 0)

@@ -508,7 +508,7 @@ def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
 
 
 def moe_q4_linear_read_error(stream=None) -> int:
-    """Reads and clears the 4-bit linear's device error word (synchronises the stream)."""
+    """Reads and clears the 4-bit linear's device error word, one for all streams (synchronises `stream`)."""
     code = ctypes.c_int32(0)
     _check(lib().moe_q4_linear_read_error(ctypes.byref(code), _stream(stream)), "moe_q4_linear_read_error")
     return code.value

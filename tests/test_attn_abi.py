@@ -157,3 +157,91 @@ def test_binding_refuses_scattered_tensors():
         moe.make_kv_cache(k.transpose(2, 3), k.transpose(2, 3))
     c = moe.make_kv_cache(torch.zeros(3, 16, 2, 64).transpose(1, 2), torch.zeros(3, 16, 2, 64).transpose(1, 2))
     assert (c.page_stride, c.head_stride, c.token_stride) == (2048, 64, 128)
+
+
+def _on_gpu(t):
+    """A host tensor that says it is on the GPU, for calls that are refused before the library."""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+
+    return t.as_subclass(OnGpu)
+
+
+def _binding_call(kind=lambda t: t, **kw):
+    """One call of a binding on tensors that are right but for `kw`: name -> tensor."""
+    torch = pytest.importorskip("torch")
+    bf, i32 = torch.bfloat16, torch.int32
+    a = dict(q=torch.zeros(8, 8, 64, dtype=bf), k=torch.zeros(8, 2, 64, dtype=bf), v=torch.zeros(8, 2, 64, dtype=bf),
+             out=torch.zeros(8, 8, 64, dtype=bf), lse=torch.zeros(8, 8), cu=torch.zeros(5, dtype=i32),
+             kv=torch.zeros(4, dtype=i32), table=torch.zeros(4, 5, dtype=i32), cache=torch.zeros(10, 2, 16, 64, dtype=bf),
+             positions=torch.zeros(8, dtype=i32), gamma=torch.ones(64, dtype=bf), x=torch.zeros(4, 256, dtype=bf),
+             y=torch.zeros(4, 48, dtype=bf), res=torch.zeros(4, 48, dtype=bf), codes=torch.zeros(48, 128, dtype=torch.uint8),
+             scales=torch.zeros(48, 4, dtype=bf), ws=torch.zeros(1 << 20, dtype=torch.uint8), call="attn")
+    a.update(kw)
+    a = {n: kind(t) if isinstance(t, torch.Tensor) else t for n, t in a.items()}
+    if a["call"] == "q4":
+        moe.moe_q4_linear(moe.make_q4_linear_shape(4, 256, 48), a["x"], moe.make_q4_weight(a["codes"], a["scales"], [0] * 16),
+                          a["y"], residual=a["res"], stream=0)
+        return
+    shape = moe.make_attn_shape(**GOOD)
+    batch, cache = moe.make_attn_batch(a["cu"], a["kv"], a["table"]), moe.make_kv_cache(a["cache"], a["cache"].clone())
+    if a["call"] == "rope":
+        rope = moe.make_rope(64, q_gamma=a["gamma"], device="cpu")
+        rope.on_host &= kind is not _on_gpu  # its table
+        moe.moe_rope_append(shape, rope, a["q"], a["k"], a["v"], cache, batch, a["out"], a["positions"], a["ws"], 0)
+    else:
+        moe.moe_paged_attention(shape, a["q"], cache, batch, a["out"], lse=a["lse"], workspace=a["ws"], stream=0)
+
+
+@pytest.mark.parametrize("call,name,make", [
+    ("attn", "lse", lambda t: t.zeros(8, 8, dtype=t.bfloat16)), ("attn", "lse", lambda t: t.zeros(7, 8)),
+    ("attn", "lse", lambda t: t.zeros(8, 7)), ("attn", "q", lambda t: t.zeros(8, 8, 64)),
+    ("attn", "q", lambda t: t.zeros(7, 8, 64, dtype=t.bfloat16)), ("attn", "out", lambda t: t.zeros(8, 8, 64).half()),
+    ("attn", "out", lambda t: t.zeros(8, 8, 56).bfloat16()), ("attn", "out", lambda t: t.zeros(8, 4, 64).bfloat16()),
+    ("attn", "cu", lambda t: t.zeros(5)), ("attn", "cu", lambda t: t.zeros(4).int()), ("attn", "kv", lambda t: t.zeros(3).int()),
+    ("attn", "kv", lambda t: t.zeros(4).long()), ("attn", "table", lambda t: t.zeros(4, 4).int()),
+    ("attn", "table", lambda t: t.zeros(4, 10).int()[:, ::2]), ("attn", "cache", lambda t: t.zeros(10, 2, 16, 64)),
+    ("attn", "cache", lambda t: t.zeros(9, 2, 16, 64).bfloat16()), ("attn", "cache", lambda t: t.zeros(10, 2, 8, 64).bfloat16()),
+    ("rope", "k", lambda t: t.zeros(8, 1, 64).bfloat16()), ("rope", "v", lambda t: t.zeros(8, 2, 64)),
+    ("rope", "out", lambda t: t.zeros(8, 8, 64)), ("rope", "positions", lambda t: t.zeros(8).long()),
+    ("rope", "positions", lambda t: t.zeros(7).int()), ("rope", "gamma", lambda t: t.ones(64)),
+    ("rope", "gamma", lambda t: t.ones(60).bfloat16()), ("q4", "x", lambda t: t.zeros(4, 256)),
+    ("q4", "x", lambda t: t.zeros(3, 256).bfloat16()), ("q4", "x", lambda t: t.zeros(4, 248).bfloat16()),
+    ("q4", "y", lambda t: t.zeros(4, 48)), ("q4", "res", lambda t: t.zeros(4, 48)),
+    ("q4", "codes", lambda t: t.zeros(48, 128)), ("q4", "codes", lambda t: t.zeros(47, 128).to(t.uint8)),
+    ("q4", "scales", lambda t: t.zeros(48, 4)), ("q4", "scales", lambda t: t.zeros(48, 8).bfloat16())])
+def test_binding_refuses_wrong_types_and_sizes(call, name, make):
+    # a type, a size or a number of rows that the kernels would read or write past: refused before the library
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError) as e:
+        _binding_call(_on_gpu, call=call, **{name: make(torch)})
+    assert "on the GPU" not in str(e.value)
+
+
+@pytest.mark.parametrize("call", ["attn", "rope", "q4"])
+def test_binding_refuses_host_tensors(call):
+    with pytest.raises(ValueError, match="on the GPU"):
+        _binding_call(call=call)
+
+
+def test_binding_takes_any_stride_of_a_single_row():
+    # a tensor of one row is contiguous whatever its row stride says
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    x = torch.empty(64, 1, dtype=bf).t()
+    assert x.stride() == (1, 1) and moe._rows(x, 64, "x") == 64
+    q = torch.empty(1, 4, 64, dtype=bf).as_strided((1, 4, 64), (8, 64, 1))
+    assert moe._head_rows(q, 64, 256, "q") == 256
+    wide = torch.empty(3, 320, dtype=bf)
+    assert moe._rows(wide[:, :64], 64, "x") == 320 and moe._rows(wide[:, 5:6], 1, "x") == 320
+    assert moe._head_rows(wide[:, :256].view(3, 4, 64), 64, 256, "q") == 320
+
+
+def test_binding_follows_a_changed_shape():
+    torch = pytest.importorskip("torch")
+    s = moe.make_attn_shape(**GOOD)
+    assert moe._attn_checks(s)[0] == 8 * 8 * 64 and s._checks[5] is torch.bfloat16
+    s.n_tokens, s.dtype = 9, 0
+    assert s._checks is None and moe._attn_checks(s)[0] == 9 * 8 * 64 and s._checks[5] is torch.float32

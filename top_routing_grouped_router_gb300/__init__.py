@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 __all__ = [
@@ -67,21 +68,30 @@ class MoEQ4(ctypes.Structure):
 class MoEAttnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_seqs", "n_heads", "n_kv_heads", "head_dim", "page_size",
                                               "n_pages", "max_pages", "max_q", "dtype")]
+    _checks = None  # what _attn_checks made of the fields; a field that is set takes it away
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name != "_checks":
+            super().__setattr__("_checks", None)
 
 
 class MoEAttnBatch(ctypes.Structure):
     _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+    sizes = None  # of make_attn_batch's tensors: sequences that fit, the table's width, whether one is in host memory
 
 
 class MoEKVCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+    sizes = None  # of make_kv_cache's tensors: pages, heads, slots, head size, type, whether one is in host memory
 
 
 class MoERope(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
                 ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_gamma", ctypes.c_void_p),
                 ("k_gamma", ctypes.c_void_p)]
+    weights, on_host = None, False  # type and length of make_rope's norm weights; whether a tensor is in host memory
 
 
 class MoEQ4LinearShape(ctypes.Structure):
@@ -90,6 +100,7 @@ class MoEQ4LinearShape(ctypes.Structure):
 
 class MoEQ4Weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("codebook", ctypes.c_float * 16)]
+    sizes = None  # of make_q4_weight's tensors: codes, scales, whether one is in host memory
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -382,23 +393,46 @@ def make_attn_shape(n_tokens, n_seqs, n_heads, n_kv_heads, head_dim, page_size, 
                         int(n_pages), int(max_pages), int(max_q), _DT[act] if isinstance(act, str) else int(act))
 
 
+_INT32 = -1  # of _torch_dtype only
+
+
+def _torch_dtype(code):
+    """The torch type of MOE_DT_F32, MOE_DT_BF16 or _INT32 (None of any other)."""
+    global _torch_dtype
+    import torch
+    _torch_dtype = {MOE_DT_F32: torch.float32, MOE_DT_BF16: torch.bfloat16, _INT32: torch.int32}.get
+    return _torch_dtype(code)
+
+
+def _need(t, what, dtypes):
+    """A contiguous tensor of one of these types (an int address or None is the caller's own matter); whether it is in
+    host memory, which the call that uses it refuses."""
+    if t is None or isinstance(t, int):
+        return False
+    if str(t.dtype)[6:] not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {' or '.join(dtypes)} tensor, not {t.dtype} with strides {t.stride()}")
+    return not t.is_cuda
+
+
 def make_attn_batch(cu_q, kv_len, block_table) -> MoEAttnBatch:
     """The sequences of a batch: int32 device tensors cu_q [B + 1], kv_len [B], block_table [B][max_pages]."""
-    for t in (cu_q, kv_len, block_table):
-        if not isinstance(t, int) and not (t.is_contiguous() and t.element_size() == 4):
-            raise ValueError("cu_q, kv_len and block_table are contiguous int32 tensors")
+    named = (cu_q, "cu_q"), (kv_len, "kv_len"), (block_table, "block_table")
+    host = [_need(t, what, ("int32",)) for t, what in named]
     out = MoEAttnBatch(_ptr(cu_q), _ptr(kv_len), _ptr(block_table))
     out.tensors = (cu_q, kv_len, block_table)
+    if not any(isinstance(t, int) for t in out.tensors):
+        out.sizes = min(len(cu_q) - 1, len(kv_len), len(block_table)), block_table.shape[1], any(host)
     return out
 
 
 def make_kv_cache(k, v) -> MoEKVCache:
     """A paged cache over device tensors k, v of logical shape [pages][kv heads][slots][head dim]: any strides (the
     same for both) whose last is 1, so a [pages][slots][heads][dim] cache is passed as its transpose(1, 2)."""
-    if k.stride() != v.stride() or k.shape != v.shape or k.stride(3) != 1:
-        raise ValueError("k and v need equal shapes and strides, and contiguous head elements")
+    if k.stride() != v.stride() or k.shape != v.shape or k.stride(3) != 1 or k.dtype != v.dtype:
+        raise ValueError("k and v need equal shapes, strides and types, and contiguous head elements")
     out = MoEKVCache(_ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2))
     out.tensors = (k, v)
+    out.sizes = (*k.shape, k.dtype, not (k.is_cuda and v.is_cuda))
     return out
 
 
@@ -422,6 +456,12 @@ def make_rope(rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1
     out = MoERope(int(rot_dim), int(bool(interleaved)), mscale, float(eps), _ptr(table), _ptr(q_gamma),
                   _ptr(k_gamma))
     out.tensors = (table, q_gamma, k_gamma)
+    gammas = (q_gamma, "q_gamma"), (k_gamma, "k_gamma")
+    out.on_host = any([_need(t, what, ("float32", "bfloat16")) for t, what in gammas]) or not table.is_cuda
+    known = {(t.dtype, t.numel()) for t, _ in gammas if t is not None and not isinstance(t, int)}
+    if len(known) > 1:
+        raise ValueError(f"q_gamma and k_gamma differ: {known}")
+    out.weights = known.pop() if known else None
     return out
 
 
@@ -431,23 +471,71 @@ def make_q4_linear_shape(T, K, N, out="bf16", q_block=64) -> MoEQ4LinearShape:
 
 def make_q4_weight(codes, scales, codebook) -> MoEQ4Weight:
     """One 4-bit weight matrix: codes [N][K/2] uint8, scales [N][K/q_block] bf16, 16 codebook values (host)."""
+    host = _need(codes, "codes", ("uint8",)), _need(scales, "scales", ("bfloat16",))
     out = MoEQ4Weight(_ptr(codes), _ptr(scales), (ctypes.c_float * 16)(*[float(c) for c in codebook]))
     out.tensors = (codes, scales)
+    if not any(isinstance(t, int) for t in out.tensors):
+        out.sizes = codes.numel(), scales.numel(), any(host)
     return out
 
 
 def _row_stride(t, what):
     """Elements between the rows of a [rows][heads][dim] or [rows][cols] tensor whose rows are contiguous."""
     st = t.stride()
-    if st[-1] != 1 or (len(st) == 3 and st[1] != t.shape[2] and t.shape[1] != 1):
+    if (st[-1] != 1 and t.shape[-1] != 1) or (len(st) == 3 and st[1] != t.shape[2] and t.shape[1] != 1):
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return st[0]
+    return st[0] if t.shape[0] != 1 else t.numel()  # a single row's own stride says nothing
 
 
-def _head_rows(t, dim, what):
+def _head_rows(t, dim, wide, what):
     """_row_stride of a [rows][heads][dim] tensor, quick where the heads follow one another."""
     row, head, elem = t.stride()
-    return row if elem == 1 and head == dim else _row_stride(t, what)
+    return row if elem == 1 and head == dim and row >= wide else _row_stride(t, what)
+
+
+def _rows(t, cols, what):
+    """_row_stride of a [rows][cols] tensor."""
+    row, elem = t.stride()
+    return row if elem == 1 and row >= cols else _row_stride(t, what)
+
+
+def _wrong(*tensors):
+    """The error of the first (name, tensor, type, sizes) whose tensor is not that; its rows may be more."""
+    for what, t, dtype, (rows, *sizes) in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape[0] < rows or list(t.shape[1:]) != sizes):
+            return ValueError(f"{what}: {dtype} {[rows, *sizes]} (more rows are fine), not {t.dtype} {list(t.shape)}")
+    for what, t, *_ in tensors:
+        if t is not None and not t.is_cuda:
+            return ValueError(f"{what}: not on the GPU")
+    return ValueError("a tensor's type, size or device is wrong")
+
+
+_q4_ints = struct.Struct("5i").unpack  # the fields of MoEQ4LinearShape at once
+
+
+def _attn_checks(shape):
+    """What the tensors of a call are held against: elements of q and k, their rows' widths, the type, and the sizes of
+    the batch's and the cache's tensors."""
+    n, dtype = shape.n_tokens, _torch_dtype(shape.dtype)
+    wide, kv_wide = shape.n_heads * shape.head_dim, shape.n_kv_heads * shape.head_dim
+    shape._checks = (n * wide, n * kv_wide, wide, kv_wide, shape.head_dim, dtype, (shape.n_seqs, shape.max_pages, False),
+                     (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim, dtype, False))
+    return shape._checks
+
+
+def _check_batch(batch, cache, batch_sizes, cache_sizes):
+    """That the tensors of the batch and of the cache have these sizes; more sequences and pages are fine."""
+    if batch.sizes is not None:
+        if batch.sizes[0] < batch_sizes[0] or batch.sizes[1] != batch_sizes[1]:
+            raise ValueError("batch: tensors for %d sequences of %d pages, not %d of %d" %
+                             (*batch.sizes[:2], *batch_sizes[:2]))
+        if batch.sizes[2]:
+            raise ValueError("batch: not on the GPU")
+    if cache.sizes is not None:
+        if cache.sizes[0] < cache_sizes[0] or cache.sizes[1:5] != cache_sizes[1:5]:
+            raise ValueError(f"cache: {cache.sizes[4]} {cache.sizes[:4]}, not {cache_sizes[4]} {cache_sizes[:4]}")
+        if cache.sizes[5]:
+            raise ValueError("cache: not on the GPU")
 
 
 def _current_stream():
@@ -467,41 +555,89 @@ def moe_attn_workspace_size(shape: MoEAttnShape) -> int:
     return n.value
 
 
-# These calls are made several times a layer and step: structs pass by their addresses and
-# nothing is looked up twice, so that the host keeps ahead of kernels of a few microseconds.
+# These calls are made several times a layer and step: structs pass by their addresses, nothing is looked up twice
+# and the tensors are checked in one expression, so that the host keeps ahead of kernels of a few microseconds.
 
 def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, workspace=None, stream=None):
     """q_out = rotated q; rotated k and v into their cache slots.  q, q_out [N][heads][dim], k, v [N][kv heads][dim]
-    (rows may be slices of a wider tensor)."""
-    ref, dim = ctypes.byref, shape.head_dim
+    (rows may be slices of a wider tensor), positions int32 [N]."""
+    at = ctypes.addressof
+    need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, cache_sizes = shape._checks or _attn_checks(shape)
+    if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
+        _check_batch(batch, cache, batch_sizes, cache_sizes)
+    if (q.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype or
+            q.numel() < need or k.numel() < kv_need or v.numel() < kv_need or q_out.numel() < need or
+            not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda)):
+        n, heads, kv_heads = shape.n_tokens, shape.n_heads, shape.n_kv_heads
+        raise _wrong(("q", q, dtype, (n, heads, dim)), ("k", k, dtype, (n, kv_heads, dim)),
+                     ("v", v, dtype, (n, kv_heads, dim)), ("q_out", q_out, dtype, (n, heads, dim)))
+    if rope.weights is not None and rope.weights != (dtype, dim):
+        raise ValueError(f"q_gamma, k_gamma: {dtype} [{dim}], not {rope.weights}")
+    if rope.on_host:
+        raise ValueError("rope: not on the GPU")
+    if positions is not None and not isinstance(positions, int):
+        int32 = _torch_dtype(_INT32)
+        if (positions.dtype is not int32 or positions.numel() * wide < need or not positions.is_contiguous() or
+                not positions.is_cuda):
+            raise _wrong(("positions (contiguous)", positions, int32, (shape.n_tokens,)))
+        positions = positions.data_ptr()
     rc = (_lib or lib()).moe_rope_append(
-        ref(shape), ref(rope), q.data_ptr(), _head_rows(q, dim, "q"), k.data_ptr(), _head_rows(k, dim, "k"),
-        v.data_ptr(), _head_rows(v, dim, "v"), ref(cache), ref(batch), None if positions is None else _ptr(positions),
-        q_out.data_ptr(), _head_rows(q_out, dim, "q_out"), workspace.data_ptr(), workspace.nbytes,
-        _current_stream() if stream is None else _stream(stream))
+        at(shape), at(rope), q.data_ptr(), _head_rows(q, dim, wide, "q"), k.data_ptr(), _head_rows(k, dim, kv_wide, "k"),
+        v.data_ptr(), _head_rows(v, dim, kv_wide, "v"), at(cache), at(batch), positions, q_out.data_ptr(),
+        _head_rows(q_out, dim, wide, "q_out"), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_rope_append")
 
 
 def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, workspace=None, stream=None):
-    """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5."""
-    if lse is not None and not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
-    ref, dim = ctypes.byref, shape.head_dim
+    """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5.  q, out
+    [N][heads][dim] (rows may be slices of a wider tensor), lse fp32 [N][heads]."""
+    at = ctypes.addressof
+    need, _, wide, _, dim, dtype, batch_sizes, cache_sizes = shape._checks or _attn_checks(shape)
+    if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
+        _check_batch(batch, cache, batch_sizes, cache_sizes)
+    if (q.dtype is not dtype or out.dtype is not dtype or q.numel() < need or out.numel() < need or
+            not (q.is_cuda and out.is_cuda)):
+        sizes = shape.n_tokens, shape.n_heads, dim
+        raise _wrong(("q", q, dtype, sizes), ("out", out, dtype, sizes))
+    if lse is not None:
+        fp32 = _torch_dtype(MOE_DT_F32)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        if lse.dtype is not fp32 or lse.numel() * dim < need or not lse.is_cuda:
+            raise _wrong(("lse", lse, fp32, (shape.n_tokens, shape.n_heads)))
+        lse = lse.data_ptr()
     rc = (_lib or lib()).moe_paged_attention(
-        ref(shape), q.data_ptr(), _head_rows(q, dim, "q"), ref(cache), ref(batch), dim ** -0.5 if scale is None else scale,
-        out.data_ptr(), _head_rows(out, dim, "out"), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _current_stream() if stream is None else _stream(stream))
+        at(shape), q.data_ptr(), _head_rows(q, dim, wide, "q"), at(cache), at(batch),
+        dim ** -0.5 if scale is None else scale, out.data_ptr(), _head_rows(out, dim, wide, "out"), lse,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_paged_attention")
 
 
 def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
-    """out = x . W^T (+ residual) with a 4-bit weight (make_q4_weight)."""
-    ref = ctypes.byref
+    """out = x . W^T (+ residual) with a 4-bit weight (make_q4_weight); x [T][K] and residual [T][N] bf16, out [T][N]."""
+    at = ctypes.addressof
+    T, K, N, out_dtype, q_block = _q4_ints(shape)
+    bf16, out_dtype = _torch_dtype(MOE_DT_BF16), _torch_dtype(out_dtype)
+    if weight.sizes is not None:
+        codes, scales, on_host = weight.sizes
+        if 2 * codes != N * K or scales * q_block != N * K:
+            raise ValueError(f"weight: {codes} bytes of codes and {scales} scales for [{N}][{K}] in blocks of {q_block}")
+        if on_host:
+            raise ValueError("weight: not on the GPU")
+    if (x.dtype is not bf16 or out.dtype is not out_dtype or x.numel() < T * K or out.numel() < T * N or
+            not (x.is_cuda and out.is_cuda)):
+        raise _wrong(("x", x, bf16, (T, K)), ("out", out, out_dtype, (T, N)))
+    res_row = 0
+    if residual is not None:
+        if residual.dtype is not bf16 or residual.numel() < T * N or not residual.is_cuda:
+            raise _wrong(("residual", residual, bf16, (T, N)))
+        res_row, residual = _rows(residual, N, "residual"), residual.data_ptr()
     rc = (_lib or lib()).moe_q4_linear(
-        ref(shape), x.data_ptr(), _row_stride(x, "x"), ref(weight), None if residual is None else residual.data_ptr(),
-        0 if residual is None else _row_stride(residual, "residual"), out.data_ptr(), _row_stride(out, "out"),
+        at(shape), x.data_ptr(), _rows(x, K, "x"), at(weight), residual, res_row, out.data_ptr(), _rows(out, N, "out"),
         _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_q4_linear")

@@ -28,3 +28,38 @@ def test_a_call_without_a_workspace_is_refused():
         moe.moe_rope_append(d.shape, moe.make_rope(128), d.q, d.q[:, :4].contiguous(), d.q[:, 4:].contiguous(), d.cache,
                             d.batch, d.out)
     assert e.value.status == -4
+
+
+@pytest.mark.parametrize("what", ["negative length", "length past the table", "idle length past the table", "long chunk"])
+@pytest.mark.parametrize("tokens", [1, 700])
+def test_rope_append_records_what_attention_does(what, tokens):
+    # a cache length outside [0, max_pages * page_size], of a sequence without new tokens too, and a chunk
+    # past max_q; what the other sequences bring is stored all the same
+    q_len, kv_len = [3, 0, tokens, 2], [5, 9, tokens + 1, 4]
+    bt = make_batch("bf16", 4, 2, 64, 16, q_len, kv_len, seed=2, fill=5.0)
+    d = Dev(bt, max_q=tokens if tokens > 3 else 3)
+    x = torch.randn(bt.tokens, 4, 64, device="cuda").bfloat16()
+    rope = moe.make_rope(64)
+    append = lambda: moe.moe_rope_append(d.shape, rope, x, x[:, :2].contiguous(), x[:, 2:].contiguous(),  # noqa: E731
+                                         d.cache, d.batch, d.out, workspace=d.ws)
+    append()
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_error(d.ws) == 0
+    first_k = d.k.clone()
+    if what == "negative length":
+        d.kv_len[2] = -1
+    elif what == "length past the table":
+        d.kv_len[2] = bt.table.shape[1] * 16 + 1
+    elif what == "idle length past the table":
+        d.kv_len[1] = bt.table.shape[1] * 16 + 1
+    else:
+        d.shape.max_q = 2
+    d.k.fill_(5.0)
+    append()
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_error(d.ws) == -7
+    for b in (0, 3):
+        pages = bt.table[b, :-(-kv_len[b] // 16)].long().cuda()
+        new = slice(kv_len[b] - q_len[b], kv_len[b])
+        rows = lambda c: c[pages].transpose(0, 1).reshape(2, -1, 64)[:, new]  # noqa: E731
+        assert torch.equal(rows(d.k), rows(first_k))

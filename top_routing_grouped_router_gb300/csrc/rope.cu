@@ -158,13 +158,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     __syncthreads();
     for (int b = tid; b < a.n_seqs; b += kThreads) {
         const int c0 = ldp(a.cu_q + b), c1 = ldp(a.cu_q + b + 1), kv = ldp(a.kv_len + b);
-        if (blockIdx.x == 0 && (c0 < 0 || c1 < c0 || c1 > a.n_tokens)) record_error(a.err, MOE_ERR_DEVICE);
+        if (blockIdx.x == 0 && (c0 < 0 || c1 < c0 || c1 > a.n_tokens || c1 - c0 > a.max_q || kv < 0 ||
+                                kv > (int64_t)a.max_pages * a.page_size))
+            record_error(a.err, MOE_ERR_DEVICE);
         if (c0 < t0 + tokens && c1 > t0) {
 #pragma unroll
             for (int i = 0; i < TB; ++i)
                 if (c0 <= t0 + i && t0 + i < c1) {
                     seq[i] = b;
-                    where[i] = kv - (c1 - t0 - i);
+                    where[i] = max(kv, 0) - (c1 - t0 - i);
                 }
         }
     }

@@ -63,3 +63,26 @@ def test_rope_append_records_what_attention_does(what, tokens):
         new = slice(kv_len[b] - q_len[b], kv_len[b])
         rows = lambda c: c[pages].transpose(0, 1).reshape(2, -1, 64)[:, new]  # noqa: E731
         assert torch.equal(rows(d.k), rows(first_k))
+
+
+@pytest.mark.parametrize("what", ["falls", "first", "idle length", "idle negative length"])
+@pytest.mark.parametrize("dtype,dim,most", [("bf16", 128, 1), ("bf16", 64, 40), ("bf16", 128, 40), ("bf16", 96, 3),
+                                            ("f32", 64, 40)])
+def test_attention_records_wrong_data_of_idle_sequences(what, dtype, dim, most):
+    # a cu_q that falls between two sequences or starts late and a wrong length of a sequence without new
+    # tokens, by every kernel
+    q_len, kv_len = [most, 0, most, 0, 2], [600, 9, most, 3, 700]
+    d = Dev(make_batch(dtype, 4, 2, dim, 16, q_len, kv_len, seed=2))
+    assert d.attend(0.1) == 0
+    if what == "falls":
+        d.cu_q[1] = d.cu_q[2] + 1  # the idle one ends before it starts
+        d.shape.max_q = d.shape.n_tokens if most > 5 else 2
+    elif what == "first":
+        d.cu_q[:2] = -3
+        d.cu_q[1] = 0
+    elif what == "idle length":
+        d.kv_len[1] = d.table.shape[1] * 16 + 1
+    else:
+        d.kv_len[3] = -1
+    assert d.attend(0.1) == -7
+    assert moe.moe_read_device_error(d.ws) == 0

@@ -52,6 +52,10 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
     float *P = V + kKeys * D + warp * kKeys * 4;  // [key][row] of this warp
     // tiles from the last: with a causal mask the last tokens of a chunk have the most keys
     const TileAt at = find_tile(a, int(gridDim.x - 1 - blockIdx.x), tt, scratch);
+    // wrong lengths of sequences without a tile are recorded too, by one block (of the number that all tiles may
+    // need at most, the first is often idle)
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0)
+        for (int b = tid; b < a.n_seqs; b += kThreads) load_seq(a, b);
     if (at.b < 0) return;
     const Seq s = load_seq(a, at.b);
     const int slices = (a.group + kRows - 1) / kRows;

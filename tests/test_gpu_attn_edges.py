@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import top_routing_grouped_router_gb300 as moe  # noqa: E402
-from attn_ref import make_batch  # noqa: E402
+from attn_ref import attention, make_batch  # noqa: E402
 from test_gpu_attn import ATTN, Dev  # noqa: E402
 
 
@@ -86,3 +86,50 @@ def test_attention_records_wrong_data_of_idle_sequences(what, dtype, dim, most):
         d.kv_len[3] = -1
     assert d.attend(0.1) == -7
     assert moe.moe_read_device_error(d.ws) == 0
+
+
+# batch, one of its sequences and a place among that sequence's new tokens, for each kernel and join
+NAN = {"decode in clusters": ("few tokens", 2, 3), "decode in parts": ("decode 400 pairs", 7, 0),
+       "decode on the line": ("decode long", 0, 0),
+       "chunks whole": ("chunk ragged", 3, 60), "chunks of heads of 64": ("chunk dim 64", 1, 20),
+       "generic alone": ("chunk fp32", 0, 50), "generic in parts": ("head size 256 fp32", 0, 1)}
+
+
+def _nan_case(name, spoil):
+    # `spoil` makes values NaN and returns the rows [tokens][heads] that have to be NaN; the others are right
+    spec, b, j = NAN[name]
+    bt = make_batch(*ATTN[spec], seed=13)
+    out, lse, tol, tol_lse = attention(bt, 0.1)
+    nan = spoil(bt, b, j)
+    d = Dev(bt)
+    assert d.attend(0.1) == 0
+    got, got_lse = d.out.cpu().double(), d.lse.cpu().double()
+    assert torch.equal(got.isnan().all(-1), nan) and torch.equal(got.isnan().any(-1), nan)
+    assert torch.equal(got_lse.isnan(), nan)
+    assert ((got - out).abs() <= tol)[~nan].all() and ((got_lse - lse).abs() <= tol_lse)[~nan & lse.isfinite()].all()
+
+
+@pytest.mark.parametrize("name", list(NAN))
+def test_attention_of_a_nan_query_is_nan(name):
+    # not 0 with a log-sum of -inf, which says that the token sees no key
+    def spoil(bt, b, j):
+        t, h = int(bt.cu_q[b]) + j, bt.heads - 1
+        bt.q[t, h] = float("nan")
+        nan = torch.zeros(bt.tokens, bt.heads, dtype=torch.bool)
+        nan[t, h] = True
+        return nan
+    _nan_case(name, spoil)
+
+
+@pytest.mark.parametrize("name", [n for n in NAN if n.startswith(("chunks", "generic"))])
+def test_attention_of_a_nan_key_is_nan_for_those_who_see_it(name):
+    # the key of new token j: the tokens before it do not see it
+    def spoil(bt, b, j):
+        n, m = bt.q_len[b], bt.kv_len[b]
+        p = m - n + j
+        bt.k_cache[int(bt.table[b, p // bt.page]), 0, p % bt.page, 3] = float("nan")
+        nan = torch.zeros(bt.tokens, bt.heads, dtype=torch.bool)
+        t0 = int(bt.cu_q[b])
+        nan[t0 + j:t0 + n, :bt.heads // bt.kv_heads] = True
+        return nan
+    _nan_case(name, spoil)

@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
             const float mn = fmaxf(m[r], mx);
-            // a row that has seen nothing yet keeps m = -inf: its factor and probabilities are 0
-            const float f = mn == kNegInf ? 0.f : exp2f(m[r] - mn);
-            pr[r] = on && mn != kNegInf ? exp2f(sc[r] - mn) : 0.f;
+            // a row that has seen nothing yet keeps m = -inf; 0 in its place makes its factor 2^-inf = 0, and
+            // leaves a row whose scores are NaN what it is
+            const float z = mn == kNegInf ? 0.f : mn, f = exp2f(m[r] - z);
+            pr[r] = on ? exp2f(sc[r] - z) : 0.f;
             m[r] = mn;
             l[r] = l[r] * f + warp_sum(pr[r]);
 #pragma unroll

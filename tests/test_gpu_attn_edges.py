@@ -90,7 +90,7 @@ def test_attention_records_wrong_data_of_idle_sequences(what, dtype, dim, most):
 
 # batch, one of its sequences and a place among that sequence's new tokens, for each kernel and join
 NAN = {"decode in clusters": ("few tokens", 2, 3), "decode in parts": ("decode 400 pairs", 7, 0),
-       "decode on the line": ("decode long", 0, 0),
+       "decode on the line": ("decode long", 0, 0), "chunks cut": ("chunk over cache", 0, 100),
        "chunks whole": ("chunk ragged", 3, 60), "chunks of heads of 64": ("chunk dim 64", 1, 20),
        "generic alone": ("chunk fp32", 0, 50), "generic in parts": ("head size 256 fp32", 0, 1)}
 

@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
         for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * f0, acc[e].y * f0, acc[e].z * f0, acc[e].w * f0);
 #pragma unroll
         for (int p = 0; p < kFly; ++p) {
-            if (p0 + p >= n || pm[p] == kNegInf) continue;
+            if (p0 + p >= n || pl[p] == 0.f) continue;  // read again past the last, or no key seen; a NaN sum stays
             const float f = ex2(pm[p] - mn);
             l = fmaf(f, pl[p], l);
 #pragma unroll

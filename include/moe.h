@@ -603,7 +603,10 @@ typedef struct {
  * the weights for up to 64 rows; more rows repeat it):
  *   out[t][n] = sum_k codebook[code[n][k]] * scale[n][k / q_block] * x[t][k]
  *               (+ residual[t][n]),
- * accumulated in fp32, rounded once.
+ * accumulated in fp32, rounded once.  The codebook's values are kept to 24 bits for
+ * fp32 results and to 16 (2^-17 of a value) for bf16 ones; a codebook within 2^-20
+ * (fp32) or 2^-17 (bf16) of each value from a uniform one is taken as uniform.
+ * q_block that is neither 32 nor 64 times a power of two keeps the fp32 values.
  *   x [T][K] bf16, rows x_stride elements apart (a multiple of 8)
  *   residual [T][N] bf16, rows residual_stride apart, or NULL; out [T][N], rows
  *     out_stride apart (any stride >= N); residual may be out itself

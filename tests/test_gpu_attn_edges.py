@@ -7,8 +7,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import top_routing_grouped_router_gb300 as moe  # noqa: E402
-from attn_ref import attention, make_batch  # noqa: E402
-from test_gpu_attn import ATTN, Dev  # noqa: E402
+from attn_ref import FP32, attention, make_batch, q4_dense  # noqa: E402
+from test_gpu_attn import ATTN, NORMAL, UNIFORM, Dev  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -133,3 +133,29 @@ def test_attention_of_a_nan_key_is_nan_for_those_who_see_it(name):
         nan[t0 + j:t0 + n, :bt.heads // bt.kv_heads] = True
         return nan
     _nan_case(name, spoil)
+
+
+# ------------------------------------------------------------------------------- 4-bit linear
+
+# nearly uniform: two small values off by 2^-18 of themselves; computed in fp32 steps; a zero that rounding missed
+BENT = [v * (1 + 2.0 ** -18) if j in (7, 8) else v for j, v in enumerate(UNIFORM)]
+BOOKS = {"bent": BENT, "steps": torch.linspace(-1, 1, 16).tolist(), "zero": [0.125 * (j - 5) + (j == 5) * 1e-16 for j in range(16)]}
+
+
+@pytest.mark.parametrize("book", list(BOOKS))
+@pytest.mark.parametrize("T,K,N,q_block", [(7, 512, 300, 64), (16, 192, 2000, 32), (12, 640, 20000, 64), (20, 2048, 4200, 64)])
+def test_q4_linear_keeps_nearly_uniform_values(T, K, N, q_block, book):
+    # rows of x with a single one: each fp32 result is one weight.  A codebook value is held to 2^-20, its product
+    # with the scale and the sum of its parts round a few times more
+    g = torch.Generator().manual_seed(K)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g).to(torch.uint8)
+    scales = (torch.rand(N, K // q_block, generator=g) + 0.25).bfloat16()
+    x = torch.zeros(T, K)
+    x[torch.arange(T), torch.randperm(K, generator=g)[:T]] = 1.0
+    values = [float(torch.tensor(v).float()) for v in BOOKS[book]]
+    want = x.double() @ q4_dense(codes, scales, values, q_block).T
+    shape, weight = moe.make_q4_linear_shape(T, K, N, "f32", q_block), moe.make_q4_weight(codes.cuda(), scales.cuda(), values)
+    out = torch.empty(T, N, device="cuda")
+    moe.moe_q4_linear(shape, x.bfloat16().cuda(), weight, out)
+    over = (out.cpu().double() - want).abs() - (2.0 ** -20 + 6 * FP32) * want.abs()
+    assert (over <= 1e-12).all(), over.max()

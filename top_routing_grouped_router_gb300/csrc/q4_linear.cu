@@ -17,6 +17,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace moe {
 namespace q4 {
@@ -680,12 +681,26 @@ struct Rows {  // the variants by rows of x
     }
 };
 
+// Whether step (j - j0) stands for each codebook value well enough: within 2^-17 of the value for results
+// that are rounded to bf16 (what the two parts of a general value keep), within 2^-20 for fp32 ones (values
+// that were themselves computed in fp32, such as -1 + 2 j / 15 by steps, are off by up to 2^-20.6).  What
+// rounding leaves in the place of a zero is taken as one.
+bool affine_values(const float *book, float step, int twice_j0, bool out_f32) {
+    double most = 0.0;
+    for (int j = 0; j < 16; ++j) most = std::max(most, std::fabs(double(book[j])));
+    for (int j = 0; j < 16; ++j) {
+        const double v = book[j], off = std::fabs(v - double(step) * (j - 0.5 * twice_j0));
+        if (off > std::fabs(v) * (out_f32 ? 0x1p-20 : 0x1p-17) + most * 0x1p-40) return false;
+    }
+    return true;
+}
+
 // The rows in passes of 16 (8 when x would not fit even split over a cluster), all in one launch;
 // false if not even 8 rows fit.
 bool run_mma(const Q4Args &a, int sms, cudaStream_t st, cudaError_t *err) {
     float step = 1.f;
     int twice = 0;
-    const bool affine = q4_codebook_affine(a.codebook, &step, &twice);
+    const bool affine = q4_codebook_affine(a.codebook, &step, &twice) && affine_values(a.codebook, step, twice, a.out_f32);
     const bool fine = a.q_block == 32;
     const int stages = (a.K + kIn - 1) / kIn;
     // counted in 32 bits in the kernel

@@ -607,6 +607,8 @@ typedef struct {
  * fp32 results and to 16 (2^-17 of a value) for bf16 ones; a codebook within 2^-20
  * (fp32) or 2^-17 (bf16) of each value from a uniform one is taken as uniform.
  * q_block that is neither 32 nor 64 times a power of two keeps the fp32 values.
+ * Infinite, NaN and very large x give what the formula gives (a row of x that holds
+ * an infinity, or a value past 2^116, takes many times as long).
  *   x [T][K] bf16, rows x_stride elements apart (a multiple of 8)
  *   residual [T][N] bf16, rows residual_stride apart, or NULL; out [T][N], rows
  *     out_stride apart (any stride >= N); residual may be out itself

@@ -7,8 +7,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import top_routing_grouped_router_gb300 as moe  # noqa: E402
-from attn_ref import FP32, attention, make_batch, q4_dense  # noqa: E402
-from test_gpu_attn import ATTN, NORMAL, UNIFORM, Dev  # noqa: E402
+from attn_ref import FP32, HALF, attention, make_batch, q4_dense  # noqa: E402
+from test_gpu_attn import ATTN, NORMAL, SHIFTED, UNIFORM, Dev  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -159,3 +159,35 @@ def test_q4_linear_keeps_nearly_uniform_values(T, K, N, q_block, book):
     moe.moe_q4_linear(shape, x.bfloat16().cuda(), weight, out)
     over = (out.cpu().double() - want).abs() - (2.0 ** -20 + 6 * FP32) * want.abs()
     assert (over <= 1e-12).all(), over.max()
+
+
+@pytest.mark.parametrize("book", [UNIFORM, NORMAL, SHIFTED], ids=["uniform", "normal", "shifted"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,N,q_block", [(1, 2048, 640, 64), (7, 512, 300, 32), (12, 640, 20000, 64), (8, 8192, 64, 64),
+                                           (20, 2048, 4200, 64), (40, 4096, 2112, 128), (5, 240, 31, 48)])
+def test_q4_linear_of_infinite_and_huge_inputs(T, K, N, q_block, out, book):
+    # by the definition: an infinite x gives infinities (NaN where the weight is 0, or two cancel), one past 2^123 a
+    # finite sum, NaN NaN; the other rows are what they are
+    g = torch.Generator().manual_seed(K + N)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g).to(torch.uint8)
+    scales = (torch.rand(N, K // q_block, generator=g) * 0.1 + 0.05).bfloat16()
+    x = torch.randn(T, K, generator=g).bfloat16()
+    inf = float("inf")
+    for t, special in enumerate([[inf], [-inf, inf], [2.0 ** 126], [float("nan")], [-(2.0 ** 124), 2.0 ** 125]]):
+        if t < T:
+            for i, v in enumerate(special):
+                x[t, (37 * t + 61 * i + K // 2) % K] = v
+    values = [float(torch.tensor(v).float()) for v in book]
+    w = q4_dense(codes, scales, values, q_block)
+    want, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+    shape, weight = moe.make_q4_linear_shape(T, K, N, out, q_block), moe.make_q4_weight(codes.cuda(), scales.cuda(), values)
+    buf = torch.empty(T, N, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    moe.moe_q4_linear(shape, x.cuda(), weight, buf)
+    got = buf.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan())
+    at_inf = want.isinf()
+    assert torch.equal(got[at_inf], want[at_inf]) and not got[~at_inf].isinf().any()
+    # as for finite inputs: K products and sums in fp32, a codebook value held to 2^-17, one rounding
+    tol = size * (K + 16) * FP32 + size * 2.0 ** -17 + (HALF[out] + FP32) * want.abs()
+    at = want.isfinite()
+    assert ((got - want).abs() <= tol)[at].all()

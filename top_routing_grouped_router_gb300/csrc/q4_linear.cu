@@ -485,34 +485,58 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
         // `red`, and it adds those in order after the CTA's only barrier.
         float acc[MT][NT][4];
         auto emit_pair = [&](int n0) {
+            bool finite = true;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[i][n][e] *= m.step;
+                        finite = finite && q4_is_finite(acc[i][n][e]);
+                    }
+            if (finite && !a.res && n0 + kOut <= N) {  // the usual case: one address a row
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = n * 8 + 2 * t + c;
+                        if (row >= rows) continue;
+                        const int64_t at_out = (T0 + row) * a.out_stride + n0 + g;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float y = acc[i][n][2 * r + c];
+                                if (a.out_f32)
+                                    static_cast<float *>(a.out)[at_out + i * kStrip + 8 * r] = y;
+                                else
+                                    static_cast<uint16_t *>(a.out)[at_out + i * kStrip + 8 * r] = f32_to_bf16_bits(y);
+                            }
+                    }
+                return;
+            }
+            uint32_t again = 0;  // bit (n, c, i, r): a sum to be formed by its terms
+            static_assert(NT * 4 * MT <= 32, "");
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int row = n * 8 + 2 * t + c;
                     if (row >= rows) continue;
-                    if (!a.res && n0 + kOut <= N) {  // the usual case: one address a row
-                        const int64_t at_out = (T0 + row) * a.out_stride + n0 + g;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float y = acc[i][n][2 * r + c] * m.step;
-                                if (a.out_f32)
-                                    static_cast<float *>(a.out)[at_out + i * kStrip + 8 * r] = y;
-                                else
-                                    static_cast<uint16_t *>(a.out)[at_out + i * kStrip + 8 * r] = f32_to_bf16_bits(y);
-                            }
-                        continue;
-                    }
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const int o = n0 + i * kStrip + 8 * r + g;
-                            if (o < N) q4_emit(a, T0 + row, o, acc[i][n][2 * r + c] * m.step);
+                            if (o < N && !q4_emit(a, T0 + row, o, acc[i][n][2 * r + c]))
+                                again |= 1u << (((n * 2 + c) * MT + i) * 2 + r);
                         }
                 }
+            for (; again; again &= again - 1) {
+                const int b = __ffs(again) - 1, r = b & 1, i = (b >> 1) % MT, c = (b >> 1) / MT & 1, n = (b >> 1) / MT / 2;
+                q4_emit_by_terms(a, T0 + n * 8 + 2 * t + c, n0 + g + i * kStrip + 8 * r);
+            }
         };
         int pending = -1, done = 0;  // the pair begun and not ended, and its stages
         for (int u = u0; u < u1;) {
@@ -569,7 +593,7 @@ q4_mma_kernel(const __grid_constant__ MmaArgs m) {
             float *pb = part + (k & 1) * kCols * wide;
             auto emit = [&](int row, int n, float y) {
                 n += n0;
-                if (row < rows && n < N) q4_emit(a, T0 + row, n, y * m.step);
+                if (row < rows && n < N && !q4_emit(a, T0 + row, n, y * m.step)) q4_emit_by_terms(a, T0 + row, n);
             };
             // output n of the tile is output n mod kOut of the warps beside = n / kOut, one an input part.
             // Threads are a multiple of the tile's outputs: a thread keeps its output, rows go by.

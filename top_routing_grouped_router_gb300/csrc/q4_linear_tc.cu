@@ -368,10 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
             if (!ok || m.slices > 1) break;  // sliced: one tile a CTA, joined below
             const int n = (group + k * groups) * kOut + row;
             if (n < a.N) {
+                bool finite = true;
 #pragma unroll
                 for (int c = 0; c < kHalf; ++c) {
-                    const int r = set * kHalf + c;
-                    if (r < m.rows) q4_emit(a, m.T0 + r, n, acc[c] * m.step);
+                    acc[c] *= m.step;
+                    finite = finite && q4_is_finite(acc[c]);
+                }
+                // rows past the last are zeros
+                if (finite) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c)
+                        if (set * kHalf + c < m.rows) q4_write(a, m.T0 + set * kHalf + c, n, acc[c]);
+                } else {
+                    uint32_t again = 0;
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c)
+                        if (set * kHalf + c < m.rows) again |= uint32_t(!q4_emit(a, m.T0 + set * kHalf + c, n, acc[c])) << c;
+                    for (; again; again &= again - 1) q4_emit_by_terms(a, m.T0 + set * kHalf + __ffs(again) - 1, n);
                 }
             }
         }
@@ -400,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tc_kernel(const __grid_constan
             if (r % m.slices != slice || r >= m.rows || n >= a.N) continue;
             float y = 0.f;
             for (int s = 0; s < m.slices; ++s) y += *cl.map_shared_rank(part + idx, s);
-            q4_emit(a, m.T0 + r, n, y * m.step);
+            if (!q4_emit(a, m.T0 + r, n, y * m.step)) q4_emit_by_terms(a, m.T0 + r, n);
         }
         cl.sync();  // no CTA leaves while another reads its sums
     }

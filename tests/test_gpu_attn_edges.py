@@ -135,6 +135,42 @@ def test_attention_of_a_nan_key_is_nan_for_those_who_see_it(name):
     _nan_case(name, spoil)
 
 
+@pytest.mark.parametrize("dtype,dim,page,tokens", [("bf16", 64, 7, 2), ("bf16", 128, 7, 1), ("bf16", 64, 8, 20),
+                                                   ("f32", 8, 7, 1)])
+def test_attention_of_nearly_2_to_the_31_keys(dtype, dim, page, tokens):
+    # as many keys as a length can say, all on one page but the last, whose scores outweigh the rest: the
+    # ends of the ranges of steps and of the masks
+    width = (2 ** 31 - 1) // page
+    kv, special = width * page, 4  # the last pages hold the new tokens' keys
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(dim)
+    k = torch.zeros(special + 1, 1, page, dim)
+    k[1:] = 40.0 / dim + 0.02 * torch.randn(special, 1, page, dim, generator=g)
+    k, v = k.to(dt), torch.randn(special + 1, 1, page, dim, generator=g).to(dt)
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, -special:] = torch.arange(1, special + 1).int()
+    q = torch.ones(tokens, 1, dim, dtype=dt, device="cuda")
+    shape = moe.make_attn_shape(tokens, 1, 1, 1, dim, page, special + 1, width, tokens, act=dtype)
+    batch = moe.make_attn_batch(torch.tensor([0, tokens]).int().cuda(), torch.tensor([kv]).int().cuda(), table)
+    ws = torch.zeros(moe.moe_attn_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(tokens, 1, device="cuda")
+    moe.moe_paged_attention(shape, q, moe.make_kv_cache(k.cuda(), v.cuda()), batch, out, scale=1.0, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_error(ws) == 0
+    n = special * page
+    score = k[1:].double().reshape(n, dim).sum(1)
+    hide = torch.arange(n)[None] > torch.arange(n - tokens, n)[:, None]
+    total = torch.logsumexp(score.masked_fill(hide, -torch.inf), 1)
+    p = torch.exp(score - total[:, None]).masked_fill(hide, 0)
+    want = p @ v[1:].double().reshape(n, dim)
+    # scores of dim sums of about 40 / dim, twice in a probability; bf16 rounds the probabilities and the result;
+    # the keys of score 0 weigh 2^31 e^-40 < 2^-26 together
+    err = 2 * (dim + 8) * FP32 * 45 + (HALF["bf16"] if dtype == "bf16" else 0) + (n + 32) * FP32 + 2.0 ** -26
+    tol = err * (p @ v[1:].double().abs().reshape(n, dim)) + HALF[dtype] * want.abs() + 2.0 ** -24
+    assert ((out.cpu().double()[:, 0] - want).abs() <= tol).all()
+    assert ((lse.cpu().double()[:, 0] - total).abs() <= err + 4 * FP32 * total).all()
+
+
 # ------------------------------------------------------------------------------- 4-bit linear
 
 # nearly uniform: two small values off by 2^-18 of themselves; computed in fp32 steps; a zero that rounding missed

@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
                     }
                     const int k0 = step * kKeys;
-                    if (k0 + kKeys > seen_all) {
+                    if (k0 > seen_all - kKeys) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i)
                             if (k0 + i >= seen) x[i] = 0xff800000u;

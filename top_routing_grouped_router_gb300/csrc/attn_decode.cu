@@ -73,7 +73,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ int steps_of(const Seq &s) { return s.q_len ? max(1, (s.kv_len + kStep - 1) / kStep) : 0; }
+__device__ __forceinline__ int steps_of(const Seq &s) {
+    return s.q_len ? max(1, int((uint32_t(s.kv_len) + kStep - 1) / kStep)) : 0;  // kv_len up to 2^31 - 1
+}
 
 // Exclusive prefix of one value a thread over the block, and the sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t n, uint32_t *total, uint32_t *scratch) {
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             if (i < mine) {
                 const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes + lane / CH * (D * 2);
                 const int p = int(step0 + warp + i * kWarps) * kStep;
-                if (in_page && p + kStep <= s.kv_len) {
+                if (in_page && s.kv_len - p >= kStep) {
                     const uint16_t *ks = kc + row_off + lane_row, *vs = vc + row_off + lane_row;
 #pragma unroll
                     for (int it = 0; it < kStep / RPI; ++it, ks += next_row, vs += next_row) {
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[n][e] *= sl2;
-            if (key0 + kStep > seen_all) {
+            if (key0 > seen_all - kStep) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll

@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
         for (int j = 0; j < NJ; ++j) o[r][j] = 0.f;
     }
     const int keys = max(past + j0 + nj, 0);
-    const int per = ((keys + kKeys - 1) / kKeys + part.parts - 1) / part.parts * kKeys;
-    const int64_t k_begin = (int64_t)blockIdx.z * per;
+    const int64_t per = ((uint32_t(keys) + kKeys - 1) / kKeys + part.parts - 1) / part.parts * (int64_t)kKeys;
+    const int64_t k_begin = blockIdx.z * per;
     const int k_end = int(min(k_begin + per, (int64_t)keys));
 
     // Tiles of keys: pieces of eight elements.  Small heads request the next tile before they work on

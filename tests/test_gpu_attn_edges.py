@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 
 import top_routing_grouped_router_gb300 as moe  # noqa: E402
 from attn_ref import FP32, HALF, attention, make_batch, q4_dense  # noqa: E402
-from test_gpu_attn import ATTN, NORMAL, SHIFTED, UNIFORM, Dev  # noqa: E402
+from test_gpu_attn import ATTN, NORMAL, SHIFTED, UNIFORM, Dev, check  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -169,6 +169,47 @@ def test_attention_of_nearly_2_to_the_31_keys(dtype, dim, page, tokens):
     tol = err * (p @ v[1:].double().abs().reshape(n, dim)) + HALF[dtype] * want.abs() + 2.0 ** -24
     assert ((out.cpu().double()[:, 0] - want).abs() <= tol).all()
     assert ((lse.cpu().double()[:, 0] - total).abs() <= err + 4 * FP32 * total).all()
+
+
+def _many(seqs, most, keys, long=0):
+    """Chunk and cache lengths: up to `most` new tokens and `keys` keys, idle and empty sequences among them, one chunk
+    cut short, and one sequence of `long` keys."""
+    q = [(i * 7 + i // 5) % (most + 1) for i in range(seqs)]
+    kv = [n + (i * 53 + i // 3) % max(keys - n, 1) for i, n in enumerate(q)]
+    q[seqs // 3], kv[seqs // 3] = most, most // 2
+    q[seqs // 2], kv[seqs // 2] = 1, 0
+    if long:
+        q[seqs - 2], kv[seqs - 2] = most, long
+    return q, kv
+
+
+# name: dtype, heads, kv_heads, dim, page, (sequences, most new tokens, keys, keys of one)
+MANY = {
+    "decode even parts 130": ("bf16", 4, 1, 64, 16, (130, 1, 60, 1500)),
+    "decode even parts 150": ("bf16", 8, 1, 128, 16, (150, 2, 70, 2500)),
+    "decode line 200": ("bf16", 3, 1, 128, 16, (200, 4, 700, 0)),
+    "decode line 300": ("bf16", 4, 2, 64, 32, (300, 2, 200, 1200)),
+    "decode line 600": ("bf16", 4, 2, 128, 16, (600, 1, 90, 0)),
+    "decode one CTA a pair 300": ("bf16", 2, 1, 64, 16, (300, 8, 100, 0)),
+    "chunks whole 400": ("bf16", 4, 2, 64, 16, (400, 11, 100, 500)),
+    "chunks whole 400 heads of 128": ("bf16", 4, 1, 128, 32, (400, 7, 100, 500)),
+    "chunks whole, 17 items a CTA": ("bf16", 4, 2, 64, 16, (1500, 9, 60, 0)),
+    "chunks whole, 17 items a CTA, heads of 128": ("bf16", 8, 4, 128, 16, (760, 9, 60, 0)),
+    "chunks cut 400": ("bf16", 4, 2, 128, 16, (400, 11, 100, 3000)),
+    "chunks cut 500 heads of 64": ("bf16", 6, 2, 64, 16, (500, 9, 300, 2000)),
+    "chunks cut, 17 items a CTA": ("bf16", 4, 2, 64, 16, (1600, 9, 40, 700)),
+    "chunks cut, 17 items a CTA, heads of 128": ("bf16", 8, 4, 128, 16, (800, 9, 40, 700)),
+    "generic 40": ("f32", 3, 1, 24, 16, (40, 9, 90, 0)),
+    "generic 150": ("f32", 4, 2, 64, 5, (150, 6, 60, 400)),
+    "generic 300": ("bf16", 6, 2, 80, 16, (300, 3, 70, 0)),
+}
+
+
+@pytest.mark.parametrize("name", list(MANY))
+def test_attention_of_many_sequences(name):
+    # more sequences than one round of a scan takes, and more items a CTA than it lists at a time
+    dtype, heads, kv_heads, dim, page, sizes = MANY[name]
+    check(make_batch(dtype, heads, kv_heads, dim, page, *_many(*sizes), seed=len(name)))
 
 
 # ------------------------------------------------------------------------------- 4-bit linear

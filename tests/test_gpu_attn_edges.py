@@ -212,6 +212,22 @@ def test_attention_of_many_sequences(name):
     check(make_batch(dtype, heads, kv_heads, dim, page, *_many(*sizes), seed=len(name)))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 7, 12, 20, 33])
+def test_attention_keeps_its_bits(group, dim):
+    # groups that leave rows of a tile empty: what earlier kernels left in shared memory changes nothing
+    d = Dev(make_batch("bf16", group, 1, dim, 32, [60, 1, 247], [600, 1, 2315], seed=group, spread=2.0))
+    others = [Dev(make_batch("bf16", 8, 1, dim, 32, [300], [900], seed=s, spread=x)) for s, x in enumerate((0.1, 5.0, 50.0))]
+    first = None
+    for _ in range(4):
+        for other in others:
+            other.attend(0.3)
+            assert d.attend(0.3) == 0
+            now = d.out.clone(), d.lse.clone()
+            first = now if first is None else first
+            assert torch.equal(first[0], now[0]) and torch.equal(first[1], now[1])
+
+
 # ------------------------------------------------------------------------------- 4-bit linear
 
 # nearly uniform: two small values off by 2^-18 of themselves; computed in fp32 steps; a zero that rounding missed

@@ -758,8 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                     if (step == g.step0) {
                         m = mn;
-                    } else if (__any_sync(0xffffffffu, (mn - m) * sl2 > kLag)) {
-                        // -inf - -inf is NaN and compares false: a row that has seen nothing stays
+                    } else if (__any_sync(0xffffffffu, live && (mn - m) * sl2 > kLag)) {
+                        // -inf - -inf is NaN and compares false: a row that has seen nothing stays.  Rows past the
+                        // tile's hold what lay in shared memory, and decide nothing: results keep their bits.
                         const float f = mn == kNegInf ? 1.f : ex2((m - mn) * sl2);
                         m = mn;
                         l *= f;

@@ -228,6 +228,15 @@ def test_attention_keeps_its_bits(group, dim):
             assert torch.equal(first[0], now[0]) and torch.equal(first[1], now[1])
 
 
+@pytest.mark.parametrize("name", ["decode ragged", "chunk over cache", "chunk dim 64", "chunk fp32"])
+def test_attention_of_huge_products_and_a_tiny_scale(name):
+    # q . k of about 10^35 and a scale of 10^-35: ordinary scores
+    bt = make_batch(*ATTN[name], seed=14)
+    bt.q *= 2.0 ** 57
+    bt.k_cache *= 2.0 ** 57
+    check(bt, scale=2.0 ** -117)
+
+
 # ------------------------------------------------------------------------------- 4-bit linear
 
 # nearly uniform: two small values off by 2^-18 of themselves; computed in fp32 steps; a zero that rounding missed

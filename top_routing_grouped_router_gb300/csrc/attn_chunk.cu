@@ -701,8 +701,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
             const uint32_t ts = tmem + lanes + t * kKeys, tp = tmem + lanes + C::col_p(t), to = tmem + lanes + C::col_o(t);
             const bool neg = a.scale < 0.f;
-            // a zero scale would make -inf * 0 of masked scores: any tiny factor gives the same result
-            const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+            // a zero scale would make -inf * 0 of masked scores: the smallest normal factor moves no score by more
+            // than 4, and only scores past 10^37 by more than 0.1
+            const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
                 if (t >= g.tiles) continue;

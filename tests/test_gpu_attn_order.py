@@ -132,3 +132,13 @@ def test_q4_linear_wait_limit_starts_after_the_kernel_before(T, K, N):
             out.zero_()
     finally:
         moe.moe_debug_set_waits()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+@pytest.mark.parametrize("dtype,dim,tokens", [("bf16", 64, 1), ("bf16", 128, 40), ("bf16", 96, 40), ("f32", 64, 2)])
+def test_attention_reads_what_the_kernel_before_wrote(dtype, dim, tokens, what, graph):
+    d = Dev(make_batch(dtype, 4, 1, dim, 16, [tokens], [tokens + 8], seed=1, fill=0.5))
+    target = {"q": d.q.view(-1), "k": d.k[d.table[0, 0]].view(-1), "v": d.v[d.table[0, 0]].view(-1)}[what][:8]
+    call = lambda: moe.moe_paged_attention(d.shape, d.q, d.cache, d.batch, d.out, scale=0.1, workspace=d.ws)  # noqa: E731
+    _reads_what_was_written(target, call, lambda: d.out, graph)

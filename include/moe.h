@@ -451,7 +451,7 @@ MOE_API int moe_graphs_destroy(moe_graphs *graphs);
  * tokens' own among them (they are its last ones): new token j of a chunk of n
  * has the place kv_len[b] - n + j in its sequence.  Place p is slot p mod
  * page_size of page block_table[b][p / page_size].  Rows from cu_q[n_seqs] on
- * (padding of a graph's batch) are neither read nor written.
+ * (padding of a graph's batch) may hold anything and are not written.
  *
  * Sizes: 0 <= n_tokens <= 2^20, 0 <= n_seqs <= 2^16, n_kv_heads divides
  * n_heads <= 1024, head_dim a multiple of 8 up to 256, max_pages * page_size
@@ -566,7 +566,8 @@ MOE_API int moe_rope_append(const moe_attn_shape *shape, const moe_rope *rope, c
  * sees the keys at places 0 .. kv_len - n + j,
  *   out = sum_p softmax_p(scale * q . k_p) v_p.
  * A token that sees no key gets out = 0 and lse = -inf.  Slots at or past kv_len
- * may hold anything (NaN included).  Scores, the softmax's maximum and sum and
+ * may hold anything (NaN included); a k that is not finite reaches the tokens that
+ * see it, a v also those of the same chunk before it (as 0 * NaN in the formula).  Scores, the softmax's maximum and sum and
  * the output accumulate in fp32; with bf16 the probabilities are rounded to bf16
  * for the product with v.  Results do not depend on timing (bitwise
  * deterministic).
@@ -599,8 +600,10 @@ typedef struct {
 } moe_q4_weight;
 
 /*
- * out = x . W^T (+ residual) with a 4-bit W, for decode batches (one pass over
- * the weights for up to 64 rows; more rows repeat it):
+ * out = x . W^T (+ residual) with a 4-bit W, for decode batches.  A pass over the
+ * weights takes 16, 32 or 64 rows with a uniform codebook, q_block of 64 and up and
+ * large weights, else 8 or 16, and 8 where q_block is neither 32 nor 64 times a power
+ * of two; more rows repeat it.
  *   out[t][n] = sum_k codebook[code[n][k]] * scale[n][k / q_block] * x[t][k]
  *               (+ residual[t][n]),
  * accumulated in fp32, rounded once.  The codebook's values are kept to 24 bits for

@@ -10,8 +10,9 @@
 // Heads of 128: P_t takes the place of S_t (TMEM is full), and one warp issues P0 V, S0', P1 V, S1':
 // while one tile's softmax runs, the tensor cores work on the other's products.  What bounds it is
 // that chain: 1400 cycles of softmax and 1024 of products a tile, 2890 a step of both tiles where the
-// products alone are 2048 (2048 tokens over 16384 keys, 32 heads: 339 us, 1520 TFLOP/s).  Multiplying the
-// first half of P while the softmax works on the second made it slower (371 us).
+// products alone are 2048 (2048 tokens over 16384 keys, 32 heads: 333 us by itself, 1550 TFLOP/s; 360 with its
+// join in a row of calls, when the clocks fall).  Multiplying the first half of P while the softmax works on the
+// second made it slower (by 6 %).
 // Heads of 64: P_t lies beside S_t, the next scores are computed while the softmax works, and each
 // tile has an MMA warp of its own.
 // The running maximum m may lag behind: only when a row's maximum grows by more than 2^8 is O
@@ -53,7 +54,7 @@ struct Cfg {
     // registers.  Heads of 128 do not: P takes the place of S.
     static constexpr bool kEarly = D == 64;
     // Warps that issue MMAs, each for its tiles.  With heads of 128 one, in the order of the tiles, which
-    // keeps one tile's products beside the other's softmax (two: 420 us for a chunk of 2048, one: 341);
+    // keeps one tile's products beside the other's softmax (two: 420 us for a chunk of 2048, one at the time: 341);
     // with heads of 64, whose products are half as long, two (a mixed batch 48.4 us, with one 51).
     static constexpr int kMmaWarps = D == 64 ? 2 : 1;
     static constexpr uint32_t col_p(int t) { return kEarly ? 256 + 64 * t : 128 * t; }
@@ -72,8 +73,9 @@ struct Rec {
     int n, h, tok0, q0, q_len;  // n: parts (0: none)
 };
 
-// sum_{i < n} floor((a i + b) / m), m > 0, by the Euclid-like recursion; the sum and a n + m fit
-// 32 bits.
+// sum_{i < n} floor((a i + b) / m), m > 0, as Euclid's algorithm goes: whole multiples of m are taken out of a and b,
+// then rows and columns of the lattice points under the line change places (reciprocity of such sums: Graham,
+// Knuth, Patashnik, Concrete Mathematics, chapter 3).  The sum and a n + m fit 32 bits.
 __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     uint32_t sum = 0;
     while (n > 0) {
@@ -777,6 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                     const float z = m == kNegInf ? 0.f : m * sl2;
                     const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
+                    // probabilities in bf16 for the product (up to 2^-8 of each; error of the 2048-token chunk against 64 bits
+                    // 0.0023 of the outputs' size, with fp32 probabilities 0.0017); their sum stays in fp32
                     uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int i = 0; i < 128; i += 2) {

@@ -4,7 +4,7 @@
 //
 // q4_mma_kernel: a CTA takes 16 outputs at a time (16 to 128 where there are more, "side").  Its
 // eight warps split the inputs; where there are many outputs, sixteen warps take pairs of 16 instead,
-// each an equal piece of the line of all the CTA's pairs (16 rows x 2048 x 131072: 39 us; tiles whose inputs
+// each an equal piece of the line of all the CTA's pairs (16 rows x 2048 x 131072: 39.6 us; tiles whose inputs
 // the warps split, with a barrier and a sum each, 54).  Each warp
 // streams its part of the code rows through a cp.async ring of its own, 128 inputs a stage,
 // unpacks the codes in registers to the A operand of mma.sync (m16n8k16, outputs x inputs) and
@@ -164,7 +164,7 @@ __device__ __forceinline__ void mma16816_from(float *c, uint32_t a0, uint32_t a1
 // starts at -(16 + j0) sum x of its block (fp32, found once a CTA), which leaves sum (j - j0) x: the
 // subtraction costs no instruction, and about a factor 5 of the fp32 sum's accuracy (16 + j
 // against j - j0).  Else a table in shared memory, each value as kParts bf16 that add up to it: two
-// (16 bits, 2^-17 of a value, for results that are rounded to bf16's 2^-9) or three (24 bits, for fp32).
+// (16 bits, 2^-17 of a value, for results that are rounded to bf16's 2^-8) or three (24 bits, for fp32).
 template <int NT, int MT, bool kFine, int kParts>
 __global__ void __launch_bounds__(Var<NT, MT, kFine, kParts>::kThreads)
 q4_mma_kernel(const __grid_constant__ MmaArgs m) {

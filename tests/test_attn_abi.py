@@ -189,7 +189,7 @@ def _binding_call(kind=lambda t: t, **kw):
     batch, cache = moe.make_attn_batch(a["cu"], a["kv"], a["table"]), moe.make_kv_cache(a["cache"], a["cache"].clone())
     if a["call"] == "rope":
         rope = moe.make_rope(64, q_gamma=a["gamma"], device="cpu")
-        rope.on_host &= kind is not _on_gpu  # its table
+        rope.sizes = (*rope.sizes[:2], kind is not _on_gpu)  # its table
         moe.moe_rope_append(shape, rope, a["q"], a["k"], a["v"], cache, batch, a["out"], a["positions"], a["ws"], 0)
     else:
         moe.moe_paged_attention(shape, a["q"], cache, batch, a["out"], lse=a["lse"], workspace=a["ws"], stream=0)
@@ -231,12 +231,12 @@ def test_binding_takes_any_stride_of_a_single_row():
     torch = pytest.importorskip("torch")
     bf = torch.bfloat16
     x = torch.empty(64, 1, dtype=bf).t()
-    assert x.stride() == (1, 1) and moe._rows(x, 64, "x") == 64
+    assert x.stride() == (1, 1) and moe._row_stride(x, "x") == 64
     q = torch.empty(1, 4, 64, dtype=bf).as_strided((1, 4, 64), (8, 64, 1))
-    assert moe._head_rows(q, 64, 256, "q") == 256
+    assert moe._row_stride(q, "q") == 256
     wide = torch.empty(3, 320, dtype=bf)
-    assert moe._rows(wide[:, :64], 64, "x") == 320 and moe._rows(wide[:, 5:6], 1, "x") == 320
-    assert moe._head_rows(wide[:, :256].view(3, 4, 64), 64, 256, "q") == 320
+    assert moe._row_stride(wide[:, :64], "x") == 320 and moe._row_stride(wide[:, 5:6], "x") == 320
+    assert moe._row_stride(wide[:, :256].view(3, 4, 64), "q") == 320
 
 
 def test_binding_follows_a_changed_shape():
@@ -245,3 +245,7 @@ def test_binding_follows_a_changed_shape():
     assert moe._attn_checks(s)[0] == 8 * 8 * 64 and s._checks[5] is torch.bfloat16
     s.n_tokens, s.dtype = 9, 0
     assert s._checks is None and moe._attn_checks(s)[0] == 9 * 8 * 64 and s._checks[5] is torch.float32
+    s = moe.make_q4_linear_shape(4, 256, 48)
+    assert moe._q4_checks(s)[:4] == (1024, 192, 256, 48)
+    s.T = 5
+    assert s._checks is None and moe._q4_checks(s)[:2] == (1280, 240)

@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 __all__ = [
@@ -65,15 +64,18 @@ class MoEQ4(ctypes.Structure):
                 ("down_scales", ctypes.c_void_p), ("codebook", ctypes.c_float * 16)]
 
 
-class MoEAttnShape(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_seqs", "n_heads", "n_kv_heads", "head_dim", "page_size",
-                                              "n_pages", "max_pages", "max_q", "dtype")]
-    _checks = None  # what _attn_checks made of the fields; a field that is set takes it away
+class _Checked(ctypes.Structure):
+    _checks = None  # what a call's tensors are held against, made of the fields; a field that is set takes it away
 
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
         if name != "_checks":
             super().__setattr__("_checks", None)
+
+
+class MoEAttnShape(_Checked):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_seqs", "n_heads", "n_kv_heads", "head_dim", "page_size",
+                                              "n_pages", "max_pages", "max_q", "dtype")]
 
 
 class MoEAttnBatch(ctypes.Structure):
@@ -91,10 +93,10 @@ class MoERope(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
                 ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_gamma", ctypes.c_void_p),
                 ("k_gamma", ctypes.c_void_p)]
-    weights, on_host = None, False  # type and length of make_rope's norm weights; whether a tensor is in host memory
+    sizes = None  # of make_rope's norm weights: type, length; and whether a tensor is in host memory
 
 
-class MoEQ4LinearShape(ctypes.Structure):
+class MoEQ4LinearShape(_Checked):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "out_dtype", "q_block")]
 
 
@@ -457,11 +459,12 @@ def make_rope(rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1
                   _ptr(k_gamma))
     out.tensors = (table, q_gamma, k_gamma)
     gammas = (q_gamma, "q_gamma"), (k_gamma, "k_gamma")
-    out.on_host = any([_need(t, what, ("float32", "bfloat16")) for t, what in gammas]) or not table.is_cuda
+    on_host = any([_need(t, what, ("float32", "bfloat16")) for t, what in gammas]) or not table.is_cuda
     known = {(t.dtype, t.numel()) for t, _ in gammas if t is not None and not isinstance(t, int)}
     if len(known) > 1:
         raise ValueError(f"q_gamma and k_gamma differ: {known}")
-    out.weights = known.pop() if known else None
+    if known or on_host:
+        out.sizes = (*(known.pop() if known else (None, None)), on_host)
     return out
 
 
@@ -487,18 +490,6 @@ def _row_stride(t, what):
     return st[0] if t.shape[0] != 1 else t.numel()  # a single row's own stride says nothing
 
 
-def _head_rows(t, dim, wide, what):
-    """_row_stride of a [rows][heads][dim] tensor, quick where the heads follow one another."""
-    row, head, elem = t.stride()
-    return row if elem == 1 and head == dim and row >= wide else _row_stride(t, what)
-
-
-def _rows(t, cols, what):
-    """_row_stride of a [rows][cols] tensor."""
-    row, elem = t.stride()
-    return row if elem == 1 and row >= cols else _row_stride(t, what)
-
-
 def _wrong(*tensors):
     """The error of the first (name, tensor, type, sizes) whose tensor is not that; its rows may be more."""
     for what, t, dtype, (rows, *sizes) in tensors:
@@ -510,17 +501,31 @@ def _wrong(*tensors):
     return ValueError("a tensor's type, size or device is wrong")
 
 
-_q4_ints = struct.Struct("5i").unpack  # the fields of MoEQ4LinearShape at once
-
-
 def _attn_checks(shape):
-    """What the tensors of a call are held against: elements of q and k, their rows' widths, the type, and the sizes of
-    the batch's and the cache's tensors."""
+    """What the tensors of a call are held against: elements of q and k, their rows' widths, the type, the sizes of the
+    batch's, the cache's and the rotation's tensors, and the type of positions."""
     n, dtype = shape.n_tokens, _torch_dtype(shape.dtype)
     wide, kv_wide = shape.n_heads * shape.head_dim, shape.n_kv_heads * shape.head_dim
     shape._checks = (n * wide, n * kv_wide, wide, kv_wide, shape.head_dim, dtype, (shape.n_seqs, shape.max_pages, False),
-                     (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim, dtype, False))
+                     (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim, dtype, False),
+                     (dtype, shape.head_dim, False), _torch_dtype(_INT32))
     return shape._checks
+
+
+def _q4_checks(shape):
+    """The same of a 4-bit linear: elements of x and out, a row's of each, their types, and the weight's sizes."""
+    T, K, N, q_block = shape.T, shape.K, shape.N, shape.q_block
+    shape._checks = (T * K, T * N, K, N, _torch_dtype(MOE_DT_BF16), _torch_dtype(shape.out_dtype),
+                     (N * K // 2, N * K // q_block if q_block > 0 else 0, False))
+    return shape._checks
+
+
+def _check_rope(rope, sizes):
+    """That the rotation's norm weights have this type and length, and that its tensors are on the GPU."""
+    if rope.sizes[0] is not None and rope.sizes[:2] != sizes[:2]:
+        raise ValueError(f"q_gamma, k_gamma: {sizes[0]} [{sizes[1]}], not {rope.sizes[0]} [{rope.sizes[1]}]")
+    if rope.sizes[2]:
+        raise ValueError("rope: not on the GPU")
 
 
 def _check_batch(batch, cache, batch_sizes, cache_sizes):
@@ -562,29 +567,39 @@ def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, w
     """q_out = rotated q; rotated k and v into their cache slots.  q, q_out [N][heads][dim], k, v [N][kv heads][dim]
     (rows may be slices of a wider tensor), positions int32 [N]."""
     at = ctypes.addressof
-    need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, cache_sizes = shape._checks or _attn_checks(shape)
+    (need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, cache_sizes, rope_sizes,
+     int32) = shape._checks or _attn_checks(shape)
     if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
         _check_batch(batch, cache, batch_sizes, cache_sizes)
+    if rope.sizes is not None and rope.sizes != rope_sizes:
+        _check_rope(rope, rope_sizes)
     if (q.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype or
             q.numel() < need or k.numel() < kv_need or v.numel() < kv_need or q_out.numel() < need or
             not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda)):
         n, heads, kv_heads = shape.n_tokens, shape.n_heads, shape.n_kv_heads
         raise _wrong(("q", q, dtype, (n, heads, dim)), ("k", k, dtype, (n, kv_heads, dim)),
                      ("v", v, dtype, (n, kv_heads, dim)), ("q_out", q_out, dtype, (n, heads, dim)))
-    if rope.weights is not None and rope.weights != (dtype, dim):
-        raise ValueError(f"q_gamma, k_gamma: {dtype} [{dim}], not {rope.weights}")
-    if rope.on_host:
-        raise ValueError("rope: not on the GPU")
-    if positions is not None and not isinstance(positions, int):
-        int32 = _torch_dtype(_INT32)
+    if positions is not None and type(positions) is not int:
         if (positions.dtype is not int32 or positions.numel() * wide < need or not positions.is_contiguous() or
                 not positions.is_cuda):
             raise _wrong(("positions (contiguous)", positions, int32, (shape.n_tokens,)))
         positions = positions.data_ptr()
+    # elements between rows; heads that follow one another in rows far enough apart need no second look
+    q_row, head, elem = q.stride()
+    if head != dim or elem != 1 or q_row < wide:
+        q_row = _row_stride(q, "q")
+    k_row, head, elem = k.stride()
+    if head != dim or elem != 1 or k_row < kv_wide:
+        k_row = _row_stride(k, "k")
+    v_row, head, elem = v.stride()
+    if head != dim or elem != 1 or v_row < kv_wide:
+        v_row = _row_stride(v, "v")
+    out_row, head, elem = q_out.stride()
+    if head != dim or elem != 1 or out_row < wide:
+        out_row = _row_stride(q_out, "q_out")
     rc = (_lib or lib()).moe_rope_append(
-        at(shape), at(rope), q.data_ptr(), _head_rows(q, dim, wide, "q"), k.data_ptr(), _head_rows(k, dim, kv_wide, "k"),
-        v.data_ptr(), _head_rows(v, dim, kv_wide, "v"), at(cache), at(batch), positions, q_out.data_ptr(),
-        _head_rows(q_out, dim, wide, "q_out"), None if workspace is None else workspace.data_ptr(),
+        at(shape), at(rope), q.data_ptr(), q_row, k.data_ptr(), k_row, v.data_ptr(), v_row, at(cache), at(batch), positions,
+        q_out.data_ptr(), out_row, None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.nbytes, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_rope_append")
@@ -594,7 +609,7 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
     """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5.  q, out
     [N][heads][dim] (rows may be slices of a wider tensor), lse fp32 [N][heads]."""
     at = ctypes.addressof
-    need, _, wide, _, dim, dtype, batch_sizes, cache_sizes = shape._checks or _attn_checks(shape)
+    need, _, wide, _, dim, dtype, batch_sizes, cache_sizes, _, _ = shape._checks or _attn_checks(shape)
     if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
         _check_batch(batch, cache, batch_sizes, cache_sizes)
     if (q.dtype is not dtype or out.dtype is not dtype or q.numel() < need or out.numel() < need or
@@ -608,10 +623,15 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
         if lse.dtype is not fp32 or lse.numel() * dim < need or not lse.is_cuda:
             raise _wrong(("lse", lse, fp32, (shape.n_tokens, shape.n_heads)))
         lse = lse.data_ptr()
+    q_row, head, elem = q.stride()
+    if head != dim or elem != 1 or q_row < wide:
+        q_row = _row_stride(q, "q")
+    out_row, head, elem = out.stride()
+    if head != dim or elem != 1 or out_row < wide:
+        out_row = _row_stride(out, "out")
     rc = (_lib or lib()).moe_paged_attention(
-        at(shape), q.data_ptr(), _head_rows(q, dim, wide, "q"), at(cache), at(batch),
-        dim ** -0.5 if scale is None else scale, out.data_ptr(), _head_rows(out, dim, wide, "out"), lse,
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        at(shape), q.data_ptr(), q_row, at(cache), at(batch), dim ** -0.5 if scale is None else scale, out.data_ptr(),
+        out_row, lse, None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
         _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_paged_attention")
@@ -620,25 +640,29 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
 def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):
     """out = x . W^T (+ residual) with a 4-bit weight (make_q4_weight); x [T][K] and residual [T][N] bf16, out [T][N]."""
     at = ctypes.addressof
-    T, K, N, out_dtype, q_block = _q4_ints(shape)
-    bf16, out_dtype = _torch_dtype(MOE_DT_BF16), _torch_dtype(out_dtype)
-    if weight.sizes is not None:
-        codes, scales, on_host = weight.sizes
-        if 2 * codes != N * K or scales * q_block != N * K:
-            raise ValueError(f"weight: {codes} bytes of codes and {scales} scales for [{N}][{K}] in blocks of {q_block}")
-        if on_host:
-            raise ValueError("weight: not on the GPU")
-    if (x.dtype is not bf16 or out.dtype is not out_dtype or x.numel() < T * K or out.numel() < T * N or
+    need, out_need, K, N, bf16, out_dtype, sizes = shape._checks or _q4_checks(shape)
+    if weight.sizes is not None and weight.sizes != sizes:
+        raise ValueError("weight: (bytes of codes, scales, in host memory) %s, not %s" % (weight.sizes, sizes) if
+                         weight.sizes[:2] != sizes[:2] else "weight: not on the GPU")
+    if (x.dtype is not bf16 or out.dtype is not out_dtype or x.numel() < need or out.numel() < out_need or
             not (x.is_cuda and out.is_cuda)):
-        raise _wrong(("x", x, bf16, (T, K)), ("out", out, out_dtype, (T, N)))
+        raise _wrong(("x", x, bf16, (shape.T, K)), ("out", out, out_dtype, (shape.T, N)))
     res_row = 0
     if residual is not None:
-        if residual.dtype is not bf16 or residual.numel() < T * N or not residual.is_cuda:
-            raise _wrong(("residual", residual, bf16, (T, N)))
-        res_row, residual = _rows(residual, N, "residual"), residual.data_ptr()
-    rc = (_lib or lib()).moe_q4_linear(
-        at(shape), x.data_ptr(), _rows(x, K, "x"), at(weight), residual, res_row, out.data_ptr(), _rows(out, N, "out"),
-        _current_stream() if stream is None else _stream(stream))
+        if residual.dtype is not bf16 or residual.numel() < out_need or not residual.is_cuda:
+            raise _wrong(("residual", residual, bf16, (shape.T, N)))
+        res_row, elem = residual.stride()
+        if elem != 1 or res_row < N:
+            res_row = _row_stride(residual, "residual")
+        residual = residual.data_ptr()
+    x_row, elem = x.stride()
+    if elem != 1 or x_row < K:
+        x_row = _row_stride(x, "x")
+    out_row, elem = out.stride()
+    if elem != 1 or out_row < N:
+        out_row = _row_stride(out, "out")
+    rc = (_lib or lib()).moe_q4_linear(at(shape), x.data_ptr(), x_row, at(weight), residual, res_row, out.data_ptr(), out_row,
+                                       _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_q4_linear")
 

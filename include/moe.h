@@ -582,6 +582,89 @@ MOE_API int moe_paged_attention(const moe_attn_shape *shape, const void *q, int6
                                 int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
                                 moe_stream_t stream);
 
+/*
+ * A sliding window: a token at place p of its sequence sees the keys at places
+ * p - window + 1 .. p and, whatever the window, the sequence's first `sinks`
+ * keys (those up to p).  window >= 1, sinks >= 0, else MOE_ERR_SHAPE.
+ */
+typedef struct {
+    int32_t window, sinks;
+} moe_attn_window;
+
+/*
+ * moe_paged_attention where new token j of a chunk of n, at place
+ * p = kv_len - n + j, sees the keys of its window and the first keys only.
+ * Pages that hold no key that a token of the chunk sees are not read, nor are
+ * their entries of block_table: a caller may give such pages back.  Slots that
+ * no token of the chunk sees may hold anything, on the other pages too.
+ * Arguments, workspace (moe_attn_workspace_size), types and errors are those of
+ * moe_paged_attention, plus MOE_ERR_NULLPTR for a NULL window.
+ */
+MOE_API int moe_paged_attention_window(const moe_attn_shape *shape, const void *q, int64_t q_stride,
+                                       const moe_kv_cache *cache, const moe_attn_batch *batch,
+                                       const moe_attn_window *window, float scale, void *out, int64_t out_stride,
+                                       float *lse, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * A paged cache in 8 bits: an e4m3 code for each value (4 exponent bits, 3 of
+ * mantissa, largest 448, no infinity) and a power of two for each block of
+ * `block` consecutive slots of a page and head, of k and of v:
+ *   value = code * 2^(b - 127), b the block's byte (255: every value is NaN).
+ * Codes of slot s of head h of page p start at byte p * page_stride +
+ * h * head_stride + s * token_stride of k and of v, head_dim of them; strides
+ * are multiples of 16, so [pages][heads][slots][dim] and
+ * [pages][slots][heads][dim] both fit.  The byte of that slot's block is at
+ * p * scale_page_stride + h * scale_head_stride + s / block of k_scale and of
+ * v_scale (any alignment).  head_dim is a multiple of 16 and block divides
+ * page_size, else MOE_ERR_SHAPE.
+ */
+typedef struct {
+    void *k, *v;
+    void *k_scale, *v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride;
+    int32_t block;
+} moe_kv_cache_q8;
+
+/*
+ * Workspace bytes of moe_rope_append_q8 and moe_paged_attention_q8 for this
+ * shape and block (host only, no CUDA call): 256-byte aligned, its first 2048
+ * bytes zeroed once before first use.  moe_rope_append_q8 needs those only.
+ */
+MOE_API int moe_attn_q8_workspace_size(const moe_attn_shape *shape, int32_t block, size_t *bytes);
+
+/*
+ * moe_rope_append into an 8-bit cache.  With y the rotated k, or v, in fp32, a
+ * block of tokens and head gets the scale 2^e with the smallest e that keeps
+ * max |y| of the call's tokens in the block within 448 * 2^e (-110 <= e <= 119;
+ * -110 where all are 0), and each y the nearest code of y * 2^-e, ties to even.
+ *   - A block that holds older tokens of the sequence (places before the chunk's
+ *     first) keeps at least its scale: e = max(e, the block's).  If that grows,
+ *     the older codes are rounded again in units of the new scale, where those
+ *     of less than 2^-6 of it lose bits.  Blocks of prefixes that sequences share
+ *     must be whole, or copied before a sequence appends to them.
+ *   - An infinite or NaN y is stored as NaN and does not count in max |y|; a
+ *     finite one past 448 * 2^119 as that.
+ *   - Slots of a block past the sequence's last token are left as they are.
+ * q_out, positions and everything else as in moe_rope_append.
+ */
+MOE_API int moe_rope_append_q8(const moe_attn_shape *shape, const moe_rope *rope, const void *q, int64_t q_stride,
+                               const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                               const moe_kv_cache_q8 *cache, const moe_attn_batch *batch, const int32_t *positions,
+                               void *q_out, int64_t q_out_stride, void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
+/*
+ * moe_paged_attention over an 8-bit cache, with a window or (NULL) over all keys.
+ * dtype is that of q and out; the cache's values enter the products unrounded.
+ * The other arguments, and what is read, are those of moe_paged_attention and
+ * moe_paged_attention_window.
+ */
+MOE_API int moe_paged_attention_q8(const moe_attn_shape *shape, const void *q, int64_t q_stride,
+                                   const moe_kv_cache_q8 *cache, const moe_attn_batch *batch,
+                                   const moe_attn_window *window, float scale, void *out, int64_t out_stride, float *lse,
+                                   void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* Sizes of moe_q4_linear: T rows of x, K inputs, N outputs; 0 <= T <= 2^18,
  * K a multiple of 8, N >= 1, K and N at most 2^22, q_block even and dividing K.
  * x and the residual are bf16; out_dtype MOE_DT_BF16 or MOE_DT_F32. */

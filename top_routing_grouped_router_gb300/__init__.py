@@ -23,7 +23,8 @@ __all__ = [
     "moe_debug_set_waits", "MoEAttnShape", "MoEAttnBatch", "MoEKVCache", "MoERope", "MoEQ4LinearShape", "MoEQ4Weight",
     "make_attn_shape", "make_attn_batch", "make_kv_cache", "make_rope", "make_q4_linear_shape", "make_q4_weight",
     "moe_attn_workspace_size", "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear",
-    "moe_q4_linear_read_error",
+    "moe_q4_linear_read_error", "MoEAttnWindow", "MoEKVCacheQ8", "make_attn_window", "make_kv_cache_q8",
+    "moe_paged_attention_window", "moe_attn_q8_workspace_size", "moe_rope_append_q8", "moe_paged_attention_q8",
 ]
 
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_Q4 = 0, 1, 2
@@ -38,7 +39,8 @@ EXPORTED_SYMBOLS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_group
                     "moe_graphs_bucket", "moe_graphs_run", "moe_graphs_destroy", "moe_lora_pack_size", "moe_lora_pack",
                     "moe_static_scratch_read_error", "moe_debug_set_waits", "moe_attn_workspace_size",
                     "moe_rope_turns", "moe_rope_append", "moe_paged_attention", "moe_q4_linear",
-                    "moe_q4_linear_read_error")
+                    "moe_q4_linear_read_error", "moe_paged_attention_window", "moe_attn_q8_workspace_size",
+                    "moe_rope_append_q8", "moe_paged_attention_q8")
 
 
 class MoEError(RuntimeError):
@@ -87,6 +89,17 @@ class MoEKVCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
     sizes = None  # of make_kv_cache's tensors: pages, heads, slots, head size, type, whether one is in host memory
+
+
+class MoEAttnWindow(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
+class MoEKVCacheQ8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
+                                      "scale_head_stride")] + [("block", ctypes.c_int32)]
+    sizes = None  # of make_kv_cache_q8's tensors, as MoEKVCache's
 
 
 class MoERope(ctypes.Structure):
@@ -147,6 +160,10 @@ def lib() -> ctypes.CDLL:
                                ctypes.POINTER(ctypes.c_float)],
             "moe_rope_append": [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp],
             "moe_paged_attention": [vp, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
+            "moe_paged_attention_window": [vp, vp, i64, vp, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
+            "moe_attn_q8_workspace_size": [vp, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
+            "moe_rope_append_q8": [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp],
+            "moe_paged_attention_q8": [vp, vp, i64, vp, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
             "moe_q4_linear": [vp, vp, i64, vp, vp, i64, vp, i64, vp],
             "moe_q4_linear_read_error": [ctypes.POINTER(ctypes.c_int32), vp],
         }
@@ -438,6 +455,32 @@ def make_kv_cache(k, v) -> MoEKVCache:
     return out
 
 
+def make_kv_cache_q8(k, v, k_scale, v_scale) -> MoEKVCacheQ8:
+    """A paged cache in 8 bits: codes k, v (uint8 or float8_e4m3fn) of logical shape [pages][kv heads][slots][head dim]
+    with strides as in make_kv_cache, and the blocks' powers of two k_scale, v_scale (uint8 or float8_e8m0fnu) of
+    logical shape [pages][kv heads][slots / block], whose last stride is 1."""
+    if k.stride() != v.stride() or k.shape != v.shape or k.stride(3) != 1 or k.dtype != v.dtype:
+        raise ValueError("k and v need equal shapes, strides and types, and contiguous head elements")
+    if (k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride() or k_scale.dtype != v_scale.dtype or
+            k_scale.dim() != 3 or (k_scale.stride(2) != 1 and k_scale.shape[2] != 1)):
+        raise ValueError("k_scale and v_scale need equal shapes [pages, heads, blocks], strides and types, and contiguous blocks")
+    if str(k.dtype)[6:] not in ("uint8", "float8_e4m3fn") or str(k_scale.dtype)[6:] not in ("uint8", "float8_e8m0fnu"):
+        raise ValueError(f"codes are uint8 or float8_e4m3fn, scales uint8 or float8_e8m0fnu, not {k.dtype}, {k_scale.dtype}")
+    blocks = k_scale.shape[2]
+    if k_scale.shape[:2] != k.shape[:2] or blocks == 0 or k.shape[2] % blocks:
+        raise ValueError(f"scales {list(k_scale.shape)} do not divide the slots of a cache {list(k.shape)}")
+    out = MoEKVCacheQ8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
+                       k_scale.stride(0), k_scale.stride(1), k.shape[2] // blocks)
+    out.tensors = (k, v, k_scale, v_scale)
+    out.sizes = (*k.shape, "8-bit", not all(t.is_cuda for t in out.tensors))
+    return out
+
+
+def make_attn_window(window, sinks=0) -> MoEAttnWindow:
+    """A token sees the `window` keys up to its own, and the sequence's first `sinks` keys."""
+    return MoEAttnWindow(int(window), int(sinks))
+
+
 def moe_rope_turns(rot_dim, scaling="none", base=10000.0, factor=1.0, trained_len=0):
     """(turns, mscale): the rotation table as a list of rot_dim / 2 integers in units of 2^-64 turn (host only)."""
     turns = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
@@ -503,12 +546,13 @@ def _wrong(*tensors):
 
 def _attn_checks(shape):
     """What the tensors of a call are held against: elements of q and k, their rows' widths, the type, the sizes of the
-    batch's, the cache's and the rotation's tensors, and the type of positions."""
+    batch's, the cache's and the rotation's tensors, the type of positions, and the sizes of an 8-bit cache."""
     n, dtype = shape.n_tokens, _torch_dtype(shape.dtype)
     wide, kv_wide = shape.n_heads * shape.head_dim, shape.n_kv_heads * shape.head_dim
     shape._checks = (n * wide, n * kv_wide, wide, kv_wide, shape.head_dim, dtype, (shape.n_seqs, shape.max_pages, False),
                      (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim, dtype, False),
-                     (dtype, shape.head_dim, False), _torch_dtype(_INT32))
+                     (dtype, shape.head_dim, False), _torch_dtype(_INT32),
+                     (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim, "8-bit", False))
     return shape._checks
 
 
@@ -567,8 +611,8 @@ def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, w
     """q_out = rotated q; rotated k and v into their cache slots.  q, q_out [N][heads][dim], k, v [N][kv heads][dim]
     (rows may be slices of a wider tensor), positions int32 [N]."""
     at = ctypes.addressof
-    (need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, cache_sizes, rope_sizes,
-     int32) = shape._checks or _attn_checks(shape)
+    (need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, cache_sizes, rope_sizes, int32,
+     _) = shape._checks or _attn_checks(shape)
     if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
         _check_batch(batch, cache, batch_sizes, cache_sizes)
     if rope.sizes is not None and rope.sizes != rope_sizes:
@@ -609,7 +653,7 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
     """Causal attention of the new tokens' q over the paged cache; scale defaults to head_dim ** -0.5.  q, out
     [N][heads][dim] (rows may be slices of a wider tensor), lse fp32 [N][heads]."""
     at = ctypes.addressof
-    need, _, wide, _, dim, dtype, batch_sizes, cache_sizes, _, _ = shape._checks or _attn_checks(shape)
+    need, _, wide, _, dim, dtype, batch_sizes, cache_sizes, _, _, _ = shape._checks or _attn_checks(shape)
     if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
         _check_batch(batch, cache, batch_sizes, cache_sizes)
     if (q.dtype is not dtype or out.dtype is not dtype or q.numel() < need or out.numel() < need or
@@ -635,6 +679,85 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
         _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "moe_paged_attention")
+
+
+def moe_attn_q8_workspace_size(shape: MoEAttnShape, block: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_attn_q8_workspace_size(ctypes.byref(shape), int(block), ctypes.byref(n)), "moe_attn_q8_workspace_size")
+    return n.value
+
+
+def _head_rows(t, what, dim, wide):
+    """Elements between the rows of [rows][heads][dim] whose heads follow one another."""
+    row, head, elem = t.stride()
+    return row if head == dim and elem == 1 and row >= wide else _row_stride(t, what)
+
+
+def moe_rope_append_q8(shape, rope, q, k, v, cache, batch, q_out, positions=None, workspace=None, stream=None):
+    """moe_rope_append into an 8-bit cache (make_kv_cache_q8)."""
+    at = ctypes.addressof
+    (need, kv_need, wide, kv_wide, dim, dtype, batch_sizes, _, rope_sizes, int32,
+     cache_sizes) = shape._checks or _attn_checks(shape)
+    if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
+        _check_batch(batch, cache, batch_sizes, cache_sizes)
+    if rope.sizes is not None and rope.sizes != rope_sizes:
+        _check_rope(rope, rope_sizes)
+    if (q.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype or
+            q.numel() < need or k.numel() < kv_need or v.numel() < kv_need or q_out.numel() < need or
+            not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda)):
+        n, heads, kv_heads = shape.n_tokens, shape.n_heads, shape.n_kv_heads
+        raise _wrong(("q", q, dtype, (n, heads, dim)), ("k", k, dtype, (n, kv_heads, dim)),
+                     ("v", v, dtype, (n, kv_heads, dim)), ("q_out", q_out, dtype, (n, heads, dim)))
+    if positions is not None and type(positions) is not int:
+        if (positions.dtype is not int32 or positions.numel() * wide < need or not positions.is_contiguous() or
+                not positions.is_cuda):
+            raise _wrong(("positions (contiguous)", positions, int32, (shape.n_tokens,)))
+        positions = positions.data_ptr()
+    rc = (_lib or lib()).moe_rope_append_q8(
+        at(shape), at(rope), q.data_ptr(), _head_rows(q, "q", dim, wide), k.data_ptr(), _head_rows(k, "k", dim, kv_wide),
+        v.data_ptr(), _head_rows(v, "v", dim, kv_wide), at(cache), at(batch), positions, q_out.data_ptr(),
+        _head_rows(q_out, "q_out", dim, wide), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "moe_rope_append_q8")
+
+
+def _attend(name, shape, q, cache, cache_sizes, batch, window, out, scale, lse, workspace, stream):
+    """What moe_paged_attention_window and moe_paged_attention_q8 share: the checks of moe_paged_attention, and the call."""
+    at = ctypes.addressof
+    need, _, wide, _, dim, dtype, batch_sizes, _, _, _, _ = shape._checks
+    if batch.sizes != batch_sizes or cache.sizes != cache_sizes:
+        _check_batch(batch, cache, batch_sizes, cache_sizes)
+    if (q.dtype is not dtype or out.dtype is not dtype or q.numel() < need or out.numel() < need or
+            not (q.is_cuda and out.is_cuda)):
+        sizes = shape.n_tokens, shape.n_heads, dim
+        raise _wrong(("q", q, dtype, sizes), ("out", out, dtype, sizes))
+    if lse is not None:
+        fp32 = _torch_dtype(MOE_DT_F32)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        if lse.dtype is not fp32 or lse.numel() * dim < need or not lse.is_cuda:
+            raise _wrong(("lse", lse, fp32, (shape.n_tokens, shape.n_heads)))
+        lse = lse.data_ptr()
+    rc = getattr(_lib or lib(), name)(
+        at(shape), q.data_ptr(), _head_rows(q, "q", dim, wide), at(cache), at(batch), None if window is None else at(window),
+        dim ** -0.5 if scale is None else scale, out.data_ptr(), _head_rows(out, "out", dim, wide), lse,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, name)
+
+
+def moe_paged_attention_window(shape, q, cache, batch, window, out, scale=None, lse=None, workspace=None, stream=None):
+    """moe_paged_attention where a token sees the keys of its window and the sequence's first keys (make_attn_window)."""
+    _attend("moe_paged_attention_window", shape, q, cache, (shape._checks or _attn_checks(shape))[7], batch, window, out, scale,
+            lse, workspace, stream)
+
+
+def moe_paged_attention_q8(shape, q, cache, batch, out, window=None, scale=None, lse=None, workspace=None, stream=None):
+    """moe_paged_attention over an 8-bit cache (make_kv_cache_q8), over all keys or with a window (make_attn_window)."""
+    _attend("moe_paged_attention_q8", shape, q, cache, (shape._checks or _attn_checks(shape))[10], batch, window, out, scale,
+            lse, workspace, stream)
 
 
 def moe_q4_linear(shape, x, weight, out, residual=None, stream=None):

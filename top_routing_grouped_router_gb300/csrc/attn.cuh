@@ -21,7 +21,15 @@ struct Args {
     int64_t q_stride, out_stride;
     float scale;
     int32_t *err;
+    int32_t window, sinks;  // a token sees that many keys up to its own, and these first ones (INT32_MAX: all)
+    // of an 8-bit cache (its other strides are in bytes): powers of two, block tokens each
+    const uint8_t *k_scale, *v_scale;
+    int64_t scale_page, scale_head;
+    int32_t block;
 };
+
+// What a kernel is built for: all keys; a window; an 8-bit cache, with or without a window.
+enum Mode { kAll = 0, kWindow = 1, kQ8 = 2 };
 
 struct Seq {
     int q0;      // first row of the chunk
@@ -185,7 +193,7 @@ struct Partials {
 };
 
 size_t generic_ws_bytes(const moe_attn_shape &s);
-cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, char *ws, cudaStream_t st);
+cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, char *ws, Mode mode, cudaStream_t st);
 bool decode_supported(const moe_attn_shape &s);
 size_t decode_ws_bytes(const moe_attn_shape &s);
 cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
@@ -198,6 +206,9 @@ cudaError_t launch_combine(const Args &a, int dtype, const Partials &p, cudaStre
 
 cudaError_t launch_rope(const moe_attn_shape &s, const moe_rope &r, const attn::Args &a, const void *k, int64_t k_stride,
                         const void *v, int64_t v_stride, const int32_t *positions, cudaStream_t st);
+cudaError_t launch_rope_q8(const moe_attn_shape &s, const moe_rope &r, const attn::Args &a, const moe_kv_cache_q8 &cache,
+                           const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                           cudaStream_t st);
 cudaError_t launch_q4_linear(const moe_q4_linear_shape &s, const void *x, int64_t x_stride, const moe_q4_weight &w,
                              const void *res, int64_t res_stride, void *out, int64_t out_stride, int sms,
                              cudaStream_t st);

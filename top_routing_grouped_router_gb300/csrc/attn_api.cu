@@ -48,6 +48,23 @@ int check_cache(const moe_attn_shape &s, const moe_kv_cache *c) {
     return misaligned(c->k) || misaligned(c->v) ? MOE_ERR_ALIGN : MOE_OK;
 }
 
+// The same of an 8-bit cache: rows of codes start at 16 bytes, blocks of tokens fill a page.
+int check_cache_q8(const moe_attn_shape &s, const moe_kv_cache_q8 *c) {
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return MOE_ERR_NULLPTR;
+    if (s.head_dim % 16 || c->block <= 0 || s.page_size % c->block) return MOE_ERR_SHAPE;
+    const int64_t st[5] = {c->page_stride, c->head_stride, c->token_stride, c->scale_page_stride, c->scale_head_stride};
+    for (int64_t x : st)
+        if (x < 0 || x > (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+    if ((s.page_size > 1 && c->token_stride < s.head_dim) ||
+        (s.n_kv_heads > 1 && (c->head_stride < s.head_dim || c->scale_head_stride < s.page_size / c->block)))
+        return MOE_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)
+        if (st[i] % 16) return MOE_ERR_ALIGN;
+    return misaligned(c->k) || misaligned(c->v) ? MOE_ERR_ALIGN : MOE_OK;
+}
+
+int check_window(const moe_attn_window *w) { return w->window < 1 || w->sinks < 0 ? MOE_ERR_SHAPE : MOE_OK; }
+
 int check_batch(const moe_attn_batch *b) {
     if (!b || !b->cu_q || !b->kv_len || !b->block_table) return MOE_ERR_NULLPTR;
     return misaligned4(b->cu_q) || misaligned4(b->kv_len) || misaligned4(b->block_table) ? MOE_ERR_ALIGN : MOE_OK;
@@ -87,8 +104,23 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache &c, const moe_a
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.err = static_cast<int32_t *>(ws);
+    a.window = INT32_MAX;
     return a;
 }
+
+attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache_q8 &c, const moe_attn_batch &b, const void *q,
+                     int64_t q_stride, void *out, int64_t out_stride, void *ws) {
+    const moe_kv_cache codes{c.k, c.v, c.page_stride, c.head_stride, c.token_stride};
+    attn::Args a = make_args(s, codes, b, q, q_stride, out, out_stride, ws);
+    a.k_scale = static_cast<const uint8_t *>(c.k_scale);
+    a.v_scale = static_cast<const uint8_t *>(c.v_scale);
+    a.scale_page = c.scale_page_stride;
+    a.scale_head = c.scale_head_stride;
+    a.block = c.block;
+    return a;
+}
+
+size_t q8_ws_bytes(const moe_attn_shape &s, int) { return attn::generic_ws_bytes(s); }
 
 }  // namespace
 
@@ -141,57 +173,138 @@ int moe_rope_turns(int32_t rot_dim, int32_t scaling, double base, double factor,
     return MOE_OK;
 }
 
-int moe_rope_append(const moe_attn_shape *shape, const moe_rope *rope, const void *q, int64_t q_stride, const void *k,
-                    int64_t k_stride, const void *v, int64_t v_stride, const moe_kv_cache *cache,
-                    const moe_attn_batch *batch, const int32_t *positions, void *q_out, int64_t q_out_stride,
-                    void *workspace, size_t workspace_bytes, moe_stream_t stream) {
-    MOE_TRY(validate(shape));
-    const moe_attn_shape &s = *shape;
-    if (!rope) return MOE_ERR_NULLPTR;
-    if (rope->rot_dim <= 0 || rope->rot_dim > s.head_dim || rope->rot_dim % 16) return MOE_ERR_SHAPE;
-    if (!std::isfinite(rope->mscale)) return MOE_ERR_SHAPE;
-    if ((rope->q_gamma || rope->k_gamma) && (!(rope->eps >= 0.f) || !std::isfinite(rope->eps))) return MOE_ERR_SHAPE;
-    if (s.n_tokens == 0) return MOE_OK;
-    if (!rope->turns || !q || !k || !v || !q_out) return MOE_ERR_NULLPTR;
-    MOE_TRY(check_cache(s, cache));
+// The checks of both appends that do not depend on the cache.
+static int check_append(const moe_attn_shape &s, const moe_rope *rope, const void *q, int64_t q_stride, const void *k,
+                        int64_t k_stride, const void *v, int64_t v_stride, const moe_attn_batch *batch,
+                        const int32_t *positions, void *q_out, int64_t q_out_stride, void *workspace,
+                        size_t workspace_bytes) {
     MOE_TRY(check_batch(batch));
     MOE_TRY(check_stride(s, q_stride, s.n_heads));
     MOE_TRY(check_stride(s, q_out_stride, s.n_heads));
     MOE_TRY(check_stride(s, k_stride, s.n_kv_heads));
     MOE_TRY(check_stride(s, v_stride, s.n_kv_heads));
     MOE_TRY(check_workspace(workspace, workspace_bytes, kHdrBytes));
-    if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_out) || misaligned(rope->turns) ||
-        misaligned(rope->q_gamma) || misaligned(rope->k_gamma) || misaligned4(positions))
-        return MOE_ERR_ALIGN;
+    return misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_out) || misaligned(rope->turns) ||
+                   misaligned(rope->q_gamma) || misaligned(rope->k_gamma) || misaligned4(positions)
+               ? MOE_ERR_ALIGN
+               : MOE_OK;
+}
+
+static int check_rope(const moe_attn_shape &s, const moe_rope *rope) {
+    if (!rope) return MOE_ERR_NULLPTR;
+    if (rope->rot_dim <= 0 || rope->rot_dim > s.head_dim || rope->rot_dim % 16) return MOE_ERR_SHAPE;
+    if (!std::isfinite(rope->mscale)) return MOE_ERR_SHAPE;
+    if ((rope->q_gamma || rope->k_gamma) && (!(rope->eps >= 0.f) || !std::isfinite(rope->eps))) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int moe_rope_append(const moe_attn_shape *shape, const moe_rope *rope, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride, const moe_kv_cache *cache,
+                    const moe_attn_batch *batch, const int32_t *positions, void *q_out, int64_t q_out_stride,
+                    void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+    MOE_TRY(validate(shape));
+    const moe_attn_shape &s = *shape;
+    MOE_TRY(check_rope(s, rope));
+    if (s.n_tokens == 0) return MOE_OK;
+    if (!rope->turns || !q || !k || !v || !q_out) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_cache(s, cache));
+    MOE_TRY(check_append(s, rope, q, q_stride, k, k_stride, v, v_stride, batch, positions, q_out, q_out_stride, workspace,
+                         workspace_bytes));
     const attn::Args a = make_args(s, *cache, *batch, q, q_stride, q_out, q_out_stride, workspace);
     return launch_rc(launch_rope(s, *rope, a, k, k_stride, v, v_stride, positions,
                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int moe_paged_attention(const moe_attn_shape *shape, const void *q, int64_t q_stride, const moe_kv_cache *cache,
-                        const moe_attn_batch *batch, float scale, void *out, int64_t out_stride, float *lse,
-                        void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+int moe_rope_append_q8(const moe_attn_shape *shape, const moe_rope *rope, const void *q, int64_t q_stride, const void *k,
+                       int64_t k_stride, const void *v, int64_t v_stride, const moe_kv_cache_q8 *cache,
+                       const moe_attn_batch *batch, const int32_t *positions, void *q_out, int64_t q_out_stride,
+                       void *workspace, size_t workspace_bytes, moe_stream_t stream) {
     MOE_TRY(validate(shape));
     const moe_attn_shape &s = *shape;
-    if (!std::isfinite(scale)) return MOE_ERR_SHAPE;
+    MOE_TRY(check_rope(s, rope));
     if (s.n_tokens == 0) return MOE_OK;
-    if (!q || !out) return MOE_ERR_NULLPTR;
-    MOE_TRY(check_cache(s, cache));
+    if (!rope->turns || !q || !k || !v || !q_out) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_cache_q8(s, cache));
+    MOE_TRY(check_append(s, rope, q, q_stride, k, k_stride, v, v_stride, batch, positions, q_out, q_out_stride, workspace,
+                         workspace_bytes));
+    const attn::Args a = make_args(s, *cache, *batch, q, q_stride, q_out, q_out_stride, workspace);
+    return launch_rc(launch_rope_q8(s, *rope, a, *cache, k, k_stride, v, v_stride, positions,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// What the three calls share after the checks of the cache and the window.
+static int attend(const moe_attn_shape &s, attn::Args &a, attn::Mode mode, size_t need, const moe_attn_batch *batch,
+                  float *lse, float scale, void *workspace, size_t workspace_bytes, moe_stream_t stream) {
     MOE_TRY(check_batch(batch));
-    MOE_TRY(check_stride(s, q_stride, s.n_heads));
-    MOE_TRY(check_stride(s, out_stride, s.n_heads));
-    size_t need = 0;
-    MOE_TRY(moe_attn_workspace_size(shape, &need));
+    MOE_TRY(check_stride(s, a.q_stride, s.n_heads));
+    MOE_TRY(check_stride(s, a.out_stride, s.n_heads));
     MOE_TRY(check_workspace(workspace, workspace_bytes, need));
-    if (misaligned(q) || misaligned(out) || misaligned4(lse)) return MOE_ERR_ALIGN;
-    attn::Args a = make_args(s, *cache, *batch, q, q_stride, out, out_stride, workspace);
+    if (misaligned(a.q) || misaligned(a.out) || misaligned4(lse)) return MOE_ERR_ALIGN;
     a.lse = lse;
     a.scale = scale;
     char *hdr = static_cast<char *>(workspace), *ws = hdr + kHdrBytes;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (mode != attn::kAll) return launch_rc(attn::launch_generic(a, s.dtype, s, ws, mode, st));
     if (attn::decode_supported(s)) return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), st));
     if (attn::chunk_supported(s)) return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), st));
-    return launch_rc(attn::launch_generic(a, s.dtype, s, ws, st));
+    return launch_rc(attn::launch_generic(a, s.dtype, s, ws, mode, st));
+}
+
+int moe_paged_attention(const moe_attn_shape *shape, const void *q, int64_t q_stride, const moe_kv_cache *cache,
+                        const moe_attn_batch *batch, float scale, void *out, int64_t out_stride, float *lse,
+                        void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+    size_t need = 0;
+    MOE_TRY(moe_attn_workspace_size(shape, &need));
+    if (!std::isfinite(scale)) return MOE_ERR_SHAPE;
+    if (shape->n_tokens == 0) return MOE_OK;
+    if (!q || !out || !batch) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_cache(*shape, cache));
+    attn::Args a = make_args(*shape, *cache, *batch, q, q_stride, out, out_stride, workspace);
+    return attend(*shape, a, attn::kAll, need, batch, lse, scale, workspace, workspace_bytes, stream);
+}
+
+int moe_paged_attention_window(const moe_attn_shape *shape, const void *q, int64_t q_stride, const moe_kv_cache *cache,
+                               const moe_attn_batch *batch, const moe_attn_window *window, float scale, void *out,
+                               int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream) {
+    size_t need = 0;
+    MOE_TRY(moe_attn_workspace_size(shape, &need));
+    if (!window) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_window(window));
+    if (!std::isfinite(scale)) return MOE_ERR_SHAPE;
+    if (shape->n_tokens == 0) return MOE_OK;
+    if (!q || !out || !batch) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_cache(*shape, cache));
+    attn::Args a = make_args(*shape, *cache, *batch, q, q_stride, out, out_stride, workspace);
+    a.window = window->window;
+    a.sinks = window->sinks;
+    return attend(*shape, a, attn::kWindow, need, batch, lse, scale, workspace, workspace_bytes, stream);
+}
+
+int moe_attn_q8_workspace_size(const moe_attn_shape *shape, int32_t block, size_t *bytes) {
+    if (!bytes) return MOE_ERR_NULLPTR;
+    MOE_TRY(validate(shape));
+    if (shape->head_dim % 16 || block <= 0 || shape->page_size % block) return MOE_ERR_SHAPE;
+    *bytes = kHdrBytes + q8_ws_bytes(*shape, block);
+    return MOE_OK;
+}
+
+int moe_paged_attention_q8(const moe_attn_shape *shape, const void *q, int64_t q_stride, const moe_kv_cache_q8 *cache,
+                           const moe_attn_batch *batch, const moe_attn_window *window, float scale, void *out,
+                           int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+    MOE_TRY(validate(shape));
+    if (window) MOE_TRY(check_window(window));
+    if (!std::isfinite(scale)) return MOE_ERR_SHAPE;
+    if (shape->n_tokens == 0) return MOE_OK;
+    if (!q || !out || !batch) return MOE_ERR_NULLPTR;
+    MOE_TRY(check_cache_q8(*shape, cache));
+    attn::Args a = make_args(*shape, *cache, *batch, q, q_stride, out, out_stride, workspace);
+    if (window) {
+        a.window = window->window;
+        a.sinks = window->sinks;
+    }
+    return attend(*shape, a, attn::kQ8, kHdrBytes + q8_ws_bytes(*shape, cache->block), batch, lse, scale, workspace,
+                  workspace_bytes, stream);
 }
 
 int moe_q4_linear(const moe_q4_linear_shape *shape, const void *x, int64_t x_stride, const moe_q4_weight *weight,

@@ -3,7 +3,10 @@
 //
 // softmax in one pass: for each key tile m' = max(m, max s), l = l e^(m-m') + sum e^(s-m'),
 // o = o e^(m-m') + sum e^(s-m') v, with everything in log2 units so that e^ is exp2.
-#include "attn.cuh"
+//
+// With a window a block goes over the keys that its tokens see only: the first ones, then those from
+// its first token's window on, as one range of places.
+#include "q8.cuh"
 
 namespace moe {
 namespace attn {
@@ -28,9 +31,8 @@ int64_t max_tiles(const moe_attn_shape &s) {
 
 // Parts that each tile's keys are split into: enough blocks for the machine, at least two key
 // tiles a part of the longest sequence that the block table allows.
-int parts(const moe_attn_shape &s) {
+int parts(const moe_attn_shape &s, int64_t keys) {
     const int64_t blocks = max_tiles(s) * s.n_kv_heads * head_slices(s.n_heads / s.n_kv_heads);
-    const int64_t keys = (int64_t)s.max_pages * s.page_size;
     int64_t p = blocks > 0 ? kTargetBlocks / blocks : 1;
     const int64_t most = (keys + 2 * kKeys - 1) / (2 * kKeys);
     if (p > most) p = most;
@@ -38,10 +40,12 @@ int parts(const moe_attn_shape &s) {
     return p < 1 ? 1 : int(p);
 }
 
+int64_t all_keys(const moe_attn_shape &s) { return (int64_t)s.max_pages * s.page_size; }
+
 int smem_bytes(int D) { return (kRows * D + kKeys * (D + 4) + kKeys * D + 4 * kKeys * 4) * 4; }
 
 // NJ: output elements of a lane, head_dim <= 32 NJ.
-template <typename T, int NJ>
+template <typename T, int NJ, Mode kMode>
 __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args a, Partials part, int tt) {
     extern __shared__ float4 smem4[];
     __shared__ int scratch[4 + kThreads / 32];
@@ -76,7 +80,15 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
 #pragma unroll
         for (int j = 0; j < NJ; ++j) o[r][j] = 0.f;
     }
-    const int keys = max(past + j0 + nj, 0);
+    // the keys that the block's tokens see; with a window places [0, cut) and, `gap` further on, the others
+    int keys = max(past + j0 + nj, 0), cut = 0, gap = 0;
+    if (kMode != kAll) {
+        const int low = int(max((int64_t)past + j0 + 1 - a.window, (int64_t)0));
+        cut = min(a.sinks, low);
+        gap = low - cut;
+        keys -= gap;
+    }
+    auto place = [&](int i) { return kMode == kAll || i < cut ? i : i + gap; };
     const int64_t per = ((uint32_t(keys) + kKeys - 1) / kKeys + part.parts - 1) / part.parts * (int64_t)kKeys;
     const int64_t k_begin = blockIdx.z * per;
     const int k_end = int(min(k_begin + per, (int64_t)keys));
@@ -89,20 +101,32 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
     float kv[kFly][8], vv[kFly][8];
     // the cache offset of key lane, in every warp; slots past the last visible key are not read: they
     // may hold anything
+    float k_scale = 1.f, v_scale = 1.f;  // of that key
     auto find_key = [&](int64_t k0) {
-        const int64_t p = k0 + lane;
-        if (p >= keys) return (int64_t)-1;
-        const int pi = a.page_shift >= 0 ? int(p) >> a.page_shift : int(p) / a.page_size;
-        return load_page(a, at.b, pi) * a.page_stride + hk * a.head_stride + (int64_t)(int(p) - pi * a.page_size) * a.token_stride;
+        if (k0 + lane >= keys) return (int64_t)-1;
+        const int p = place(int(k0) + lane);
+        const int pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
+        const int64_t page = load_page(a, at.b, pi);
+        if (kMode == kQ8) {
+            const int64_t of = page * a.scale_page + hk * a.scale_head + (p - pi * a.page_size) / a.block;
+            k_scale = q8::scale_of(q8::ldp_byte(a.k_scale + of));
+            v_scale = q8::scale_of(q8::ldp_byte(a.v_scale + of));
+        }
+        return page * a.page_stride + hk * a.head_stride + (int64_t)(p - pi * a.page_size) * a.token_stride;
     };
     auto load = [&](int64_t key_off, int i0) {
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
             const int item = (i0 + i) * kThreads + tid, kk = item / pieces, c = (item - kk * pieces) * 8;
             const int64_t off = __shfl_sync(0xffffffffu, key_off, kk & 31);
+            const float ks = kMode == kQ8 ? __shfl_sync(0xffffffffu, k_scale, kk & 31) : 1.f;
+            const float vs = kMode == kQ8 ? __shfl_sync(0xffffffffu, v_scale, kk & 31) : 1.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) kv[i][e] = vv[i][e] = 0.f;
-            if (kk < kKeys && off >= 0) {
+            if (kk < kKeys && off >= 0 && kMode == kQ8) {
+                q8::unpack8(q8::ldp8b(static_cast<const uint8_t *>(a.k) + off + c), ks, kv[i]);
+                q8::unpack8(q8::ldp8b(static_cast<const uint8_t *>(a.v) + off + c), vs, vv[i]);
+            } else if (kk < kKeys && off >= 0) {
                 ldp8(static_cast<const T *>(a.k) + off + c, kv[i]);
                 ldp8(static_cast<const T *>(a.v) + off + c, vv[i]);
             }
@@ -159,7 +183,10 @@ __global__ void __launch_bounds__(kThreads, NJ == 2 ? 5 : 1) generic_kernel(Args
         float pr[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const bool on = k0 + lane < seen[r];
+            const int p = place(k0 + lane);
+            const bool on = kMode == kAll ? p < seen[r]
+                                          : uint32_t(k0) + lane < uint32_t(keys) && p < seen[r] &&
+                                                (p < a.sinks || p >= seen[r] - a.window);
             float mx = on ? sc[r] : kNegInf;
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -267,31 +294,37 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Args a, Partials part
     if (a.lse && lane == 0) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 
-template <typename T, int NJ>
-cudaError_t launch_typed(const Args &a, const Partials &p, dim3 grid, int tt, cudaStream_t st) {
+template <typename T, int NJ, Mode kMode>
+cudaError_t launch_mode(const Args &a, const Partials &p, dim3 grid, int tt, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(generic_kernel<T, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(generic_kernel<T, NJ, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    smem_bytes(32 * NJ));
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    return launch_pdl(generic_kernel<T, NJ>, grid, dim3(kThreads), smem_bytes(a.head_dim), st, a, p, tt);
+    return launch_pdl(generic_kernel<T, NJ, kMode>, grid, dim3(kThreads), smem_bytes(a.head_dim), st, a, p, tt);
+}
+
+template <typename T, int NJ>
+cudaError_t launch_typed(const Args &a, const Partials &p, dim3 grid, int tt, Mode mode, cudaStream_t st) {
+    if (mode == kAll) return launch_mode<T, NJ, kAll>(a, p, grid, tt, st);
+    return mode == kWindow ? launch_mode<T, NJ, kWindow>(a, p, grid, tt, st) : launch_mode<T, NJ, kQ8>(a, p, grid, tt, st);
 }
 
 template <typename T>
-cudaError_t launch_dim(const Args &a, const Partials &p, dim3 grid, int tt, cudaStream_t st) {
-    if (a.head_dim <= 64) return launch_typed<T, 2>(a, p, grid, tt, st);
-    if (a.head_dim <= 128) return launch_typed<T, 4>(a, p, grid, tt, st);
-    return launch_typed<T, 8>(a, p, grid, tt, st);
+cudaError_t launch_dim(const Args &a, const Partials &p, dim3 grid, int tt, Mode mode, cudaStream_t st) {
+    if (a.head_dim <= 64) return launch_typed<T, 2>(a, p, grid, tt, mode, st);
+    if (a.head_dim <= 128) return launch_typed<T, 4>(a, p, grid, tt, mode, st);
+    return launch_typed<T, 8>(a, p, grid, tt, mode, st);
 }
 
 }  // namespace
 
 size_t generic_ws_bytes(const moe_attn_shape &s) {
-    const int p = parts(s);
+    const int p = parts(s, all_keys(s));
     return p > 1 ? (size_t)p * s.n_tokens * s.n_heads * (s.head_dim + 2) * 4 : 0;
 }
 
@@ -301,15 +334,17 @@ cudaError_t launch_combine(const Args &a, int dtype, const Partials &p, cudaStre
                                : launch_pdl(combine_kernel<uint16_t>, grid, dim3(kThreads), 0, st, a, p);
 }
 
-cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, char *ws, cudaStream_t st) {
+cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, char *ws, Mode mode, cudaStream_t st) {
     Partials p{};
-    p.parts = parts(s);
+    // with a window no tile has more keys than its own tokens' (fewer parts, never more: the workspace is for all keys)
+    const int64_t seen = (int64_t)a.window + a.sinks + kRows;
+    p.parts = parts(s, mode == kAll || seen > all_keys(s) ? all_keys(s) : seen);
     p.o = reinterpret_cast<float *>(ws);
     p.ml = reinterpret_cast<float2 *>(p.o + (size_t)p.parts * s.n_tokens * s.n_heads * s.head_dim);
     const dim3 grid(unsigned(max_tiles(s)), unsigned(s.n_kv_heads * head_slices(a.group)), unsigned(p.parts));
     const int tt = tokens_per_tile(a.group);
-    const cudaError_t e = dtype == MOE_DT_F32 ? launch_dim<float>(a, p, grid, tt, st)
-                                              : launch_dim<uint16_t>(a, p, grid, tt, st);
+    const cudaError_t e = dtype == MOE_DT_F32 ? launch_dim<float>(a, p, grid, tt, mode, st)
+                                              : launch_dim<uint16_t>(a, p, grid, tt, mode, st);
     if (e != cudaSuccess || p.parts == 1) return e;
     return launch_combine(a, dtype, p, st);
 }

@@ -196,7 +196,10 @@ size_t generic_ws_bytes(const moe_attn_shape &s);
 cudaError_t launch_generic(const Args &a, int dtype, const moe_attn_shape &s, char *ws, Mode mode, cudaStream_t st);
 bool decode_supported(const moe_attn_shape &s);
 size_t decode_ws_bytes(const moe_attn_shape &s);
-cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
+bool decode_q8_supported(const moe_attn_shape &s, int block);
+cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, Mode mode, cudaStream_t st);
+cudaError_t launch_decode_window(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
+cudaError_t launch_decode_q8(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
 bool chunk_supported(const moe_attn_shape &s);
 size_t chunk_ws_bytes(const moe_attn_shape &s);
 cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, cudaStream_t st);

@@ -120,7 +120,9 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache_q8 &c, const mo
     return a;
 }
 
-size_t q8_ws_bytes(const moe_attn_shape &s, int) { return attn::generic_ws_bytes(s); }
+size_t q8_ws_bytes(const moe_attn_shape &s, int block) {
+    return attn::decode_q8_supported(s, block) ? attn::decode_ws_bytes(s) : attn::generic_ws_bytes(s);
+}
 
 }  // namespace
 
@@ -244,9 +246,9 @@ static int attend(const moe_attn_shape &s, attn::Args &a, attn::Mode mode, size_
     a.scale = scale;
     char *hdr = static_cast<char *>(workspace), *ws = hdr + kHdrBytes;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (mode != attn::kAll) return launch_rc(attn::launch_generic(a, s.dtype, s, ws, mode, st));
-    if (attn::decode_supported(s)) return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), st));
-    if (attn::chunk_supported(s)) return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), st));
+    if (mode == attn::kQ8 ? attn::decode_q8_supported(s, a.block) : attn::decode_supported(s))
+        return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), mode, st));
+    if (mode == attn::kAll && attn::chunk_supported(s)) return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), st));
     return launch_rc(attn::launch_generic(a, s.dtype, s, ws, mode, st));
 }
 

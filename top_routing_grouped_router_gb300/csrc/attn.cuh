@@ -201,8 +201,9 @@ cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, cha
 cudaError_t launch_decode_window(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
 cudaError_t launch_decode_q8(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
 bool chunk_supported(const moe_attn_shape &s);
+bool chunk_q8_supported(const moe_attn_shape &s, int block);
 size_t chunk_ws_bytes(const moe_attn_shape &s);
-cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, cudaStream_t st);
+cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, Mode mode, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int dtype, const Partials &p, cudaStream_t st);
 
 }  // namespace attn

@@ -121,7 +121,9 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache_q8 &c, const mo
 }
 
 size_t q8_ws_bytes(const moe_attn_shape &s, int block) {
-    return attn::decode_q8_supported(s, block) ? attn::decode_ws_bytes(s) : attn::generic_ws_bytes(s);
+    return attn::decode_q8_supported(s, block)  ? attn::decode_ws_bytes(s)
+           : attn::chunk_q8_supported(s, block) ? attn::chunk_ws_bytes(s)
+                                                : attn::generic_ws_bytes(s);
 }
 
 }  // namespace
@@ -248,7 +250,8 @@ static int attend(const moe_attn_shape &s, attn::Args &a, attn::Mode mode, size_
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (mode == attn::kQ8 ? attn::decode_q8_supported(s, a.block) : attn::decode_supported(s))
         return launch_rc(attn::launch_decode(a, s, hdr, ws, tc::sm_count(), mode, st));
-    if (mode == attn::kAll && attn::chunk_supported(s)) return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), st));
+    if (mode == attn::kQ8 ? attn::chunk_q8_supported(s, a.block) : attn::chunk_supported(s))
+        return launch_rc(attn::launch_chunk(a, s, ws, tc::sm_count(), mode, st));
     return launch_rc(attn::launch_generic(a, s.dtype, s, ws, mode, st));
 }
 

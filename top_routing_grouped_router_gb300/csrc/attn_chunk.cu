@@ -19,10 +19,16 @@
 // rescaled (by the softmax warps, in TMEM); until then the larger probabilities are exact in bf16
 // terms all the same, since the scale of a row cancels.
 //
+// With a window an item goes over the steps that hold a key which one of its tokens sees: the first
+// keys' steps, then, `skip` steps further on, those from its first token's window on.
+//
+// Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
+// more warps turn them into the bf16 tiles that the tensor cores read: exactly, with their power of two.
+//
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
 // share's end leave fp32 partial results that a second kernel joins.
-#include "attn.cuh"
+#include "q8.cuh"
 #include "tma_nd.cuh"
 
 namespace moe {
@@ -32,22 +38,27 @@ namespace {
 using namespace tc;
 
 // Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMAs, loads, the list of
-// segments, and with heads of 64 the MMAs of tile 1.  It gives up registers that the softmax takes: 8 x 32 x 208 + 4 x 32 x 80 is within the launch's
-// 12 x 32 x 168.
-constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 80;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "");
+// segments, and with heads of 64 the MMAs of tile 1; a fourth, over an 8-bit cache: codes to bf16.
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11, kConvWarp = 12;
+constexpr int kConvThreads = 128;
 constexpr int kM = 128, kKeys = 128;
 constexpr int kMaxCtas = 160;   // one per SM (152)
 constexpr int kMaxSegs = 16;    // segments prepared at a time
 constexpr float kLag = 8.f;     // log2 of the growth of a row's maximum that O tolerates
 constexpr int kJoinRows = 16;   // rows of a block of the join kernel
 
-template <int D>
+template <int D, Mode kMode>
 struct Cfg {
+    static constexpr bool kCodes = kMode == kQ8;
+    // The third warpgroup (and the fourth) gives up registers that the softmax takes, within the launch's.
+    static constexpr int kThreads = kCodes ? 512 : 384, kLaunchRegs = kCodes ? 128 : 168;
+    static constexpr int kSoftmaxRegs = kCodes ? 192 : 208, kOtherRegs = kCodes ? 64 : 80;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");
     static constexpr int kTile = kM * D * 2;                  // one Q tile, one K or V stage
-    static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 2048;
+    static constexpr int kStages = kCodes ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;
+    static constexpr int kRaw = kKeys * D;                    // a stage of codes
+    static constexpr int kRaws = kCodes ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kSmem = (2 + kStages) * kTile + kRaws * kRaw + 1024 + 2048;
     static_assert(kSmem <= 232448, "");
     // TMEM columns of tile t: S at 128 t, P and O here.  Heads of 64 leave room for P beside S: the scores
     // of the next step are computed while the softmax works on this one's, which the softmax holds in
@@ -67,6 +78,7 @@ struct Seg {
     int step0, step1;                   // key steps of this share
     int slot;                           // -1: whole item; else the slot of the partial results
     int tiles;                          // 1 or 2
+    int low, skip;                      // with a window: the first key of its first token's, and the steps left out
 };
 // What the join kernel needs of an item that starts in a CTA's share and goes on past it.
 struct Rec {
@@ -146,8 +158,31 @@ __device__ __forceinline__ uint32_t steps_before(const Seq &s, uint32_t i, Item 
 // starting and ending an item costs, about two steps' time (a mixed batch of short and long
 // items: 85 us with none, the slowest CTA 1.45 times the mean).
 constexpr uint32_t kSetup = 2;
-__device__ __forceinline__ uint32_t places_before(const Seq &s, uint32_t i, Item it, bool whole) {
-    return whole ? i : steps_before(s, i, it) + i * kSetup;
+
+// With a window of w, item i begins at key low_i = max(0, c + i * tokens), c = kv_len - q_len + 1 - w, but for the
+// first keys' steps; it leaves out skip_i = max(0, floor(low_i / kKeys) - sink steps) of them.
+__device__ __forceinline__ uint32_t sink_steps(const Args &a) { return (uint32_t(a.sinks) + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int64_t low_before(const Args &a, const Seq &s) { return (int64_t)s.kv_len - s.q_len + 1 - a.window; }
+template <Mode kMode>
+__device__ __forceinline__ uint32_t skip_of(const Args &a, const Seq &s, uint32_t i, Item it) {
+    if (kMode == kAll) return 0;
+    const int64_t low = low_before(a, s) + (int64_t)i * it.tokens;
+    const uint32_t from = low > 0 ? uint32_t(low) / kKeys : 0, sink = sink_steps(a);
+    return from > sink ? from - sink : 0;
+}
+// sum of skip_j, j < i: the items from j1 on, the first with one, by their closed form.
+template <Mode kMode>
+__device__ __forceinline__ uint32_t skips_before(const Args &a, const Seq &s, uint32_t i, Item it) {
+    if (kMode == kAll) return 0;
+    const int64_t c = low_before(a, s), need = ((int64_t)sink_steps(a) + 1) * kKeys - c;
+    if (need >= (int64_t)i * it.tokens) return 0;
+    const uint32_t j1 = need <= 0 ? 0 : it.div(uint32_t(need) + it.tokens - 1);
+    if (j1 >= i) return 0;
+    return step_sum(i - j1, it, uint32_t(c + (int64_t)j1 * it.tokens)) - (i - j1) * sink_steps(a);
+}
+template <Mode kMode>
+__device__ __forceinline__ uint32_t places_before(const Args &a, const Seq &s, uint32_t i, Item it, bool whole) {
+    return whole ? i : steps_before(s, i, it) - skips_before<kMode>(a, s, i, it) + i * kSetup;
 }
 // Where no sequence can hold more keys than this, items are not cut (each takes one place on the
 // line), and the join is not launched.
@@ -247,7 +282,9 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t p, uint64_t v, uint32
 }
 
 // The block's barrier where its warps are in different code, and its form that ORs a value.
+template <int kThreads>
 __device__ __forceinline__ void meet() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+template <int kThreads>
 __device__ __forceinline__ bool meet_any(bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
@@ -274,22 +311,25 @@ struct Ctx {
     bool whole;         // items are not cut
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ CUtensorMap map_q,
+template <int D, Mode kMode>
+__global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_v,
                                                             const __grid_constant__ Ctx c) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kMode>;
+    constexpr int kThreads = C::kThreads;
     constexpr int kSlabs = D / 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *ctrl = smem + (2 + C::kStages) * C::kTile;
+    uint8_t *raw = smem + (2 + C::kStages) * C::kTile;
+    uint8_t *ctrl = raw + C::kRaws * C::kRaw;
     uint64_t *kv_full = reinterpret_cast<uint64_t *>(ctrl);  // [kStages]
     uint64_t *kv_empty = kv_full + C::kStages;               // [kStages]
     uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
     uint64_t *v_zero = o_empty + 2, *drain = v_zero + C::kStages;  // [kStages], [2]
-    Seg *segs = reinterpret_cast<Seg *>(drain + 2);  // [kMaxSegs]
+    uint64_t *raw_full = drain + 2, *raw_empty = raw_full + C::kRaws;  // [kRaws] each
+    Seg *segs = reinterpret_cast<Seg *>(raw_empty + C::kRaws);  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
     int *nseg = reinterpret_cast<int *>(scan + 16);
     volatile int *abort = nseg + 1;
@@ -310,9 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(smem_u32(&kv_full[i]), 1);
+            mbar_init(smem_u32(&kv_full[i]), C::kCodes ? kConvThreads / 32 : 1);
             mbar_init(smem_u32(&kv_empty[i]), C::kMmaWarps);
             mbar_init(smem_u32(&v_zero[i]), 1);
+        }
+        for (int i = 0; i < C::kRaws; ++i) {
+            mbar_init(smem_u32(&raw_full[i]), 1);
+            mbar_init(smem_u32(&raw_empty[i]), kConvThreads / 32);
         }
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_empty), C::kMmaWarps);
@@ -359,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         *sum = total;
         return before + incl - n;
     };
-    auto seq_places = [&](const Seq &s) { return places_before(s, items_of(s, it), it, c.whole); };
+    auto seq_places = [&](const Seq &s) { return places_before<kMode>(a, s, items_of(s, it), it, c.whole); };
     uint32_t total = 0, n0 = 0, before0 = 0;
     bool rows_ok = true;
     Seq s0{};
@@ -459,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 uint32_t lo = 0, n = items_of(s, it), at_lo = 0;
                 while (n > 1) {
                     const uint32_t each = (n + 31) / 32, cand = lo + lane * each;
-                    const uint32_t before = lane * each < n ? places_before(s, cand, it, c.whole) : ~0u;
+                    const uint32_t before = lane * each < n ? places_before<kMode>(a, s, cand, it, c.whole) : ~0u;
                     const uint32_t last = 31 - __clz(__ballot_sync(0xffffffffu, before <= rem));
                     at_lo = __shfl_sync(0xffffffffu, before, last);
                     lo += last * each;
@@ -469,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 item0 = first + h * per_head + at_lo;
                 located = true;
             }
-            const uint32_t steps = item_steps(s, i, it), setup = c.whole ? 0 : kSetup;
+            const uint32_t skip = skip_of<kMode>(a, s, i, it), steps = item_steps(s, i, it) - skip, setup = c.whole ? 0 : kSetup;
             const uint32_t places = c.whole ? 1 : steps + kSetup, end = min(item0 + places, u_end);
             // steps begin after the item's setup; a share that ends within it leaves the item to the next
             const uint32_t from = max(w, item0 + setup);
@@ -487,6 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     g.step1 = c.whole ? int(steps) : int(end - item0 - setup);
                     g.slot = whole ? -1 : int(cta * 2 + (starts ? 1 : 0));
                     g.tiles = s.q_len - g.tok0 > int(tt) ? 2 : 1;
+                    if (kMode != kAll) {
+                        g.low = int(max(low_before(a, s) + g.tok0, (int64_t)0));
+                        g.skip = int(skip);
+                    }
                     segs[k] = g;
                     if (!whole && starts) {
                         const int last = int(sh.owner(item0 + places - 1));
@@ -514,17 +562,110 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             *cur_seq = s;
         }
     };
+    // the sequence's step that step i of a segment is, and whether rows of it are of keys that no token of the item
+    // sees between the first keys and the window: rows [from, to) of the step from key k0 on
+    const uint32_t sinks_end = kMode == kAll ? 0 : sink_steps(a);
+    auto real = [&](const Seg &g, int i) { return kMode == kAll || uint32_t(i) < sinks_end ? i : i + g.skip; };
+    auto hidden = [&](const Seg &g, int k0, int &from, int &to) {
+        from = max(a.sinks - k0, 0);
+        to = min(g.low - k0, kKeys);
+        return kMode != kAll && from < to;
+    };
     bool ok = true;
-    if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        int stage = 0;                      // ring position
+    if (C::kCodes && warp >= kConvWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        // ------------------------------------------------ codes to bf16
+        // Tiles alternate: k, v of a step.  A thread takes one 16-byte piece of a row, then that of the row 128 *
+        // 16 / D further on.
+        constexpr int kPieces = D / 16, kRowsAt = kConvThreads / kPieces, kTimes = kKeys / kRowsAt;
+        const int at = tid - kConvWarp * 32, row0 = at / kPieces, piece = at % kPieces;
+        int stage = 0, rs = 0;
+        uint32_t phase = 0, r_phase = 0;
+        for (uint32_t u = u_begin; u < u_end && ok;) {
+            meet<kThreads>();
+            const int ns = *nseg;
+            u = cursor[3];
+            for (int k = 0; k < ns && ok; ++k) {
+                const Seg g = segs[k];
+                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                // lane i < 8: the scales of keys 16 i .. 16 i + 15 of a step, k's and v's; found a step ahead
+                auto bytes_of = [&](int step) {
+                    const int p = real(g, step) * kKeys + lane * 16;
+                    if (lane >= kKeys / 16 || p >= keys || (p >= a.sinks && p + 16 <= g.low)) return 127u | 127u << 8;
+                    const int pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
+                    const int64_t of = load_page(a, g.b, pi) * a.scale_page + g.h * a.scale_head + (p - pi * a.page_size) / a.block;
+                    return q8::ldp_byte(a.k_scale + of) | q8::ldp_byte(a.v_scale + of) << 8;
+                };
+                uint32_t bytes = bytes_of(g.step0);
+                for (int step = g.step0; step < g.step1 && ok; ++step) {
+                    const uint32_t next = step + 1 < g.step1 ? bytes_of(step + 1) : 0;
+                    const int k0 = real(g, step) * kKeys, live = keys - k0;
+                    int from, to;
+                    const bool hide = hidden(g, k0, from, to);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt) && mbar_wait(smem_u32(&raw_full[rs]), r_phase, wt);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t src = smem_u32(raw + rs * C::kRaw) + at * 16;
+                        const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile) + piece / 4 * (kKeys * 128) + row0 * 128;
+                        // the two 16-byte halves of a piece's bf16 values, in the order in which eight lanes that store
+                        // together fall in different banks
+                        const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
+#pragma unroll
+                        for (int i = 0; i < kTimes; ++i) {
+                            const int row = row0 + i * kRowsAt;
+                            uint4 w = lds_v4(src + i * (kConvThreads * 16));
+                            if (row >= live || (hide && row >= from && row < to)) w = make_uint4(0, 0, 0, 0);
+                            const uint32_t byte = __shfl_sync(0xffffffffu, bytes, row / 16) >> (8 * kv) & 255;
+                            const float f = q8::scale_of(byte);
+                            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t h[2] = {q8::to_f16x2(x[e]), q8::to_f16x2(x[e] >> 16)};
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+                                    y[2 * e + j] = pack_bf16(v.x * f, v.y * f);
+                                }
+                            }
+                            const uint32_t to_row = dst + i * (kRowsAt * 128);
+                            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                            sts_v4(to_row + ((c0 ^ (row & 7)) * 16), half ? hi : lo);
+                            sts_v4(to_row + (((c0 ^ 1) ^ (row & 7)) * 16), half ? lo : hi);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&kv_full[stage]));
+                            mbar_arrive(smem_u32(&raw_empty[rs]));
+                        }
+                        if (++stage == C::kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                        if (++rs == C::kRaws) {
+                            rs = 0;
+                            r_phase ^= 1;
+                        }
+                    }
+                    bytes = next;
+                }
+            }
+            ok = !meet_any<kThreads>(!ok);
+        }
+    } else if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        int stage = 0;                      // ring position (the load warp's: of the ring that TMA fills)
         uint32_t phase = 0, q_phase = 0;
         uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
         uint32_t z_phase = 0;               // bit i: stage i
         uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
         for (uint32_t u = u_begin; u < u_end && ok;) {
             if (warp == kListWarp) list();
-            meet();
+            meet<kThreads>();
             const int ns = *nseg;
             u = cursor[3];
             if (warp == kLoadWarp) {
@@ -535,8 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
                     const int boxes_max = kKeys / box;
                     auto page_of = [&](int step) {  // lane i: the page of box i of the step
-                        const int p = step * kKeys + lane * box;
-                        return lane < boxes_max && p < keys ? load_page(a, g.b, p / ps) : -1;
+                        const int p = real(g, step) * kKeys + lane * box;
+                        const bool seen = kMode == kAll || p < a.sinks || p + box > g.low;
+                        return lane < boxes_max && p < keys && seen ? load_page(a, g.b, p / ps) : -1;
                     };
                     int page = page_of(g.step0);
                     ok = mbar_wait(smem_u32(q_empty), q_phase ^ 1, wt);
@@ -558,22 +700,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         const int next = step + 1 < g.step1 ? page_of(step + 1) : -1;
                         const int have = __popc(__ballot_sync(0xffffffffu, page >= 0));
                         for (int kv = 0; kv < 2; ++kv) {
-                            ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt);
+                            ok = mbar_wait(smem_u32(C::kCodes ? &raw_empty[stage] : &kv_empty[stage]), phase ^ 1, wt);
                             if (!__all_sync(0xffffffffu, ok)) {
                                 ok = false;
                                 break;
                             }
-                            const uint32_t full = smem_u32(&kv_full[stage]);
-                            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(have * box * D * 2));
+                            const uint32_t full = smem_u32(C::kCodes ? &raw_full[stage] : &kv_full[stage]);
+                            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(have * box * D * (C::kCodes ? 1 : 2)));
                             __syncwarp();
                             if (page >= 0) {
-                                const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile + lane * box * 128);
-                                const int tok = ps > kKeys ? step * kKeys % ps : 0;
-                                for (int d = 0; d < kSlabs; ++d)
-                                    tma_load_4d(dst + d * kKeys * 128, kv ? &map_v : &map_k, d * 64, tok, g.h, page, full);
+                                const int tok = ps > kKeys ? real(g, step) * kKeys % ps : 0;
+                                if constexpr (C::kCodes) {
+                                    tma_load_4d(smem_u32(raw + stage * C::kRaw + lane * box * D), kv ? &map_v : &map_k, 0, tok,
+                                                g.h, page, full);
+                                } else {
+                                    const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile + lane * box * 128);
+                                    for (int d = 0; d < kSlabs; ++d)
+                                        tma_load_4d(dst + d * kKeys * 128, kv ? &map_v : &map_k, d * 64, tok, g.h, page, full);
+                                }
                             }
                             ring_waited |= 1u << stage;
-                            if (++stage == C::kStages) {
+                            if (++stage == (C::kCodes ? C::kRaws : C::kStages)) {
                                 stage = 0;
                                 phase ^= 1;
                             }
@@ -634,20 +781,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             release_k();
                         }
                         if (!wait(&kv_full[v_stage], v_phase)) break;
-                        // keys past the last that the item sees: their slots may hold anything (or were not
-                        // loaded), and 0 * NaN is NaN: the first warp zeroes the rows
-                        const int live = keys - step * kKeys;
-                        if (live < kKeys && t0 == 0) {
-                            const int from = max(live, 0);
+                        // keys that the item does not see, past its last and before its window: their slots may hold
+                        // anything (or were not loaded), and 0 * NaN is NaN: the first warp zeroes the rows (over an
+                        // 8-bit cache they came as zeros)
+                        const int k0 = real(g, step) * kKeys, live = keys - k0;
+                        int from, to;
+                        const bool hide = hidden(g, k0, from, to), zero = !C::kCodes && (live < kKeys || hide);
+                        if (zero && t0 == 0) {
                             const uint32_t vb = smem_u32(smem + (2 + v_stage) * C::kTile);
-                            for (int i = from * 8 + lane; i < kKeys * 8; i += 32)
+                            auto clear = [&](int first, int end) {
+                                for (int i = first * 8 + lane; i < end * 8; i += 32)
 #pragma unroll
-                                for (int d = 0; d < kSlabs; ++d)
-                                    sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                                    for (int d = 0; d < kSlabs; ++d)
+                                        sts_v4(vb + d * kKeys * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                            };
+                            clear(max(live, 0), kKeys);
+                            if (hide) clear(from, to);
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
                             if (C::kMmaWarps == 2 && lane == 0) mbar_arrive(smem_u32(&v_zero[v_stage]));
-                        } else if (live < kKeys) {
+                        } else if (zero) {
                             if (!wait(&v_zero[v_stage], z_phase >> v_stage & 1)) break;
                             z_phase ^= 1u << v_stage;
                         }
@@ -675,14 +828,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
             }
             // the segment list is free; a role that gave up ends the CTA
-            ok = !meet_any(!ok);
+            ok = !meet_any<kThreads>(!ok);
         }
         // an aborting CTA waits for its own copies and MMAs before it gives up its memory
         if (warp == kLoadWarp && !ok) {
-            for (int i = 0; i < C::kStages; ++i) {
+            for (int i = 0; i < (C::kCodes ? C::kRaws : C::kStages); ++i) {
                 // the last fill of stage i was in the current phase if i < stage, else in the one before
                 const uint32_t par = i < stage ? phase : phase ^ 1;
-                if (ring_waited >> i & 1) mbar_wait_drain(smem_u32(&kv_full[i]), par, wt);
+                if (ring_waited >> i & 1) mbar_wait_drain(smem_u32(C::kCodes ? &raw_full[i] : &kv_full[i]), par, wt);
             }
             mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
         }
@@ -692,10 +845,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_wait_drain(bar, 0, wt);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         uint32_t s_phase = 0, o_phase = 0;
         for (uint32_t u = u_begin; u < u_end && ok;) {
-            meet();
+            meet<kThreads>();
             const int ns = *nseg;
             u = cursor[3];
             // ------------------------------------------------ softmax and epilogue, one row a thread
@@ -735,11 +888,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
                     }
-                    const int k0 = step * kKeys;
+                    const int k0 = real(g, step) * kKeys;
                     if (k0 > seen_all - kKeys) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i)
                             if (k0 + i >= seen) x[i] = 0xff800000u;
+                    }
+                    if (kMode != kAll && k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys) {
+                        // before the window of a row of the tile
+                        const int from = a.sinks - k0, to = max(seen - a.window, 0) - k0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i >= from && i < to) x[i] = 0xff800000u;
                     }
                     float mx[4];
 #pragma unroll
@@ -777,7 +937,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             tmem_st16(to + i, w);
                         }
                     }
-                    const float z = m == kNegInf ? 0.f : m * sl2;
+                    float z = m == kNegInf ? 0.f : m * sl2;
+                    // x * sl2 - z is off by z's rounding, the same for a whole row, where it cancels: but from 2^31 on
+                    // its power of two may pass fp32's largest number.  Far below that the difference is taken first.
+                    const bool far = fabsf(z) > 0x1p26f;
+                    if (__any_sync(0xffffffffu, far && live)) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) x[i] = far ? __float_as_uint(__uint_as_float(x[i]) - m) : x[i];
+                        z = far ? 0.f : z;
+                    }
                     const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
                     // probabilities in bf16 for the product (up to 2^-8 of each; error of the 2048-token chunk against 64 bits
                     // 0.0023 of the outputs' size, with fp32 probabilities 0.0017); their sum stays in fp32
@@ -843,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m * sl2 + log2f(l)) * kLn2;
                 }
             }
-            ok = !meet_any(!ok);
+            ok = !meet_any<kThreads>(!ok);
         }
     }
 
@@ -938,29 +1106,38 @@ int max_ctas(const moe_attn_shape &s) {
 }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int D>
+template <int D, Mode kMode>
 bool set_smem_attr() {
+    using C = Cfg<D, kMode>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        if (cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(chunk_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return false;
         // the softmax's registers come from the launch's: fewer, and the kernel would wait for them for ever
         cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, chunk_kernel<D>) != cudaSuccess || fa.numRegs < kLaunchRegs) return false;
+        if (cudaFuncGetAttributes(&fa, chunk_kernel<D, kMode>) != cudaSuccess || fa.numRegs < C::kLaunchRegs) return false;
         attr_set[dev] = true;
     }
     return true;
 }
 
-template <int D>
+template <int D, Mode kMode>
 cudaError_t launch_typed(const Ctx &c, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, int grid,
                          cudaStream_t st) {
-    if (!set_smem_attr<D>()) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_pdl(chunk_kernel<D>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, st, mq, mk, mv, c);
+    using C = Cfg<D, kMode>;
+    if (!set_smem_attr<D, kMode>()) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_pdl(chunk_kernel<D, kMode>, dim3(grid), dim3(C::kThreads), C::kSmem, st, mq, mk, mv, c);
     if (e != cudaSuccess || c.whole) return e;
     return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * kM / kJoinRows), dim3(kJoinThreads), 0, st, c);
+}
+
+template <Mode kMode>
+cudaError_t launch_dim(const Ctx &c, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, int grid,
+                       cudaStream_t st) {
+    return c.a.head_dim == 128 ? launch_typed<128, kMode>(c, mq, mk, mv, grid, st)
+                               : launch_typed<64, kMode>(c, mq, mk, mv, grid, st);
 }
 
 }  // namespace
@@ -974,12 +1151,15 @@ bool chunk_supported(const moe_attn_shape &s) {
            max_places(s) < 2147483648.0;
 }
 
+// Over an 8-bit cache sixteen keys of a step share a scale.
+bool chunk_q8_supported(const moe_attn_shape &s, int block) { return chunk_supported(s) && block % 16 == 0; }
+
 size_t chunk_ws_bytes(const moe_attn_shape &s) {
     const size_t slots = 2 * (size_t)max_ctas(s);
     return round256(kMaxCtas * sizeof(Rec)) + round256(slots * 2 * kM * sizeof(float2)) + slots * 2 * kM * s.head_dim * 4;
 }
 
-cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, cudaStream_t st) {
+cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int sms, Mode mode, cudaStream_t st) {
     Ctx c{};
     c.a = a;
     c.tt = uint32_t(kM / a.group);
@@ -998,14 +1178,16 @@ cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int s
     const uint64_t qd[3] = {D, (uint64_t)s.n_heads, (uint64_t)s.n_tokens}, qs[2] = {D * 2, (uint64_t)a.q_stride * 2};
     const uint32_t qb[3] = {64, (uint32_t)a.group, c.tt};
     // a dimension of one element is never stepped over: any legal stride stands in for its own
-    const uint64_t row = D * 2;
+    const uint64_t elem = mode == kQ8 ? 1 : 2, row = D * elem;
     const uint64_t kd[4] = {D, (uint64_t)s.page_size, (uint64_t)s.n_kv_heads, (uint64_t)s.n_pages};
-    const uint64_t ks[3] = {(uint64_t)a.token_stride * 2, s.n_kv_heads > 1 ? (uint64_t)a.head_stride * 2 : row,
-                            s.n_pages > 1 ? (uint64_t)a.page_stride * 2 : row};
-    const uint32_t kb[4] = {64, (uint32_t)(s.page_size < kKeys ? s.page_size : kKeys), 1, 1};
-    if (!make_map_nd(&mq, a.q, 3, qd, qs, qb) || !make_map_nd(&mk, a.k, 4, kd, ks, kb) || !make_map_nd(&mv, a.v, 4, kd, ks, kb))
+    const uint64_t ks[3] = {(uint64_t)a.token_stride * elem, s.n_kv_heads > 1 ? (uint64_t)a.head_stride * elem : row,
+                            s.n_pages > 1 ? (uint64_t)a.page_stride * elem : row};
+    const uint32_t kb[4] = {mode == kQ8 ? (uint32_t)D : 64, (uint32_t)(s.page_size < kKeys ? s.page_size : kKeys), 1, 1};
+    auto make_kv = mode == kQ8 ? make_map_bytes : make_map_nd;
+    if (!make_map_nd(&mq, a.q, 3, qd, qs, qb) || !make_kv(&mk, a.k, 4, kd, ks, kb) || !make_kv(&mv, a.v, 4, kd, ks, kb))
         return cudaErrorInvalidValue;
-    return D == 128 ? launch_typed<128>(c, mq, mk, mv, grid, st) : launch_typed<64>(c, mq, mk, mv, grid, st);
+    if (mode == kAll) return launch_dim<kAll>(c, mq, mk, mv, grid, st);
+    return mode == kWindow ? launch_dim<kWindow>(c, mq, mk, mv, grid, st) : launch_dim<kQ8>(c, mq, mk, mv, grid, st);
 }
 
 }  // namespace attn

@@ -59,8 +59,9 @@ bool make_map_slabs(CUtensorMap *m, const void *base, uint64_t rows, uint64_t co
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                 const uint32_t *box) {
+namespace {
+bool make_map_any(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                  const uint32_t *box, CUtensorMapDataType type, CUtensorMapSwizzle swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (!fn || rank < 2 || rank > 4) return false;
     cuuint64_t d[4], st[3];
@@ -71,9 +72,19 @@ bool make_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dim
         es[i] = 1;
         if (i > 0) st[i - 1] = strides[i - 1];
     }
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(base), d, st, bx, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, type, cuuint32_t(rank), const_cast<void *>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool make_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box) {
+    return make_map_any(m, base, rank, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_map_bytes(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box) {
+    return make_map_any(m, base, rank, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 int sm_count() {

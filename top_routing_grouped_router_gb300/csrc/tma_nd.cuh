@@ -19,6 +19,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // swizzle: box[0] is 64 elements.
 bool make_map_nd(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
                  const uint32_t *box);
+// The same of bytes, not swizzled: box[0] is a multiple of 16.
+bool make_map_bytes(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box);
 
 }  // namespace tc
 }  // namespace moe

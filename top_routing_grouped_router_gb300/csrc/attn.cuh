@@ -25,7 +25,7 @@ struct Args {
     // of an 8-bit cache (its other strides are in bytes): powers of two, block tokens each
     const uint8_t *k_scale, *v_scale;
     int64_t scale_page, scale_head;
-    int32_t block;
+    int32_t block, block_shift;  // log2(block), -1 if it is no power of two
 };
 
 // What a kernel is built for: all keys; a window; an 8-bit cache, with or without a window.

@@ -75,6 +75,14 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
     return (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) ? MOE_ERR_ALIGN : MOE_OK;
 }
 
+// -1 if n is no power of two.
+int log2_of(int n) {
+    if (n & (n - 1)) return -1;
+    int i = 0;
+    while ((1 << i) < n) ++i;
+    return i;
+}
+
 attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache &c, const moe_attn_batch &b, const void *q,
                      int64_t q_stride, void *out, int64_t out_stride, void *ws) {
     attn::Args a{};
@@ -96,9 +104,7 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache &c, const moe_a
     a.n_pages = s.n_pages;
     a.max_pages = s.max_pages;
     a.max_q = s.max_q;
-    a.page_shift = -1;
-    if ((s.page_size & (s.page_size - 1)) == 0)
-        for (a.page_shift = 0; (1 << a.page_shift) < s.page_size;) ++a.page_shift;
+    a.page_shift = log2_of(s.page_size);
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;
@@ -117,6 +123,7 @@ attn::Args make_args(const moe_attn_shape &s, const moe_kv_cache_q8 &c, const mo
     a.scale_page = c.scale_page_stride;
     a.scale_head = c.scale_head_stride;
     a.block = c.block;
+    a.block_shift = log2_of(c.block);
     return a;
 }
 

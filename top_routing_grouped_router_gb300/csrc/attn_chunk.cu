@@ -23,7 +23,13 @@
 // keys' steps, then, `skip` steps further on, those from its first token's window on.
 //
 // Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
-// more warps turn them into the bf16 tiles that the tensor cores read: exactly, with their power of two.
+// more warps turn them into the fp16 tiles that the tensor cores read: one instruction for two codes,
+// exact.  (To bf16, with their powers of two, they took three times the instructions, next to which the
+// softmax starved: 750 us for 2048 tokens over 16384 keys.)  The powers of two go elsewhere.  A row of Q
+// becomes fp16 in units of its own that bring its largest element to 2^14 (fp16 then holds elements
+// down to 2^-28 of that exactly).  The scale of sixteen keys is a factor of their scores, that of their
+// values moves the exponents of their probabilities, which are fp16 times 2^7; O is in units of the
+// largest scale of v so far (of a step's, where that is smaller by more than 2^8, down to 2^-60 of it).
 //
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
@@ -38,7 +44,7 @@ namespace {
 using namespace tc;
 
 // Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMAs, loads, the list of
-// segments, and with heads of 64 the MMAs of tile 1; a fourth, over an 8-bit cache: codes to bf16.
+// segments, and with heads of 64 the MMAs of tile 1; a fourth, over an 8-bit cache: codes to fp16.
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11, kConvWarp = 12;
 constexpr int kConvThreads = 128;
 constexpr int kM = 128, kKeys = 128;
@@ -55,10 +61,11 @@ struct Cfg {
     static constexpr int kSoftmaxRegs = kCodes ? 192 : 208, kOtherRegs = kCodes ? 64 : 80;
     static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");
     static constexpr int kTile = kM * D * 2;                  // one Q tile, one K or V stage
-    static constexpr int kStages = kCodes ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;
+    static constexpr int kStages = kCodes ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 8;
     static constexpr int kRaw = kKeys * D;                    // a stage of codes
-    static constexpr int kRaws = kCodes ? (D == 128 ? 4 : 8) : 0;
-    static constexpr int kSmem = (2 + kStages) * kTile + kRaws * kRaw + 1024 + 2048;
+    static constexpr int kRaws = kCodes ? (D == 128 ? 2 : 6) : 0;
+    static constexpr int kCtrl = kCodes && D == 64 ? 3072 : 2048;
+    static constexpr int kSmem = (2 + kStages) * kTile + kRaws * kRaw + 1024 + kCtrl;
     static_assert(kSmem <= 232448, "");
     // TMEM columns of tile t: S at 128 t, P and O here.  Heads of 64 leave room for P beside S: the scores
     // of the next step are computed while the softmax works on this one's, which the softmax holds in
@@ -80,6 +87,17 @@ struct Seg {
     int tiles;                          // 1 or 2
     int low, skip;                      // with a window: the first key of its first token's, and the steps left out
 };
+// The scales of a step over an 8-bit cache, by groups of 16 keys: k's as factors, v's as bytes (-1: a group
+// without one), and the largest of these.  A ring of kScaleSlots steps: the step that takes a place again
+// is converted once the scores of a step behind its last user's are under way.
+struct Scales {
+    float k[8];
+    int v[8];
+    int top, pad[3];
+};
+constexpr int kScaleSlots = 8;
+constexpr int kProbBits = 7;  // probabilities times 2^7: with kLag at most 2^15 in fp16
+
 // What the join kernel needs of an item that starts in a CTA's share and goes on past it.
 struct Rec {
     int n, h, tok0, q0, q_len;  // n: parts (0: none)
@@ -329,7 +347,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
     uint64_t *v_zero = o_empty + 2, *drain = v_zero + C::kStages;  // [kStages], [2]
     uint64_t *raw_full = drain + 2, *raw_empty = raw_full + C::kRaws;  // [kRaws] each
-    Seg *segs = reinterpret_cast<Seg *>(raw_empty + C::kRaws);  // [kMaxSegs]
+    uint64_t *sc_full = raw_empty + C::kRaws, *q_ready = sc_full + (C::kCodes ? kScaleSlots : 0);  // [2]
+    Scales *scales = reinterpret_cast<Scales *>(ctrl + (q_ready + 3 - kv_full) / 2 * 16);  // [kScaleSlots], 16-byte aligned
+    Seg *segs = reinterpret_cast<Seg *>(scales + (C::kCodes ? kScaleSlots : 0));  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
     int *nseg = reinterpret_cast<int *>(scan + 16);
     volatile int *abort = nseg + 1;
@@ -358,6 +378,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             mbar_init(smem_u32(&raw_full[i]), 1);
             mbar_init(smem_u32(&raw_empty[i]), kConvThreads / 32);
         }
+        for (int i = 0; C::kCodes && i < kScaleSlots; ++i) mbar_init(smem_u32(&sc_full[i]), 1);
+        for (int t = 0; C::kCodes && t < 2; ++t) mbar_init(smem_u32(&q_ready[t]), kM);
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_empty), C::kMmaWarps);
         for (int t = 0; t < 2; ++t) {
@@ -574,12 +596,18 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     bool ok = true;
     if (C::kCodes && warp >= kConvWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        // ------------------------------------------------ codes to bf16
+        // ------------------------------------------------ codes to fp16
         // Tiles alternate: k, v of a step.  A thread takes one 16-byte piece of a row, then that of the row 128 *
         // 16 / D further on.
         constexpr int kPieces = D / 16, kRowsAt = kConvThreads / kPieces, kTimes = kKeys / kRowsAt;
         const int at = tid - kConvWarp * 32, row0 = at / kPieces, piece = at % kPieces;
-        int stage = 0, rs = 0;
+        // the two 16-byte halves of a piece's values, in the order in which eight lanes that store together fall in
+        // different banks; a row's number mod 8, which the swizzle takes, is the same in all of a thread's pieces
+        const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
+        const uint32_t to0 = piece / 4 * (kKeys * 128) + row0 * 128 + ((c0 ^ (row0 & 7)) * 16);
+        const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) * 16);
+        static_assert(kRowsAt % 8 == 0 && kTimes % 4 == 0, "");
+        int stage = 0, rs = 0, slot = 0;
         uint32_t phase = 0, r_phase = 0;
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
@@ -588,20 +616,46 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
                 const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
-                // lane i < 8: the scales of keys 16 i .. 16 i + 15 of a step, k's and v's; found a step ahead
-                auto bytes_of = [&](int step) {
-                    const int p = real(g, step) * kKeys + lane * 16;
-                    if (lane >= kKeys / 16 || p >= keys || (p >= a.sinks && p + 16 <= g.low)) return 127u | 127u << 8;
-                    const int pi = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
-                    const int64_t of = load_page(a, g.b, pi) * a.scale_page + g.h * a.scale_head + (p - pi * a.page_size) / a.block;
-                    return q8::ldp_byte(a.k_scale + of) | q8::ldp_byte(a.v_scale + of) << 8;
+                // lanes 0-7: the bytes of k of keys 16 i .. 16 i + 15 of a step, lanes 8-15 those of v.  Their page is
+                // asked for two steps ahead and they themselves one; nothing looks at either before it is needed.
+                const uint8_t *bytes = (lane < 8 ? a.k_scale : a.v_scale) + g.h * a.scale_head;
+                auto page_of = [&](int step) {
+                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
+                    if (step >= g.step1 || lane >= 16 || p >= keys || (p >= a.sinks && p + 16 <= g.low)) return -1;
+                    return ldp(a.table + (size_t)g.b * a.max_pages + (a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size));
                 };
-                uint32_t bytes = bytes_of(g.step0);
+                int byte;  // -1: none
+                auto byte_of = [&](int step, int page) {
+                    byte = -1;
+                    if (page < 0 || page >= a.n_pages) return;  // the load warp records pages that do not exist
+                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
+                    const int slot = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
+                    const int block = a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block;
+                    byte = int(q8::ldp_byte(bytes + page * a.scale_page + block));
+                };
+                byte_of(g.step0, page_of(g.step0));
+                int page = page_of(g.step0 + 1);
                 for (int step = g.step0; step < g.step1 && ok; ++step) {
-                    const uint32_t next = step + 1 < g.step1 ? bytes_of(step + 1) : 0;
+                    // a group whose byte says NaN has NaN codes, and no scale
+                    const uint32_t nans = __ballot_sync(0xffffffffu, byte == 255);
+                    if (warp == kConvWarp) {
+                        const int own = byte == 255 ? -1 : byte;
+                        const int top = __reduce_max_sync(0xffffffffu, lane >= 8 ? own : -1);
+                        if (lane < 8)
+                            scales[slot].k[lane] = own < 0 ? 1.f : q8::scale_of(own);
+                        else if (lane < 16)
+                            scales[slot].v[lane - 8] = own;
+                        if (lane == 0) scales[slot].top = top;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sc_full[slot]));
+                        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                    }
+                    byte_of(step + 1, page);
+                    page = page_of(step + 2);
                     const int k0 = real(g, step) * kKeys, live = keys - k0;
                     int from, to;
-                    const bool hide = hidden(g, k0, from, to);
+                    const bool hide = hidden(g, k0, from, to), edge = live < kKeys || hide || nans != 0;
+#pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt) && mbar_wait(smem_u32(&raw_full[rs]), r_phase, wt);
                         if (!__all_sync(0xffffffffu, ok)) {
@@ -609,32 +663,32 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             break;
                         }
                         const uint32_t src = smem_u32(raw + rs * C::kRaw) + at * 16;
-                        const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile) + piece / 4 * (kKeys * 128) + row0 * 128;
-                        // the two 16-byte halves of a piece's bf16 values, in the order in which eight lanes that store
-                        // together fall in different banks
-                        const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
+                        const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile);
+                        // four pieces at a time: their loads before the first conversion
 #pragma unroll
-                        for (int i = 0; i < kTimes; ++i) {
-                            const int row = row0 + i * kRowsAt;
-                            uint4 w = lds_v4(src + i * (kConvThreads * 16));
-                            if (row >= live || (hide && row >= from && row < to)) w = make_uint4(0, 0, 0, 0);
-                            const uint32_t byte = __shfl_sync(0xffffffffu, bytes, row / 16) >> (8 * kv) & 255;
-                            const float f = q8::scale_of(byte);
-                            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                            uint32_t y[8];
+                        for (int i0 = 0; i0 < kTimes; i0 += 4) {
+                            uint4 w[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t h[2] = {q8::to_f16x2(x[e]), q8::to_f16x2(x[e] >> 16)};
+                            for (int i = 0; i < 4; ++i) w[i] = lds_v4(src + (i0 + i) * (kConvThreads * 16));
+                            if (edge) {
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-                                    y[2 * e + j] = pack_bf16(v.x * f, v.y * f);
+                                for (int i = 0; i < 4; ++i) {
+                                    const int row = row0 + (i0 + i) * kRowsAt;
+                                    if (nans >> (row / 16 + 8 * kv) & 1) w[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    if (row >= live || (hide && row >= from && row < to)) w[i] = make_uint4(0, 0, 0, 0);
                                 }
                             }
-                            const uint32_t to_row = dst + i * (kRowsAt * 128);
-                            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                            sts_v4(to_row + ((c0 ^ (row & 7)) * 16), half ? hi : lo);
-                            sts_v4(to_row + (((c0 ^ 1) ^ (row & 7)) * 16), half ? lo : hi);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                                uint32_t y[8];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) q8::to_f16x4(x[e], y[2 * e], y[2 * e + 1]);
+                                const uint32_t to_row = dst + (i0 + i) * (kRowsAt * 128);
+                                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                                sts_v4(to_row + to0, half ? hi : lo);
+                                sts_v4(to_row + to1, half ? lo : hi);
+                            }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
@@ -651,7 +705,6 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             r_phase ^= 1;
                         }
                     }
-                    bytes = next;
                 }
             }
             ok = !meet_any<kThreads>(!ok);
@@ -662,6 +715,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
         uint32_t phase = 0, q_phase = 0;
         uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
         uint32_t z_phase = 0;               // bit i: stage i
+        uint32_t qr_phase = 0;              // bit t: tile t
         uint32_t ring_waited = 0;           // load warp: stages whose fill was issued (for the drain)
         for (uint32_t u = u_begin; u < u_end && ok;) {
             if (warp == kListWarp) list();
@@ -731,7 +785,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             } else if (warp == kMmaWarp || (C::kMmaWarps == 2 && warp == kMma1Warp)) {
                 // ------------------------------------------------ MMAs of tiles t0 .. t1 - 1
                 const int t0 = warp == kMmaWarp ? 0 : 1, t_end = C::kMmaWarps == 2 ? t0 + 1 : 2;
-                const uint32_t id_s = instr_desc(kM, kKeys), id_o = instr_desc(kM, D) | (1u << 16);
+                // operands bf16, or fp16 where they come from codes
+                constexpr uint32_t kF16 = C::kCodes ? (1u << 7) | (1u << 10) : 0;
+                const uint32_t id_s = instr_desc(kM, kKeys) & ~kF16, id_o = (instr_desc(kM, D) & ~kF16) | (1u << 16);
                 auto wait = [&](uint64_t *bar, uint32_t par) {
                     const bool r = mbar_wait(smem_u32(bar), par, wt);
                     ok = __all_sync(0xffffffffu, r);
@@ -751,8 +807,14 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     const Seg g = segs[k];
                     const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
                     const int t1 = min(t_end, g.tiles);  // none: the warp only keeps step with the ring
-                    if (!wait(q_full, q_phase)) break;
-                    q_phase ^= 1;
+                    if constexpr (C::kCodes) {
+                        for (int t = t0; t < t1 && ok; ++t) wait(&q_ready[t], (qr_phase >> t) & 1);
+                        if (!ok) break;
+                        for (int t = t0; t < t1; ++t) qr_phase ^= 1u << t;
+                    } else {
+                        if (!wait(q_full, q_phase)) break;
+                        q_phase ^= 1;
+                    }
                     if (!wait(&kv_full[stage], phase)) break;
                     tc_fence_after();
                     for (int t = t0; t < t1; ++t) issue_s(t, stage);
@@ -847,6 +909,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         uint32_t s_phase = 0, o_phase = 0;
+        uint32_t q_phase = 0, sc_step = 0;  // over an 8-bit cache: the segment's Q; steps so far
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
             const int ns = *nseg;
@@ -861,7 +924,46 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
+                const uint32_t sc_first = sc_step;
+                if constexpr (C::kCodes) {  // also where the tile is empty: the next Q's parity would be the last one's
+                    sc_step += g.step1 - g.step0;
+                    ok = mbar_wait(smem_u32(q_full), q_phase, wt);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    q_phase ^= 1;
+                }
                 if (t >= g.tiles) continue;
+                float row_sl2 = sl2;  // the factor of this row's scores
+                if constexpr (C::kCodes) {
+                    // this row of Q in units of 2^-x with x from its largest exponent (an infinity counts as the largest
+                    // number), to fp16, in its place
+                    const uint32_t row = smem_u32(smem + t * C::kTile) + r * 128;
+                    uint4 w[D / 8];
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        w[i] = lds_v4(row + i / 8 * (kM * 128) + (((i & 7) ^ (r & 7)) * 16));
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                                     __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+                    }
+                    const int x = min(127 + 14 - min(int(max(top & 0xffffu, top >> 16) >> 7), 254), 126);
+                    const float up = __uint_as_float(uint32_t(x + 127) << 23), down = __uint_as_float(uint32_t(127 - x) << 23);
+                    auto f16 = [up](uint32_t v) {
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(__uint_as_float(v & 0xffff0000u) * up), "f"(__uint_as_float(v << 16) * up));
+                        return h;
+                    };
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+                        sts_v4(row + i / 8 * (kM * 128) + (((i & 7) ^ (r & 7)) * 16),
+                               make_uint4(f16(w[i].x), f16(w[i].y), f16(w[i].z), f16(w[i].w)));
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(smem_u32(&q_ready[t]));
+                    row_sl2 = sl2 * down;
+                }
+                int unit_v = -1, most_v = 0;  // O is in units of 2^(unit_v - 127 - kProbBits); the largest byte so far
                 const int j = g.tok0 + t * int(tt) + r / int(G);  // this row's token in the chunk
                 const bool live = r < int(G * tt) && j < g.q_len;
                 const int past = g.kv_len - g.q_len;
@@ -901,15 +1003,51 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                         for (int i = 0; i < 128; ++i)
                             if (i >= from && i < to) x[i] = 0xff800000u;
                     }
-                    float mx[4];
+                    float mn;
+                    uint32_t sc_at = 0;  // this step's scales
+                    int top_v = -1;
+                    auto factor = [&](uint32_t k) { return fmaxf(row_sl2 * __uint_as_float(k), 1.17549435e-38f); };
+                    if constexpr (C::kCodes) {
+                        const uint32_t at = sc_first + uint32_t(step - g.step0);
+                        ok = mbar_wait(smem_u32(&sc_full[at % kScaleSlots]), at / kScaleSlots & 1, wt);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        sc_at = smem_u32(&scales[at % kScaleSlots]);
+                        top_v = int(lds_u32(sc_at + 64));
+                        mn = m;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+                        for (int q = 0; q < 8; ++q) {
+                            const uint32_t *y = x + 16 * q;
+                            float a0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+                            float a1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
 #pragma unroll
-                    for (int i = 8; i < 128; i += 8)
+                            for (int i = 6; i < 14; i += 4) {
+                                a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                                a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                            }
+                            a0 = fmaxf(max3(a0, __uint_as_float(y[14]), __uint_as_float(y[15])), a1);
+                            mn = fmaxf(mn, __fmul_rn(factor(lds_u32(sc_at + 4 * q)), a0));
+                        }
+                    } else {
+                        float mx[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
-                    const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+#pragma unroll
+                        for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
+                        mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                    }
+                    // m: of the scores, or over an 8-bit cache of the scores times their factors
+                    const float m_sl2 = C::kCodes ? 1.f : sl2;
+                    const int old_unit = unit_v < 0 ? top_v : unit_v;
+                    if constexpr (C::kCodes) {
+                        most_v = max(most_v, top_v);
+                        if (top_v > unit_v || (top_v >= 0 && top_v < unit_v - 8 && top_v >= most_v - 60)) unit_v = top_v;
+                    }
                     if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
                         ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
                         if (!__all_sync(0xffffffffu, ok)) {
@@ -921,12 +1059,13 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     }
                     if (step == g.step0) {
                         m = mn;
-                    } else if (__any_sync(0xffffffffu, live && (mn - m) * sl2 > kLag)) {
+                    } else if (__any_sync(0xffffffffu, live && (mn - m) * m_sl2 > kLag) || (C::kCodes && unit_v != old_unit)) {
                         // -inf - -inf is NaN and compares false: a row that has seen nothing stays.  Rows past the
                         // tile's hold what lay in shared memory, and decide nothing: results keep their bits.
-                        const float f = mn == kNegInf ? 1.f : ex2((m - mn) * sl2);
+                        float f = mn == kNegInf ? 1.f : ex2((m - mn) * m_sl2);
                         m = mn;
                         l *= f;
+                        if (C::kCodes) f *= __uint_as_float(uint32_t(max(old_unit - unit_v, -126) + 127) << 23);
 #pragma unroll
                         for (int i = 0; i < D; i += 16) {
                             float o[16];
@@ -937,33 +1076,67 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             tmem_st16(to + i, w);
                         }
                     }
-                    float z = m == kNegInf ? 0.f : m * sl2;
+                    float z = m == kNegInf ? 0.f : m * m_sl2;
                     // x * sl2 - z is off by z's rounding, the same for a whole row, where it cancels: but from 2^31 on
-                    // its power of two may pass fp32's largest number.  Far below that the difference is taken first.
-                    const bool far = fabsf(z) > 0x1p26f;
-                    if (__any_sync(0xffffffffu, far && live)) {
+                    // its power of two may pass fp32's largest number, from 2^24 on fp16's.  Far below that the difference
+                    // is taken first (kAll goes without: the test costs a mixed batch of heads of 64 4 %).
+                    const bool far = kMode != kAll && fabsf(z) > (C::kCodes ? 0x1p20f : 0x1p26f);
+                    if constexpr (kMode != kAll) {
+                        if (__any_sync(0xffffffffu, far && live)) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) x[i] = far ? __float_as_uint(__uint_as_float(x[i]) - m) : x[i];
-                        z = far ? 0.f : z;
+                            for (int i = 0; i < 128; ++i) {
+                                const float y = C::kCodes ? __fmul_rn(__uint_as_float(x[i]), factor(lds_u32(sc_at + i / 16 * 4)))
+                                                          : __uint_as_float(x[i]);  // rounded as in the maximum
+                                x[i] = far ? __float_as_uint(y - m) : x[i];
+                            }
+                            z = far ? 0.f : z;
+                        }
                     }
-                    const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
-                    // probabilities in bf16 for the product (up to 2^-8 of each; error of the 2048-token chunk against 64 bits
-                    // 0.0023 of the outputs' size, with fp32 probabilities 0.0017); their sum stays in fp32
-                    uint64_t sum[2] = {0, 0};
+                    if constexpr (C::kCodes) {
+                        // probabilities in fp16, times 2^kProbBits and what their group's scale of v is of O's unit (at
+                        // most 1); their sum, without either, stays in fp32
 #pragma unroll
-                    for (int i = 0; i < 128; i += 2) {
-                        float p0, p1;
-                        unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2p, zp), p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair(p0, p1));
-                        x[i / 2] = pack_bf16(p0, p1);
-                        if (i == 62) tmem_st32(tp, x);
+                        for (int q = 0; q < 8; ++q) {
+                            const int byte = int(lds_u32(sc_at + 32 + 4 * q));
+                            const int d = kProbBits + (byte < 0 ? 0 : max(byte - unit_v, -120));
+                            const float zq = float(d) - z, kq = far ? 1.f : factor(lds_u32(sc_at + 4 * q));
+                            const uint64_t kp = pair(kq, kq), zp = pair(zq, zq);
+                            uint64_t sum = 0;
+#pragma unroll
+                            for (int i = 16 * q; i < 16 * q + 16; i += 2) {
+                                float p0, p1;
+                                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kp, zp), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                sum = add2(sum, pair(p0, p1));
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x[i / 2]) : "f"(p1), "f"(p0));
+                            }
+                            float s0, s1;
+                            unpair(sum, s0, s1);
+                            l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - d) << 23), l);
+                            if (q == 3) tmem_st32(tp, x);
+                        }
+                        tmem_st32(tp + 32, x + 32);
+                    } else {
+                        const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
+                        // probabilities in bf16 for the product (up to 2^-8 of each; error of the 2048-token chunk against 64 bits
+                        // 0.0023 of the outputs' size, with fp32 probabilities 0.0017); their sum stays in fp32
+                        uint64_t sum[2] = {0, 0};
+#pragma unroll
+                        for (int i = 0; i < 128; i += 2) {
+                            float p0, p1;
+                            unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sl2p, zp), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair(p0, p1));
+                            x[i / 2] = pack_bf16(p0, p1);
+                            if (i == 62) tmem_st32(tp, x);
+                        }
+                        tmem_st32(tp + 32, x + 32);
+                        float s0, s1;
+                        unpair(add2(sum[0], sum[1]), s0, s1);
+                        l += s0 + s1;
                     }
-                    tmem_st32(tp + 32, x + 32);
-                    float s0, s1;
-                    unpair(add2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(smem_u32(&p_full[t]));
@@ -978,7 +1151,12 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 tc_fence_after();
                 const int64_t tok = g.q0 + j;
                 const int head = g.h * int(G) + r % int(G);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float inv = l == 0.f ? 0.f : 1.f / l, unit = 1.f;
+                if constexpr (C::kCodes) {
+                    unit = q8::scale_of(max(unit_v, 0)) * (1.f / (1 << kProbBits));
+                    inv *= unit;
+                }
+                const float m_log2 = C::kCodes ? m : m * sl2;
                 const size_t prow = (size_t)max(g.slot, 0) * 2 * kM + t * kM + r;
                 uint16_t *dst = static_cast<uint16_t *>(a.out) + tok * a.out_stride + (int64_t)head * D;
 #pragma unroll
@@ -988,6 +1166,10 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     if (g.slot >= 0) {
                         if (live) {
                             uint4 *to = reinterpret_cast<uint4 *>(c.part_o) + ((size_t)g.slot * (D / 4) + i / 4) * 2 * kM + t * kM + r;
+                            if (C::kCodes) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * unit);
+                            }
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 to[e * 2 * kM] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -1006,9 +1188,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 mbar_arrive(smem_u32(&o_empty[t]));
                 if (live) {
                     if (g.slot >= 0)
-                        c.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m * sl2, l);
+                        c.part_ml[prow] = make_float2(m == kNegInf ? kNegInf : m_log2, l);
                     else if (a.lse)
-                        a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m * sl2 + log2f(l)) * kLn2;
+                        a.lse[tok * a.n_heads + head] = l == 0.f ? kNegInf : (m_log2 + log2f(l)) * kLn2;
                 }
             }
             ok = !meet_any<kThreads>(!ok);

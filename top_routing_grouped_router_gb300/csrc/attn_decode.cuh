@@ -87,11 +87,6 @@ __device__ __forceinline__ void mma16816h(float *c, const uint32_t *a, uint32_t 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four codes as fp16, two and two.
-__device__ __forceinline__ void codes4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-}
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -558,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             if (page < 0) return;
             const int p = key_of(i), slot = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
             off = page * a.page_stride + (int64_t)slot * a.token_stride;
-            const int64_t of = page * a.scale_page + h * a.scale_head + slot / a.block;
+            const int64_t of = page * a.scale_page + h * a.scale_head + (a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block);
             sc = q8::ldp_byte(a.k_scale + of) | q8::ldp_byte(a.v_scale + of) << 8;
         };
         auto copy_q8 = [&](int i) {
@@ -651,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t lo, hi;
-                            codes4(x[e], lo, hi);
+                            q8::to_f16x4(x[e], lo, hi);
                             mma16816h(e & 1 ? odd[n] : sc[n], q[c * 4 + e], lo, hi);
                         }
                     }
@@ -768,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t even0, odd0, even1, odd1;
-                        codes4(__byte_perm(vf[2 * e], 0, 0x3120), even0, odd0);
-                        codes4(__byte_perm(vf[2 * e + 1], 0, 0x3120), even1, odd1);
+                        q8::to_f16x4(__byte_perm(vf[2 * e], 0, 0x3120), even0, odd0);
+                        q8::to_f16x4(__byte_perm(vf[2 * e + 1], 0, 0x3120), even1, odd1);
                         mma16816h(o[2 * (c + e)], p, even0, even1);
                         mma16816h(o[2 * (c + e) + 1], p, odd0, odd1);
                     }

@@ -34,6 +34,11 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t codes) {
     asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
     return r;
 }
+// Four codes as fp16, two and two.
+__device__ __forceinline__ void to_f16x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
 // The nearest codes of two values (ties to even, past 448 the largest; NaN stays NaN).
 __device__ __forceinline__ uint32_t from_f32(float lo, float hi) {
     uint32_t r;

@@ -56,10 +56,12 @@ constexpr int kJoinRows = 16;   // rows of a block of the join kernel
 template <int D, Mode kMode>
 struct Cfg {
     static constexpr bool kCodes = kMode == kQ8;
-    // The third warpgroup (and the fourth) gives up registers that the softmax takes, within the launch's.
+    // The third warpgroup gives up registers that the softmax takes, within the launch's.  With a fourth every
+    // thread has 128, which the compiler does not exceed whatever a warpgroup takes later: there the softmax reads the
+    // scores twice from TMEM, 32 at a time (all at once they spilled: 657 us for 2048 tokens over 16384 keys).
     static constexpr int kThreads = kCodes ? 512 : 384, kLaunchRegs = kCodes ? 128 : 168;
-    static constexpr int kSoftmaxRegs = kCodes ? 192 : 208, kOtherRegs = kCodes ? 64 : 80;
-    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");
+    static constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+    static_assert(kCodes || 256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");
     static constexpr int kTile = kM * D * 2;                  // one Q tile, one K or V stage
     static constexpr int kStages = kCodes ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 8;
     static constexpr int kRaw = kKeys * D;                    // a stage of codes
@@ -87,15 +89,16 @@ struct Seg {
     int tiles;                          // 1 or 2
     int low, skip;                      // with a window: the first key of its first token's, and the steps left out
 };
-// The scales of a step over an 8-bit cache, by groups of 16 keys: k's as factors, v's as bytes (-1: a group
-// without one), and the largest of these.  A ring of kScaleSlots steps: the step that takes a place again
-// is converted once the scores of a step behind its last user's are under way.
+// The scales of the steps over an 8-bit cache, found by the converting warps for kBatch steps of a segment at
+// a time: a step's 16 bytes are those of its eight groups of 16 keys, k's, then v's.  A group without a scale (no
+// keys, or NaN) has k's byte 127 (a factor of 1) and the largest of the step's for v.  A ring of as many
+// batches as there are stages: the batch that takes a place again begins when at least half as many
+// steps, each of them of a batch of its own at most, have been multiplied since.
+constexpr int kBatch = 8;
 struct Scales {
-    float k[8];
-    int v[8];
-    int top, pad[3];
+    uint4 bytes[kBatch];
+    uint32_t nan[kBatch];  // bit i: byte i says NaN
 };
-constexpr int kScaleSlots = 8;
 constexpr int kProbBits = 7;  // probabilities times 2^7: with kLag at most 2^15 in fp16
 
 // What the join kernel needs of an item that starts in a CTA's share and goes on past it.
@@ -347,9 +350,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
     uint64_t *v_zero = o_empty + 2, *drain = v_zero + C::kStages;  // [kStages], [2]
     uint64_t *raw_full = drain + 2, *raw_empty = raw_full + C::kRaws;  // [kRaws] each
-    uint64_t *sc_full = raw_empty + C::kRaws, *q_ready = sc_full + (C::kCodes ? kScaleSlots : 0);  // [2]
-    Scales *scales = reinterpret_cast<Scales *>(ctrl + (q_ready + 3 - kv_full) / 2 * 16);  // [kScaleSlots], 16-byte aligned
-    Seg *segs = reinterpret_cast<Seg *>(scales + (C::kCodes ? kScaleSlots : 0));  // [kMaxSegs]
+    uint64_t *sc_full = raw_empty + C::kRaws, *q_ready = sc_full + (C::kCodes ? C::kStages : 0);  // [kStages], [2]
+    Scales *scales = reinterpret_cast<Scales *>(ctrl + (q_ready + 3 - kv_full) / 2 * 16);  // [kStages], 16-byte aligned
+    Seg *segs = reinterpret_cast<Seg *>(scales + (C::kCodes ? C::kStages : 0));  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
     int *nseg = reinterpret_cast<int *>(scan + 16);
     volatile int *abort = nseg + 1;
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             mbar_init(smem_u32(&raw_full[i]), 1);
             mbar_init(smem_u32(&raw_empty[i]), kConvThreads / 32);
         }
-        for (int i = 0; C::kCodes && i < kScaleSlots; ++i) mbar_init(smem_u32(&sc_full[i]), 1);
+        for (int i = 0; C::kCodes && i < C::kStages; ++i) mbar_init(smem_u32(&sc_full[i]), kConvThreads / 32);
         for (int t = 0; C::kCodes && t < 2; ++t) mbar_init(smem_u32(&q_ready[t]), kM);
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_empty), C::kMmaWarps);
@@ -595,7 +598,6 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     };
     bool ok = true;
     if (C::kCodes && warp >= kConvWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         // ------------------------------------------------ codes to fp16
         // Tiles alternate: k, v of a step.  A thread takes one 16-byte piece of a row, then that of the row 128 *
         // 16 / D further on.
@@ -607,51 +609,77 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
         const uint32_t to0 = piece / 4 * (kKeys * 128) + row0 * 128 + ((c0 ^ (row0 & 7)) * 16);
         const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) * 16);
         static_assert(kRowsAt % 8 == 0 && kTimes % 4 == 0, "");
-        int stage = 0, rs = 0, slot = 0;
-        uint32_t phase = 0, r_phase = 0;
+        // scales: each of the four warps finds those of two steps of a batch, lanes 0-7 and 16-23 of k, the others of
+        // v.  The pages of the next batch (of the next segment's first, at the end of one) are asked for when a batch
+        // begins, its bytes a step later; nothing looks at either before it is needed.
+        const bool of_v = lane & 8;
+        int stage = 0, rs = 0, batch = 0;  // batch: its place in the ring
+        uint32_t phase = 0, r_phase = 0, sc_phase = 0;
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
             const int ns = *nseg;
             u = cursor[3];
+            int page = -1, byte = -1;  // -1: none
+            auto key_at = [&](const Seg &g, int first) {  // of the batch that begins with step `first`, the lane's
+                return real(g, first + 2 * (warp - kConvWarp) + (lane >> 4)) * kKeys + (lane & 7) * 16;
+            };
+            auto keys_of = [&](const Seg &g) { return int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len)); };
+            auto find_page = [&](const Seg &g, int first) {
+                const int p = key_at(g, first);
+                page = -1;
+                if (first + 2 * (warp - kConvWarp) + (lane >> 4) >= g.step1 || p >= keys_of(g) || (p >= a.sinks && p + 16 <= g.low)) return;
+                page = ldp(a.table + (size_t)g.b * a.max_pages + (a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size));
+            };
+            auto find_byte = [&](const Seg &g, int first) {
+                byte = -1;
+                if (page < 0 || page >= a.n_pages) return;  // the load warp records pages that do not exist
+                const int p = key_at(g, first);
+                const int slot = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
+                const int block = a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block;
+                byte = int(q8::ldp_byte((of_v ? a.v_scale : a.k_scale) + page * a.scale_page + g.h * a.scale_head + block));
+            };
+            if (ns > 0) {
+                find_page(segs[0], segs[0].step0);
+                find_byte(segs[0], segs[0].step0);
+            }
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
-                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
-                // lanes 0-7: the bytes of k of keys 16 i .. 16 i + 15 of a step, lanes 8-15 those of v.  Their page is
-                // asked for two steps ahead and they themselves one; nothing looks at either before it is needed.
-                const uint8_t *bytes = (lane < 8 ? a.k_scale : a.v_scale) + g.h * a.scale_head;
-                auto page_of = [&](int step) {
-                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
-                    if (step >= g.step1 || lane >= 16 || p >= keys || (p >= a.sinks && p + 16 <= g.low)) return -1;
-                    return ldp(a.table + (size_t)g.b * a.max_pages + (a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size));
-                };
-                int byte;  // -1: none
-                auto byte_of = [&](int step, int page) {
-                    byte = -1;
-                    if (page < 0 || page >= a.n_pages) return;  // the load warp records pages that do not exist
-                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
-                    const int slot = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
-                    const int block = a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block;
-                    byte = int(q8::ldp_byte(bytes + page * a.scale_page + block));
-                };
-                byte_of(g.step0, page_of(g.step0));
-                int page = page_of(g.step0 + 1);
+                const int keys = keys_of(g);
+                uint32_t nan_at = 0;
                 for (int step = g.step0; step < g.step1 && ok; ++step) {
-                    // a group whose byte says NaN has NaN codes, and no scale
-                    const uint32_t nans = __ballot_sync(0xffffffffu, byte == 255);
-                    if (warp == kConvWarp) {
-                        const int own = byte == 255 ? -1 : byte;
-                        const int top = __reduce_max_sync(0xffffffffu, lane >= 8 ? own : -1);
-                        if (lane < 8)
-                            scales[slot].k[lane] = own < 0 ? 1.f : q8::scale_of(own);
-                        else if (lane < 16)
-                            scales[slot].v[lane - 8] = own;
-                        if (lane == 0) scales[slot].top = top;
+                    const int in_batch = (step - g.step0) % kBatch;
+                    if (in_batch == 0) {
+                        const uint32_t nans = __ballot_sync(0xffffffffu, byte == 255);
+                        int own = byte == 255 ? -1 : byte, top = own;
+#pragma unroll
+                        for (int w = 1; w <= 4; w <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, w));
+                        if (own < 0) own = of_v ? max(top, 0) : 127;
+                        Scales &to = scales[batch];
+                        const int at = 2 * (warp - kConvWarp) + (lane >> 4);
+                        reinterpret_cast<uint8_t *>(&to.bytes[at])[lane & 15] = uint8_t(own);
+                        if ((lane & 15) == 0) to.nan[at] = nans >> (lane & 16) & 0xffff;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sc_full[slot]));
-                        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                        if (lane == 0) mbar_arrive(smem_u32(&sc_full[batch]));
+                        ok = mbar_wait(smem_u32(&sc_full[batch]), sc_phase, wt);  // the other warps' too
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        nan_at = smem_u32(&to.nan[0]);
+                        if (++batch == C::kStages) {
+                            batch = 0;
+                            sc_phase ^= 1;
+                        }
                     }
-                    byte_of(step + 1, page);
-                    page = page_of(step + 2);
+                    const bool last = step + kBatch - in_batch >= g.step1;  // of the segment's batches
+                    if (in_batch == 0) {
+                        page = -1;
+                        if (!last)
+                            find_page(g, step + kBatch);
+                        else if (k + 1 < ns)
+                            find_page(segs[k + 1], segs[k + 1].step0);
+                    }
+                    const uint32_t nans = lds_u32(nan_at + 4 * in_batch);
                     const int k0 = real(g, step) * kKeys, live = keys - k0;
                     int from, to;
                     const bool hide = hidden(g, k0, from, to), edge = live < kKeys || hide || nans != 0;
@@ -705,12 +733,18 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             r_phase ^= 1;
                         }
                     }
+                    if (in_batch == 0) {
+                        if (!last)
+                            find_byte(g, step + kBatch);
+                        else if (k + 1 < ns)
+                            find_byte(segs[k + 1], segs[k + 1].step0);
+                    }
                 }
             }
             ok = !meet_any<kThreads>(!ok);
         }
     } else if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if constexpr (!C::kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         int stage = 0;                      // ring position (the load warp's: of the ring that TMA fills)
         uint32_t phase = 0, q_phase = 0;
         uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
@@ -907,9 +941,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             mbar_wait_drain(bar, 0, wt);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        if constexpr (!C::kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         uint32_t s_phase = 0, o_phase = 0;
-        uint32_t q_phase = 0, sc_step = 0;  // over an 8-bit cache: the segment's Q; steps so far
+        uint32_t q_phase = 0, sc_batch = 0;  // over an 8-bit cache: the segment's Q; batches of scales so far
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
             const int ns = *nseg;
@@ -924,9 +958,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
-                const uint32_t sc_first = sc_step;
+                const uint32_t sc_first = sc_batch;
                 if constexpr (C::kCodes) {  // also where the tile is empty: the next Q's parity would be the last one's
-                    sc_step += g.step1 - g.step0;
+                    sc_batch += uint32_t(g.step1 - g.step0 + kBatch - 1) / kBatch;
                     ok = mbar_wait(smem_u32(q_full), q_phase, wt);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -937,7 +971,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 if (t >= g.tiles) continue;
                 float row_sl2 = sl2;  // the factor of this row's scores
                 if constexpr (C::kCodes) {
-                    // this row of Q in units of 2^-x with x from its largest exponent (an infinity counts as the largest
+                    // this row of Q (or -Q, for a negative scale) in units of 2^-x with x from its largest exponent (an infinity counts as the largest
                     // number), to fp16, in its place
                     const uint32_t row = smem_u32(smem + t * C::kTile) + r * 128;
                     uint4 w[D / 8];
@@ -949,7 +983,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
                     }
                     const int x = min(127 + 14 - min(int(max(top & 0xffffu, top >> 16) >> 7), 254), 126);
-                    const float up = __uint_as_float(uint32_t(x + 127) << 23), down = __uint_as_float(uint32_t(127 - x) << 23);
+                    const float up = __uint_as_float(uint32_t(x + 127) << 23 | (neg ? 1u << 31 : 0u)), down = __uint_as_float(uint32_t(127 - x) << 23);
                     auto f16 = [up](uint32_t v) {
                         uint32_t h;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(__uint_as_float(v & 0xffff0000u) * up), "f"(__uint_as_float(v << 16) * up));
@@ -978,59 +1012,157 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     }
                     s_phase ^= 1;
                     tc_fence_after();
-                    uint32_t x[128];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32_issue(ts + i * 32, x + i * 32);
-                    tmem_ld_done(x);
-                    if (C::kEarly) {
-                        tc_fence_before();
-                        mbar_arrive(smem_u32(&s_empty[t]));
-                    }
-                    if (neg) {
-#pragma unroll
-                        for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
-                    }
-                    const int k0 = real(g, step) * kKeys;
-                    if (k0 > seen_all - kKeys) {
-#pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (k0 + i >= seen) x[i] = 0xff800000u;
-                    }
-                    if (kMode != kAll && k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys) {
-                        // before the window of a row of the tile
-                        const int from = a.sinks - k0, to = max(seen - a.window, 0) - k0;
-#pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i >= from && i < to) x[i] = 0xff800000u;
-                    }
-                    float mn;
-                    uint32_t sc_at = 0;  // this step's scales
-                    int top_v = -1;
-                    auto factor = [&](uint32_t k) { return fmaxf(row_sl2 * __uint_as_float(k), 1.17549435e-38f); };
                     if constexpr (C::kCodes) {
-                        const uint32_t at = sc_first + uint32_t(step - g.step0);
-                        ok = mbar_wait(smem_u32(&sc_full[at % kScaleSlots]), at / kScaleSlots & 1, wt);
+                        const uint32_t nth = uint32_t(step - g.step0), n = sc_first + nth / kBatch, at = n % C::kStages;
+                        ok = mbar_wait(smem_u32(&sc_full[at]), n / C::kStages & 1, wt);
                         if (!__all_sync(0xffffffffu, ok)) {
                             ok = false;
                             break;
                         }
-                        sc_at = smem_u32(&scales[at % kScaleSlots]);
-                        top_v = int(lds_u32(sc_at + 64));
-                        mn = m;
+                        const uint4 sc = lds_v4(smem_u32(&scales[at].bytes[nth % kBatch]));  // this step's scales
+                        // byte of the step's half h, and the factor of the scores of one of its groups
+                        auto byte_at = [](uint32_t lo, uint32_t hi, int h, int q) { return (h ? hi : lo) >> (q * 8) & 255; };
+                        auto factor = [&](int h, int q) {
+                            return fmaxf(row_sl2 * __uint_as_float(byte_at(sc.x, sc.y, h, q) << 23), 1.17549435e-38f);
+                        };
+                        const int k0 = real(g, step) * kKeys;
+                        const int from = a.sinks - k0, to_w = max(seen - a.window, 0) - k0;
+                        const bool edge = k0 > seen_all - kKeys ||
+                                          (k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys);
+                        // 64 scores at a time, twice, in loops: with all of it unrolled instructions came too slowly (968 us
+                        // for 2048 tokens over 16384 keys)
+                        uint32_t x[64];
+                        auto take = [&](int h) {
+                            tmem_ld32_issue(ts + h * 64, x);
+                            tmem_ld32_issue(ts + h * 64 + 32, x + 32);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint32_t *y = x + 16 * q;
-                            float a0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
-                            float a1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
+                            for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
+                            if (__builtin_expect(edge, 0)) {  // keys past the row's last, and before its window
+                                const int last = seen - k0 - h * 64, f = from - h * 64, t = to_w - h * 64;
 #pragma unroll
-                            for (int i = 6; i < 14; i += 4) {
-                                a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                                a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                                for (int i = 0; i < 64; ++i)
+                                    if (i >= last || (i >= f && i < t)) x[i] = 0xff800000u;
                             }
-                            a0 = fmaxf(max3(a0, __uint_as_float(y[14]), __uint_as_float(y[15])), a1);
-                            mn = fmaxf(mn, __fmul_rn(factor(lds_u32(sc_at + 4 * q)), a0));
+                        };
+                        float mn = m;  // of the scores times their factors
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            take(h);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t *y = x + 16 * q;
+                                float a0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+                                float a1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
+#pragma unroll
+                                for (int i = 6; i < 14; i += 4) {
+                                    a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                                    a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                                }
+                                a0 = fmaxf(max3(a0, __uint_as_float(y[14]), __uint_as_float(y[15])), a1);
+                                mn = fmaxf(mn, __fmul_rn(factor(h, q), a0));
+                            }
+                        }
+                        if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
+                            ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                ok = false;
+                                break;
+                            }
+                            o_phase ^= 1;
+                            tc_fence_after();
+                        }
+                        int top_v = 0;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) top_v = max(top_v, int(byte_at(sc.z, sc.w, q / 4, q % 4)));
+                        const int old_unit = unit_v < 0 ? top_v : unit_v;
+                        most_v = max(most_v, top_v);
+                        if (top_v > unit_v || (top_v < unit_v - 8 && top_v >= most_v - 60)) unit_v = top_v;
+                        if (step == g.step0) {
+                            m = mn;
+                        } else if (__any_sync(0xffffffffu, live && mn - m > kLag) || unit_v != old_unit) {
+                            // as over a bf16 cache, and with the change of O's unit
+                            float f = mn == kNegInf ? 1.f : ex2(m - mn);
+                            m = mn;
+                            l *= f;
+                            f *= __uint_as_float(uint32_t(max(old_unit - unit_v, -126) + 127) << 23);
+#pragma unroll
+                            for (int i = 0; i < D; i += 16) {
+                                float o[16];
+                                uint32_t w[16];
+                                tmem_ld16(to + i, o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+                                tmem_st16(to + i, w);
+                            }
+                        }
+                        // scores past 2^24 would pass fp16's largest number by m's rounding, which stays in x * factor - m:
+                        // far below that the product is rounded first, as it was in the maximum
+                        const float z = m == kNegInf ? 0.f : m;
+                        const bool far = fabsf(z) > 0x1p20f, any_far = __any_sync(0xffffffffu, far && live);
+                        // probabilities in fp16, times 2^kProbBits and what their group's scale of v is of O's unit (at
+                        // most 1); their sum, without either, stays in fp32
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            take(h);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int d = kProbBits + max(int(byte_at(sc.z, sc.w, h, q)) - unit_v, -120);
+                                float kq = factor(h, q), zq = float(d) - z;
+                                if (__builtin_expect(any_far, 0)) {
+#pragma unroll
+                                    for (int i = 16 * q; i < 16 * q + 16; ++i)
+                                        x[i] = far ? __float_as_uint(__fmul_rn(__uint_as_float(x[i]), kq) - m) : x[i];
+                                    kq = far ? 1.f : kq;
+                                    zq = far ? float(d) : zq;
+                                }
+                                const uint64_t kp = pair(kq, kq), zp = pair(zq, zq);
+                                uint64_t sum = 0;
+#pragma unroll
+                                for (int i = 16 * q; i < 16 * q + 16; i += 2) {
+                                    float p0, p1;
+                                    unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kp, zp), p0, p1);
+                                    p0 = ex2(p0);
+                                    p1 = ex2(p1);
+                                    sum = add2(sum, pair(p0, p1));
+                                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x[i / 2]) : "f"(p1), "f"(p0));
+                                }
+                                float s0, s1;
+                                unpair(sum, s0, s1);
+                                l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - d) << 23), l);
+                            }
+                            tmem_st32(tp + 32 * h, x);  // heads of 128: over scores that this thread has read
+                        }
+                        if (C::kEarly) {
+                            tc_fence_before();
+                            mbar_arrive(smem_u32(&s_empty[t]));
                         }
                     } else {
+                        uint32_t x[128];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tmem_ld32_issue(ts + i * 32, x + i * 32);
+                        tmem_ld_done(x);
+                        if (C::kEarly) {
+                            tc_fence_before();
+                            mbar_arrive(smem_u32(&s_empty[t]));
+                        }
+                        if (neg) {
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) x[i] ^= 0x80000000u;
+                        }
+                        const int k0 = real(g, step) * kKeys;
+                        if (k0 > seen_all - kKeys) {
+#pragma unroll
+                            for (int i = 0; i < 128; ++i)
+                                if (k0 + i >= seen) x[i] = 0xff800000u;
+                        }
+                        if (kMode != kAll && k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys) {
+                            // before the window of a row of the tile
+                            const int from = a.sinks - k0, to = max(seen - a.window, 0) - k0;
+#pragma unroll
+                            for (int i = 0; i < 128; ++i)
+                                if (i >= from && i < to) x[i] = 0xff800000u;
+                        }
                         float mx[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
@@ -1039,85 +1171,46 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
-                        mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-                    }
-                    // m: of the scores, or over an 8-bit cache of the scores times their factors
-                    const float m_sl2 = C::kCodes ? 1.f : sl2;
-                    const int old_unit = unit_v < 0 ? top_v : unit_v;
-                    if constexpr (C::kCodes) {
-                        most_v = max(most_v, top_v);
-                        if (top_v > unit_v || (top_v >= 0 && top_v < unit_v - 8 && top_v >= most_v - 60)) unit_v = top_v;
-                    }
-                    if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
-                        ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        o_phase ^= 1;
-                        tc_fence_after();
-                    }
-                    if (step == g.step0) {
-                        m = mn;
-                    } else if (__any_sync(0xffffffffu, live && (mn - m) * m_sl2 > kLag) || (C::kCodes && unit_v != old_unit)) {
-                        // -inf - -inf is NaN and compares false: a row that has seen nothing stays.  Rows past the
-                        // tile's hold what lay in shared memory, and decide nothing: results keep their bits.
-                        float f = mn == kNegInf ? 1.f : ex2((m - mn) * m_sl2);
-                        m = mn;
-                        l *= f;
-                        if (C::kCodes) f *= __uint_as_float(uint32_t(max(old_unit - unit_v, -126) + 127) << 23);
-#pragma unroll
-                        for (int i = 0; i < D; i += 16) {
-                            float o[16];
-                            uint32_t w[16];
-                            tmem_ld16(to + i, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-                            tmem_st16(to + i, w);
-                        }
-                    }
-                    float z = m == kNegInf ? 0.f : m * m_sl2;
-                    // x * sl2 - z is off by z's rounding, the same for a whole row, where it cancels: but from 2^31 on
-                    // its power of two may pass fp32's largest number, from 2^24 on fp16's.  Far below that the difference
-                    // is taken first (kAll goes without: the test costs a mixed batch of heads of 64 4 %).
-                    const bool far = kMode != kAll && fabsf(z) > (C::kCodes ? 0x1p20f : 0x1p26f);
-                    if constexpr (kMode != kAll) {
-                        if (__any_sync(0xffffffffu, far && live)) {
-#pragma unroll
-                            for (int i = 0; i < 128; ++i) {
-                                const float y = C::kCodes ? __fmul_rn(__uint_as_float(x[i]), factor(lds_u32(sc_at + i / 16 * 4)))
-                                                          : __uint_as_float(x[i]);  // rounded as in the maximum
-                                x[i] = far ? __float_as_uint(y - m) : x[i];
+                        const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                        if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
+                            ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                ok = false;
+                                break;
                             }
-                            z = far ? 0.f : z;
+                            o_phase ^= 1;
+                            tc_fence_after();
                         }
-                    }
-                    if constexpr (C::kCodes) {
-                        // probabilities in fp16, times 2^kProbBits and what their group's scale of v is of O's unit (at
-                        // most 1); their sum, without either, stays in fp32
+                        if (step == g.step0) {
+                            m = mn;
+                        } else if (__any_sync(0xffffffffu, live && (mn - m) * sl2 > kLag)) {
+                            // -inf - -inf is NaN and compares false: a row that has seen nothing stays.  Rows past the
+                            // tile's hold what lay in shared memory, and decide nothing: results keep their bits.
+                            const float f = mn == kNegInf ? 1.f : ex2((m - mn) * sl2);
+                            m = mn;
+                            l *= f;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int byte = int(lds_u32(sc_at + 32 + 4 * q));
-                            const int d = kProbBits + (byte < 0 ? 0 : max(byte - unit_v, -120));
-                            const float zq = float(d) - z, kq = far ? 1.f : factor(lds_u32(sc_at + 4 * q));
-                            const uint64_t kp = pair(kq, kq), zp = pair(zq, zq);
-                            uint64_t sum = 0;
+                            for (int i = 0; i < D; i += 16) {
+                                float o[16];
+                                uint32_t w[16];
+                                tmem_ld16(to + i, o);
 #pragma unroll
-                            for (int i = 16 * q; i < 16 * q + 16; i += 2) {
-                                float p0, p1;
-                                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kp, zp), p0, p1);
-                                p0 = ex2(p0);
-                                p1 = ex2(p1);
-                                sum = add2(sum, pair(p0, p1));
-                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x[i / 2]) : "f"(p1), "f"(p0));
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+                                tmem_st16(to + i, w);
                             }
-                            float s0, s1;
-                            unpair(sum, s0, s1);
-                            l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - d) << 23), l);
-                            if (q == 3) tmem_st32(tp, x);
                         }
-                        tmem_st32(tp + 32, x + 32);
-                    } else {
+                        float z = m == kNegInf ? 0.f : m * sl2;
+                        // x * sl2 - z is off by z's rounding, the same for a whole row, where it cancels: but from 2^31 on
+                        // its power of two may pass fp32's largest number.  Far below that the difference is taken first
+                        // (kAll goes without: the test costs a mixed batch of heads of 64 4 %).
+                        if constexpr (kMode != kAll) {
+                            const bool far = fabsf(z) > 0x1p26f;
+                            if (__any_sync(0xffffffffu, far && live)) {
+#pragma unroll
+                                for (int i = 0; i < 128; ++i) x[i] = far ? __float_as_uint(__uint_as_float(x[i]) - m) : x[i];
+                                z = far ? 0.f : z;
+                            }
+                        }
                         const uint64_t sl2p = pair(sl2, sl2), zp = pair(-z, -z);
                         // probabilities in bf16 for the product (up to 2^-8 of each; error of the 2048-token chunk against 64 bits
                         // 0.0023 of the outputs' size, with fp32 probabilities 0.0017); their sum stays in fp32
@@ -1297,9 +1390,11 @@ bool set_smem_attr() {
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
         if (cudaFuncSetAttribute(chunk_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return false;
+        if constexpr (!C::kCodes) {
         // the softmax's registers come from the launch's: fewer, and the kernel would wait for them for ever
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, chunk_kernel<D, kMode>) != cudaSuccess || fa.numRegs < C::kLaunchRegs) return false;
+        }
         attr_set[dev] = true;
     }
     return true;

@@ -7,10 +7,10 @@
 // shift; what falls below 2^-9 of the scale is rounded).
 //
 // One launch, two kinds of blocks of threads.  The first write k and v: a task is one head's k or v
-// over one block of tokens.  Its warps hold the rotated values in registers (a lane two pieces of
-// eight elements of up to four tokens), agree on the largest through shared memory and store the
-// codes: k and v are read once.  The others rotate q, a token or four at a time, and share a token's
-// cosines and sines between its heads.
+// over one block of tokens.  Its warps keep the rotated values in shared memory while they agree on the
+// largest, and then store the codes: k and v are read once.  (In registers, four tokens a lane, the kernel took
+// 184 of them, and q's blocks waited for one another: 4043 tokens 44 us; two tokens a lane 28.)  The
+// others rotate q, a token or four at a time, and share a token's cosines and sines between its heads.
 #include "q8.cuh"
 #include "rope.cuh"
 
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxPairs = 128;
+constexpr int kMostKept = 64 << 10;  // bytes of shared memory for the values of a block of threads
 
 struct Q8Args {
     RopeArgs r;
@@ -30,6 +31,7 @@ struct Q8Args {
     int32_t warps;       // of a task
     int32_t groups;      // blocks of threads a block of tokens
     int32_t kv_blocks;   // blocks of threads that store k and v
+    int32_t hold;        // tokens of a task that shared memory holds (0: they are worked out twice)
 };
 
 // What a lane of a group of LG lanes holds of a head: pieces of eight elements at da and db.
@@ -102,9 +104,13 @@ __device__ __forceinline__ void rotate(uint64_t *f, const uint64_t *c, const uin
     }
 }
 
-// A fraction of a turn in units of 2^-64, exact at every position, to (cos, sin) times mscale.
+// The angle's cosine and sine times mscale.  turn * pos modulo 2^64 is the fraction of a turn in units of 2^-64,
+// exact at every position; its upper half (pos as a signed number), in units of 2^-32 turn, is off by 1.5e-9
+// radians at most, a fortieth of fp32's half step next to 1.
 __device__ __forceinline__ void angle(uint64_t turn, int pos, float mscale, float &c, float &s) {
-    sincospif(__ll2float_rn(int64_t(turn * uint64_t(int64_t(pos)))) * 0x1p-63f, &s, &c);
+    const uint32_t lo = uint32_t(turn), hi = uint32_t(turn >> 32), p = uint32_t(pos);
+    const uint32_t part = hi * p + __umulhi(lo, p) - (pos < 0 ? lo : 0u);
+    sincospif(__int2float_rn(int(part)) * 0x1p-31f, &s, &c);  // half turns
     c *= mscale;
     s *= mscale;
 }
@@ -205,69 +211,64 @@ __device__ __forceinline__ int exponent_of(float top) {
 
 template <typename T, int LG>
 __device__ __forceinline__ void store_kv(const Q8Args &c) {
-    constexpr int RPW = 32 / LG;                         // tokens a warp works on at a time
-    constexpr int ITER = RPW >= 16 ? 1 : RPW == 8 ? 2 : 4;  // and times
-    constexpr int TW = RPW * ITER;
+    constexpr int RPW = 32 / LG;  // tokens a warp works on at a time
+    extern __shared__ float4 kept[];
     __shared__ int scratch[2 + kWarps];
-    __shared__ float tops[kWarps];
+    __shared__ uint32_t tops[kWarps];
     const RopeArgs &r = c.r;
     const attn::Args &a = r.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LaneOf at(r, lane % LG);
     const Piece p = find_piece(a, blockIdx.x / c.groups, c.block, scratch);
     if (p.b < 0) return;  // the whole block
-    const int W = c.warps, sub = warp % W, task = int(blockIdx.x % c.groups) * (kWarps / W) + warp / W;
+    const int W = c.warps, sub = warp & (W - 1), task = int(blockIdx.x % c.groups) * (kWarps / W) + warp / W;
     const bool on = task < 2 * a.n_kv_heads, is_v = task >= a.n_kv_heads;
     const int h = is_v ? task - a.n_kv_heads : task, n = p.hi - p.lo, old = p.lo - p.start;
-    const int rounds = (n + W * TW - 1) / (W * TW);
-    const int row0 = sub * TW + lane / LG;  // the lane's first token of the piece
-    const T *src = static_cast<const T *>(is_v ? r.v_in : r.k_in) + p.row * (is_v ? r.v_stride : r.k_stride) + h * at.D;
+    const int t0 = sub * RPW + lane / LG, stride_t = W * RPW;  // the lane's tokens of the piece: t0, t0 + stride_t, ..
     const int64_t row_stride = is_v ? r.v_stride : r.k_stride;
+    const T *src = static_cast<const T *>(is_v ? r.v_in : r.k_in) + p.row * row_stride + h * at.D;
     const T *gamma = is_v ? nullptr : static_cast<const T *>(r.gk);
-    const bool turn = !is_v && at.turned;
+    const bool turn = !is_v && at.turned, held = n <= c.hold;
     const float inv_d = 1.f / float(at.D);
+    // a lane's 16 values of a token lie lanes apart, so that a warp's stores and loads meet no bank twice
+    float4 *mine = kept + (size_t)(warp / W) * c.hold * (LG * 4) + lane % LG;
 
-    uint64_t f[ITER][8];
-    Raw<T> raw[ITER][2];
-    auto load = [&](int round) {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int t = round * W * TW + row0 + i * RPW;
-            if (on && t < n) {
-                if (at.on_a) raw[i][0].load(src + t * row_stride + at.da);
-                if (at.on_b) raw[i][1].load(src + t * row_stride + at.db);
-            }
+    Raw<T> na, nb;
+    auto load = [&](int t) {
+        if (on && t < n) {
+            if (at.on_a) na.load(src + t * row_stride + at.da);
+            if (at.on_b) nb.load(src + t * row_stride + at.db);
         }
     };
-    // the round's values: normed, rotated
-    auto work = [&](int round, const uint64_t *turns) {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int t = round * W * TW + row0 + i * RPW;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[i][e] = 0;
-            if (on && t < n) {
-                if (at.on_a) raw[i][0].get(f[i]);
-                if (at.on_b) raw[i][1].get(f[i] + 4);
-            }
-            if (gamma) norm<LG>(f[i], gamma, at, inv_d, r.eps);
-            if (turn && on && t < n) {
-                const int pos = r.positions ? ldp(r.positions + p.row + t) : p.lo + t;
-                uint64_t co[4], si[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float c0, c1, s0, s1;
-                    angle(turns[2 * e], pos, r.mscale, c0, s0);
-                    angle(turns[2 * e + 1], pos, r.mscale, c1, s1);
-                    co[e] = attn::pair(c0, c1);
-                    si[e] = attn::pair(s0, s1);
-                }
-                rotate(f[i], co, si, r.interleaved);
-            }
-        }
-    };
-    load(0);
     uint64_t turns[8];
+    // token t's values: normed, rotated; an infinity becomes NaN (x + 0 x), which the maximum passes over and the
+    // codes keep
+    auto work = [&](int t, uint64_t *f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0;
+        if (on && t < n) {
+            if (at.on_a) na.get(f);
+            if (at.on_b) nb.get(f + 4);
+        }
+        load(t + stride_t);
+        if (gamma) norm<LG>(f, gamma, at, inv_d, r.eps);
+        if (turn && on && t < n) {
+            const int pos = r.positions ? ldp(r.positions + p.row + t) : p.lo + t;
+            uint64_t co[4], si[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float c0, c1, s0, s1;
+                angle(turns[2 * e], pos, r.mscale, c0, s0);
+                angle(turns[2 * e + 1], pos, r.mscale, c1, s1);
+                co[e] = attn::pair(c0, c1);
+                si[e] = attn::pair(s0, s1);
+            }
+            rotate(f, co, si, r.interleaved);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = attn::fma2(f[e], 0, f[e]);
+    };
+    load(t0);
     if (turn) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -278,37 +279,41 @@ __device__ __forceinline__ void store_kv(const Q8Args &c) {
     }
     const int pi = p.start / a.page_size, slot = p.start - pi * a.page_size;
     const int page = ldp(a.table + (size_t)p.b * a.max_pages + pi);
+
+    uint32_t top = 0;  // the bits of the largest size: those of numbers of one sign are in the numbers' order
+    for (int t = t0; t - lane / LG < n; t += stride_t) {
+        uint64_t f[8];
+        work(t, f);
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float x, y;
+            attn::unpair(f[e], x, y);
+            m = fmaxf(m, fmaxf(fabsf(x), fabsf(y)));
+        }
+        top = max(top, __float_as_uint(m));
+        if (held && t < n) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                float4 v;
+                attn::unpair(f[e], v.x, v.y);
+                attn::unpair(f[e + 1], v.z, v.w);
+                mine[(t * 4 + e / 2) * LG] = v;
+            }
+        }
+    }
     const bool page_ok = page >= 0 && page < a.n_pages;
     if (!page_ok && tid == 0) record_error(a.err, MOE_ERR_DEVICE);
     uint8_t *dst = static_cast<uint8_t *>(const_cast<void *>(is_v ? a.v : a.k)) + (page_ok ? page : 0) * a.page_stride +
                    h * a.head_stride + slot * a.token_stride;
     uint8_t *scale = (is_v ? c.v_scale : c.k_scale) + (page_ok ? page : 0) * c.scale_page + h * c.scale_head + slot / c.block;
-    int was = on && page_ok && old > 0 ? int(q8::ldp_byte(scale)) - 127 : q8::kLowest;
-
-    uint32_t top = 0;  // the bits of the largest size: those of numbers of one sign are in the numbers' order
-    for (int i = 0; i < rounds; ++i) {
-        if (i > 0) load(i);
-        work(i, turns);
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < ITER; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // an infinity becomes NaN (x + 0 x), which the maximum passes over and the codes keep
-                f[j][e] = attn::fma2(f[j][e], 0, f[j][e]);
-                float x, y;
-                attn::unpair(f[j][e], x, y);
-                m = fmaxf(m, fmaxf(fabsf(x), fabsf(y)));
-            }
-        top = max(top, __float_as_uint(m));
-    }
+    const int was = on && page_ok && old > 0 ? int(q8::ldp_byte(scale)) - 127 : q8::kLowest;
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) tops[warp] = __uint_as_float(top);
+    if (lane == 0) tops[warp] = top;
     __syncthreads();
-    float m = 0.f;
-    for (int w = warp / W * W; w < warp / W * W + W; ++w) m = fmaxf(m, tops[w]);
+    for (int w = warp - sub; w < warp - sub + W; ++w) top = max(top, tops[w]);
     if (!on || !page_ok) return;
-    const int e_new = exponent_of(m), e = old > 0 ? max(e_new, was) : e_new;
+    const int e_new = exponent_of(__uint_as_float(top)), e = old > 0 ? max(e_new, was) : e_new;
 
     if (old > 0 && e > was) {  // the old codes in units of the larger scale
         const int chunks = at.D / 16;
@@ -320,7 +325,8 @@ __device__ __forceinline__ void store_kv(const Q8Args &c) {
             uint32_t *x = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t lo = q8::to_f16x2(x[j]), hi = q8::to_f16x2(x[j] >> 16);
+                uint32_t lo, hi;
+                q8::to_f16x4(x[j], lo, hi);
                 const __half2 a0 = __hmul2(*reinterpret_cast<const __half2 *>(&lo), down);
                 const __half2 a1 = __hmul2(*reinterpret_cast<const __half2 *>(&hi), down);
                 x[j] = q8::from_f16x2(*reinterpret_cast<const uint32_t *>(&a0)) |
@@ -333,30 +339,31 @@ __device__ __forceinline__ void store_kv(const Q8Args &c) {
     const float up = q8::scale_of(uint32_t(min(max(127 - e, 0), 254)));
     const uint64_t up2 = attn::pair(up, up);
     dst += old * a.token_stride;
-    for (int i = 0; i < rounds; ++i) {
-        if (rounds > 1) {  // the registers hold one round: the others are worked out again
-            load(i);
-            work(i, turns);
+    if (!held) load(t0);
+    for (int t = t0; t - lane / LG < n; t += stride_t) {
+        uint64_t f[8];
+        if (held) {
+            if (t >= n) break;  // no shuffles here
 #pragma unroll
-            for (int j = 0; j < ITER; ++j)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[j][k] = attn::fma2(f[j][k], 0, f[j][k]);
-        }
-#pragma unroll
-        for (int j = 0; j < ITER; ++j) {
-            const int t = i * W * TW + row0 + j * RPW;
-            if (t >= n) continue;
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float x, y;
-                attn::unpair(attn::mul2(f[j][k], up2), x, y);
-                w[k] = q8::from_f32(x, y);
+            for (int e = 0; e < 8; e += 2) {
+                const float4 v = mine[(t * 4 + e / 2) * LG];
+                f[e] = attn::pair(v.x, v.y);
+                f[e + 1] = attn::pair(v.z, v.w);
             }
-            uint8_t *to = dst + t * a.token_stride;
-            if (at.on_a) *reinterpret_cast<uint2 *>(to + at.da) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-            if (at.on_b) *reinterpret_cast<uint2 *>(to + at.db) = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
+        } else {
+            work(t, f);
         }
+        if (t >= n) continue;
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float x, y;
+            attn::unpair(attn::mul2(f[k], up2), x, y);
+            w[k] = q8::from_f32(x, y);
+        }
+        uint8_t *to = dst + t * a.token_stride;
+        if (at.on_a) *reinterpret_cast<uint2 *>(to + at.da) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        if (at.on_b) *reinterpret_cast<uint2 *>(to + at.db) = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
 }
 
@@ -383,9 +390,10 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
     Raw<T> na, nb;
     const T *q_in = static_cast<const T *>(a.q) + (int64_t)t0 * a.q_stride;
     T *out = static_cast<T *>(a.out) + (int64_t)t0 * a.out_stride;
+    const int q_row = int(a.q_stride), out_row = int(a.out_stride);
     auto load = [&]() {
         if (tk < tokens) {
-            const T *src = q_in + tk * a.q_stride + h * at.D;
+            const T *src = q_in + (int64_t)tk * q_row + h * at.D;
             if (at.on_a) na.load(src + at.da);
             if (at.on_b) nb.load(src + at.db);
         }
@@ -424,7 +432,7 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
     for (int left = (tokens * heads + kGroups - 1) / kGroups; left > 0; --left) {
         const int k = tk < tokens ? tk : 0;
         const bool on = tk < tokens && seq[k] >= 0;
-        T *dst = out + k * a.out_stride + h * at.D;
+        T *dst = out + (int64_t)k * out_row + h * at.D;
         uint64_t f[8] = {};
         if (on && at.on_a) na.get(f);
         if (on && at.on_b) nb.get(f + 4);
@@ -451,7 +459,7 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
 }
 
 template <typename T, int LG, int TB>
-__global__ void __launch_bounds__(kThreads) rope_q8_kernel(const __grid_constant__ Q8Args c) {
+__global__ void __launch_bounds__(kThreads, 3) rope_q8_kernel(const __grid_constant__ Q8Args c) {
     // the table and the norms' weights too may be what the kernel before this one writes
     griddep_wait();
     griddep_launch_dependents();
@@ -461,21 +469,36 @@ __global__ void __launch_bounds__(kThreads) rope_q8_kernel(const __grid_constant
         turn_q<T, LG, TB>(c);
 }
 
+template <typename T, int LG, int TB>
+cudaError_t launch_tokens(const Q8Args &c, int64_t grid, size_t smem, cudaStream_t st) {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(rope_q8_kernel<T, LG, TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKept);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    return launch_pdl(rope_q8_kernel<T, LG, TB>, dim3(unsigned(grid)), dim3(kThreads), smem, st, c);
+}
+
 template <typename T, int LG>
 cudaError_t launch_lanes(Q8Args &c, const moe_attn_shape &s, cudaStream_t st) {
-    constexpr int RPW = 32 / LG, TW = RPW * (RPW >= 16 ? 1 : RPW == 8 ? 2 : 4);
-    // as many warps a task as hold the new tokens of a block at once
-    const int most = std::min(c.block, s.max_q);
-    for (c.warps = 1; c.warps < kWarps && c.warps * TW < most;) c.warps *= 2;
+    constexpr int RPW = 32 / LG;
+    // as many warps a task as new tokens of a block need to be worked on at once, if not more than eight
+    const int most = std::max(std::min(c.block, s.max_q), 1);
+    for (c.warps = 1; c.warps < kWarps && c.warps * RPW < most;) c.warps *= 2;
     c.groups = (2 * s.n_kv_heads * c.warps + kWarps - 1) / kWarps;
+    size_t smem = (size_t)(kWarps / c.warps) * most * LG * 64;
+    c.hold = most;
+    if (smem > kMostKept) c.hold = 0, smem = 0;
     // blocks of tokens that the chunks can touch: the host knows how many tokens and sequences there are
     const int64_t pieces = std::min<int64_t>(s.n_tokens, (int64_t)s.n_tokens / c.block + 2 * (int64_t)s.n_seqs);
     const int tb = s.n_tokens >= 4 * 152 ? 4 : 1;
     const int64_t grid = pieces * c.groups + (s.n_tokens + tb - 1) / tb;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     c.kv_blocks = int(pieces * c.groups);
-    return tb == 4 ? launch_pdl(rope_q8_kernel<T, LG, 4>, dim3(unsigned(grid)), dim3(kThreads), 0, st, c)
-                   : launch_pdl(rope_q8_kernel<T, LG, 1>, dim3(unsigned(grid)), dim3(kThreads), 0, st, c);
+    return tb == 4 ? launch_tokens<T, LG, 4>(c, grid, smem, st) : launch_tokens<T, LG, 1>(c, grid, smem, st);
 }
 
 template <typename T>

@@ -53,9 +53,26 @@ struct LaneOf {
     }
 };
 
+// The lane's weights of a norm, as pairs like the values.
+template <typename T>
+__device__ __forceinline__ void load_gamma(uint64_t *g, const T *gamma, const LaneOf &at) {
+    Raw<T> w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = 0;
+    if (!gamma) return;
+    if (at.on_a) {
+        w.load_cached(gamma + at.da);
+        w.get(g);
+    }
+    if (at.on_b) {
+        w.load_cached(gamma + at.db);
+        w.get(g + 4);
+    }
+}
+
 // f[0..3], f[4..7]: the two pieces, as pairs of neighbouring elements.
-template <int LG, typename T>
-__device__ __forceinline__ void norm(uint64_t *f, const T *gamma, const LaneOf &at, float inv_d, float eps) {
+template <int LG>
+__device__ __forceinline__ void norm(uint64_t *f, const uint64_t *g, float inv_d, float eps) {
     uint64_t s2 = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s2 = attn::fma2(f[e], f[e], s2);
@@ -66,20 +83,8 @@ __device__ __forceinline__ void norm(uint64_t *f, const T *gamma, const LaneOf &
     for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float rs = rsqrtf(ss * inv_d + eps);
     const uint64_t rs2 = attn::pair(rs, rs);
-    uint64_t g[4];
-    Raw<T> w;
-    if (at.on_a) {
-        w.load_cached(gamma + at.da);
-        w.get(g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = attn::mul2(attn::mul2(f[e], rs2), g[e]);
-    }
-    if (at.on_b) {
-        w.load_cached(gamma + at.db);
-        w.get(g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 + e] = attn::mul2(attn::mul2(f[4 + e], rs2), g[e]);
-    }
+    for (int e = 0; e < 8; ++e) f[e] = attn::mul2(attn::mul2(f[e], rs2), g[e]);
 }
 
 __device__ __forceinline__ void rotate(uint64_t *f, const uint64_t *c, const uint64_t *s, bool interleaved) {
@@ -251,7 +256,11 @@ __device__ __forceinline__ void store_kv(const Q8Args &c) {
             if (at.on_b) nb.get(f + 4);
         }
         load(t + stride_t);
-        if (gamma) norm<LG>(f, gamma, at, inv_d, r.eps);
+        if (gamma) {
+            uint64_t g[8];
+            load_gamma(g, gamma, at);
+            norm<LG>(f, g, inv_d, r.eps);
+        }
         if (turn && on && t < n) {
             const int pos = r.positions ? ldp(r.positions + p.row + t) : p.lo + t;
             uint64_t co[4], si[4];
@@ -376,11 +385,11 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
     const int tid = threadIdx.x, t0 = (int(blockIdx.x) - c.kv_blocks) * TB, tokens = min(TB, a.n_tokens - t0);
     const int pairs = r.rot_dim / 2, heads = a.n_heads;
     const LaneOf at(r, tid % LG);
-    constexpr int kGroups = kThreads / LG, kTurns = (TB * kMaxPairs + kThreads - 1) / kThreads;
-    uint64_t turn[kTurns];
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i)
-        if (tid + i * kThreads < TB * pairs) turn[i] = ldp_turn(r.turns + (tid + i * kThreads) % pairs);
+    constexpr int kGroups = kThreads / LG;
+    // a thread's pair in every token whose angles it finds: 32, 64 or 128 threads a token
+    const int shift = pairs <= 32 ? 5 : pairs <= 64 ? 6 : 7, pair = tid & ((1 << shift) - 1);
+    uint64_t turn = 0;
+    if (pair < pairs) turn = ldp_turn(r.turns + pair);
     // a group takes heads group, group + kGroups, .. of the block's tokens; the next is requested ahead
     int tk = 0, h = tid / LG;
     auto settle = [&]() {
@@ -416,19 +425,18 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-        const int j = tid + i * kThreads, k = j / pairs, p = j - k * pairs;
-        if (j < tokens * pairs && seq[k] >= 0) {
+    for (int k = tid >> shift; k < tokens; k += kThreads >> shift)
+        if (pair < pairs && seq[k] >= 0) {
             float co, si;
-            angle(turn[i], r.positions ? ldp(r.positions + t0 + k) : where[k], r.mscale, co, si);
-            float *to = reinterpret_cast<float *>(&cs[k][place_of(p >> 1)]) + (p & 1);
+            angle(turn, r.positions ? ldp(r.positions + t0 + k) : where[k], r.mscale, co, si);
+            float *to = reinterpret_cast<float *>(&cs[k][place_of(pair >> 1)]) + (pair & 1);
             to[0] = co;
             to[2] = si;
         }
-    }
     __syncthreads();
     const float inv_d = 1.f / float(at.D);
+    uint64_t gq[8];
+    load_gamma(gq, static_cast<const T *>(r.gq), at);
     for (int left = (tokens * heads + kGroups - 1) / kGroups; left > 0; --left) {
         const int k = tk < tokens ? tk : 0;
         const bool on = tk < tokens && seq[k] >= 0;
@@ -439,7 +447,7 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
         h += kGroups;
         settle();
         if (left > 1) load();
-        if (r.gq) norm<LG>(f, static_cast<const T *>(r.gq), at, inv_d, r.eps);
+        if (r.gq) norm<LG>(f, gq, inv_d, r.eps);
         if (at.turned) {
             uint64_t co[4], si[4];
 #pragma unroll
@@ -459,7 +467,7 @@ __device__ __forceinline__ void turn_q(const Q8Args &c) {
 }
 
 template <typename T, int LG, int TB>
-__global__ void __launch_bounds__(kThreads, 3) rope_q8_kernel(const __grid_constant__ Q8Args c) {
+__global__ void __launch_bounds__(kThreads, 2) rope_q8_kernel(const __grid_constant__ Q8Args c) {
     // the table and the norms' weights too may be what the kernel before this one writes
     griddep_wait();
     griddep_launch_dependents();
@@ -485,19 +493,22 @@ cudaError_t launch_tokens(const Q8Args &c, int64_t grid, size_t smem, cudaStream
 template <typename T, int LG>
 cudaError_t launch_lanes(Q8Args &c, const moe_attn_shape &s, cudaStream_t st) {
     constexpr int RPW = 32 / LG;
-    // as many warps a task as new tokens of a block need to be worked on at once, if not more than eight
+    // as many warps a task as leave each at least four turns on the new tokens of a block (one for every token it
+    // works on at once: 4043 tokens 21.1 us, most of it the start of 8 x 552 warps)
     const int most = std::max(std::min(c.block, s.max_q), 1);
-    for (c.warps = 1; c.warps < kWarps && c.warps * RPW < most;) c.warps *= 2;
+    for (c.warps = 1; c.warps < kWarps && c.warps * RPW * 4 < most;) c.warps *= 2;
     c.groups = (2 * s.n_kv_heads * c.warps + kWarps - 1) / kWarps;
     size_t smem = (size_t)(kWarps / c.warps) * most * LG * 64;
     c.hold = most;
     if (smem > kMostKept) c.hold = 0, smem = 0;
     // blocks of tokens that the chunks can touch: the host knows how many tokens and sequences there are
     const int64_t pieces = std::min<int64_t>(s.n_tokens, (int64_t)s.n_tokens / c.block + 2 * (int64_t)s.n_seqs);
-    const int tb = s.n_tokens >= 4 * 152 ? 4 : 1;
+    // tokens of a block that rotates q: more for fewer starts once that leaves a block on each SM
+    const int tb = s.n_tokens >= 16 * 152 ? 16 : s.n_tokens >= 4 * 152 ? 4 : 1;
     const int64_t grid = pieces * c.groups + (s.n_tokens + tb - 1) / tb;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     c.kv_blocks = int(pieces * c.groups);
+    if (tb == 16) return launch_tokens<T, LG, 16>(c, grid, smem, st);
     return tb == 4 ? launch_tokens<T, LG, 4>(c, grid, smem, st) : launch_tokens<T, LG, 1>(c, grid, smem, st);
 }
 

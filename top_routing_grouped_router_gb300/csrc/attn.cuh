@@ -200,6 +200,7 @@ bool decode_q8_supported(const moe_attn_shape &s, int block);
 cudaError_t launch_decode(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, Mode mode, cudaStream_t st);
 cudaError_t launch_decode_window(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
 cudaError_t launch_decode_q8(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
+cudaError_t launch_decode_q8_half(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st);
 bool chunk_supported(const moe_attn_shape &s);
 bool chunk_q8_supported(const moe_attn_shape &s, int block);
 size_t chunk_ws_bytes(const moe_attn_shape &s);

@@ -29,6 +29,9 @@
 // 2^-28 of that exactly; scores get the unit back), probabilities times 2^14.  A block's scale of k is
 // a factor of its scores.  O is kept in units of a block's scale of v, and changes its unit when a block
 // with a larger scale, or a much smaller one, comes; probabilities carry the rest.
+// Up to 8 query rows a key head (kHalf) the products are turned round: keys, then values' columns, are the
+// 16 rows of a tile and the queries its 8 columns, which halves the products, the softmax and O's registers
+// (a full 8-bit batch of groups of 8: 120 us as 16 x 8 tiles, half of them empty).
 #pragma once
 
 #include "q8.cuh"
@@ -95,6 +98,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// An 8 x 8 matrix of 16-bit elements, two of a row a lane, with rows and columns exchanged.
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 // 2^e, -126 <= e <= 127
@@ -272,7 +281,7 @@ __device__ __forceinline__ void join_parts(const Parts &p, uint32_t n, int rows,
 }
 
 // kCluster: CTAs of a pair, 0 where the work is scheduled on the device.
-template <int D, int kCluster, Mode kMode>
+template <int D, int kCluster, Mode kMode, bool kHalf>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Parts parts) {
     namespace cg = cooperative_groups;
     using C = Cfg<D, kMode>;
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             }
         };
         load_q(q0, 0);
-        if (rows > 8) {
+        if (!kHalf && rows > 8) {
             load_q(q1, 1);
         } else {
 #pragma unroll
@@ -602,6 +611,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             const int x0 = unit(top0), x1 = unit(top1);
             sl2_0 *= pow2(-x0);
             sl2_1 *= pow2(-x1);
+            if constexpr (kHalf) {  // of the rows 2 t4 and 2 t4 + 1
+                const float own = sl2_0;
+                sl2_0 = __shfl_sync(0xffffffffu, own, t4 * 8);
+                sl2_1 = __shfl_sync(0xffffffffu, own, t4 * 8 + 4);
+            }
             auto to_f16 = [](uint32_t v, float f) {
                 return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
             };
@@ -610,11 +624,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
                 for (int e = 0; e < 4; ++e) q[ks][e] = to_f16(q[ks][e], (e & 1) ? pow2(x1) : pow2(x0));
         }
-        const int seen0 = on0 ? past + int(j0) + 1 : 0, seen1 = on1 ? past + int(j1) + 1 : 0;
+        // keys that the lane's two rows of scores see: g and g + 8, or 2 t4 and 2 t4 + 1
+        const bool see0 = kHalf ? t4 * 2 < rows : on0, see1 = kHalf ? t4 * 2 + 1 < rows : on1;
+        const int seen0 = see0 ? past + int(kHalf ? t4 * 2 / G : j0) + 1 : 0;
+        const int seen1 = see1 ? past + int(kHalf ? (t4 * 2 + 1) / G : j1) + 1 : 0;
         const int seen_all = past + 1;  // keys that every row sees
-        float o[NT][4];
+        constexpr int OT = kHalf ? D / 16 : NT;
+        float o[OT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < OT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
@@ -634,7 +652,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             __syncwarp();
             const uint32_t kb = ring + (i % C::kStages) * C::kStageBytes, vb = kb + kStep * D * E;
             float sc[2][4] = {};
-            if constexpr (kMode == kQ8) {
+            if constexpr (kHalf) {
+                float odd[4] = {};
+#pragma unroll
+                for (int c = 0; c < KS / 4; ++c) {
+                    const uint4 w0 = lds16(kb + g * D + at_k(g, c * 4 + t4) * 16), w1 = lds16(kb + (g + 8) * D + at_k(g + 8, c * 4 + t4) * 16);
+                    const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t k4[4];  // keys g and g + 8, two columns each, then the next two
+                        q8::to_f16x4(y0[e], k4[0], k4[2]);
+                        q8::to_f16x4(y1[e], k4[1], k4[3]);
+                        mma16816h(e & 1 ? odd : sc[0], k4, q[c * 4 + e][0], q[c * 4 + e][2]);
+                    }
+                }
+                const float ks = q8::scale_of(bytes & 255), f0 = sl2_0 * ks, f1 = sl2_1 * ks;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[0][e] = (sc[0][e] + odd[e]) * (e & 1 ? f1 : f0);
+            } else if constexpr (kMode == kQ8) {
                 float odd[2][4] = {};
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
@@ -681,28 +716,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[n][e] *= sl2;
             }
+            constexpr int SN = kHalf ? 1 : 2;  // tiles of scores
+            auto key_at = [&](int n, int e) { return key0 + (kHalf ? (e >> 1) * 8 + g : n * 8 + t4 * 2 + (e & 1)); };
+            auto first_row = [](int e) { return kHalf ? (e & 1) == 0 : e < 2; };
             if (key0 > seen_all - kStep) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < SN; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + n * 8 + t4 * 2 + (e & 1);
-                        if (key >= (e < 2 ? seen0 : seen1)) sc[n][e] = kNegInf;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (key_at(n, e) >= (first_row(e) ? seen0 : seen1)) sc[n][e] = kNegInf;
             }
             if (kMode != kAll && key0 < s.kv_len - a.window && key0 > a.sinks - kStep) {  // before a row's window
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < SN; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + n * 8 + t4 * 2 + (e & 1);
-                        if (key >= a.sinks && key < (e < 2 ? seen0 : seen1) - a.window) sc[n][e] = kNegInf;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (key_at(n, e) >= a.sinks && key_at(n, e) < (first_row(e) ? seen0 : seen1) - a.window) sc[n][e] = kNegInf;
             }
-            float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-            float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+            float x0 = kHalf ? fmaxf(sc[0][0], sc[0][2]) : fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+            float x1 = kHalf ? fmaxf(sc[0][1], sc[0][3]) : fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
 #pragma unroll
-            for (int w = 1; w <= 2; w <<= 1) {
+            for (int w = kHalf ? 4 : 1; w <= (kHalf ? 16 : 2); w <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
             }
@@ -730,25 +764,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                     f1 *= u;
                 }
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][0] *= f0;
-                    o[j][1] *= f0;
-                    o[j][2] *= f1;
-                    o[j][3] *= f1;
-                }
+                for (int j = 0; j < OT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] *= first_row(e) ? f0 : f1;
                 m0 = n_0;
                 m1 = n_1;
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                sc[n][0] = ex2(sc[n][0] - z0);
-                sc[n][1] = ex2(sc[n][1] - z0);
-                sc[n][2] = ex2(sc[n][2] - z1);
-                sc[n][3] = ex2(sc[n][3] - z1);
-                l0 += sc[n][0] + sc[n][1];  // this lane's columns; the quad's are added at the end
-                l1 += sc[n][2] + sc[n][3];
+            for (int n = 0; n < SN; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = ex2(sc[n][e] - (first_row(e) ? z0 : z1));
+                l0 += sc[n][0] + sc[n][kHalf ? 2 : 1];  // this lane's keys; the others' are added at the end
+                l1 += sc[n][kHalf ? 1 : 2] + sc[n][3];
             }
-            if constexpr (kMode == kQ8) {
+            if constexpr (kHalf) {
+                // as below; a turned matrix of probabilities is the tiles' second operand
+                const int ev = bytes >> 8;
+                const float f = ev == 255 ? q8::scale_of(255) : pow2(max(14 + ev - max(unit_v, 0), -126));
+                const uint32_t p0 = turned(pack_f16(sc[0][0] * f, sc[0][1] * f)), p1 = turned(pack_f16(sc[0][2] * f, sc[0][3] * f));
+                const int r = lane & 15;
+#pragma unroll
+                for (int c = 0; c < D / 16; c += 2) {
+                    uint32_t vf[4];
+                    ldsm4t(vb + r * D + at_v(r, c + (lane >> 4)) * 16, vf);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t v4[4];  // columns 2 g and 2 g + 1 of keys 2 t4 (+ 1), then of the keys 8 further on
+                        q8::to_f16x4(__byte_perm(vf[2 * e], 0, 0x3120), v4[0], v4[1]);
+                        q8::to_f16x4(__byte_perm(vf[2 * e + 1], 0, 0x3120), v4[2], v4[3]);
+                        mma16816h(o[c + e], v4, p0, p1);
+                    }
+                }
+            } else if constexpr (kMode == kQ8) {
                 // probabilities in fp16, in units that take in the difference of the block's scale to O's
                 const int ev = bytes >> 8;
                 const float f = ev == 255 ? q8::scale_of(255) : pow2(max(14 + ev - max(unit_v, 0), -126));
@@ -790,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         }
         cp_wait<0>();
 #pragma unroll
-        for (int w = 1; w <= 2; w <<= 1) {
+        for (int w = kHalf ? 4 : 1; w <= (kHalf ? 16 : 2); w <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, w);
             l1 += __shfl_xor_sync(0xffffffffu, l1, w);
         }
@@ -798,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         if constexpr (kMode == kQ8) {
             const float u = q8::scale_of(max(unit_v, 0));
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < OT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[j][e] = o[j][e] * pow2(-14) * u;
         }
@@ -807,7 +854,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         float *jo = reinterpret_cast<float *>(smem);
         float2 *jm = reinterpret_cast<float2 *>(jo + kWarps * kRows * D);
         __syncthreads();
-        if constexpr (kMode == kQ8) {  // tiles of even and of odd columns
+        if constexpr (kHalf) {
+#pragma unroll
+            for (int c = 0; c < OT; ++c) {
+                float *to = jo + (warp * kRows + t4 * 2) * D + c * 16 + g * 2;
+                *reinterpret_cast<float2 *>(to) = make_float2(o[c][0], o[c][2]);
+                *reinterpret_cast<float2 *>(to + D) = make_float2(o[c][1], o[c][3]);
+            }
+        } else if constexpr (kMode == kQ8) {  // tiles of even and of odd columns
 #pragma unroll
             for (int j = 0; j < NT; j += 2) {
                 float *to = jo + (warp * kRows + g) * D + j * 8 + t4 * 4;
@@ -822,9 +876,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             if (rows > 8)
                 *reinterpret_cast<float2 *>(jo + (warp * kRows + g + 8) * D + j * 8 + t4 * 2) = make_float2(o[j][2], o[j][3]);
         }
-        if (t4 == 0) {
-            jm[warp * kRows + g] = make_float2(m0, l0);
-            jm[warp * kRows + g + 8] = make_float2(m1, l1);
+        if (kHalf ? g == 0 : t4 == 0) {
+            jm[warp * kRows + (kHalf ? t4 * 2 : g)] = make_float2(m0, l0);
+            jm[warp * kRows + (kHalf ? t4 * 2 + 1 : g + 8)] = make_float2(m1, l1);
         }
         __syncthreads();
         auto write_out = [&](int r, int d, float4 v, float m, float l) {
@@ -935,13 +989,13 @@ int cluster_of(const moe_attn_shape &s, int64_t keys) {
     return 0;
 }
 
-template <int D, int kCluster, Mode kMode>
+template <int D, int kCluster, Mode kMode, bool kHalf>
 cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int grid, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kCluster, kMode>,
+        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kCluster, kMode, kHalf>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (Cfg<D, kMode>::kSmem));
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
@@ -962,26 +1016,26 @@ cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = kCluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kCluster, kMode>, a, p);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kCluster, kMode, kHalf>, a, p);
 }
 
-template <int kCluster, Mode kMode>
+template <int kCluster, Mode kMode, bool kHalf>
 cudaError_t launch_dim(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int grid, cudaStream_t st) {
-    return s.head_dim == 128 ? launch_typed<128, kCluster, kMode>(a, s, hdr, ws, grid, st)
-                             : launch_typed<64, kCluster, kMode>(a, s, hdr, ws, grid, st);
+    return s.head_dim == 128 ? launch_typed<128, kCluster, kMode, kHalf>(a, s, hdr, ws, grid, st)
+                             : launch_typed<64, kCluster, kMode, kHalf>(a, s, hdr, ws, grid, st);
 }
 
-template <Mode kMode>
+template <Mode kMode, bool kHalf = false>
 cudaError_t launch(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, int sms, cudaStream_t st) {
     const int grid = sms * kCtasPerSm < kMaxGrid ? sms * kCtasPerSm : kMaxGrid;
     int64_t keys = (int64_t)s.max_pages * s.page_size;  // of a pair, at most: with a window its steps' only
     if (kMode != kAll) keys = std::min(keys, (int64_t)a.window + a.sinks + s.max_q + 2 * kStep);
     switch (cluster_of(s, keys)) {
-    case 8: return launch_dim<8, kMode>(a, s, hdr, ws, grid, st);
-    case 4: return launch_dim<4, kMode>(a, s, hdr, ws, grid, st);
-    case 2: return launch_dim<2, kMode>(a, s, hdr, ws, grid, st);
-    case 1: return launch_dim<1, kMode>(a, s, hdr, ws, grid, st);
-    default: return launch_dim<0, kMode>(a, s, hdr, ws, grid, st);
+    case 8: return launch_dim<8, kMode, kHalf>(a, s, hdr, ws, grid, st);
+    case 4: return launch_dim<4, kMode, kHalf>(a, s, hdr, ws, grid, st);
+    case 2: return launch_dim<2, kMode, kHalf>(a, s, hdr, ws, grid, st);
+    case 1: return launch_dim<1, kMode, kHalf>(a, s, hdr, ws, grid, st);
+    default: return launch_dim<0, kMode, kHalf>(a, s, hdr, ws, grid, st);
     }
 }
 

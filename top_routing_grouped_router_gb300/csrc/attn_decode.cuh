@@ -39,6 +39,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace attn {
@@ -638,7 +639,123 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
         float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
         int unit_v = -1, most_v = 0;  // 8-bit values: O is in units of 2^(unit_v - 127 - 14); the largest byte so far
 
-        for (int i = 0; i < mine; ++i) {
+        // the products turned round, N steps at a time (of an 8-bit cache, whose steps have one scale each)
+        auto half_steps = [&](auto count, int i, int copied) {
+            constexpr int N = decltype(count)::value;
+            float sc[N][4], odd[N][4];
+            uint32_t bytes[N], kb[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                bytes[n] = __shfl_sync(0xffffffffu, ((i + n) ^ copied) < 32 ? sc_cur : sc_prev, (i + n) & 31);
+                kb[n] = ring + ((i + n) % C::kStages) * C::kStageBytes;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = odd[n][e] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < KS / 4; ++c)
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const uint4 w0 = lds16(kb[n] + g * D + at_k(g, c * 4 + t4) * 16), w1 = lds16(kb[n] + (g + 8) * D + at_k(g + 8, c * 4 + t4) * 16);
+                    const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t k4[4];  // keys g and g + 8, two columns each, then the next two
+                        q8::to_f16x4(y0[e], k4[0], k4[2]);
+                        q8::to_f16x4(y1[e], k4[1], k4[3]);
+                        mma16816h(e & 1 ? odd[n] : sc[n], k4, q[c * 4 + e][0], q[c * 4 + e][2]);
+                    }
+                }
+            float x0 = m0, x1 = m1;  // of the rows 2 t4 and 2 t4 + 1
+            int top = -1;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const float ks = q8::scale_of(bytes[n] & 255), f0 = sl2_0 * ks, f1 = sl2_1 * ks;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = (sc[n][e] + odd[n][e]) * (e & 1 ? f1 : f0);
+                const int key0 = key_of(i + n);
+                if (key0 > seen_all - kStep || (key0 < s.kv_len - a.window && key0 > a.sinks - kStep)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + (e >> 1) * 8 + g, seen = e & 1 ? seen1 : seen0;
+                        if (key >= seen || (key >= a.sinks && key < seen - a.window)) sc[n][e] = kNegInf;
+                    }
+                }
+                x0 = fmaxf(x0, fmaxf(sc[n][0], sc[n][2]));
+                x1 = fmaxf(x1, fmaxf(sc[n][1], sc[n][3]));
+                const int ev = bytes[n] >> 8;
+                top = max(top, ev < 255 ? ev : -1);
+            }
+#pragma unroll
+            for (int w = 4; w <= 16; w <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
+            }
+            const float z0 = x0 == kNegInf ? 0.f : x0, z1 = x1 == kNegInf ? 0.f : x1;
+            const int old_unit = unit_v < 0 ? top : unit_v;
+            most_v = max(most_v, top);
+            if (top > unit_v || (top >= 0 && top < unit_v - 6 && top >= most_v - 60)) unit_v = top;
+            if (__any_sync(0xffffffffu, x0 != m0 || x1 != m1) || unit_v != old_unit) {
+                const float u = pow2(max(old_unit - unit_v, -126));
+                float f0 = ex2(m0 - z0), f1 = ex2(m1 - z1);
+                l0 *= f0;
+                l1 *= f1;
+                f0 *= u;
+                f1 *= u;
+#pragma unroll
+                for (int j = 0; j < OT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] *= e & 1 ? f1 : f0;
+                m0 = x0;
+                m1 = x1;
+            }
+            uint32_t p[N][2];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = ex2(sc[n][e] - (e & 1 ? z1 : z0));
+                l0 += sc[n][0] + sc[n][2];  // this lane's keys; the others' are added at the end
+                l1 += sc[n][1] + sc[n][3];
+                // in fp16, as below; turned, the tiles' second operand
+                const int ev = bytes[n] >> 8;
+                const float f = ev == 255 ? q8::scale_of(255) : pow2(max(14 + ev - max(unit_v, 0), -126));
+                p[n][0] = turned(pack_f16(sc[n][0] * f, sc[n][1] * f));
+                p[n][1] = turned(pack_f16(sc[n][2] * f, sc[n][3] * f));
+            }
+            const int r = lane & 15;
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2)
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    uint32_t vf[4];
+                    ldsm4t(kb[n] + kStep * D + r * D + at_v(r, c + (lane >> 4)) * 16, vf);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t v4[4];  // columns 2 g and 2 g + 1 of keys 2 t4 (+ 1), then of the keys 8 further on
+                        q8::to_f16x4(__byte_perm(vf[2 * e], 0, 0x3120), v4[0], v4[1]);
+                        q8::to_f16x4(__byte_perm(vf[2 * e + 1], 0, 0x3120), v4[2], v4[3]);
+                        mma16816h(o[c + e], v4, p[n][0], p[n][1]);
+                    }
+                }
+        };
+        if constexpr (kHalf) {
+            // two steps together, for more independent instructions and half the reductions (one at a time: a full
+            // batch 108 us)
+            int i = 0;
+            for (; i + 2 <= mine; i += 2) {
+                copy_q8(i + C::kStages - 1);
+                cp_wait<C::kStages - 2>();
+                __syncwarp();
+                half_steps(std::integral_constant<int, 2>{}, i, i + C::kStages - 1);
+                __syncwarp();  // the stages are read before a lane's next copy lands in them
+                copy_q8(i + C::kStages);
+            }
+            if (i < mine) {
+                cp_wait<C::kStages - 2>();
+                __syncwarp();
+                half_steps(std::integral_constant<int, 1>{}, i, i + C::kStages - 2);
+            }
+        }
+        for (int i = 0; i < (kHalf ? 0 : mine); ++i) {
             uint32_t bytes = 0;  // the step's scales
             if constexpr (kMode == kQ8) {
                 copy_q8(i + C::kStages - 1);
@@ -652,24 +769,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             __syncwarp();
             const uint32_t kb = ring + (i % C::kStages) * C::kStageBytes, vb = kb + kStep * D * E;
             float sc[2][4] = {};
-            if constexpr (kHalf) {
-                float odd[4] = {};
-#pragma unroll
-                for (int c = 0; c < KS / 4; ++c) {
-                    const uint4 w0 = lds16(kb + g * D + at_k(g, c * 4 + t4) * 16), w1 = lds16(kb + (g + 8) * D + at_k(g + 8, c * 4 + t4) * 16);
-                    const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t k4[4];  // keys g and g + 8, two columns each, then the next two
-                        q8::to_f16x4(y0[e], k4[0], k4[2]);
-                        q8::to_f16x4(y1[e], k4[1], k4[3]);
-                        mma16816h(e & 1 ? odd : sc[0], k4, q[c * 4 + e][0], q[c * 4 + e][2]);
-                    }
-                }
-                const float ks = q8::scale_of(bytes & 255), f0 = sl2_0 * ks, f1 = sl2_1 * ks;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[0][e] = (sc[0][e] + odd[e]) * (e & 1 ? f1 : f0);
-            } else if constexpr (kMode == kQ8) {
+            if constexpr (kMode == kQ8) {
                 float odd[2][4] = {};
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
@@ -716,27 +816,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[n][e] *= sl2;
             }
-            constexpr int SN = kHalf ? 1 : 2;  // tiles of scores
-            auto key_at = [&](int n, int e) { return key0 + (kHalf ? (e >> 1) * 8 + g : n * 8 + t4 * 2 + (e & 1)); };
-            auto first_row = [](int e) { return kHalf ? (e & 1) == 0 : e < 2; };
             if (key0 > seen_all - kStep) {
 #pragma unroll
-                for (int n = 0; n < SN; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key_at(n, e) >= (first_row(e) ? seen0 : seen1)) sc[n][e] = kNegInf;
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + n * 8 + t4 * 2 + (e & 1);
+                        if (key >= (e < 2 ? seen0 : seen1)) sc[n][e] = kNegInf;
+                    }
             }
             if (kMode != kAll && key0 < s.kv_len - a.window && key0 > a.sinks - kStep) {  // before a row's window
 #pragma unroll
-                for (int n = 0; n < SN; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key_at(n, e) >= a.sinks && key_at(n, e) < (first_row(e) ? seen0 : seen1) - a.window) sc[n][e] = kNegInf;
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + n * 8 + t4 * 2 + (e & 1);
+                        if (key >= a.sinks && key < (e < 2 ? seen0 : seen1) - a.window) sc[n][e] = kNegInf;
+                    }
             }
-            float x0 = kHalf ? fmaxf(sc[0][0], sc[0][2]) : fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-            float x1 = kHalf ? fmaxf(sc[0][1], sc[0][3]) : fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+            float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+            float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
 #pragma unroll
-            for (int w = kHalf ? 4 : 1; w <= (kHalf ? 16 : 2); w <<= 1) {
+            for (int w = 1; w <= 2; w <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
             }
@@ -764,38 +865,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                     f1 *= u;
                 }
 #pragma unroll
-                for (int j = 0; j < OT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][e] *= first_row(e) ? f0 : f1;
+                for (int j = 0; j < OT; ++j) {
+                    o[j][0] *= f0;
+                    o[j][1] *= f0;
+                    o[j][2] *= f1;
+                    o[j][3] *= f1;
+                }
                 m0 = n_0;
                 m1 = n_1;
             }
 #pragma unroll
-            for (int n = 0; n < SN; ++n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[n][e] = ex2(sc[n][e] - (first_row(e) ? z0 : z1));
-                l0 += sc[n][0] + sc[n][kHalf ? 2 : 1];  // this lane's keys; the others' are added at the end
-                l1 += sc[n][kHalf ? 1 : 2] + sc[n][3];
+            for (int n = 0; n < 2; ++n) {
+                sc[n][0] = ex2(sc[n][0] - z0);
+                sc[n][1] = ex2(sc[n][1] - z0);
+                sc[n][2] = ex2(sc[n][2] - z1);
+                sc[n][3] = ex2(sc[n][3] - z1);
+                l0 += sc[n][0] + sc[n][1];  // this lane's columns; the quad's are added at the end
+                l1 += sc[n][2] + sc[n][3];
             }
-            if constexpr (kHalf) {
-                // as below; a turned matrix of probabilities is the tiles' second operand
-                const int ev = bytes >> 8;
-                const float f = ev == 255 ? q8::scale_of(255) : pow2(max(14 + ev - max(unit_v, 0), -126));
-                const uint32_t p0 = turned(pack_f16(sc[0][0] * f, sc[0][1] * f)), p1 = turned(pack_f16(sc[0][2] * f, sc[0][3] * f));
-                const int r = lane & 15;
-#pragma unroll
-                for (int c = 0; c < D / 16; c += 2) {
-                    uint32_t vf[4];
-                    ldsm4t(vb + r * D + at_v(r, c + (lane >> 4)) * 16, vf);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t v4[4];  // columns 2 g and 2 g + 1 of keys 2 t4 (+ 1), then of the keys 8 further on
-                        q8::to_f16x4(__byte_perm(vf[2 * e], 0, 0x3120), v4[0], v4[1]);
-                        q8::to_f16x4(__byte_perm(vf[2 * e + 1], 0, 0x3120), v4[2], v4[3]);
-                        mma16816h(o[c + e], v4, p0, p1);
-                    }
-                }
-            } else if constexpr (kMode == kQ8) {
+            if constexpr (kMode == kQ8) {
                 // probabilities in fp16, in units that take in the difference of the block's scale to O's
                 const int ev = bytes >> 8;
                 const float f = ev == 255 ? q8::scale_of(255) : pow2(max(14 + ev - max(unit_v, 0), -126));

@@ -1069,11 +1069,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 // fewer than their number says: eight CTAs find places within one part of the chip only), and no
 // sequence with more than 8 steps a warp (104 pairs of up to 1819 keys, 14 steps: 13.8 us with
 // clusters of two, 12.2 scheduled; 40 pairs of up to 1989, clusters of four: 9.3, 9.6).
+// Where a window bounds the keys most pairs have as many, and a warp may have more steps: 12, and 40 if
+// there are more than 16 pairs (256 pairs, window 2048: 46.9 us with clusters of one, 51.3 scheduled; 64 pairs, 9000:
+// clusters of four 50.4, 55.0; but 4 pairs, 9000: 18.4, 16.1; over an 8-bit cache 27.7, 31.1; 28.8, 36.4; 12.4, 11.7).
 int cluster_of(const moe_attn_shape &s, int64_t keys) {
     const int64_t pairs = (int64_t)s.n_seqs * s.n_kv_heads;
+    const int steps = keys >= (int64_t)s.max_pages * s.page_size ? 8 : pairs > 16 ? 40 : 12;
     const int sizes[4] = {8, 4, 2, 1}, most[4] = {32, 72, 152, 304};
     for (int i = 0; i < 4; ++i)
-        if (pairs <= most[i]) return keys <= 8 * kWarps * kStep * sizes[i] ? sizes[i] : 0;
+        if (pairs <= most[i]) return keys <= steps * kWarps * kStep * sizes[i] ? sizes[i] : 0;
     return 0;
 }
 

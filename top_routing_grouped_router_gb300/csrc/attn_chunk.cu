@@ -23,19 +23,22 @@
 // keys' steps, then, `skip` steps further on, those from its first token's window on.
 //
 // Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
-// more warps turn them into the fp16 tiles that the tensor cores read: one instruction for two codes,
-// exact.  (To bf16, with their powers of two, they took three times the instructions, next to which the
-// softmax starved: 750 us for 2048 tokens over 16384 keys.)  The powers of two go elsewhere.  A row of Q
-// becomes fp16 in units of its own that bring its largest element to 2^14 (fp16 then holds elements
-// down to 2^-28 of that exactly).  The scale of sixteen keys is a factor of their scores, that of their
-// values moves the exponents of their probabilities, which are fp16 times 2^7; O is in units of the
-// largest scale of v so far (of a step's, where that is smaller by more than 2^8, down to 2^-60 of it).
+// more warps turn them into the fp16 tiles that the tensor cores read.  All factors are powers of two.  A tile's
+// values are in units of the largest scale of k in the step, and for v of the largest so far (of a step's,
+// where that is smaller by more than 2^8, down to 2^-60 of it), which O is kept in too.  fp16 holds all codes
+// exactly down to scales 2^-15 of those; k of smaller ones to 2^-33 of the step's largest value, and of v's scales
+// probabilities take what is beyond 2^-15 (a loop that few steps need).  A row of Q becomes fp16 in units of
+// its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
+// What was slower than that (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
+// of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542.
 //
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
 // share's end leave fp32 partial results that a second kernel joins.
 #include "q8.cuh"
 #include "tma_nd.cuh"
+
+#include <algorithm>
 
 namespace moe {
 namespace attn {
@@ -44,8 +47,9 @@ namespace {
 using namespace tc;
 
 // Warps 0-3, 4-7: softmax of tile 0, 1; the third warpgroup: MMAs, loads, the list of
-// segments, and with heads of 64 the MMAs of tile 1; a fourth, over an 8-bit cache: codes to fp16.
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11, kConvWarp = 12;
+// segments, and with heads of 64 the MMAs of tile 1 or, over an 8-bit cache, the steps' scales; a fourth, over an 8-bit
+// cache: codes to fp16.
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kListWarp = 10, kMma1Warp = 11, kScaleWarp = 11, kConvWarp = 12;
 constexpr int kConvThreads = 128;
 constexpr int kM = 128, kKeys = 128;
 constexpr int kMaxCtas = 160;   // one per SM (152)
@@ -56,15 +60,15 @@ constexpr int kJoinRows = 16;   // rows of a block of the join kernel
 template <int D, Mode kMode>
 struct Cfg {
     static constexpr bool kCodes = kMode == kQ8;
-    // The third warpgroup gives up registers that the softmax takes, within the launch's.  With a fourth every
-    // thread has 128, which the compiler does not exceed whatever a warpgroup takes later: there the softmax reads the
-    // scores twice from TMEM, 32 at a time (all at once they spilled: 657 us for 2048 tokens over 16384 keys).
+    // The third warpgroup gives up registers that the softmax takes, within the launch's: 8 x 32 x 208 + 4 x 32 x 80 is
+    // within 12 x 32 x 168.  With a fourth every thread has 128, which the compiler does not exceed whatever a warpgroup
+    // takes later (scores of a whole step in registers spilled: 657 us for 2048 tokens over 16384 keys).
     static constexpr int kThreads = kCodes ? 512 : 384, kLaunchRegs = kCodes ? 128 : 168;
     static constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
     static_assert(kCodes || 256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");
     static constexpr int kTile = kM * D * 2;                  // one Q tile, one K or V stage
     static constexpr int kStages = kCodes ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 8;
-    static constexpr int kRaw = kKeys * D;                    // a stage of codes
+    static constexpr int kRaw = kKeys * D;                    // a tile of codes
     static constexpr int kRaws = kCodes ? (D == 128 ? 2 : 6) : 0;
     static constexpr int kCtrl = kCodes && D == 64 ? 3072 : 2048;
     static constexpr int kSmem = (2 + kStages) * kTile + kRaws * kRaw + 1024 + kCtrl;
@@ -76,7 +80,7 @@ struct Cfg {
     // Warps that issue MMAs, each for its tiles.  With heads of 128 one, in the order of the tiles, which
     // keeps one tile's products beside the other's softmax (two: 420 us for a chunk of 2048, one at the time: 341);
     // with heads of 64, whose products are half as long, two (a mixed batch 48.4 us, with one 51).
-    static constexpr int kMmaWarps = D == 64 ? 2 : 1;
+    static constexpr int kMmaWarps = D == 64 && !kCodes ? 2 : 1;
     static constexpr uint32_t col_p(int t) { return kEarly ? 256 + 64 * t : 128 * t; }
     static constexpr uint32_t col_o(int t) { return kEarly ? 384 + 64 * t : 256 + 128 * t; }
 };
@@ -89,16 +93,22 @@ struct Seg {
     int tiles;                          // 1 or 2
     int low, skip;                      // with a window: the first key of its first token's, and the steps left out
 };
-// The scales of the steps over an 8-bit cache, found by the converting warps for kBatch steps of a segment at
-// a time: a step's 16 bytes are those of its eight groups of 16 keys, k's, then v's.  A group without a scale (no
-// keys, or NaN) has k's byte 127 (a factor of 1) and the largest of the step's for v.  A ring of as many
-// batches as there are stages: the batch that takes a place again begins when at least half as many
-// steps, each of them of a batch of its own at most, have been multiplied since.
-constexpr int kBatch = 8;
+// What a step over an 8-bit cache needs of its scales, in a ring of kScaleSlots: for each group of 16 keys the
+// factors (fp16) that bring its codes of k (low half) and of v to the step's units; the unit of k as the scores'
+// factor, that of v (and O) as a byte.
 struct Scales {
-    uint4 bytes[kBatch];
-    uint32_t nan[kBatch];  // bit i: byte i says NaN
+    uint32_t mul[8];
+    float k;
+    int unit;
+    uint32_t edge;   // whether any of the following matters to the codes:
+    uint32_t nan;    // the groups whose byte says NaN, k's in bits 0-7, v's in 8-15
+    int live;        // rows from here on hold no key that the item sees, nor do
+    int from, to;    // these
+    int wide;        // whether a group's scale of v is less than 2^-15 of the unit:
+    int8_t rest[8];  // what its probabilities take of that, as an exponent
+    int pad[2];
 };
+constexpr int kScaleSlots = 8;
 constexpr int kProbBits = 7;  // probabilities times 2^7: with kLag at most 2^15 in fp16
 
 // What the join kernel needs of an item that starts in a CTA's share and goes on past it.
@@ -350,9 +360,10 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     uint64_t *s_full = q_empty + 1, *s_empty = s_full + 2, *p_full = s_empty + 2, *o_full = p_full + 2, *o_empty = o_full + 2;  // [2] each
     uint64_t *v_zero = o_empty + 2, *drain = v_zero + C::kStages;  // [kStages], [2]
     uint64_t *raw_full = drain + 2, *raw_empty = raw_full + C::kRaws;  // [kRaws] each
-    uint64_t *sc_full = raw_empty + C::kRaws, *q_ready = sc_full + (C::kCodes ? C::kStages : 0);  // [kStages], [2]
-    Scales *scales = reinterpret_cast<Scales *>(ctrl + (q_ready + 3 - kv_full) / 2 * 16);  // [kStages], 16-byte aligned
-    Seg *segs = reinterpret_cast<Seg *>(scales + (C::kCodes ? C::kStages : 0));  // [kMaxSegs]
+    constexpr int kSlots = C::kCodes ? kScaleSlots : 0;
+    uint64_t *sc_full = raw_empty + C::kRaws, *sc_empty = sc_full + kSlots, *q_ready = sc_empty + kSlots;  // [2]
+    Scales *scales = reinterpret_cast<Scales *>(ctrl + (q_ready + 3 - kv_full) / 2 * 16);  // 16-byte aligned
+    Seg *segs = reinterpret_cast<Seg *>(scales + kSlots);  // [kMaxSegs]
     uint32_t *scan = reinterpret_cast<uint32_t *>(segs + kMaxSegs);  // [16]
     int *nseg = reinterpret_cast<int *>(scan + 16);
     volatile int *abort = nseg + 1;
@@ -381,7 +392,10 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             mbar_init(smem_u32(&raw_full[i]), 1);
             mbar_init(smem_u32(&raw_empty[i]), kConvThreads / 32);
         }
-        for (int i = 0; C::kCodes && i < C::kStages; ++i) mbar_init(smem_u32(&sc_full[i]), kConvThreads / 32);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&sc_full[i]), 1);
+            mbar_init(smem_u32(&sc_empty[i]), 8 + kConvThreads / 32);
+        }
         for (int t = 0; C::kCodes && t < 2; ++t) mbar_init(smem_u32(&q_ready[t]), kM);
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_empty), C::kMmaWarps);
@@ -597,154 +611,160 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
         return kMode != kAll && from < to;
     };
     bool ok = true;
-    if (C::kCodes && warp >= kConvWarp) {
-        // ------------------------------------------------ codes to fp16
-        // Tiles alternate: k, v of a step.  A thread takes one 16-byte piece of a row, then that of the row 128 *
-        // 16 / D further on.
-        constexpr int kPieces = D / 16, kRowsAt = kConvThreads / kPieces, kTimes = kKeys / kRowsAt;
-        const int at = tid - kConvWarp * 32, row0 = at / kPieces, piece = at % kPieces;
-        // the two 16-byte halves of a piece's values, in the order in which eight lanes that store together fall in
-        // different banks; a row's number mod 8, which the swizzle takes, is the same in all of a thread's pieces
-        const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
-        const uint32_t to0 = piece / 4 * (kKeys * 128) + row0 * 128 + ((c0 ^ (row0 & 7)) * 16);
-        const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) * 16);
-        static_assert(kRowsAt % 8 == 0 && kTimes % 4 == 0, "");
-        // scales: each of the four warps finds those of two steps of a batch, lanes 0-7 and 16-23 of k, the others of
-        // v.  The pages of the next batch (of the next segment's first, at the end of one) are asked for when a batch
-        // begins, its bytes a step later; nothing looks at either before it is needed.
-        const bool of_v = lane & 8;
-        int stage = 0, rs = 0, batch = 0;  // batch: its place in the ring
-        uint32_t phase = 0, r_phase = 0, sc_phase = 0;
+    if (!C::kCodes && warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (C::kCodes && warp == kScaleWarp) {
+        // ------------------------------------------------ scales
+        // Lanes 0-7: k's byte of keys 16 i .. 16 i + 15 of a step, lanes 8-15 v's.  Their page is asked for two steps ahead
+        // and they themselves one; nothing looks at either before it is needed.
+        const bool of_v = lane >= 8;
+        int slot = 0;
+        uint32_t phase = 0;
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
             const int ns = *nseg;
             u = cursor[3];
-            int page = -1, byte = -1;  // -1: none
-            auto key_at = [&](const Seg &g, int first) {  // of the batch that begins with step `first`, the lane's
-                return real(g, first + 2 * (warp - kConvWarp) + (lane >> 4)) * kKeys + (lane & 7) * 16;
-            };
-            auto keys_of = [&](const Seg &g) { return int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len)); };
-            auto find_page = [&](const Seg &g, int first) {
-                const int p = key_at(g, first);
-                page = -1;
-                if (first + 2 * (warp - kConvWarp) + (lane >> 4) >= g.step1 || p >= keys_of(g) || (p >= a.sinks && p + 16 <= g.low)) return;
-                page = ldp(a.table + (size_t)g.b * a.max_pages + (a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size));
-            };
-            auto find_byte = [&](const Seg &g, int first) {
-                byte = -1;
-                if (page < 0 || page >= a.n_pages) return;  // the load warp records pages that do not exist
-                const int p = key_at(g, first);
-                const int slot = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
-                const int block = a.block_shift >= 0 ? slot >> a.block_shift : slot / a.block;
-                byte = int(q8::ldp_byte((of_v ? a.v_scale : a.k_scale) + page * a.scale_page + g.h * a.scale_head + block));
-            };
-            if (ns > 0) {
-                find_page(segs[0], segs[0].step0);
-                find_byte(segs[0], segs[0].step0);
-            }
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
-                const int keys = keys_of(g);
-                uint32_t nan_at = 0;
-                for (int step = g.step0; step < g.step1 && ok; ++step) {
-                    const int in_batch = (step - g.step0) % kBatch;
-                    if (in_batch == 0) {
-                        const uint32_t nans = __ballot_sync(0xffffffffu, byte == 255);
-                        int own = byte == 255 ? -1 : byte, top = own;
-#pragma unroll
-                        for (int w = 1; w <= 4; w <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, w));
-                        if (own < 0) own = of_v ? max(top, 0) : 127;
-                        Scales &to = scales[batch];
-                        const int at = 2 * (warp - kConvWarp) + (lane >> 4);
-                        reinterpret_cast<uint8_t *>(&to.bytes[at])[lane & 15] = uint8_t(own);
-                        if ((lane & 15) == 0) to.nan[at] = nans >> (lane & 16) & 0xffff;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sc_full[batch]));
-                        ok = mbar_wait(smem_u32(&sc_full[batch]), sc_phase, wt);  // the other warps' too
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        nan_at = smem_u32(&to.nan[0]);
-                        if (++batch == C::kStages) {
-                            batch = 0;
-                            sc_phase ^= 1;
-                        }
+                const int keys = int(min((int64_t)g.kv_len - g.q_len + g.tok0 + tt2, (int64_t)g.kv_len));
+                const uint8_t *bytes = (of_v ? a.v_scale : a.k_scale) + g.h * a.scale_head;
+                auto page_of = [&](int step) {
+                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
+                    if (step >= g.step1 || lane >= 16 || p >= keys || (p >= a.sinks && p + 16 <= g.low)) return -1;
+                    return ldp(a.table + (size_t)g.b * a.max_pages + (a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size));
+                };
+                int byte;  // -1: none
+                auto byte_of = [&](int step, int page) {
+                    byte = -1;
+                    if (page < 0 || page >= a.n_pages) return;  // the load warps record pages that do not exist
+                    const int p = real(g, step) * kKeys + (lane & 7) * 16;
+                    const int at = a.page_shift >= 0 ? p & (a.page_size - 1) : p % a.page_size;
+                    const int block = a.block_shift >= 0 ? at >> a.block_shift : at / a.block;
+                    byte = int(q8::ldp_byte(bytes + page * a.scale_page + block));
+                };
+                byte_of(g.step0, page_of(g.step0));
+                int page = page_of(g.step0 + 1), unit = -1, most = 0;  // of v: O's unit, the largest byte so far
+                for (int step = g.step0; step < g.step1; ++step) {
+                    const uint32_t nan = __ballot_sync(0xffffffffu, byte == 255) & 0xffff;
+                    const int own = byte == 255 ? -1 : byte;
+                    const int top_k = __reduce_max_sync(0xffffffffu, lane < 8 ? own : -1);
+                    const int top_v = __reduce_max_sync(0xffffffffu, of_v ? own : -1);
+                    most = max(most, top_v);
+                    if (top_v > unit || (top_v >= 0 && top_v < unit - 8 && top_v >= most - 60)) unit = top_v;
+                    // 2^(own - unit) in fp16, 1 for a group without a scale
+                    const int d = own < 0 ? 0 : own - (of_v ? unit : top_k);
+                    const int rest = of_v ? min(max(d + 15, -100), 0) : 0, in = d - rest;
+                    const uint32_t f = in >= -14 ? uint32_t(15 + in) << 10 : in >= -24 ? 1u << (24 + in) : 0u;
+                    const uint32_t f_v = __shfl_down_sync(0xffffffffu, f, 8);
+                    const bool wide = __any_sync(0xffffffffu, rest != 0);
+                    ok = mbar_wait(smem_u32(&sc_empty[slot]), phase ^ 1, wt);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
                     }
-                    const bool last = step + kBatch - in_batch >= g.step1;  // of the segment's batches
-                    if (in_batch == 0) {
-                        page = -1;
-                        if (!last)
-                            find_page(g, step + kBatch);
-                        else if (k + 1 < ns)
-                            find_page(segs[k + 1], segs[k + 1].step0);
+                    Scales &to = scales[slot];
+                    if (lane < 8) to.mul[lane] = f | f_v << 16;
+                    if (of_v && lane < 16) to.rest[lane - 8] = int8_t(rest);
+                    if (lane == 0) {
+                        const int k0 = real(g, step) * kKeys;
+                        int from, end;
+                        const bool hide = hidden(g, k0, from, end);
+                        to.live = keys - k0;
+                        to.from = hide ? from : kKeys;
+                        to.to = hide ? end : 0;
+                        to.nan = nan;
+                        to.edge = hide || keys - k0 < kKeys || nan != 0;
+                        to.wide = wide;
+                        to.k = top_k < 0 ? 1.f : q8::scale_of(top_k);
+                        to.unit = max(unit, 0);
                     }
-                    const uint32_t nans = lds_u32(nan_at + 4 * in_batch);
-                    const int k0 = real(g, step) * kKeys, live = keys - k0;
-                    int from, to;
-                    const bool hide = hidden(g, k0, from, to), edge = live < kKeys || hide || nans != 0;
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt) && mbar_wait(smem_u32(&raw_full[rs]), r_phase, wt);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t src = smem_u32(raw + rs * C::kRaw) + at * 16;
-                        const uint32_t dst = smem_u32(smem + (2 + stage) * C::kTile);
-                        // four pieces at a time: their loads before the first conversion
-#pragma unroll
-                        for (int i0 = 0; i0 < kTimes; i0 += 4) {
-                            uint4 w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) w[i] = lds_v4(src + (i0 + i) * (kConvThreads * 16));
-                            if (edge) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int row = row0 + (i0 + i) * kRowsAt;
-                                    if (nans >> (row / 16 + 8 * kv) & 1) w[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    if (row >= live || (hide && row >= from && row < to)) w[i] = make_uint4(0, 0, 0, 0);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                                uint32_t y[8];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) q8::to_f16x4(x[e], y[2 * e], y[2 * e + 1]);
-                                const uint32_t to_row = dst + (i0 + i) * (kRowsAt * 128);
-                                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                                sts_v4(to_row + to0, half ? hi : lo);
-                                sts_v4(to_row + to1, half ? lo : hi);
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&kv_full[stage]));
-                            mbar_arrive(smem_u32(&raw_empty[rs]));
-                        }
-                        if (++stage == C::kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                        if (++rs == C::kRaws) {
-                            rs = 0;
-                            r_phase ^= 1;
-                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sc_full[slot]));
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        phase ^= 1;
                     }
-                    if (in_batch == 0) {
-                        if (!last)
-                            find_byte(g, step + kBatch);
-                        else if (k + 1 < ns)
-                            find_byte(segs[k + 1], segs[k + 1].step0);
-                    }
+                    byte_of(step + 1, page);
+                    page = page_of(step + 2);
                 }
             }
             ok = !meet_any<kThreads>(!ok);
         }
+    } else if (C::kCodes && warp >= kConvWarp) {
+        // ------------------------------------------------ codes to fp16
+        // Tiles alternate: k, v of a step.  A thread takes one 16-byte piece of a row, then that of the row 128 *
+        // 16 / D further on.
+        if constexpr (C::kCodes) {
+            constexpr int kPieces = D / 16, kRowsAt = kConvThreads / kPieces, kTimes = kKeys / kRowsAt;
+            static_assert(kRowsAt % 8 == 0 && kTimes % 4 == 0, "");
+            const int at = tid - kConvWarp * 32, row0 = at / kPieces, piece = at % kPieces;
+            // the two 16-byte halves of a piece's values in the order in which eight lanes that store together fall in
+            // different banks; a row's number mod 8, which the swizzle takes, is the same in all of a thread's pieces
+            const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
+            const uint32_t to0 = piece / 4 * (kKeys * 128) + row0 * 128 + ((c0 ^ (row0 & 7)) * 16);
+            const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) * 16);
+            int stage = 0, rs = 0, slot = 0;
+            uint32_t phase = 0, r_phase = 0, sc_phase = 0;
+            for (uint32_t u = u_begin; u < u_end && ok;) {
+                meet<kThreads>();
+                const int ns = *nseg;
+                u = cursor[3];
+                int tiles = 0;
+                for (int k = 0; k < ns; ++k) tiles += 2 * (segs[k].step1 - segs[k].step0);
+                for (int i = 0; i < tiles; ++i) {
+                    const uint32_t sc = smem_u32(&scales[slot]), kv = i & 1;
+                    if (!kv) ok = mbar_wait(smem_u32(&sc_full[slot]), sc_phase, wt);
+                    ok = ok && mbar_wait(smem_u32(&raw_full[rs]), r_phase, wt) && mbar_wait(smem_u32(&kv_empty[stage]), phase ^ 1, wt);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src = smem_u32(raw + rs * C::kRaw) + at * 16, dst = smem_u32(smem + (2 + stage) * C::kTile);
+                    const bool edge = lds_u32(sc + 40) != 0;
+                    // four pieces at a time: their loads before the first conversion
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kTimes; i0 += 4) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = lds_v4(src + (i0 + j) * (kConvThreads * 16));
+                        if (__builtin_expect(edge, 0)) {
+                            const uint32_t nan = lds_u32(sc + 44) >> (8 * kv);
+                            const int live = int(lds_u32(sc + 48)), from = int(lds_u32(sc + 52)), to = int(lds_u32(sc + 56));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int row = row0 + (i0 + j) * kRowsAt;
+                                if (nan >> (row / 16) & 1) w[j] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                if (row >= live || (row >= from && row < to)) w[j] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t mul = __byte_perm(lds_u32(sc + (row0 + (i0 + j) * kRowsAt) / 16 * 4), 0, kv ? 0x3232 : 0x1010);
+                            const uint32_t x[4] = {half ? w[j].z : w[j].x, half ? w[j].w : w[j].y, half ? w[j].x : w[j].z,
+                                                   half ? w[j].y : w[j].w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q8::to_f16x4(x[e], y[2 * e], y[2 * e + 1]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(mul));
+                            sts_v4(dst + to0 + (i0 + j) * (kRowsAt * 128), make_uint4(y[0], y[1], y[2], y[3]));
+                            sts_v4(dst + to1 + (i0 + j) * (kRowsAt * 128), make_uint4(y[4], y[5], y[6], y[7]));
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&kv_full[stage]));
+                        mbar_arrive(smem_u32(&raw_empty[rs]));
+                        if (kv) mbar_arrive(smem_u32(&sc_empty[slot]));
+                    }
+                    if (++stage == C::kStages) stage = 0, phase ^= 1;
+                    if (++rs == C::kRaws) rs = 0, r_phase ^= 1;
+                    if (kv && ++slot == kScaleSlots) slot = 0, sc_phase ^= 1;
+                }
+                ok = !meet_any<kThreads>(!ok);
+            }
+        }
     } else if (warp >= kMmaWarp) {
-        if constexpr (!C::kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         int stage = 0;                      // ring position (the load warp's: of the ring that TMA fills)
         uint32_t phase = 0, q_phase = 0;
         uint32_t p_phase = 0, oe_phase = 3, se_phase = 0;  // bit t: tile t
@@ -935,7 +955,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             }
             mbar_wait_drain(smem_u32(q_full), q_phase ^ 1, wt);
         }
-        if (warp == kMmaWarp || warp == kMma1Warp) {  // every MMA and every arrival of its commits is over before the CTA ends
+        if (warp == kMmaWarp || (!C::kCodes && warp == kMma1Warp)) {  // every MMA and every arrival of its commits is over before the CTA ends
             const uint32_t bar = smem_u32(&drain[warp == kMmaWarp ? 0 : 1]);
             mma_commit_warp(bar);
             mbar_wait_drain(bar, 0, wt);
@@ -943,7 +963,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
     } else {
         if constexpr (!C::kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         uint32_t s_phase = 0, o_phase = 0;
-        uint32_t q_phase = 0, sc_batch = 0;  // over an 8-bit cache: the segment's Q; batches of scales so far
+        uint32_t q_phase = 0;
+        uint32_t step_n = 0;  // over an 8-bit cache: steps done so far
         for (uint32_t u = u_begin; u < u_end && ok;) {
             meet<kThreads>();
             const int ns = *nseg;
@@ -958,9 +979,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
             const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
             for (int k = 0; k < ns && ok; ++k) {
                 const Seg g = segs[k];
-                const uint32_t sc_first = sc_batch;
+                const bool here = t < g.tiles;
                 if constexpr (C::kCodes) {  // also where the tile is empty: the next Q's parity would be the last one's
-                    sc_batch += uint32_t(g.step1 - g.step0 + kBatch - 1) / kBatch;
                     ok = mbar_wait(smem_u32(q_full), q_phase, wt);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -968,9 +988,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     }
                     q_phase ^= 1;
                 }
-                if (t >= g.tiles) continue;
+                if (!C::kCodes && !here) continue;
                 float row_sl2 = sl2;  // the factor of this row's scores
-                if constexpr (C::kCodes) {
+                if (C::kCodes && here) {
                     // this row of Q (or -Q, for a negative scale) in units of 2^-x with x from its largest exponent (an infinity counts as the largest
                     // number), to fp16, in its place
                     const uint32_t row = smem_u32(smem + t * C::kTile) + r * 128;
@@ -997,7 +1017,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     mbar_arrive(smem_u32(&q_ready[t]));
                     row_sl2 = sl2 * down;
                 }
-                int unit_v = -1, most_v = 0;  // O is in units of 2^(unit_v - 127 - kProbBits); the largest byte so far
+                int unit_v = 0;  // O is in units of 2^(unit_v - 127 - kProbBits)
                 const int j = g.tok0 + t * int(tt) + r / int(G);  // this row's token in the chunk
                 const bool live = r < int(G * tt) && j < g.q_len;
                 const int past = g.kv_len - g.q_len;
@@ -1005,6 +1025,19 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 const int seen_all = past + g.tok0 + t * int(tt) + 1;  // keys that every row of the tile sees
                 float m = kNegInf, l = 0.f;
                 for (int step = g.step0; step < g.step1; ++step) {
+                    if constexpr (C::kCodes) {
+                        const uint32_t slot = step_n % kScaleSlots;
+                        ok = mbar_wait(smem_u32(&sc_full[slot]), step_n / kScaleSlots & 1, wt);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        ++step_n;
+                        if (!here) {
+                            if (lane == 0) mbar_arrive(smem_u32(&sc_empty[slot]));
+                            continue;
+                        }
+                    }
                     ok = mbar_wait(smem_u32(&s_full[t]), s_phase, wt);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -1013,126 +1046,120 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     s_phase ^= 1;
                     tc_fence_after();
                     if constexpr (C::kCodes) {
-                        const uint32_t nth = uint32_t(step - g.step0), n = sc_first + nth / kBatch, at = n % C::kStages;
-                        ok = mbar_wait(smem_u32(&sc_full[at]), n / C::kStages & 1, wt);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint4 sc = lds_v4(smem_u32(&scales[at].bytes[nth % kBatch]));  // this step's scales
-                        // byte of the step's half h, and the factor of the scores of one of its groups
-                        auto byte_at = [](uint32_t lo, uint32_t hi, int h, int q) { return (h ? hi : lo) >> (q * 8) & 255; };
-                        auto factor = [&](int h, int q) {
-                            return fmaxf(row_sl2 * __uint_as_float(byte_at(sc.x, sc.y, h, q) << 23), 1.17549435e-38f);
-                        };
+                        const uint32_t slot = (step_n - 1) % kScaleSlots, sc = smem_u32(&scales[slot]);
+                        const float factor = fmaxf(row_sl2 * __uint_as_float(lds_u32(sc + 32)), 1.17549435e-38f);  // of the scores
+                        const int old_unit = unit_v;
+                        unit_v = int(lds_u32(sc + 36));
+                        const bool wide = lds_u32(sc + 60) != 0;
+                        const uint32_t rest[2] = {lds_u32(sc + 64), lds_u32(sc + 68)};
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sc_empty[slot]));
                         const int k0 = real(g, step) * kKeys;
-                        const int from = a.sinks - k0, to_w = max(seen - a.window, 0) - k0;
-                        const bool edge = k0 > seen_all - kKeys ||
-                                          (k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys);
-                        // 64 scores at a time, twice, in loops: with all of it unrolled instructions came too slowly (968 us
-                        // for 2048 tokens over 16384 keys)
-                        uint32_t x[64];
-                        auto take = [&](int h) {
-                            tmem_ld32_issue(ts + h * 64, x);
-                            tmem_ld32_issue(ts + h * 64 + 32, x + 32);
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                            for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
-                            if (__builtin_expect(edge, 0)) {  // keys past the row's last, and before its window
-                                const int last = seen - k0 - h * 64, f = from - h * 64, t = to_w - h * 64;
-#pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (i >= last || (i >= f && i < t)) x[i] = 0xff800000u;
-                            }
-                        };
-                        float mn = m;  // of the scores times their factors
+                        // what few steps need works on TMEM in loops, so that the others' instructions stay close together
+                        auto each = [&](uint32_t col, int n, auto f) {
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            take(h);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint32_t *y = x + 16 * q;
-                                float a0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
-                                float a1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
-#pragma unroll
-                                for (int i = 6; i < 14; i += 4) {
-                                    a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                                    a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
-                                }
-                                a0 = fmaxf(max3(a0, __uint_as_float(y[14]), __uint_as_float(y[15])), a1);
-                                mn = fmaxf(mn, __fmul_rn(factor(h, q), a0));
-                            }
-                        }
-                        if (C::kEarly && step > g.step0) {  // the step before is added to O, its P is free
-                            ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
-                            if (!__all_sync(0xffffffffu, ok)) {
-                                ok = false;
-                                break;
-                            }
-                            o_phase ^= 1;
-                            tc_fence_after();
-                        }
-                        int top_v = 0;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) top_v = max(top_v, int(byte_at(sc.z, sc.w, q / 4, q % 4)));
-                        const int old_unit = unit_v < 0 ? top_v : unit_v;
-                        most_v = max(most_v, top_v);
-                        if (top_v > unit_v || (top_v < unit_v - 8 && top_v >= most_v - 60)) unit_v = top_v;
-                        if (step == g.step0) {
-                            m = mn;
-                        } else if (__any_sync(0xffffffffu, live && mn - m > kLag) || unit_v != old_unit) {
-                            // as over a bf16 cache, and with the change of O's unit
-                            float f = mn == kNegInf ? 1.f : ex2(m - mn);
-                            m = mn;
-                            l *= f;
-                            f *= __uint_as_float(uint32_t(max(old_unit - unit_v, -126) + 127) << 23);
-#pragma unroll
-                            for (int i = 0; i < D; i += 16) {
-                                float o[16];
+                            for (int c = 0; c < n; c += 16) {
+                                float v[16];
                                 uint32_t w[16];
-                                tmem_ld16(to + i, o);
+                                tmem_ld16(col + c, v);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-                                tmem_st16(to + i, w);
+                                for (int e = 0; e < 16; ++e) w[e] = f(v[e], c + e);
+                                tmem_st16(col + c, w);
                             }
+                            tmem_st_wait();
+                        };
+                        if (k0 > seen_all - kKeys || (k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys)) {
+                            // keys past the row's last, and before its window
+                            const int last = seen - k0, from = a.sinks - k0, end = max(seen - a.window, 0) - k0;
+                            each(ts, 128, [&](float v, int i) { return i >= last || (i >= from && i < end) ? 0xff800000u : __float_as_uint(v); });
                         }
-                        // scores past 2^24 would pass fp16's largest number by m's rounding, which stays in x * factor - m:
-                        // far below that the product is rounded first, as it was in the maximum
-                        const float z = m == kNegInf ? 0.f : m;
-                        const bool far = fabsf(z) > 0x1p20f, any_far = __any_sync(0xffffffffu, far && live);
-                        // probabilities in fp16, times 2^kProbBits and what their group's scale of v is of O's unit (at
-                        // most 1); their sum, without either, stays in fp32
+                        // 64 scores at a time with the maximum so far, as if the halves were steps: the second's maximum may pass
+                        // the first's by 2^kLag before the first's probabilities are brought down too
+                        float sum_l = 0.f;
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            take(h);
+                            uint32_t x[64];
+                            auto load = [&]() {
+                                tmem_ld32_issue(ts + h * 64, x);
+                                tmem_ld32_issue(ts + h * 64 + 32, x + 32);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int d = kProbBits + max(int(byte_at(sc.z, sc.w, h, q)) - unit_v, -120);
-                                float kq = factor(h, q), zq = float(d) - z;
-                                if (__builtin_expect(any_far, 0)) {
+                                for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
+                            };
+                            load();
+                            float mx[4];
 #pragma unroll
-                                    for (int i = 16 * q; i < 16 * q + 16; ++i)
-                                        x[i] = far ? __float_as_uint(__fmul_rn(__uint_as_float(x[i]), kq) - m) : x[i];
-                                    kq = far ? 1.f : kq;
-                                    zq = far ? float(d) : zq;
+                            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+#pragma unroll
+                            for (int i = 8; i < 64; i += 8)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
+                            // m: of the scores times their factor
+                            const float mn = fmaxf(__fmul_rn(factor, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]))), m);
+                            if (C::kEarly && h == 0 && step > g.step0) {  // the step before is added to O, its P is free
+                                ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) break;
+                                o_phase ^= 1;
+                                tc_fence_after();
+                            }
+                            if (step == g.step0 && h == 0) {
+                                m = mn;
+                            } else if (__any_sync(0xffffffffu, live && mn - m > kLag) || (h == 0 && unit_v != old_unit)) {
+                                // as over a bf16 cache, and with the change of O's unit
+                                const float f = mn == kNegInf ? 1.f : ex2(m - mn);
+                                const float fu = h ? f : f * __uint_as_float(uint32_t(min(max(old_unit - unit_v, -126), 127) + 127) << 23);
+                                m = mn;
+                                l *= f;
+                                sum_l *= f;
+                                if (step > g.step0) each(to, D, [&](float v, int) { return __float_as_uint(v * fu); });
+                                if (h) {
+                                    tmem_st_wait();
+                                    each(tp, 32, [&](float v, int) {
+                                        const uint32_t u = __float_as_uint(v);
+                                        const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                                        uint32_t r;
+                                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(q.y * f), "f"(q.x * f));
+                                        return r;
+                                    });
                                 }
-                                const uint64_t kp = pair(kq, kq), zp = pair(zq, zq);
-                                uint64_t sum = 0;
+                            }
+                            // scores past 2^24 would pass fp16's largest number by m's rounding, which stays in x * factor -
+                            // m: far below that the product is rounded first, as it was in the maximum
+                            const float z = m == kNegInf ? 0.f : m;
+                            const bool far = fabsf(z) > 0x1p20f || wide;
+                            float apart = 0.f;  // the sum of the probabilities where some of them take part of v's scale
+                            if (wide || __any_sync(0xffffffffu, far && live)) {
+                                each(ts + h * 64, 64, [&](float v, int i) {
+                                    if (!far) return __float_as_uint(v);
+                                    v = __fmul_rn(v, factor) - z;
+                                    if (!wide) return __float_as_uint(v);
+                                    apart += ex2(v);
+                                    return __float_as_uint(v + float(int8_t(rest[h] >> (i / 16 * 8))));
+                                });
+                                load();
+                            }
+                            // probabilities in fp16, times 2^kProbBits; their sum, without that, stays in fp32
+                            const float kf = far ? 1.f : factor, zf = kProbBits - (far ? 0.f : z);
+                            const uint64_t kp = pair(kf, kf), zp = pair(zf, zf);
+                            uint64_t sum[2] = {0, 0};
 #pragma unroll
-                                for (int i = 16 * q; i < 16 * q + 16; i += 2) {
-                                    float p0, p1;
-                                    unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kp, zp), p0, p1);
-                                    p0 = ex2(p0);
-                                    p1 = ex2(p1);
-                                    sum = add2(sum, pair(p0, p1));
-                                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x[i / 2]) : "f"(p1), "f"(p0));
-                                }
-                                float s0, s1;
-                                unpair(sum, s0, s1);
-                                l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - d) << 23), l);
+                            for (int i = 0; i < 64; i += 2) {
+                                float p0, p1;
+                                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kp, zp), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair(p0, p1));
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x[i / 2]) : "f"(p1), "f"(p0));
                             }
                             tmem_st32(tp + 32 * h, x);  // heads of 128: over scores that this thread has read
+                            float s0, s1;
+                            unpair(add2(sum[0], sum[1]), s0, s1);
+                            sum_l += wide ? apart : (s0 + s1) * (1.f / (1 << kProbBits));
                         }
+                        if (!ok) break;
+                        l += sum_l;
                         if (C::kEarly) {
                             tc_fence_before();
                             mbar_arrive(smem_u32(&s_empty[t]));
@@ -1235,6 +1262,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     mbar_arrive(smem_u32(&p_full[t]));
                 }
                 if (!ok) break;
+                if (!here) continue;
                 ok = mbar_wait(smem_u32(&o_full[t]), o_phase, wt);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
@@ -1246,7 +1274,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 const int head = g.h * int(G) + r % int(G);
                 float inv = l == 0.f ? 0.f : 1.f / l, unit = 1.f;
                 if constexpr (C::kCodes) {
-                    unit = q8::scale_of(max(unit_v, 0)) * (1.f / (1 << kProbBits));
+                    unit = q8::scale_of(unit_v) * (1.f / (1 << kProbBits));
                     inv *= unit;
                 }
                 const float m_log2 = C::kCodes ? m : m * sl2;
@@ -1390,11 +1418,9 @@ bool set_smem_attr() {
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
         if (cudaFuncSetAttribute(chunk_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return false;
-        if constexpr (!C::kCodes) {
         // the softmax's registers come from the launch's: fewer, and the kernel would wait for them for ever
         cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, chunk_kernel<D, kMode>) != cudaSuccess || fa.numRegs < C::kLaunchRegs) return false;
-        }
+        if (cudaFuncGetAttributes(&fa, chunk_kernel<D, kMode>) != cudaSuccess || (!C::kCodes && fa.numRegs < C::kLaunchRegs)) return false;
         attr_set[dev] = true;
     }
     return true;
@@ -1459,7 +1485,7 @@ cudaError_t launch_chunk(const Args &a, const moe_attn_shape &s, char *ws, int s
     const uint64_t kd[4] = {D, (uint64_t)s.page_size, (uint64_t)s.n_kv_heads, (uint64_t)s.n_pages};
     const uint64_t ks[3] = {(uint64_t)a.token_stride * elem, s.n_kv_heads > 1 ? (uint64_t)a.head_stride * elem : row,
                             s.n_pages > 1 ? (uint64_t)a.page_stride * elem : row};
-    const uint32_t kb[4] = {mode == kQ8 ? (uint32_t)D : 64, (uint32_t)(s.page_size < kKeys ? s.page_size : kKeys), 1, 1};
+    const uint32_t kb[4] = {mode == kQ8 ? (uint32_t)D : 64, uint32_t(std::min(s.page_size, kKeys)), 1, 1};
     auto make_kv = mode == kQ8 ? make_map_bytes : make_map_nd;
     if (!make_map_nd(&mq, a.q, 3, qd, qs, qb) || !make_kv(&mk, a.k, 4, kd, ks, kb) || !make_kv(&mv, a.v, 4, kd, ks, kb))
         return cudaErrorInvalidValue;

@@ -100,7 +100,7 @@ struct Scales {
     uint32_t mul[8];
     float k;
     int unit;
-    uint32_t edge;   // whether any of the following matters to the codes:
+    uint32_t flags;  // bit 0: the next four matter; bits 1, 2: not all factors of k, of v are 1
     uint32_t nan;    // the groups whose byte says NaN, k's in bits 0-7, v's in 8-15
     int live;        // rows from here on hold no key that the item sees, nor do
     int from, to;    // these
@@ -656,6 +656,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     const uint32_t f = in >= -14 ? uint32_t(15 + in) << 10 : in >= -24 ? 1u << (24 + in) : 0u;
                     const uint32_t f_v = __shfl_down_sync(0xffffffffu, f, 8);
                     const bool wide = __any_sync(0xffffffffu, rest != 0);
+                    const uint32_t scaled = __ballot_sync(0xffffffffu, in != 0);
                     ok = mbar_wait(smem_u32(&sc_empty[slot]), phase ^ 1, wt);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                         to.from = hide ? from : kKeys;
                         to.to = hide ? end : 0;
                         to.nan = nan;
-                        to.edge = hide || keys - k0 < kKeys || nan != 0;
+                        to.flags = (hide || keys - k0 < kKeys || nan != 0 ? 1 : 0) | (scaled & 0xff ? 2 : 0) | (scaled & 0xff00 ? 4 : 0);
                         to.wide = wide;
                         to.k = top_k < 0 ? 1.f : q8::scale_of(top_k);
                         to.unit = max(unit, 0);
@@ -696,12 +697,13 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
         if constexpr (C::kCodes) {
             constexpr int kPieces = D / 16, kRowsAt = kConvThreads / kPieces, kTimes = kKeys / kRowsAt;
             static_assert(kRowsAt % 8 == 0 && kTimes % 4 == 0, "");
-            const int at = tid - kConvWarp * 32, row0 = at / kPieces, piece = at % kPieces;
-            // the two 16-byte halves of a piece's values in the order in which eight lanes that store together fall in
-            // different banks; a row's number mod 8, which the swizzle takes, is the same in all of a thread's pieces
-            const int half = piece / 4 & 1, c0 = 2 * (piece % 4) + half;
+            // Eight lanes that store together hold four pieces of one 64-element slab of two rows, whose places the swizzle
+            // makes the even and the odd ones; a row's number mod 8 is the same in all of a thread's pieces.
+            const int at = tid - kConvWarp * 32, piece = D == 128 ? (at & 3) | (at >> 1 & 4) : at & 3;
+            const int row0 = D == 128 ? at >> 4 << 1 | (at >> 2 & 1) : at >> 2, c0 = 2 * (piece % 4);
+            const uint32_t from = row0 * D + piece * 16;
             const uint32_t to0 = piece / 4 * (kKeys * 128) + row0 * 128 + ((c0 ^ (row0 & 7)) * 16);
-            const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) * 16);
+            const uint32_t to1 = piece / 4 * (kKeys * 128) + row0 * 128 + (((c0 + 1) ^ (row0 & 7)) * 16);
             int stage = 0, rs = 0, slot = 0;
             uint32_t phase = 0, r_phase = 0, sc_phase = 0;
             for (uint32_t u = u_begin; u < u_end && ok;) {
@@ -718,36 +720,44 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                         ok = false;
                         break;
                     }
-                    const uint32_t src = smem_u32(raw + rs * C::kRaw) + at * 16, dst = smem_u32(smem + (2 + stage) * C::kTile);
-                    const bool edge = lds_u32(sc + 40) != 0;
+                    const uint32_t src = smem_u32(raw + rs * C::kRaw) + from, dst = smem_u32(smem + (2 + stage) * C::kTile);
+                    const uint32_t flags = lds_u32(sc + 40);
                     // four pieces at a time: their loads before the first conversion
 #pragma unroll 1
                     for (int i0 = 0; i0 < kTimes; i0 += 4) {
-                        uint4 w[4];
+                        uint32_t w[4][4], y[4][8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = lds_v4(src + (i0 + j) * (kConvThreads * 16));
-                        if (__builtin_expect(edge, 0)) {
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 v = lds_v4(src + (i0 + j) * (kConvThreads * 16));
+                            w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+                        }
+                        if (__builtin_expect(flags & 1, 0)) {
                             const uint32_t nan = lds_u32(sc + 44) >> (8 * kv);
-                            const int live = int(lds_u32(sc + 48)), from = int(lds_u32(sc + 52)), to = int(lds_u32(sc + 56));
+                            const int live = int(lds_u32(sc + 48)), first = int(lds_u32(sc + 52)), end = int(lds_u32(sc + 56));
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int row = row0 + (i0 + j) * kRowsAt;
-                                if (nan >> (row / 16) & 1) w[j] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                if (row >= live || (row >= from && row < to)) w[j] = make_uint4(0, 0, 0, 0);
+                                const bool off = row >= live || (row >= first && row < end), bad = nan >> (row / 16) & 1;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) w[j][e] = off ? 0u : bad ? 0x7f7f7f7fu : w[j][e];
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q8::to_f16x4(w[j][e], y[j][2 * e], y[j][2 * e + 1]);
+                        if (flags & (2 << kv)) {  // not all of the tile's scales are its unit
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t mul = __byte_perm(lds_u32(sc + (row0 + (i0 + j) * kRowsAt) / 16 * 4), 0, kv ? 0x3232 : 0x1010);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[j][e]) : "r"(mul));
                             }
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t mul = __byte_perm(lds_u32(sc + (row0 + (i0 + j) * kRowsAt) / 16 * 4), 0, kv ? 0x3232 : 0x1010);
-                            const uint32_t x[4] = {half ? w[j].z : w[j].x, half ? w[j].w : w[j].y, half ? w[j].x : w[j].z,
-                                                   half ? w[j].y : w[j].w};
-                            uint32_t y[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) q8::to_f16x4(x[e], y[2 * e], y[2 * e + 1]);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(mul));
-                            sts_v4(dst + to0 + (i0 + j) * (kRowsAt * 128), make_uint4(y[0], y[1], y[2], y[3]));
-                            sts_v4(dst + to1 + (i0 + j) * (kRowsAt * 128), make_uint4(y[4], y[5], y[6], y[7]));
+                            sts_v4(dst + to0 + (i0 + j) * (kRowsAt * 128), make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]));
+                            sts_v4(dst + to1 + (i0 + j) * (kRowsAt * 128), make_uint4(y[j][4], y[j][5], y[j][6], y[j][7]));
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -1,11 +1,14 @@
 """One decoder layer with 4-bit weights, served from a paged cache: the attention half
 (moe_q4_linear, moe_rope_append, moe_paged_attention) around the MoE block
-(moe_forward_rmsnorm), for prompts in chunks and for single tokens.
+(moe_forward_rmsnorm), for prompts in chunks and for single tokens.  The cache holds 16-bit values or
+8-bit ones (moe_rope_append_q8, moe_paged_attention_q8), and the layer sees all keys or a window and a few first ones
+(moe_paged_attention_window).
 
     python examples/decoder_layer.py
 
-builds a layer with random weights, runs two requests' prompts in chunks of different
-lengths, then a few decode steps captured in a CUDA graph, and prints what a step takes.
+builds layers with random weights, runs two requests' prompts in chunks of different
+lengths, then a few decode steps captured in a CUDA graph, and prints what a step takes: with a 16-bit cache, then
+with an 8-bit one and a window.
 """
 import math
 import os
@@ -33,7 +36,9 @@ class DecoderLayer:
     """Weights, cache and workspaces of one layer; `step` runs it on new tokens of any of its sequences."""
 
     def __init__(self, hidden=2048, heads=32, kv_heads=4, dim=128, experts=128, top_k=8, inner=768, pages=256,
-                 page_size=16, max_seqs=8, max_pages=64, rope_base=1e6, seed=0):
+                 page_size=16, max_seqs=8, max_pages=64, rope_base=1e6, seed=0, scale_block=None, window=None, sinks=0):
+        """scale_block: None for a 16-bit cache, or the tokens that share a scale of an 8-bit one; window: None, or how many
+        keys a token sees up to its own, beside the sequence's first `sinks`."""
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.hidden, self.heads, self.kv_heads, self.dim = hidden, heads, kv_heads, dim
@@ -50,8 +55,12 @@ class DecoderLayer:
         self.gate, self.up, self.down = gate[0], up[0], down[0]
         self.expert_scales = gate[1], up[1], down[1]
         self.q4 = moe.MoEQ4(*(s.data_ptr() for s in self.expert_scales), (moe.MoEQ4._fields_[3][1])(*CODEBOOK))
-        cache = [torch.zeros(pages, kv_heads, page_size, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
-        self.cache = moe.make_kv_cache(*cache)
+        self.scale_block, self.window = scale_block, moe.make_attn_window(window, sinks) if window else None
+        zeros = lambda dtype, *s: [torch.zeros(pages, kv_heads, *s, dtype=dtype, device="cuda") for _ in range(2)]  # noqa: E731
+        if scale_block:
+            self.cache = moe.make_kv_cache_q8(*zeros(torch.float8_e4m3fn, page_size, dim), *zeros(torch.uint8, page_size // scale_block))
+        else:
+            self.cache = moe.make_kv_cache(*zeros(torch.bfloat16, page_size, dim))
         # the host's view of the cache: which pages a sequence holds, and how many keys
         self.free = list(range(pages))
         self.lengths = [0] * max_seqs
@@ -82,7 +91,8 @@ class DecoderLayer:
         p["moe"] = moe.make_shape(n, self.hidden, self.experts, self.top_k, self.inner, "bf16", "q4", q_block=GROUP)
         p["in"] = moe.make_q4_linear_shape(n, self.hidden, self.qkv_cols, q_block=GROUP)
         p["out"] = moe.make_q4_linear_shape(n, self.heads * self.dim, self.hidden, q_block=GROUP)
-        p["attn_ws"] = torch.zeros(moe.moe_attn_workspace_size(p["attn"]), dtype=torch.uint8, device="cuda")
+        size = moe.moe_attn_q8_workspace_size(p["attn"], self.scale_block) if self.scale_block else moe.moe_attn_workspace_size(p["attn"])
+        p["attn_ws"] = torch.zeros(size, dtype=torch.uint8, device="cuda")
         p["moe_ws"] = torch.zeros(moe.moe_workspace_size(p["moe"]), dtype=torch.uint8, device="cuda")
         buf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
         p["qkv"], p["o"] = buf(n, self.qkv_cols), buf(n, self.heads, self.dim)
@@ -96,8 +106,14 @@ class DecoderLayer:
         moe.moe_q4_linear(p["in"], xn, self.w_qkv, p["qkv"])
         q, k, v = p["qkv"].split([hq * d, hk * d, hk * d], 1)
         q, k, v = q.view(n, hq, d), k.view(n, hk, d), v.view(n, hk, d)
-        moe.moe_rope_append(p["attn"], self.rope, q, k, v, self.cache, p["batch"], q, workspace=p["attn_ws"])
-        moe.moe_paged_attention(p["attn"], q, self.cache, p["batch"], p["o"], workspace=p["attn_ws"])
+        append = moe.moe_rope_append_q8 if self.scale_block else moe.moe_rope_append
+        append(p["attn"], self.rope, q, k, v, self.cache, p["batch"], q, workspace=p["attn_ws"])
+        if self.scale_block:
+            moe.moe_paged_attention_q8(p["attn"], q, self.cache, p["batch"], p["o"], window=self.window, workspace=p["attn_ws"])
+        elif self.window:
+            moe.moe_paged_attention_window(p["attn"], q, self.cache, p["batch"], self.window, p["o"], workspace=p["attn_ws"])
+        else:
+            moe.moe_paged_attention(p["attn"], q, self.cache, p["batch"], p["o"], workspace=p["attn_ws"])
         moe.moe_q4_linear(p["out"], p["o"].view(n, hq * d), self.w_out, p["hs"], residual=x)
         moe.moe_forward_rmsnorm(p["moe"], p["hs"], self.norm2, self.eps, self.w_router, None, self.gate, self.up, self.down,
                                 self.q4, p["y"], workspace=p["moe_ws"])
@@ -110,16 +126,15 @@ class DecoderLayer:
         return linear or attn, moe.moe_read_device_error(p["moe_ws"])
 
 
-def main():
-    build.build()
-    layer = DecoderLayer()
+def serve(what, **kw):
+    layer = DecoderLayer(**kw)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     rows = lambda n: torch.randn(n, layer.hidden, generator=g, device="cuda").bfloat16()  # noqa: E731
     for chunks in ({0: 100, 1: 37}, {0: 60}):  # the prompts, the longer one in two chunks
         p = layer.plan(chunks)
         layer.step(p, rows(p["tokens"]))
-        print("chunks", chunks, "errors", layer.errors(p))
+        print(what, "chunks", chunks, "errors", layer.errors(p))
     p, x = layer.plan({0: 1, 1: 1}), rows(2)  # a decode step
     layer.step(p, x)
     side = torch.cuda.Stream()
@@ -134,7 +149,13 @@ def main():
         graph.replay()
     end.record()
     torch.cuda.synchronize()
-    print("decode step of 2 sequences: %.1f us, errors %s" % (start.elapsed_time(end) * 10, layer.errors(p)))
+    print("%s: decode step of 2 sequences %.1f us, errors %s" % (what, start.elapsed_time(end) * 10, layer.errors(p)))
+
+
+def main():
+    build.build()
+    serve("16-bit cache")
+    serve("8-bit cache, window of 64", scale_block=16, window=64, sinks=4)
 
 
 if __name__ == "__main__":

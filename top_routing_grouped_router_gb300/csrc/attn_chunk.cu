@@ -1033,6 +1033,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 const int past = g.kv_len - g.q_len;
                 const int seen = live ? max(past + j + 1, 0) : 0;
                 const int seen_all = past + g.tok0 + t * int(tt) + 1;  // keys that every row of the tile sees
+                // and that one of them sees (0 where none does; lengths go up to 2^31 - 1)
+                const int seen_most = int(max(min((int64_t)seen_all + tt - 1, (int64_t)g.kv_len), (int64_t)0));
                 float m = kNegInf, l = 0.f;
                 for (int step = g.step0; step < g.step1; ++step) {
                     if constexpr (C::kCodes) {
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             }
                             tmem_st_wait();
                         };
-                        if (k0 > seen_all - kKeys || (k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys)) {
+                        if (k0 > seen_all - kKeys || (k0 < seen_most - a.window && k0 > a.sinks - kKeys)) {
                             // keys past the row's last, and before its window
                             const int last = seen - k0, from = a.sinks - k0, end = max(seen - a.window, 0) - k0;
                             each(ts, 128, [&](float v, int i) { return i >= last || (i >= from && i < end) ? 0xff800000u : __float_as_uint(v); });
@@ -1193,7 +1195,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             for (int i = 0; i < 128; ++i)
                                 if (k0 + i >= seen) x[i] = 0xff800000u;
                         }
-                        if (kMode != kAll && k0 < max(seen_all + int(tt) - 1, 0) - a.window && k0 > a.sinks - kKeys) {
+                        if (kMode != kAll && k0 < seen_most - a.window && k0 > a.sinks - kKeys) {
                             // before the window of a row of the tile
                             const int from = a.sinks - k0, to = max(seen - a.window, 0) - k0;
 #pragma unroll

@@ -186,6 +186,22 @@ def test_q8_scales_that_differ_widely(name):
     check(bt, block=16)
 
 
+@pytest.mark.parametrize("name", ["few tokens", "chunk alone", "chunk over cache", "chunk dim 64", "chunk fp32"])
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+@pytest.mark.parametrize("power_of", [8, 18, 26])
+def test_q8_a_large_block_that_few_tokens_see(name, what, power_of):
+    # the last tokens' keys or values are far larger than all before: those who do not see them get what they see as
+    # exactly as ever, and those who do what dominates
+    bt = make_batch(*BATCH[name], seed=19)
+    for b, m in enumerate(bt.kv_len):
+        page, slot = int(bt.table[b, (m - 1) // bt.page]), (m - 1) % bt.page // 16 * 16
+        for c in (bt.k_cache,) * (what != "v") + (bt.v_cache,) * (what != "k"):
+            c[page, :, slot:slot + 16] = (c[page, :, slot:slot + 16].double() * 2.0 ** power_of).to(c.dtype)
+    if what == "k":
+        bt.q *= 0.125
+    check(bt, block=16)
+
+
 @pytest.mark.parametrize("name", ["decode ragged", "chunk ragged", "odd pages", "chunk fp32"])
 @pytest.mark.parametrize("block", [None, 8])
 def test_what_no_token_sees_is_not_read(name, block):

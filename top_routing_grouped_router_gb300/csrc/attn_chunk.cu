@@ -24,11 +24,11 @@
 //
 // Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
 // more warps turn them into the fp16 tiles that the tensor cores read.  All factors are powers of two.  A tile's
-// values are in units of the largest scale of k in the step, and for v of the largest so far (of a step's,
-// where that is smaller by more than 2^8, down to 2^-60 of it), which O is kept in too.  fp16 holds all codes
-// exactly down to scales 2^-15 of those; k of smaller ones to 2^-33 of the step's largest value, and of v's scales
-// probabilities take what is beyond 2^-15 (a loop that few steps need).  A row of Q becomes fp16 in units of
-// its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
+// values are in units of 2^-7 of the largest scale of k in the step, and for v of the largest so far (of a
+// step's, where that is smaller by more than 2^8, down to 2^-60 of it), which O is kept in too.  fp16 holds all
+// codes of scales down to 2^-22 of the largest exactly, and those of smaller ones to 2^-40 of the largest value;
+// of v's scales probabilities take what is beyond 2^-22 (a loop that few steps need).  A row of Q becomes
+// fp16 in units of its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
 // What was slower than that (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
 // of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542.
 //
@@ -108,6 +108,7 @@ struct Scales {
     int8_t rest[8];  // what its probabilities take of that, as an exponent
     int pad[2];
 };
+constexpr int kHeadroom = 7;  // 448 * 2^7 is within fp16
 constexpr int kScaleSlots = 8;
 constexpr int kProbBits = 7;  // probabilities times 2^7: with kLag at most 2^15 in fp16
 
@@ -650,8 +651,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     const int top_v = __reduce_max_sync(0xffffffffu, of_v ? own : -1);
                     most = max(most, top_v);
                     if (top_v > unit || (top_v >= 0 && top_v < unit - 8 && top_v >= most - 60)) unit = top_v;
-                    // 2^(own - unit) in fp16, 1 for a group without a scale
-                    const int d = own < 0 ? 0 : own - (of_v ? unit : top_k);
+                    // 2^(own - its unit) in fp16, 1 for a group without a scale
+                    const int unit_k = max(top_k - kHeadroom, 0), unit_v = max(unit - kHeadroom, 0);
+                    const int d = own < 0 ? 0 : own - (of_v ? unit_v : unit_k);
                     const int rest = of_v ? min(max(d + 15, -100), 0) : 0, in = d - rest;
                     const uint32_t f = in >= -14 ? uint32_t(15 + in) << 10 : in >= -24 ? 1u << (24 + in) : 0u;
                     const uint32_t f_v = __shfl_down_sync(0xffffffffu, f, 8);
@@ -675,8 +677,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                         to.nan = nan;
                         to.flags = (hide || keys - k0 < kKeys || nan != 0 ? 1 : 0) | (scaled & 0xff ? 2 : 0) | (scaled & 0xff00 ? 4 : 0);
                         to.wide = wide;
-                        to.k = top_k < 0 ? 1.f : q8::scale_of(top_k);
-                        to.unit = max(unit, 0);
+                        to.k = top_k < 0 ? 1.f : q8::scale_of(unit_k);
+                        to.unit = unit_v;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sc_full[slot]));
@@ -1033,8 +1035,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                 const int past = g.kv_len - g.q_len;
                 const int seen = live ? max(past + j + 1, 0) : 0;
                 const int seen_all = past + g.tok0 + t * int(tt) + 1;  // keys that every row of the tile sees
-                // and that one of them sees (0 where none does; lengths go up to 2^31 - 1)
-                const int seen_most = int(max(min((int64_t)seen_all + tt - 1, (int64_t)g.kv_len), (int64_t)0));
+                // the first key of the window of one of them (at most: lengths go up to 2^31 - 1)
+                const int low_most = int(max(min((int64_t)seen_all + tt - 1, (int64_t)g.kv_len), (int64_t)0)) - a.window;
                 float m = kNegInf, l = 0.f;
                 for (int step = g.step0; step < g.step1; ++step) {
                     if constexpr (C::kCodes) {
@@ -1080,7 +1082,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             }
                             tmem_st_wait();
                         };
-                        if (k0 > seen_all - kKeys || (k0 < seen_most - a.window && k0 > a.sinks - kKeys)) {
+                        if (k0 > seen_all - kKeys || (k0 < low_most && k0 > a.sinks - kKeys)) {
                             // keys past the row's last, and before its window
                             const int last = seen - k0, from = a.sinks - k0, end = max(seen - a.window, 0) - k0;
                             each(ts, 128, [&](float v, int i) { return i >= last || (i >= from && i < end) ? 0xff800000u : __float_as_uint(v); });
@@ -1195,7 +1197,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             for (int i = 0; i < 128; ++i)
                                 if (k0 + i >= seen) x[i] = 0xff800000u;
                         }
-                        if (kMode != kAll && k0 < seen_most - a.window && k0 > a.sinks - kKeys) {
+                        if (kMode != kAll && k0 < low_most && k0 > a.sinks - kKeys) {
                             // before the window of a row of the tile
                             const int from = a.sinks - k0, to = max(seen - a.window, 0) - k0;
 #pragma unroll

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             u = item + step1;
             more = u < u_end;
         }
-        const int rows = min(s.q_len * int(G), kRows), past = s.kv_len - s.q_len;
+        const int rows = min(s.q_len * int(G), kHalf ? kRows / 2 : kRows), past = s.kv_len - s.q_len;
 
         // the warp's keys: steps step0 + warp, + kWarps, ...  The cache offset of lane r's key row (r <
         // 16), or of the first row where a step lies within a page, is found a step before the copy.

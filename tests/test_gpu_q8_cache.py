@@ -326,6 +326,42 @@ def test_q8_far_pages(q_len):
     assert ((d.out.cpu().double() - out).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("name", ["decode ragged", "decode line 200", "few tokens cut short", "chunk ragged", "chunk cut short", "chunk dim 64",
+                                  "odd pages"])
+@pytest.mark.parametrize("block,window", [(None, 60), (16, 60), (16, None), (8, 60)])
+def test_without_the_sums_the_outputs_are_the_same(name, block, window):
+    bt = make_batch(*BATCH[name], seed=5)
+    d = Dev(bt, math.gcd(block, bt.page) if block else None)
+    d.attend(0.1, window, 4)
+    torch.cuda.synchronize()
+    first = d.out.clone()
+    d.out.fill_(7.0)
+    d.lse.fill_(7.0)
+    d.attend(0.1, window, 4, lse=False)
+    assert d.errors() == 0
+    assert torch.equal(d.out, first) and (d.lse == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block,window", [(None, 20), (16, 20), (16, None)])
+@pytest.mark.parametrize("longest", [60, 900])
+def test_more_sequences_than_a_scan_and_a_list_hold(dim, block, window, longest):
+    # rounds of 128, 384 and 512 sequences; up to 512 keys no item is cut, and a CTA has dozens of them
+    ql = [(i * 7) % 4 for i in range(1300)]
+    kl = [n + (i * 13) % 50 for i, n in enumerate(ql)]
+    ql[700], kl[700], ql[1299], kl[1299] = 40, 50, 21, longest
+    check(make_batch("bf16", 8, 4, dim, 16, ql, kl, seed=6), block, window, 3)
+
+
+@pytest.mark.parametrize("ql,kl", [([1, 1, 1], [100, 90, 70]), ([40, 25, 30], [100, 90, 94])])
+@pytest.mark.parametrize("block,window", [(None, 50), (16, None), (8, 50)])
+def test_sequences_that_share_pages(ql, kl, block, window):
+    bt = make_batch("bf16", 8, 2, 128, 16, ql, kl, seed=8)
+    bt.table[1, :4] = bt.table[0, :4]  # whole pages of a common prefix
+    bt.table[2] = bt.table[0]
+    check(bt, block, window, 5)
+
+
 # ------------------------------------------------------------------------------- rotary append
 
 APPEND = {
@@ -512,6 +548,25 @@ def test_append_in_place_and_in_a_graph():
     a.run(q_out=q)
     torch.cuda.synchronize()
     assert torch.equal(q[:a.bt.tokens], out[:a.bt.tokens])
+
+
+def test_append_to_far_pages():
+    # byte offsets past 2^32 in the cache
+    a = Append(APPEND["decode page scales"], seed=4)
+    before, d = a.state(), a.d
+    n = (1 << 32) // (2 * 64 * 128) + 8
+    at = n - a.bt.pages
+    big = [torch.empty(n, *c.shape[1:], dtype=torch.uint8, device="cuda") for c in (d.k, d.v, d.ks, d.vs)]
+    for to, c in zip(big, (d.k, d.v, d.ks, d.vs)):
+        to[at:] = c
+    d.shape.n_pages = n
+    d.cache = moe.make_kv_cache_q8(*big)
+    d.table += at
+    a.run()
+    assert d.errors() == 0
+    for to, c in zip((d.k, d.v, d.ks, d.vs), big):
+        to.copy_(c[at:])
+    a.check(before)
 
 
 @pytest.mark.parametrize("what", ["negative length", "length past the table", "idle length past the table", "long chunk",

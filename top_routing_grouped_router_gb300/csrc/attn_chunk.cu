@@ -1368,7 +1368,10 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
         float4 v[kFly][E];
 #pragma unroll
         for (int p = 0; p < kFly; ++p) {
-            const int i = min(p0 + p, n - 1);
+            pm[p] = kNegInf;
+            pl[p] = 0.f;
+            if (p0 + p >= n) continue;
+            const int i = p0 + p;
             const size_t slot = (size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0);
             asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(pm[p]), "=f"(pl[p]) : "l"(c.part_ml + slot * 2 * kM + row));
 #pragma unroll
@@ -1385,7 +1388,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
         for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * f0, acc[e].y * f0, acc[e].z * f0, acc[e].w * f0);
 #pragma unroll
         for (int p = 0; p < kFly; ++p) {
-            if (p0 + p >= n || pl[p] == 0.f) continue;  // read again past the last, or no key seen; a NaN sum stays
+            if (pl[p] == 0.f) continue;  // past the last, or no key seen; a NaN sum stays
             const float f = ex2(pm[p] - mn);
             l = fmaf(f, pl[p], l);
 #pragma unroll

@@ -20,7 +20,9 @@
 // terms all the same, since the scale of a row cancels.
 //
 // With a window an item goes over the steps that hold a key which one of its tokens sees: the first
-// keys' steps, then, `skip` steps further on, those from its first token's window on.
+// keys' steps, then, `skip` steps further on, those from its first token's window on.  A window of 4096 over 16384
+// keys, 2048 tokens, 32 heads: 129 us (products alone 73), 116 of them this kernel at the chain's rate, which has 1.25
+// steps more than the window in each item and starts and ends 2.7 items a CTA; 13 are the join.
 //
 // Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
 // more warps turn them into the fp16 tiles that the tensor cores read.  All factors are powers of two.  A tile's
@@ -29,8 +31,13 @@
 // codes of scales down to 2^-22 of the largest exactly, and those of smaller ones to 2^-40 of the largest value;
 // of v's scales probabilities take what is beyond 2^-22 (a loop that few steps need).  A row of Q becomes
 // fp16 in units of its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
-// What was slower than that (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
-// of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542.
+// 2048 tokens over 16384 keys, 32 heads: 427 us in a row of calls (1210 TFLOP/s), 411 of them this kernel.  The bound is the same
+// chain: a tile's softmax takes 2450 cycles, since the launch's 512 threads leave it 128 registers and it takes its
+// scores in two halves, each with its own wait for TMEM; with the tile's products (1024) and barriers that makes
+// about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it, on half of the issue slots that are left.
+// What was slower (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
+// of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542; loops over TMEM
+// unrolled, whose instructions then miss their cache, 536; half of P multiplied during the second half's softmax, 470.
 //
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a
@@ -1344,7 +1351,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
 // Joins the parts of the items that were cut.  Block (cta, y): the item that starts in the share of
 // `cta` and goes on, rows [16 y, 16 y + 16) of its 256; 16 threads a row.  Four parts are requested
 // together, their maxima and sums with their outputs (one warp a row, part by part, took 19 us
-// for a mixed batch's 150 cut items).
+// for a mixed batch's 150 cut items).  After a chunk of 2048 tokens it takes 16 us, for 40 MB of parts that one
+// kernel writes and the other reads; joining two parts in the first kernel, by the warp that comes last, took as long.
 constexpr int kJoinThreads = kJoinRows * 16;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ Ctx c) {

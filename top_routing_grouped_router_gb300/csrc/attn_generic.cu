@@ -6,6 +6,9 @@
 //
 // With a window a block goes over the keys that its tokens see only: the first ones, then those from
 // its first token's window on, as one range of places.
+//
+// Over an 8-bit cache a row's codes become fp32 values as a tile is staged, with their block's power of two.  Six
+// sequences of 1 to 5 tokens, fp32, that see up to 700 keys: 16.7 us, most of it two launches and the latency between them.
 #include "q8.cuh"
 
 namespace moe {

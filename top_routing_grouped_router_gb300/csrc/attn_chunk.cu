@@ -31,7 +31,7 @@
 // codes of scales down to 2^-22 of the largest exactly, and those of smaller ones to 2^-40 of the largest value;
 // of v's scales probabilities take what is beyond 2^-22 (a loop that few steps need).  A row of Q becomes
 // fp16 in units of its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
-// 2048 tokens over 16384 keys, 32 heads: 427 us in a row of calls (1210 TFLOP/s), 411 of them this kernel.  The bound is the same
+// 2048 tokens over 16384 keys, 32 heads: 429 us in a row of calls (1200 TFLOP/s), 413 of them this kernel.  The bound is the same
 // chain: a tile's softmax takes 2450 cycles, since the launch's 512 threads leave it 128 registers and it takes its
 // scores in two halves, each with its own wait for TMEM; with the tile's products (1024) and barriers that makes
 // about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it, on half of the issue slots that are left.
@@ -1089,11 +1089,13 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             }
                             tmem_st_wait();
                         };
-                        if (k0 > seen_all - kKeys || (k0 < low_most && k0 > a.sinks - kKeys)) {
-                            // keys past the row's last, and before its window
-                            const int last = seen - k0, from = a.sinks - k0, end = max(seen - a.window, 0) - k0;
-                            each(ts, 128, [&](float v, int i) { return i >= last || (i >= from && i < end) ? 0xff800000u : __float_as_uint(v); });
-                        }
+                        const bool edge = k0 > seen_all - kKeys || (k0 < low_most && k0 > a.sinks - kKeys);
+                        // keys past the row's last, and before its window: with heads of 64, whose items have few steps
+                        // and many of them at an edge, in registers (mixed batch with a window 53 us, in loops 54.7; heads of
+                        // 128, 2048 tokens over 16384 keys: 461, in loops 428)
+                        const int last = seen - k0, from = a.sinks - k0, end = max(seen - a.window, 0) - k0;
+                        auto off = [&](int i) { return i >= last || (i >= from && i < end); };
+                        if (D == 128 && edge) each(ts, 128, [&](float v, int i) { return off(i) ? 0xff800000u : __float_as_uint(v); });
                         // 64 scores at a time with the maximum so far, as if the halves were steps: the second's maximum may pass
                         // the first's by 2^kLag before the first's probabilities are brought down too
                         float sum_l = 0.f;
@@ -1108,6 +1110,11 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                                 for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
                             };
                             load();
+                            if (D == 64 && edge) {
+#pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if (off(h * 64 + i)) x[i] = 0xff800000u;
+                            }
                             float mx[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
@@ -1153,6 +1160,7 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             float apart = 0.f;  // the sum of the probabilities where some of them take part of v's scale
                             if (wide || __any_sync(0xffffffffu, far && live)) {
                                 each(ts + h * 64, 64, [&](float v, int i) {
+                                    if (D == 64 && off(h * 64 + i)) return 0xff800000u;
                                     if (!far) return __float_as_uint(v);
                                     v = __fmul_rn(v, factor) - z;
                                     if (!wide) return __float_as_uint(v);

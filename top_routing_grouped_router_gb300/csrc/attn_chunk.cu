@@ -34,12 +34,12 @@
 // 2048 tokens over 16384 keys, 32 heads: 429 us in a row of calls (1200 TFLOP/s), 413 of them this kernel.  The bound is the same
 // chain: a tile's softmax takes 2450 cycles, since the launch's 512 threads leave it 128 registers and it takes its
 // scores in two halves, each with its own wait for TMEM; with the tile's products (1024) and barriers that makes
-// about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it.  Shared memory is the next bound: products,
-// codes and fp16 tiles move 320 KB a step, 2500 cycles at 128 bytes each.
+// about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it.  No unit is full: issue
+// slots 52 %, ALU 41, shared memory 39, tensor pipe 52.
 // What was slower (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
 // of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542; loops over TMEM
 // unrolled, whose instructions then miss their cache, 536; half of P multiplied during the second half's softmax, 470; the next
-// step's scores of 64 keys before P V, in the columns that P leaves free, 548 (products of 64 keys read Q twice as often).
+// step's scores of 64 keys before P V, in the columns that P leaves free, 548.
 //
 // K and V tiles come by TMA through the block table, one box a page.  All items are laid end
 // to end as steps of 128 keys and each CTA takes an equal share of that line; items cut by a

@@ -353,6 +353,41 @@ def test_more_sequences_than_a_scan_and_a_list_hold(dim, block, window, longest)
     check(make_batch("bf16", 8, 4, dim, 16, ql, kl, seed=6), block, window, 3)
 
 
+FEW_PAIRS = {
+    # up to eight (sequence, key head) pairs with many keys: heads, kv_heads, dim, page, chunk lengths, cache lengths
+    "one pair": (8, 1, 128, 16, [1], [5003]),
+    "one pair dim 64": (5, 1, 64, 64, [3], [2000]),
+    "wide group": (32, 2, 128, 16, [1], [3001]),
+    "four pairs": (16, 2, 128, 32, [1, 2], [2500, 1900]),
+    "most empty": (8, 1, 64, 16, [1, 0, 1, 2], [4000, 70, 5, 1]),
+    "eight pairs": (32, 4, 128, 16, [1, 2], [6000, 4001]),
+    "cut short": (8, 4, 64, 16, [4], [2]),
+}
+
+
+@pytest.mark.parametrize("name", list(FEW_PAIRS))
+@pytest.mark.parametrize("block", [None, 16, 32])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (700, 3), (1500, 900), (3300, 0), (600, 0)])
+def test_few_pairs_with_many_keys(name, block, window, sinks):
+    heads, kvh, dim, page, ql, kl = FEW_PAIRS[name]
+    if block is not None and page % block or block is None and window is None:
+        pytest.skip("no such case")
+    bt = make_batch("bf16", heads, kvh, dim, page, ql, kl, seed=12)
+    if name == "cut short":  # a table for many more keys
+        bt.table = torch.nn.functional.pad(bt.table, (0, 200), value=-7)
+    d = check(bt, block, window, sinks)
+    first = d.out.clone()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        for _ in range(3):  # the next begins while the one before ends
+            d.attend(dim ** -0.5, window, sinks, stream=side)
+    d.out.fill_(7.0)
+    g.replay()
+    assert d.errors() == 0
+    assert torch.equal(d.out, first)
+
+
 @pytest.mark.parametrize("ql,kl", [([1, 1, 1], [100, 90, 70]), ([40, 25, 30], [100, 90, 94])])
 @pytest.mark.parametrize("block,window", [(None, 50), (16, None), (8, 50)])
 def test_sequences_that_share_pages(ql, kl, block, window):

@@ -15,7 +15,7 @@
 // kPiece steps' time).  A pair that a CTA holds whole is written out at once; the others leave (max, sum, unnormalised O) in the workspace, and the CTAs that
 // arrive last join them in the order of the keys, so the bits do not depend on timing.
 //
-// Where the host sees that the pairs are few and no sequence can be long, a cluster of eight, four
+// Where the host sees that the pairs are few and no sequence can be long, a cluster of (sixteen,) eight, four
 // or two CTAs (or one CTA) takes each pair: nothing is scheduled on the device, and the parts meet
 // in shared memory (8 sequences of 150 to 1100 keys, 4 key heads: 7.5 us, 9.3 through the
 // workspace; one sequence of 2000 keys 7.1 us, 9.3).
@@ -1075,8 +1075,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 // Where a window bounds the keys most pairs have as many, and a warp may have more steps: 12, and 40 if
 // there are more than 16 pairs (256 pairs, window 2048: 46.9 us with clusters of one, 51.3 scheduled; 64 pairs, 9000:
 // clusters of four 50.4, 55.0; but 4 pairs, 9000: 18.4, 16.1; over an 8-bit cache 27.7, 31.1; 28.8, 36.4; 12.4, 11.7).
+// With a window or over an 8-bit cache up to eight pairs may have clusters of sixteen, which few parts of the chip hold
+// two of (16 pairs, window 300: 10.8 us, clusters of eight 5.4): 4 pairs, window 300: 5.2, 4.8; 1000: 5.5, 6.1; 4097: 8.5, 11.3;
+// 12000: 14.3, scheduled 16.7 (one pair, 14000: 15.6, 14.5); 8 pairs, 2500: 9.4, 8.8; 4097: 10.9, 11.5; 12000: 16.4, 17.4 (8 bits: 4.8, 4.7; 5.0, 5.5;
+// 6.8, 8.4; 10.3, 12.1; 7.2, 7.1; 8.0, 8.5; 12.1, 13.3).
+template <Mode kMode>
 int cluster_of(const moe_attn_shape &s, int64_t keys) {
     const int64_t pairs = (int64_t)s.n_seqs * s.n_kv_heads;
+    if (kMode != kAll && pairs <= 8 && keys > (pairs <= 4 ? 600 : 3200)) {
+        const int steps = keys >= (int64_t)s.max_pages * s.page_size ? 8 : 12;
+        if (keys <= steps * kWarps * kStep * 16) return 16;
+    }
     const int steps = keys >= (int64_t)s.max_pages * s.page_size ? 8 : pairs > 16 ? 40 : 12;
     const int sizes[4] = {8, 4, 2, 1}, most[4] = {32, 72, 152, 304};
     for (int i = 0; i < 4; ++i)
@@ -1093,6 +1102,11 @@ cudaError_t launch_typed(const Args &a, const moe_attn_shape &s, char *hdr, char
         const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kCluster, kMode, kHalf>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (Cfg<D, kMode>::kSmem));
         if (e != cudaSuccess) return e;
+        if (kCluster > 8) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(decode_kernel<D, kCluster, kMode, kHalf>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
         attr_set[dev] = true;
     }
     float *o = reinterpret_cast<float *>(ws);
@@ -1125,7 +1139,11 @@ cudaError_t launch(const Args &a, const moe_attn_shape &s, char *hdr, char *ws, 
     const int grid = sms * kCtasPerSm < kMaxGrid ? sms * kCtasPerSm : kMaxGrid;
     int64_t keys = (int64_t)s.max_pages * s.page_size;  // of a pair, at most: with a window its steps' only
     if (kMode != kAll) keys = std::min(keys, (int64_t)a.window + a.sinks + s.max_q + 2 * kStep);
-    switch (cluster_of(s, keys)) {
+    const int cluster = cluster_of<kMode>(s, keys);
+    if constexpr (kMode != kAll) {
+        if (cluster == 16) return launch_dim<16, kMode, kHalf>(a, s, hdr, ws, grid, st);
+    }
+    switch (cluster) {
     case 8: return launch_dim<8, kMode, kHalf>(a, s, hdr, ws, grid, st);
     case 4: return launch_dim<4, kMode, kHalf>(a, s, hdr, ws, grid, st);
     case 2: return launch_dim<2, kMode, kHalf>(a, s, hdr, ws, grid, st);

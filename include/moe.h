@@ -656,7 +656,9 @@ MOE_API int moe_rope_append_q8(const moe_attn_shape *shape, const moe_rope *rope
 
 /*
  * moe_paged_attention over an 8-bit cache, with a window or (NULL) over all keys.
- * dtype is that of q and out; the cache's values enter the products unrounded.
+ * dtype is that of q and out; the cache's values enter the products unrounded (bf16: but for
+ * bits below 2^-40 of the largest value within 128 keys, where scales differ that much, and bits of
+ * q below 2^-38 of a row's largest element).
  * The other arguments, and what is read, are those of moe_paged_attention and
  * moe_paged_attention_window.
  */

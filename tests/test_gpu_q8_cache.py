@@ -353,6 +353,42 @@ def test_more_sequences_than_a_scan_and_a_list_hold(dim, block, window, longest)
     check(make_batch("bf16", 8, 4, dim, 16, ql, kl, seed=6), block, window, 3)
 
 
+@pytest.mark.parametrize("block", [None, 16])
+def test_graphs_of_different_kernels_share_a_workspace(block):
+    # one after another on a stream: what one leaves in the workspace does not disturb the next
+    names = ["decode line 200", "chunk over cache", "decode ragged", "chunk many long", "head size 16", "chunk dim 64"]
+    runs = [Dev(make_batch(*BATCH[n], seed=i), block) for i, n in enumerate(names)]
+    ws = torch.zeros(max(d.ws.numel() for d in runs), dtype=torch.uint8, device="cuda")
+    graphs, first, side = [], [], torch.cuda.Stream()
+    for d in runs:
+        d.attend(0.1, 200, 4)
+        assert d.errors() == 0
+        first.append((d.out.clone(), d.lse.clone()))
+        d.ws = ws
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            d.attend(0.1, 200, 4, stream=side)
+        graphs.append(g)
+    for order in ([0, 1, 2, 3, 4, 5], [5, 3, 1, 0, 2, 4], [1, 1, 0, 0, 3, 2, 5, 4]):
+        for d in runs:
+            d.out.fill_(7.0)
+            d.lse.fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+        assert runs[0].errors() == 0
+        for d, (out, lse) in zip(runs, first):
+            assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
+
+
+@pytest.mark.parametrize("q_len", [1, 30])
+@pytest.mark.parametrize("block,window", [(None, 40), (16, None)])
+def test_a_page_that_a_sequence_lists_twice(q_len, block, window):
+    bt = make_batch("bf16", 8, 2, 64, 16, [q_len], [96], seed=3)
+    bt.table[0, 3] = bt.table[0, 1]
+    bt.table[0, 4] = bt.table[0, 1]
+    check(bt, block, window, 2)
+
+
 FEW_PAIRS = {
     # up to eight (sequence, key head) pairs with many keys: heads, kv_heads, dim, page, chunk lengths, cache lengths
     "one pair": (8, 1, 128, 16, [1], [5003]),

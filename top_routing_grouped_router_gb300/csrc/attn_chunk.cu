@@ -408,7 +408,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
         }
         for (int t = 0; C::kCodes && t < 2; ++t) mbar_init(smem_u32(&q_ready[t]), kM);
         mbar_init(smem_u32(q_full), 1);
-        mbar_init(smem_u32(q_empty), C::kMmaWarps);
+        // over an 8-bit cache also the eight softmax warps, which wait for Q by its parity even where their tile is empty: a
+        // Q that came before one of them had seen the last would look like the one before
+        mbar_init(smem_u32(q_empty), C::kMmaWarps + (C::kCodes ? 8 : 0));
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&s_full[t]), 1);
             mbar_init(smem_u32(&s_empty[t]), kM);
@@ -1008,6 +1010,8 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                         break;
                     }
                     q_phase ^= 1;
+                    // a present tile's Q stays until its scores are found: that is the MMA warp's arrival
+                    if (lane == 0) mbar_arrive(smem_u32(q_empty));
                 }
                 if (!C::kCodes && !here) continue;
                 float row_sl2 = sl2;  // the factor of this row's scores

@@ -26,12 +26,13 @@
 //
 // Over an 8-bit cache (kQ8) TMA brings codes, half as many bytes, into a ring of their own, and four
 // more warps turn them into the fp16 tiles that the tensor cores read.  All factors are powers of two.  A tile's
-// values are in units of 2^-7 of the largest scale of k in the step, and for v of the largest so far (of a
-// step's, where that is smaller by more than 2^8, down to 2^-60 of it), which O is kept in too.  fp16 holds all
+// values are in units of the largest scale of k in the step, and for v of the largest so far (of a
+// step's, where that is smaller by more than 2^8, down to 2^-60 of it), which O is kept in too: codes of that scale need no
+// factor (434 us with one for each, 424).  Where a scale lies below 2^-15 of the largest the unit is 2^-7 of that: fp16 then holds all
 // codes of scales down to 2^-22 of the largest exactly, and those of smaller ones to 2^-40 of the largest value;
 // of v's scales probabilities take what is beyond 2^-22 (a loop that few steps need).  A row of Q becomes
 // fp16 in units of its own that bring its largest element to 2^14; probabilities are fp16 times 2^7.
-// 2048 tokens over 16384 keys, 32 heads: 429 us in a row of calls (1200 TFLOP/s), 413 of them this kernel.  The bound is the same
+// 2048 tokens over 16384 keys, 32 heads: 424 us in a row of calls (1215 TFLOP/s), the join among them.  The bound is the same
 // chain: a tile's softmax takes 2450 cycles, since the launch's 512 threads leave it 128 registers and it takes its
 // scores in two halves, each with its own wait for TMEM; with the tile's products (1024) and barriers that makes
 // about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it.  No unit is full: issue
@@ -118,6 +119,7 @@ struct Scales {
     int pad[2];
 };
 constexpr int kHeadroom = 7;  // 448 * 2^7 is within fp16
+constexpr int kDeep = 15;     // the smallest code, 2^-9, times 2^-15 is fp16's smallest number
 constexpr int kScaleSlots = 8;
 constexpr int kProbBits = 7;  // probabilities times 2^7: with kLag at most 2^15 in fp16
 
@@ -654,16 +656,22 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                     byte = int(q8::ldp_byte(bytes + page * a.scale_page + block));
                 };
                 byte_of(g.step0, page_of(g.step0));
-                int page = page_of(g.step0 + 1), unit = -1, most = 0;  // of v: O's unit, the largest byte so far
+                int page = page_of(g.step0 + 1), unit = -1, most = 0, room = 0;  // of v: O's unit is 2^-room of `unit`; the largest byte so far
                 for (int step = g.step0; step < g.step1; ++step) {
                     const uint32_t nan = __ballot_sync(0xffffffffu, byte == 255) & 0xffff;
                     const int own = byte == 255 ? -1 : byte;
                     const int top_k = __reduce_max_sync(0xffffffffu, lane < 8 ? own : -1);
                     const int top_v = __reduce_max_sync(0xffffffffu, of_v ? own : -1);
                     most = max(most, top_v);
-                    if (top_v > unit || (top_v >= 0 && top_v < unit - 8 && top_v >= most - 60)) unit = top_v;
+                    if (top_v > unit || (top_v >= 0 && top_v < unit - 8 && top_v >= most - 60)) {
+                        unit = top_v;
+                        room = 0;
+                    }
+                    // kHeadroom where a scale needs it; O keeps its until its unit changes
+                    const bool deep_k = __any_sync(0xffffffffu, lane < 8 && own >= 0 && own < top_k - kDeep);
+                    if (__any_sync(0xffffffffu, of_v && own >= 0 && own < unit - kDeep)) room = kHeadroom;
                     // 2^(own - its unit) in fp16, 1 for a group without a scale
-                    const int unit_k = max(top_k - kHeadroom, 0), unit_v = max(unit - kHeadroom, 0);
+                    const int unit_k = max(top_k - (deep_k ? kHeadroom : 0), 0), unit_v = max(unit - room, 0);
                     const int d = own < 0 ? 0 : own - (of_v ? unit_v : unit_k);
                     const int rest = of_v ? min(max(d + 15, -100), 0) : 0, in = d - rest;
                     const uint32_t f = in >= -14 ? uint32_t(15 + in) << 10 : in >= -24 ? 1u << (24 + in) : 0u;

@@ -580,7 +580,11 @@ def _check_batch(batch, cache, batch_sizes, cache_sizes):
                              (*batch.sizes[:2], *batch_sizes[:2]))
         if batch.sizes[2]:
             raise ValueError("batch: not on the GPU")
-    if cache.sizes is not None:
+    if cache.sizes is None:  # put together by hand: the library reads as much as its own kind of cache holds
+        kind = MoEKVCacheQ8 if cache_sizes[4] == "8-bit" else MoEKVCache
+        if not isinstance(cache, kind):
+            raise ValueError(f"cache: a {kind.__name__}, not a {type(cache).__name__}")
+    else:
         if cache.sizes[0] < cache_sizes[0] or cache.sizes[1:5] != cache_sizes[1:5]:
             raise ValueError(f"cache: {cache.sizes[4]} {cache.sizes[:4]}, not {cache_sizes[4]} {cache_sizes[:4]}")
         if cache.sizes[5]:

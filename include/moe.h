@@ -656,9 +656,15 @@ MOE_API int moe_rope_append_q8(const moe_attn_shape *shape, const moe_rope *rope
 
 /*
  * moe_paged_attention over an 8-bit cache, with a window or (NULL) over all keys.
- * dtype is that of q and out; the cache's values enter the products unrounded (bf16: but for
- * bits below 2^-40 of the largest value within 128 keys, where scales differ that much, and bits of
- * q below 2^-38 of a row's largest element).
+ * dtype is that of q and out.  With fp32 the cache's values enter the products unrounded; with
+ * bf16 too, but for what lies far below the largest (a scale's largest value is 448 of it):
+ *   - bits of q below 2^-38 of the largest element of its row and head;
+ *   - where scales within 128 keys differ that much, bits of k below 2^-40 and parts of v below
+ *     2^-38 of the largest value of theirs;
+ *   - values of v below 2^-60 of the largest of the keys before them in the sequence, which may count
+ *     as 0, for a token that does not see that largest one too.  How the keys are split among the
+ *     GPU's blocks decides which do; equal calls give equal bits.
+ * and probabilities are rounded to fp16 (2^-11 of each) for the product with v.
  * The other arguments, and what is read, are those of moe_paged_attention and
  * moe_paged_attention_window.
  */

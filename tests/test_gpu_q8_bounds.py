@@ -70,3 +70,56 @@ def test_scales_apart(name):
         hold(bt, 16)
         if d % 5 == 1:
             hold(bt, 16, window=150, sinks=20)
+
+
+FAR = {
+    # heads, kv_heads, dim, chunk, keys, window (None: all keys, of which no token's scores choose the large ones)
+    "decode window": (4, 2, 128, 4, 400, 351),
+    "decode window, many rows": (16, 4, 64, 4, 400, 351),
+    "decode": (8, 2, 128, 1, 900, None),
+    "decode, many rows": (24, 2, 64, 1, 900, None),
+    "chunk window": (8, 1, 128, 200, 700, 455),
+    "chunk window dim 64": (16, 2, 64, 200, 700, 455),
+    "chunk": (8, 1, 128, 60, 700, None),
+    "chunk dim 64": (16, 2, 64, 60, 700, None),
+}
+
+
+@pytest.mark.parametrize("name", list(FAR))
+@pytest.mark.parametrize("power", [20, 36, 58, 75, 100])
+def test_values_that_lie_far_apart(name, power):
+    # keys 32 to 47 hold values 2^power larger than the others, those on to 255 nothing: with a window the first two
+    # tokens see two and one of them, without one nobody gives them weight
+    heads, kv_heads, dim, n, m, window = FAR[name]
+    bt = make_batch("bf16", heads, kv_heads, dim, 16, [n], [m], seed=power)
+    place = lambda p: (bt.table[0, p // 16].long(), slice(None), p % 16)  # noqa: E731
+    g = torch.Generator().manual_seed(1)
+    if window is None:
+        bt.q[:] = torch.randn(dim, generator=g).bfloat16()
+    for p in range(32, 256):
+        bt.v_cache[place(p)] *= 2.0 ** power if p < 48 else 0.0
+        if window is None and p < 48:
+            bt.k_cache[place(p)] = -16 * bt.q[0, 0].sign()  # scores of about -16 * 0.8 * sqrt(dim)
+    d = Dev(bt, 16)
+    d.attend(dim ** -0.5, window, 0)
+    assert d.errors() == 0
+    got = d.out.cpu().double()
+    assert got.isfinite().all()
+    out, tol = attention8(bt, dim ** -0.5, window)
+    seers = 2 if window else 0
+    assert ((got - out).abs() <= tol)[:seers].all()
+    if power < 60:  # the others as if the large values were not there
+        largest = 2 * max(float(bt.v_cache[place(p)].abs().max()) for p in range(32, 48))
+        for p in range(32, 48):
+            bt.v_cache[place(p)] = 0.0
+        out, tol = attention8(bt, dim ** -0.5, window)
+        # but for keys 0 to 31, which lie within 128 keys of the large ones: a tile of a chunk holds their values times 2^-15 in fp16
+        # and takes the rest into their probabilities, times 2^7, of which fp16 keeps what is above 2^-25: 2^-54 of the largest
+        # value.  In decode a pair of steps has one unit, and probabilities times 2^14 and a scale's distance to it lose what
+        # is below 2^-25: 2^-39.  A key's part is then off by that or, where it is smaller, by all of itself.
+        least = 2.0 ** (-54 if n * heads // kv_heads > 16 else -39) * largest
+        for p in range(m):
+            bt.v_cache[place(p)] = bt.v_cache[place(p)].abs().clamp(max=least) if p < 32 else 0.0
+        tol += attention8(bt, dim ** -0.5, window)[0]
+        over = ((got - out).abs() - tol)[seers:]
+        assert (over <= 0).all(), over.max()

@@ -41,3 +41,11 @@ def test_a_cache_put_together_by_hand_has_to_be_of_the_calls_kind(name, kind):
     else:
         with pytest.raises(ValueError, match="cache: a MoEKVCache"):
             _call(name, POINTERS[kind])
+
+
+@pytest.mark.parametrize("name", list(TAKES))
+def test_a_workspace_in_host_memory_is_refused(name):
+    with pytest.raises(ValueError, match="workspace: not on the GPU"):
+        _call(name, POINTERS[TAKES[name]], torch.zeros(1024, dtype=torch.uint8))  # too small: the library refuses it too
+    with pytest.raises(moe.MoEError):
+        _call(name, POINTERS[TAKES[name]], _on_gpu(torch.zeros(1024, dtype=torch.uint8)))

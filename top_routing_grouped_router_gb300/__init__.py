@@ -632,6 +632,8 @@ def moe_rope_append(shape, rope, q, k, v, cache, batch, q_out, positions=None, w
                 not positions.is_cuda):
             raise _wrong(("positions (contiguous)", positions, int32, (shape.n_tokens,)))
         positions = positions.data_ptr()
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace: not on the GPU")
     # elements between rows; heads that follow one another in rows far enough apart need no second look
     q_row, head, elem = q.stride()
     if head != dim or elem != 1 or q_row < wide:
@@ -664,6 +666,8 @@ def moe_paged_attention(shape, q, cache, batch, out, scale=None, lse=None, works
             not (q.is_cuda and out.is_cuda)):
         sizes = shape.n_tokens, shape.n_heads, dim
         raise _wrong(("q", q, dtype, sizes), ("out", out, dtype, sizes))
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace: not on the GPU")
     if lse is not None:
         fp32 = _torch_dtype(MOE_DT_F32)
         if not lse.is_contiguous():
@@ -717,6 +721,8 @@ def moe_rope_append_q8(shape, rope, q, k, v, cache, batch, q_out, positions=None
                 not positions.is_cuda):
             raise _wrong(("positions (contiguous)", positions, int32, (shape.n_tokens,)))
         positions = positions.data_ptr()
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace: not on the GPU")
     rc = (_lib or lib()).moe_rope_append_q8(
         at(shape), at(rope), q.data_ptr(), _head_rows(q, "q", dim, wide), k.data_ptr(), _head_rows(k, "k", dim, kv_wide),
         v.data_ptr(), _head_rows(v, "v", dim, kv_wide), at(cache), at(batch), positions, q_out.data_ptr(),
@@ -736,6 +742,8 @@ def _attend(name, shape, q, cache, cache_sizes, batch, window, out, scale, lse, 
             not (q.is_cuda and out.is_cuda)):
         sizes = shape.n_tokens, shape.n_heads, dim
         raise _wrong(("q", q, dtype, sizes), ("out", out, dtype, sizes))
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace: not on the GPU")
     if lse is not None:
         fp32 = _torch_dtype(MOE_DT_F32)
         if not lse.is_contiguous():

@@ -49,3 +49,10 @@ def test_a_workspace_in_host_memory_is_refused(name):
         _call(name, POINTERS[TAKES[name]], torch.zeros(1024, dtype=torch.uint8))  # too small: the library refuses it too
     with pytest.raises(moe.MoEError):
         _call(name, POINTERS[TAKES[name]], _on_gpu(torch.zeros(1024, dtype=torch.uint8)))
+
+
+@pytest.mark.parametrize("value,kept", [(5, 5), (2**31 - 1, 2**31 - 1), (2**31, 2**31 - 1), (2**32 + 5, 2**31 - 1), (2**62, 2**31 - 1),
+                                        (0, 0), (-1, -1), (-2**32 + 5, -1)])
+def test_windows_past_32_bits_do_not_wrap(value, kept):
+    w = moe.make_attn_window(value, value)
+    assert (w.window, w.sinks) == (kept, kept)

@@ -478,7 +478,8 @@ def make_kv_cache_q8(k, v, k_scale, v_scale) -> MoEKVCacheQ8:
 
 def make_attn_window(window, sinks=0) -> MoEAttnWindow:
     """A token sees the `window` keys up to its own, and the sequence's first `sinks` keys."""
-    return MoEAttnWindow(int(window), int(sinks))
+    fit = lambda x: max(-1, min(int(x), (1 << 31) - 1))  # noqa: E731 -- no sequence is longer; below 0 stays refused
+    return MoEAttnWindow(fit(window), fit(sinks))
 
 
 def moe_rope_turns(rot_dim, scaling="none", base=10000.0, factor=1.0, trained_len=0):

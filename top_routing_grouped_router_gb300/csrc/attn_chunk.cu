@@ -35,8 +35,8 @@
 // 2048 tokens over 16384 keys, 32 heads: 424 us in a row of calls (1215 TFLOP/s), the join among them.  The bound is the same
 // chain: a tile's softmax takes 2450 cycles, since the launch's 512 threads leave it 128 registers and it takes its
 // scores in two halves, each with its own wait for TMEM; with the tile's products (1024) and barriers that makes
-// about 3900 a step of both tiles.  The conversion (1257 cycles a tile) runs beside it.  No unit is full: issue
-// slots 52 %, ALU 41, shared memory 39, tensor pipe 52.
+// about 3900 a step of both tiles.  The conversion (1257 cycles a tile whose codes all have factors) runs beside it.  No
+// unit is full: issue slots 49 %, ALU 40, shared memory 39, tensor pipe 52.
 // What was slower (2048 tokens over 16384 keys): codes to bf16, 750 us; the scales in the softmax, by groups
 // of 16 keys, 624; the softmax twice over the scores, 505; codes converted by the softmax's warps, 542; loops over TMEM
 // unrolled, whose instructions then miss their cache, 536; half of P multiplied during the second half's softmax, 470; the next
@@ -71,8 +71,9 @@ template <int D, Mode kMode>
 struct Cfg {
     static constexpr bool kCodes = kMode == kQ8;
     // The third warpgroup gives up registers that the softmax takes, within the launch's: 8 x 32 x 208 + 4 x 32 x 80 is
-    // within 12 x 32 x 168.  With a fourth every thread has 128, which the compiler does not exceed whatever a warpgroup
-    // takes later (scores of a whole step in registers spilled: 657 us for 2048 tokens over 16384 keys).
+    // within 12 x 32 x 168.  With a fourth the launch gives every thread 128 and the kernel leaves it at that: scores of a
+    // whole step in registers spilled (657 us for 2048 tokens over 16384 keys), so they come in halves.  setmaxnreg
+    // would let the compiler give the softmax more, although the number that it reports stays the launch's; not tried.
     static constexpr int kThreads = kCodes ? 512 : 384, kLaunchRegs = kCodes ? 128 : 168;
     static constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
     static_assert(kCodes || 256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "");

@@ -1072,13 +1072,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
 // fewer than their number says: eight CTAs find places within one part of the chip only), and no
 // sequence with more than 8 steps a warp (104 pairs of up to 1819 keys, 14 steps: 13.8 us with
 // clusters of two, 12.2 scheduled; 40 pairs of up to 1989, clusters of four: 9.3, 9.6).
-// Where a window bounds the keys most pairs have as many, and a warp may have more steps: 12, and 40 if
-// there are more than 16 pairs (256 pairs, window 2048: 46.9 us with clusters of one, 51.3 scheduled; 64 pairs, 9000:
-// clusters of four 50.4, 55.0; but 4 pairs, 9000: 18.4, 16.1; over an 8-bit cache 27.7, 31.1; 28.8, 36.4; 12.4, 11.7).
+// Where a window bounds the keys most pairs have as many, and a warp may have more steps: 12, and 40 if there are more
+// than 16 pairs.  us of a call with clusters (their size), and scheduled:
+//   pairs  window   16 bits                8 bits
+//     256    2048   46.9 (1)      51.3     27.7    31.1
+//      64    9000   50.4 (4)      55.0     28.8    36.4
+//       4    9000   18.4 (8)      16.1     12.4    11.7      why eight stop at 12 steps (sixteen go on, below)
 // With a window or over an 8-bit cache up to eight pairs may have clusters of sixteen, which few parts of the chip hold
-// two of (16 pairs, window 300: 10.8 us, clusters of eight 5.4): 4 pairs, window 300: 5.2, 4.8; 1000: 5.5, 6.1; 4097: 8.5, 11.3;
-// 12000: 14.3, scheduled 16.7 (one pair, 14000: 15.6, 14.5); 8 pairs, 2500: 9.4, 8.8; 4097: 10.9, 11.5; 12000: 16.4, 17.4 (8 bits: 4.8, 4.7; 5.0, 5.5;
-// 6.8, 8.4; 10.3, 12.1; 7.2, 7.1; 8.0, 8.5; 12.1, 13.3).
+// two of (16 pairs, window 300: 10.8 us, clusters of eight 5.4).  us of a call with sixteen, and with eight (from 12000 on:
+// scheduled):
+//   pairs  window   16 bits                8 bits
+//       4     300   5.2            4.8     4.8      4.7
+//       4    1000   5.5            6.1     5.0      5.5      sixteen from 600 keys on
+//       4    4097   8.5           11.3     6.8      8.4
+//       4   12000   14.3          16.7     10.3    12.1
+//       1   14000   15.6          14.5     -        -        why sixteen stop at 12 steps too
+//       8    2500   9.4            8.8     7.2      7.1
+//       8    4097   10.9          11.5     8.0      8.5      sixteen from 3200 keys on
+//       8   12000   16.4          17.4     12.1    13.3
 template <Mode kMode>
 int cluster_of(const moe_attn_shape &s, int64_t keys) {
     const int64_t pairs = (int64_t)s.n_seqs * s.n_kv_heads;

@@ -11,9 +11,10 @@
 // largest, and then store the codes: k and v are read once.  (In registers, four tokens a lane, the kernel took
 // 184 of them, and q's blocks waited for one another: 4043 tokens 44 us; two tokens a lane 28.)  The
 // others rotate q, a token, four or sixteen at a time, and share a token's cosines and sines between its heads.
-// 4043 tokens, 32 + 4 heads of 128 with a norm: 21 us on the GPU (the bytes alone 11.7), 14.7 for q alone and 10.7 for k and v; both are
-// bound by instructions (67 for a row of q of 128 elements, 0.48 of the issue slots) and by chains of them that 16 warps an
-// SM do not cover.  8 tokens: 3.6 us, latency.
+// 4043 tokens, 32 + 4 heads of 128 with a norm: 21 us on the GPU (the bytes alone 11.7), 14.7 for q alone and 10.7 for k and v.  The bound
+// is latency: instructions (67 for a row of q of 128 elements) take 0.48 of the issue slots, in chains that 13.6 warps an SM do not
+// cover.  One launch gives q's blocks, with one row in flight a group of lanes, the shared memory of k's and v's (two blocks an SM) and the
+// registers of the larger part (113).  8 tokens: 3.6 us, latency.
 #include "q8.cuh"
 #include "rope.cuh"
 
@@ -114,7 +115,8 @@ __device__ __forceinline__ void rotate(uint64_t *f, const uint64_t *c, const uin
 
 // The angle's cosine and sine times mscale.  turn * pos modulo 2^64 is the fraction of a turn in units of 2^-64,
 // exact at every position; its upper half (pos as a signed number), in units of 2^-32 turn, is off by 1.5e-9
-// radians at most, a fortieth of fp32's half step next to 1.
+// radians at most.  Beside that fp32 rounds the angle, as it does in the append to a 16-bit cache: by up to 9.4e-8
+// radians next to half a turn.
 __device__ __forceinline__ void angle(uint64_t turn, int pos, float mscale, float &c, float &s) {
     const uint32_t lo = uint32_t(turn), hi = uint32_t(turn >> 32), p = uint32_t(pos);
     const uint32_t part = hi * p + __umulhi(lo, p) - (pos < 0 ? lo : 0u);

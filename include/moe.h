@@ -596,7 +596,9 @@ typedef struct {
  * p = kv_len - n + j, sees the keys of its window and the first keys only.
  * Pages that hold no key that a token of the chunk sees are not read, nor are
  * their entries of block_table: a caller may give such pages back.  Slots that
- * no token of the chunk sees may hold anything, on the other pages too.
+ * no token of the chunk sees may hold anything, on the other pages too.  A k that
+ * is not finite reaches the tokens that see it, a v any token of its sequence's
+ * chunk (as 0 * NaN in the formula).
  * Arguments, workspace (moe_attn_workspace_size), types and errors are those of
  * moe_paged_attention, plus MOE_ERR_NULLPTR for a NULL window.
  */

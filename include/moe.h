@@ -663,9 +663,10 @@ MOE_API int moe_rope_append_q8(const moe_attn_shape *shape, const moe_rope *rope
  *   - bits of q below 2^-38 of the largest element of its row and head;
  *   - where scales within 128 keys differ that much, bits of k below 2^-40 and parts of v below
  *     2^-38 of the largest value of theirs;
- *   - values of v below 2^-60 of the largest of the keys before them in the sequence, which may count
- *     as 0, for a token that does not see that largest one too.  How the keys are split among the
- *     GPU's blocks decides which do; equal calls give equal bits.
+ *   - values of v below 2^-60 of the largest of the keys before them in the sequence, or below 2^-100
+ *     of the largest of those after them, which may count as 0, for a token that does not see that
+ *     largest one too.  How the keys are split among the GPU's blocks decides which do; equal calls
+ *     give equal bits.
  * Probabilities are rounded to fp16 (2^-11 of each) for the product with v then.
  * The tensor cores take bf16 with heads of 64 or 128, blocks of 16 tokens or a multiple and, for more
  * than 16 query rows a key head, pages of 16, 32, 64 or a multiple of 128.  Everything else (a scale for

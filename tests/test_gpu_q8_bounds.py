@@ -123,3 +123,44 @@ def test_values_that_lie_far_apart(name, power):
         tol += attention8(bt, dim ** -0.5, window)[0]
         over = ((got - out).abs() - tol)[seers:]
         assert (over <= 0).all(), over.max()
+
+
+BEFORE = {
+    # heads, kv_heads, dim, chunk, keys: the last block of 16 keys holds large values, which only its own tokens see
+    "decode": (4, 2, 128, 4, 401),
+    "decode, many rows": (16, 4, 64, 4, 401),
+    "decode long": (4, 2, 128, 4, 6001),
+    "decode long, many rows": (16, 4, 64, 4, 6001),
+    "chunk": (8, 1, 128, 60, 700),
+    "chunk dim 64": (16, 2, 64, 60, 700),
+    "chunk cut": (8, 1, 128, 60, 3000),
+}
+
+
+@pytest.mark.parametrize("name", list(BEFORE))
+@pytest.mark.parametrize("power", [60, 90, 126, 127, 128, 135, 180])
+def test_small_values_before_large_ones(name, power):
+    # values of 2^-90 and, 2^power larger, those of the last block
+    heads, kv_heads, dim, n, m = BEFORE[name]
+    bt = make_batch("bf16", heads, kv_heads, dim, 16, [n], [m], seed=power)
+    start = (m - 1) // 16 * 16
+    place = lambda p: (bt.table[0, p // 16].long(), slice(None), p % 16)  # noqa: E731
+    for p in range(m):
+        bt.v_cache[place(p)] *= 2.0 ** (-90 if p < start else power - 90)
+    d = Dev(bt, 16)
+    d.attend(dim ** -0.5)
+    assert d.errors() == 0
+    got = d.out.cpu().double()
+    seers = n - (m - start)  # the first row that sees the large values
+    out, tol = attention8(bt, dim ** -0.5)
+    assert ((got - out).abs() <= tol)[seers:].all()
+    # the rows before: right, but for the keys that lie within 128 of the large ones, which may count as 0 (and, once they are
+    # less than 2^-100 of them, all of them: fp32 then holds no part of them in units of the large ones)
+    for p in range(start, m):
+        bt.v_cache[place(p)] = 0.0
+    out, tol = attention8(bt, dim ** -0.5)
+    for p in range(m):
+        bt.v_cache[place(p)] = bt.v_cache[place(p)].abs() if start - 128 <= p < start or power > 100 else 0.0
+    tol += attention8(bt, dim ** -0.5)[0]
+    over = ((got - out).abs() - tol)[:seers]
+    assert (over <= 0).all(), over.max()

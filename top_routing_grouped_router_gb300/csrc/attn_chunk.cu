@@ -1150,9 +1150,9 @@ __global__ void __launch_bounds__((Cfg<D, kMode>::kThreads), 1) chunk_kernel(con
                             if (step == g.step0 && h == 0) {
                                 m = mn;
                             } else if (__any_sync(0xffffffffu, live && mn - m > kLag) || (h == 0 && unit_v != old_unit)) {
-                                // as over a bf16 cache, and with the change of O's unit
+                                // as over a bf16 cache, and with the change of O's unit (by 2^-127 and less to 0)
                                 const float f = mn == kNegInf ? 1.f : ex2(m - mn);
-                                const float fu = h ? f : f * __uint_as_float(uint32_t(min(max(old_unit - unit_v, -126), 127) + 127) << 23);
+                                const float fu = h ? f : f * __uint_as_float(uint32_t(min(max(old_unit - unit_v, -127), 127) + 127) << 23);
                                 m = mn;
                                 l *= f;
                                 sum_l *= f;

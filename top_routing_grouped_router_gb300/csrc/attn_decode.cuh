@@ -110,7 +110,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// 2^e, -126 <= e <= 127
+// 2^e, -126 <= e <= 127; 0 for -127: what a sum in units of less than that of the new one becomes
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 // 2^x by the hardware unit (relative error about 2^-22; 0 for -inf).
 __device__ __forceinline__ float ex2(float x) {
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
             most_v = max(most_v, top);
             if (top > unit_v || (top >= 0 && top < unit_v - 6 && top >= most_v - 60)) unit_v = top;
             if (__any_sync(0xffffffffu, x0 != m0 || x1 != m1) || unit_v != old_unit) {
-                const float u = pow2(max(old_unit - unit_v, -126));
+                const float u = pow2(max(old_unit - unit_v, -127));
                 float f0 = ex2(m0 - z0), f1 = ex2(m1 - z1);
                 l0 *= f0;
                 l1 *= f1;
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(Args a, Pa
                 l0 *= f0;
                 l1 *= f1;
                 if constexpr (kMode == kQ8) {
-                    const float u = pow2(max(old_unit - unit_v, -126));
+                    const float u = pow2(max(old_unit - unit_v, -127));
                     f0 *= u;
                     f1 *= u;
                 }
